@@ -80,6 +80,10 @@ extern "C" {
                                        pkv_attention_options did not hold for
                                        some request; it was attended without
                                        the hint (results unaffected)            */
+#define PKV_DEVERR_NO_BLOCKS 0x20u  /* pkv_build_step_tables: the free queue
+                                       held too few blocks for some request      */
+#define PKV_DEVERR_REF_COUNT 0x40u  /* pkv_release_blocks: a block was released
+                                       more often than it was held               */
 
 /* Shape of the physical pool. */
 typedef struct pkv_cache_layout {
@@ -88,6 +92,37 @@ typedef struct pkv_cache_layout {
   int32_t num_kv_heads; /* kv heads per token                                 */
   int32_t head_dim;     /* 64 or 128                                          */
 } pkv_cache_layout;
+
+/* Scores and masks other than plain causal attention. For the query row t of
+ * request r at position p = num_computed_tokens[r] + i (t = query_start_loc[r]
+ * + i) and q head h, with x_j = scale * q . k_j:
+ *   score_j = cap(x_j) - alibi_slopes[h] * |p - j|,
+ *   cap(x)  = softcap * tanh(x / softcap), or x when softcap is 0,
+ * and the softmax runs over the keys key_begin[t] <= j < key_end[t]. A row
+ * whose range holds no key gets zeros. The ranges state, among others,
+ *   - documents packed into one sequence: key_begin = the start of the
+ *     document that holds p;
+ *   - a prefix that is seen in both directions: key_end = max(p + 1, prefix
+ *     length);
+ *   - a sliding window of W tokens: key_begin = p - W + 1;
+ *   - padding that sees nothing: key_end <= key_begin.
+ * The cache blocks in front of a row's (or a tile of rows') first key and
+ * behind its last one are not read: their table entries may be stale or -1.
+ * Masked keys never reach the output, whatever their K and V rows hold.
+ * Every field is off at zero. The pages name no such scores; the entry points
+ * are those of plain attention (pkv_attention_options). */
+typedef struct pkv_score_options {
+  float softcap;             /* 0 = off, else softcap and scale / softcap both in
+                                [1e-30, 1e30] (else PKV_ERR_BAD_SHAPE)          */
+  const float* alibi_slopes; /* device fp32 [num_q_heads], finite; NULL = off   */
+  const int32_t* key_begin;  /* device int32 [num_tokens]; NULL = 0; values
+                                below 0 count as 0                              */
+  const int32_t* key_end;    /* device int32 [num_tokens]; NULL = p + 1; values
+                                above seq_lens[r] count as seq_lens[r]. May lie
+                                past p + 1: the keys of the step's later tokens
+                                are in the cache by then                        */
+  int32_t reserved[4];       /* must be zero                                    */
+} pkv_score_options;
 
 /* Optional tuning and tracing of pkv_paged_attention; pass NULL for the
  * defaults. */
@@ -123,7 +158,10 @@ typedef struct pkv_attention_options {
   int32_t shared_prefix_len;
   int32_t shared_first_req;
   int32_t shared_num_reqs;
-  int32_t reserved[4]; /* must be zero */
+  /* [0]: 0, or PKV_OPTIONS_SCORES when the struct has the field `scores` below
+   * (a caller built before that field existed leaves it 0, and the library
+   * then does not read past trace_events). [1..3] must be zero. */
+  int32_t reserved[4];
   /* Tracing: NULL, or PKV_TRACE_EVENTS cudaEvent_t handles (as void*) owned
    * by the caller. The call records them on `stream` around its kernels:
    * [0] before the plan kernel, [1] before the prefill kernel, [2] before
@@ -132,7 +170,14 @@ typedef struct pkv_attention_options {
    * kernel is not needed). The events keep the kernels from overlapping
    * (see "Launches" above), so a traced call can be a little slower. */
   void** trace_events;
+  /* Capped, biased or range-masked scores; NULL = plain causal attention. Read
+   * only when reserved[0] is PKV_OPTIONS_SCORES. A shared-prefix hint may be
+   * given with it: the prefix is then attended once under each row's own
+   * scores and range. */
+  const pkv_score_options* scores;
 } pkv_attention_options;
+
+#define PKV_OPTIONS_SCORES 1
 
 #define PKV_TRACE_EVENTS 5
 

@@ -26,3 +26,4 @@ from .paged_oracle import (  # noqa: F401
     partial_attention,
     combine_partials,
 )
+from .scored_oracle import scored_attention  # noqa: F401

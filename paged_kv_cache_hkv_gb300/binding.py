@@ -27,6 +27,8 @@ DEVERR_BLOCK_RANGE = 0x2
 DEVERR_LENGTHS = 0x4
 DEVERR_TIMEOUT = 0x8
 DEVERR_SHARED = 0x10
+DEVERR_NO_BLOCKS = 0x20
+DEVERR_REF_COUNT = 0x40
 
 
 class pkv_cache_layout(ctypes.Structure):
@@ -37,10 +39,19 @@ class pkv_cache_layout(ctypes.Structure):
 PKV_TRACE_EVENTS = 5
 
 
+PKV_OPTIONS_SCORES = 1
+
+
+class pkv_score_options(ctypes.Structure):
+    _fields_ = [("softcap", c_float), ("alibi_slopes", c_void_p), ("key_begin", c_void_p),
+                ("key_end", c_void_p), ("reserved", c_i32 * 4)]
+
+
 class pkv_attention_options(ctypes.Structure):
     _fields_ = [("decode_splits", c_i32), ("shared_prefix_len", c_i32),
                 ("shared_first_req", c_i32), ("shared_num_reqs", c_i32),
-                ("reserved", c_i32 * 4), ("trace_events", ctypes.POINTER(c_void_p))]
+                ("reserved", c_i32 * 4), ("trace_events", ctypes.POINTER(c_void_p)),
+                ("scores", ctypes.POINTER(pkv_score_options))]
 
 
 _SIGNATURES = {
@@ -217,10 +228,32 @@ def pkv_copy_blocks(dst_pool, src_pool, block_pairs, stream=None):
         _ptr(block_pairs), block_pairs.shape[0], lay, _stream(stream)))
 
 
-def _options(decode_splits, trace_events=None, shared_prefix=None):
+def _scores(q, softcap, alibi_slopes, key_begin, key_end):
+    """pkv_score_options of a call on q [T, Hq, D] (None when all are off)."""
+    softcap = float(softcap or 0.0)
+    if softcap == 0.0 and alibi_slopes is None and key_begin is None and key_end is None:
+        return None
+    if alibi_slopes is not None:
+        _require(alibi_slopes, torch.float32, "alibi_slopes")
+        if alibi_slopes.shape != (q.shape[1],) or not alibi_slopes.is_contiguous():
+            raise ValueError("alibi_slopes must be a contiguous [Hq] tensor")
+    for t, n in ((key_begin, "key_begin"), (key_end, "key_end")):
+        if t is not None:
+            _require(t, torch.int32, n)
+            if t.shape != (q.shape[0],) or not t.is_contiguous():
+                raise ValueError(f"{n} must be a contiguous [T] tensor")
+    o = pkv_score_options()
+    o.softcap = softcap
+    o.alibi_slopes, o.key_begin, o.key_end = _ptr(alibi_slopes), _ptr(key_begin), _ptr(key_end)
+    o._keep = (alibi_slopes, key_begin, key_end)
+    return o
+
+
+def _options(decode_splits, trace_events=None, shared_prefix=None, scores=None):
     """Options struct (or None for the defaults). shared_prefix: None, or
-    (shared_prefix_len, shared_first_req, shared_num_reqs) -- see pagedkv.h."""
-    if decode_splits is None and trace_events is None and shared_prefix is None:
+    (shared_prefix_len, shared_first_req, shared_num_reqs) -- see pagedkv.h;
+    scores: None, or what _scores returns."""
+    if decode_splits is None and trace_events is None and shared_prefix is None and scores is None:
         return None
     o = pkv_attention_options()
     o.decode_splits = int(decode_splits or 0)
@@ -235,6 +268,10 @@ def _options(decode_splits, trace_events=None, shared_prefix=None):
         arr = (c_void_p * PKV_TRACE_EVENTS)(*[c_void_p(h) for h in handles])
         o.trace_events = ctypes.cast(arr, ctypes.POINTER(c_void_p))
         o._keep = arr
+    if scores is not None:
+        o.reserved[0] = PKV_OPTIONS_SCORES
+        o.scores = ctypes.pointer(scores)
+        o._keep_scores = scores
     return ctypes.pointer(o)
 
 
@@ -253,11 +290,14 @@ def pkv_attention_workspace_size(num_reqs: int, num_q_heads: int, kv_cache,
 def pkv_paged_attention(out, q, kv_cache, block_table, seq_lens, query_start_loc,
                         num_computed_tokens, *, max_query_len: int, max_seq_len: int,
                         scale: float, workspace, decode_splits=None, trace_events=None,
-                        shared_prefix=None, stream=None):
+                        shared_prefix=None, softcap=0.0, alibi_slopes=None, key_begin=None,
+                        key_end=None, stream=None):
     """out [T, Hq, D] bf16 <- attention of one mixed step (see pagedkv.h).
 
     trace_events: optional list of PKV_TRACE_EVENTS torch.cuda.Event (created
-    with enable_timing=True) recorded around the call's kernels."""
+    with enable_timing=True) recorded around the call's kernels.
+    softcap, alibi_slopes (fp32 [Hq]), key_begin, key_end (int32 [T]): capped,
+    biased or range-masked scores (pkv_score_options in pagedkv.h)."""
     for t, n in ((out, "out"), (q, "q"), (kv_cache, "kv_cache")):
         _require(t, torch.bfloat16, n)
     for t, n in ((block_table, "block_table"), (seq_lens, "seq_lens"),
@@ -274,7 +314,8 @@ def pkv_paged_attention(out, q, kv_cache, block_table, seq_lens, query_start_loc
         block_table.shape[1], _ptr(seq_lens), _ptr(query_start_loc), _ptr(num_computed_tokens),
         seq_lens.shape[0], q.shape[0], int(max_query_len), int(max_seq_len), q.shape[1],
         float(scale), lay, _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _options(decode_splits, trace_events, shared_prefix), _stream(stream)))
+        _options(decode_splits, trace_events, shared_prefix,
+                 _scores(q, softcap, alibi_slopes, key_begin, key_end)), _stream(stream)))
     return out
 
 
@@ -282,10 +323,12 @@ def pkv_paged_attention_with_write(out, q, kv_cache, key, value, block_table, se
                                    query_start_loc, num_computed_tokens, *, max_query_len: int,
                                    max_seq_len: int, scale: float, workspace, slot_mapping=None,
                                    decode_splits=None, trace_events=None, shared_prefix=None,
+                                   softcap=0.0, alibi_slopes=None, key_begin=None, key_end=None,
                                    stream=None):
     """The step of one layer in one call: slot mapping and cache write of the
     new tokens, then attention (see pagedkv.h). slot_mapping (int64 [T])
-    receives the slots when given."""
+    receives the slots when given. softcap, alibi_slopes, key_begin, key_end:
+    as in pkv_paged_attention."""
     for t, n in ((out, "out"), (q, "q"), (kv_cache, "kv_cache"), (key, "key"),
                  (value, "value")):
         _require(t, torch.bfloat16, n)
@@ -309,7 +352,8 @@ def pkv_paged_attention_with_write(out, q, kv_cache, key, value, block_table, se
         _ptr(seq_lens), _ptr(query_start_loc), _ptr(num_computed_tokens), seq_lens.shape[0],
         q.shape[0], int(max_query_len), int(max_seq_len), q.shape[1], float(scale), lay,
         _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _options(decode_splits, trace_events, shared_prefix), _stream(stream)))
+        _options(decode_splits, trace_events, shared_prefix,
+                 _scores(q, softcap, alibi_slopes, key_begin, key_end)), _stream(stream)))
     return out
 
 
@@ -324,7 +368,9 @@ def pkv_get_device_errors(clear: bool = True, stream=None) -> int:
 def pkv_paged_attention_static_workspace(out, q, kv_cache, block_table, seq_lens,
                                          query_start_loc, num_computed_tokens, *,
                                          max_query_len: int, max_seq_len: int, scale: float,
-                                         decode_splits=None, shared_prefix=None, stream=None):
+                                         decode_splits=None, shared_prefix=None, softcap=0.0,
+                                         alibi_slopes=None, key_begin=None, key_end=None,
+                                         stream=None):
     """pkv_paged_attention without a caller workspace: for callers that cannot
     allocate device memory, the library uses its built-in scratch array (see
     pagedkv.h for the size limit and the one-stream rule)."""
@@ -342,8 +388,9 @@ def pkv_paged_attention_static_workspace(out, q, kv_cache, block_table, seq_lens
         _ptr(out), _ptr(q), q.stride(0), _ptr(kv_cache), _ptr(block_table),
         block_table.shape[1], _ptr(seq_lens), _ptr(query_start_loc), _ptr(num_computed_tokens),
         seq_lens.shape[0], q.shape[0], int(max_query_len), int(max_seq_len), q.shape[1],
-        float(scale), layout_of(kv_cache), _options(decode_splits, None, shared_prefix),
-        _stream(stream)))
+        float(scale), layout_of(kv_cache),
+        _options(decode_splits, None, shared_prefix,
+                 _scores(q, softcap, alibi_slopes, key_begin, key_end)), _stream(stream)))
     return out
 
 
@@ -363,7 +410,8 @@ class StepCalls:
     def __init__(self, *, slot_mapping, block_table, query_start_loc, num_computed_tokens,
                  kv_cache, key, value, out, q, seq_lens, max_query_len: int,
                  max_seq_len: int, scale: float, workspace, decode_splits=None,
-                 shared_prefix=None, fused_write=False, write_in_attention=False):
+                 shared_prefix=None, fused_write=False, write_in_attention=False, softcap=0.0,
+                 alibi_slopes=None, key_begin=None, key_end=None):
         _require(slot_mapping, torch.int64, "slot_mapping")
         for t, n in ((block_table, "block_table"), (query_start_loc, "query_start_loc"),
                      (num_computed_tokens, "num_computed_tokens"), (seq_lens, "seq_lens")):
@@ -378,7 +426,8 @@ class StepCalls:
             raise ValueError("out and block_table must be contiguous")
         lay = layout_of(kv_cache)
         self.lib = load()
-        self._opts = _options(decode_splits, None, shared_prefix)
+        self._opts = _options(decode_splits, None, shared_prefix,
+                              _scores(q, softcap, alibi_slopes, key_begin, key_end))
         self.slot_args = (
             _ptr(slot_mapping), _ptr(block_table), block_table.shape[1], _ptr(query_start_loc),
             _ptr(num_computed_tokens), num_computed_tokens.shape[0], slot_mapping.shape[0],

@@ -148,6 +148,36 @@ int32_t shared_hint(const pkv_attention_options* opt, const pkv_cache_layout& l,
   return PKV_OK;
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The score options of the call, checked: *scored = some field is in use.
+int32_t score_params(const pkv_attention_options* opt, float scale, pkv::ScoreParams* s,
+                     bool* scored) {
+  *s = pkv::ScoreParams{0.f, nullptr, nullptr, nullptr};
+  *scored = false;
+  if (!opt || opt->reserved[0] == 0) return PKV_OK;
+  if (opt->reserved[0] != PKV_OPTIONS_SCORES) return PKV_ERR_BAD_SHAPE;
+  const pkv_score_options* o = opt->scores;
+  if (!o) return PKV_OK;
+  for (int i = 0; i < 4; ++i)
+    if (o->reserved[i] != 0) return PKV_ERR_BAD_SHAPE;
+  // the kernels' factors softcap * log2(e) and 2 log2(e) scale / softcap stay
+  // normal fp32 numbers
+  if (o->softcap != 0.f) {
+    const float ratio = scale / o->softcap;
+    if (!(o->softcap >= 1e-30f && o->softcap <= 1e30f && ratio >= 1e-30f && ratio <= 1e30f))
+      return PKV_ERR_BAD_SHAPE;
+  }
+  if (!aligned4(o->alibi_slopes) || !aligned4(o->key_begin) || !aligned4(o->key_end))
+    return PKV_ERR_MISALIGNED;
+  s->softcap = o->softcap;
+  s->slopes = o->alibi_slopes;
+  s->key_begin = o->key_begin;
+  s->key_end = o->key_end;
+  *scored = s->softcap > 0.f || s->slopes || s->key_begin || s->key_end;
+  return PKV_OK;
+}
+
 struct WsLayout {
   size_t hdr, dec_prefix, pf_req, pf_prefix, part_ml, part_o, bound, casc_use, casc_ml, casc_o,
       total;
@@ -188,7 +218,8 @@ WsLayout ws_layout(int num_reqs, int virt_heads, int gw, int head_dim, long long
 int32_t decode_splits_for(DeviceInfo* d, int head_dim, int num_kv_heads, int group,
                           int block_size, const pkv_attention_options* opt, long long* splits) {
   if (opt) {
-    for (int i = 0; i < 4; ++i)
+    if (opt->reserved[0] != 0 && opt->reserved[0] != PKV_OPTIONS_SCORES) return PKV_ERR_BAD_SHAPE;
+    for (int i = 1; i < 4; ++i)
       if (opt->reserved[i] != 0) return PKV_ERR_BAD_SHAPE;
     if (opt->decode_splits < 0) return PKV_ERR_BAD_SHAPE;
     if (opt->decode_splits > 0) {
@@ -388,6 +419,9 @@ static int32_t attention_impl(void* out, const void* q, int64_t q_row_stride, co
       max_seq_len < 0)
     return PKV_ERR_BAD_SHAPE;
   if (!(scale > 0.f) || scale > 3.0e38f) return PKV_ERR_BAD_SHAPE;  // positive and finite
+  pkv::AttnArgs a;
+  st = score_params(options, scale, &a.score, &a.scored);
+  if (st != PKV_OK) return st;
   const int64_t row = static_cast<int64_t>(num_q_heads) * layout.head_dim;
   if (q_row_stride == 0) q_row_stride = row;
   if (q_row_stride < row) return PKV_ERR_BAD_SHAPE;
@@ -448,7 +482,6 @@ static int32_t attention_impl(void* out, const void* q, int64_t q_row_stride, co
   ws.casc_ml = reinterpret_cast<float2*>(wsb + wl.casc_ml);
   ws.casc_o = reinterpret_cast<float*>(wsb + wl.casc_o);
 
-  pkv::AttnArgs a;
   a.out = static_cast<uint16_t*>(out);
   a.q = static_cast<const uint16_t*>(q);
   a.q_stride = q_row_stride;

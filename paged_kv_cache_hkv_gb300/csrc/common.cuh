@@ -13,6 +13,8 @@ constexpr uint32_t kErrBlockRange = 0x2u;
 constexpr uint32_t kErrLengths = 0x4u;
 constexpr uint32_t kErrTimeout = 0x8u;
 constexpr uint32_t kErrShared = 0x10u;
+constexpr uint32_t kErrNoBlocks = 0x20u;
+constexpr uint32_t kErrRefCount = 0x40u;
 
 // The attention kernels move keys in chunks of 16 (one decode stage, one
 // MMA K step). A cache block holds 8, 16 or 32 tokens, so a chunk is two
@@ -238,6 +240,55 @@ __device__ __forceinline__ int warp_upper_index(const int32_t* a, int n, long lo
     lo = idx_k;
   }
   return lo;
+}
+
+// ---------------------------------------------------------------- scores
+constexpr float kLog2e = 1.4426950408889634f;
+
+// tanh of u for z = 2 log2(e) u. With e = 2^z = exp(2u): tanh u = 1 - 2 / (e + 1),
+// whose absolute error of a few 2^-24 is a relative error of the same size
+// only away from 0; below |u| = 1/4 the odd series u - u^3/3 + 2u^5/15 -
+// 17u^7/315 + 62u^9/2835 (next term below 1e-8 of the value) keeps it relative. A score
+// softcap * tanh(u) so carries an error of a few 2^-24 of its own size, whatever the cap.
+__device__ __forceinline__ float tanh_log2(float z) {
+  const float u = z * 0.34657359027997264f, w = u * u;  // ln(2) / 2
+  const float e = exp2f(z);
+  const float big = 1.f - __fdividef(2.f, e + 1.f);
+  const float small =
+      u * (1.f + w * (-1.f / 3 + w * (2.f / 15 + w * (-17.f / 315 + w * (62.f / 2835)))));
+  return fabsf(u) < 0.25f ? small : big;
+}
+
+// Capped, biased or range-masked scores (pkv_score_options), as the attention
+// kernels take them.
+struct ScoreParams {
+  float softcap;             // 0 = off
+  const float* slopes;       // distance bias per q head, or null
+  const int32_t* key_begin;  // first key of each query row, or null (0)
+  const int32_t* key_end;    // past the last key of each query row, or null (p + 1)
+};
+
+// Keys [lo, hi) that a row sees; lo == hi == 0 for a row that sees none.
+struct KeyRange {
+  int lo, hi;
+};
+
+// Range of batch row t at position pos of a sequence of L keys, its part from
+// key `base` on (the rest is attended elsewhere; 0 = all of it).
+__device__ __forceinline__ KeyRange row_keys(const ScoreParams& s, long long t, int pos, int L,
+                                             int base) {
+  int lo = s.key_begin ? __ldg(s.key_begin + t) : 0;
+  int hi = s.key_end ? __ldg(s.key_end + t) : pos + 1;
+  lo = max(lo, base);
+  hi = min(hi, L);
+  return lo < hi ? KeyRange{lo, hi} : KeyRange{0, 0};
+}
+
+// 16-key chunks that a decode row streams for its range. A row without keys
+// streams one masked chunk, so that its (zero) output is written like any
+// other's.
+__device__ __forceinline__ int range_chunks(const KeyRange& k) {
+  return k.lo < k.hi ? ((k.hi + kChunkKeys - 1) / kChunkKeys) - k.lo / kChunkKeys : 1;
 }
 
 }  // namespace pkv

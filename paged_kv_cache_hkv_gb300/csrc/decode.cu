@@ -78,6 +78,10 @@ struct DecodeParams {
   const int32_t* shared_use;
   const float2* shared_ml;
   const float* shared_o;
+  // Capped, biased or range-masked scores (the kernel's SCORED variant); with
+  // a cap, scale_log2 holds 2 log2(e) scale / softcap instead.
+  bool scored;
+  ScoreParams score;
 };
 
 // CTA that owns position x of the decode stream: ranges start at floor(c * N / C).
@@ -167,7 +171,10 @@ constexpr float kRescaleLog2 = 8.f;
 constexpr int kDecodeMaxSlab = 8;                        // virtual heads per CTA at most
 constexpr int kDecodeThreads = (kDecodeMaxSlab + 1) * 32;  // + the producer warp
 
-template <int D, int GW, int SH>
+// SCORED: the scores are capped, biased or masked by key ranges
+// (ScoreParams). A request then streams only the chunks that hold keys of its
+// row's range, and the metadata of a chunk carries the range's place in it.
+template <int D, int GW, int SH, bool SCORED>
 __global__ void __launch_bounds__(kDecodeThreads)
     decode_kernel(const __grid_constant__ CUtensorMap kv_map, const DecodeParams p) {
   using C = DecodeCfg<D, GW>;
@@ -219,10 +226,26 @@ __global__ void __launch_bounds__(kDecodeThreads)
   // the producer's first loads go out before the barrier: the first
   // request's lengths and the 32 block-table entries from its first chunk on
   int L = 0, t = 0, nent = 0, skip = 0, win_r = -1, win_base = 0, win_val = -1;
+  // SCORED: the row's keys [lo, L) (L is then the end of its range, not of the
+  // sequence) and the position its distances count from: the row's own,
+  // clamped into its range. Distances to the clamped position differ from the
+  // true ones by a constant over the range, which leaves the softmax; they
+  // stay small, so that a bias of slope * distance keeps its precision where
+  // a row sees only keys far from it.
+  int lo = 0, ref = 0;
+  auto set_range = [&](int rr, int tt, int seq_len) {
+    const KeyRange k =
+        row_keys(p.score, tt, seq_len - 1, seq_len, chunk_off(rr) * kChunkKeys);
+    const KeyRange all = row_keys(p.score, tt, seq_len - 1, seq_len, 0);
+    lo = k.lo;
+    L = k.hi;
+    ref = max(min(seq_len - 1, all.hi - 1), all.lo);
+    return k.lo / kChunkKeys;  // the first chunk
+  };
   if (warp == VH) {
     L = __ldg(p.seq_lens + r);
     t = __ldg(p.qsl + r);
-    skip = chunk_off(r);  // chunk = blk + skip
+    skip = SCORED ? set_range(r, t, L) : chunk_off(r);  // chunk = blk + skip
     nent = (L + (1 << sh) - 1) >> sh;  // table entries the request uses
     win_r = r;
     win_base = entry_of(blk + skip);
@@ -253,7 +276,9 @@ __global__ void __launch_bounds__(kDecodeThreads)
         nx_pn = __ldg(p.dec_prefix + r + 2);
         nx_L = __ldg(p.seq_lens + r + 1);
         nx_t = __ldg(p.qsl + r + 1);
-        nx_off = chunk_off(r + 1);
+        nx_off = SCORED ? row_keys(p.score, nx_t, nx_L - 1, nx_L, chunk_off(r + 1) * kChunkKeys).lo /
+                              kChunkKeys
+                        : chunk_off(r + 1);
         const int e = entry_of(nx_off) + lane;
         nx_win = e < p.max_blocks
                      ? __ldg(p.block_table + static_cast<long long>(r + 1) * p.max_blocks + e)
@@ -288,7 +313,8 @@ __global__ void __launch_bounds__(kDecodeThreads)
         // attended elsewhere, leaves a partial for the combine kernel
         const long long a = pr;
         const long long cf = owner_cta(a, N, Cn), cl = owner_cta(a + nblk - 1, N, Cn);
-        out_base = (cf == cl && skip == 0) ? -1 : static_cast<int>((r + c) * p.virt_heads);
+        const bool partly = SCORED ? chunk_off(r) != 0 : skip != 0;
+        out_base = (cf == cl && !partly) ? -1 : static_cast<int>((r + c) * p.virt_heads);
       }
       // table entries of chunk blk: e0, and e0 + 1 for 8-token blocks
       const int ab = blk + skip;  // the chunk's place in the request
@@ -302,23 +328,33 @@ __global__ void __launch_bounds__(kDecodeThreads)
       }
       const int phys = __shfl_sync(0xffffffffu, win_val, e0 - win_base);
       const int nvalid = min(kChunkKeys, L - ab * kChunkKeys);
+      const int klo = SCORED ? max(0, lo - ab * kChunkKeys) : 0;  // visible: [klo, nvalid)
+      const bool none = SCORED && klo >= nvalid;                  // the row sees no key at all
       bool valid = phys >= 0 && phys < p.num_blocks;
+      bool first = true;    // 8-token blocks: keys 0..7 of the chunk are wanted
       bool second = false;  // 8-token blocks: the chunk's keys 8..15 exist
       int phys1 = -1;
       if constexpr (sh == 3) {
         phys1 = __shfl_sync(0xffffffffu, win_val, e_hi - win_base);
         second = nvalid > 8;
+        if constexpr (SCORED) {
+          first = klo < 8;
+          valid = valid || !first;
+        }
         if (second) valid = valid && phys1 >= 0 && phys1 < p.num_blocks;
       }
+      if (none) valid = false;
       const int flags = (new_piece ? kFirst : 0) | ((blk == nblk - 1 || x == x1 - 1) ? kLast : 0) |
                         (valid ? 0 : kInvalid);
       if (lane == 0) {
-        meta[s] = make_int4(flags, nvalid, t, out_base);
+        meta[s] = SCORED ? make_int4(flags | (klo << 8) | (max(nvalid, 0) << 16),
+                                     ref - ab * kChunkKeys, t, out_base)
+                         : make_int4(flags, nvalid, t, out_base);
         unsigned char* stage = base + s * lay.stage_bytes;
-        const uint32_t kv_tx = (sh == 3 && !second) ? lay.kv_bytes / 2 : lay.kv_bytes;
+        const uint32_t kv_tx = (sh == 3 && !(first && second)) ? lay.kv_bytes / 2 : lay.kv_bytes;
         const uint32_t q_tx = static_cast<uint32_t>(VH) * GW * D * 2u;
         const uint32_t tx = (valid ? kv_tx : 0u) + (new_piece ? q_tx : 0u);
-        if (!valid) atomicOr(&g_errors_decode, kErrBlockRange);
+        if (!valid && !none) atomicOr(&g_errors_decode, kErrBlockRange);
         if (tx) {
           fence_proxy_async_smem();
           mbar_arrive_expect_tx(&full[s], tx);
@@ -327,13 +363,13 @@ __global__ void __launch_bounds__(kDecodeThreads)
             const int hk0 = slab * KH;
             if constexpr (sh == 4) {  // K and V of the block: 32 consecutive rows
               tma_load_3d_hint(stage, &kv_map, 0, hk0, phys * 32, &full[s], l2_policy);
-            } else if constexpr (sh == 5) {  // half (blk & 1) of the K rows and of the V rows
-              const int row = phys * 64 + (blk & 1) * 16;
+            } else if constexpr (sh == 5) {  // half (ab & 1) of the K rows and of the V rows
+              const int row = phys * 64 + (ab & 1) * 16;
               tma_load_3d_hint(stage, &kv_map, 0, hk0, row, &full[s], l2_policy);
               tma_load_3d_hint(stage + 16 * lay.row_bytes, &kv_map, 0, hk0, row + 32, &full[s],
                                l2_policy);
             } else {  // two blocks of 8, each its 16 consecutive K and V rows
-              tma_load_3d_hint(stage, &kv_map, 0, hk0, phys * 16, &full[s], l2_policy);
+              if (first) tma_load_3d_hint(stage, &kv_map, 0, hk0, phys * 16, &full[s], l2_policy);
               if (second)
                 tma_load_3d_hint(stage + 16 * lay.row_bytes, &kv_map, 0, hk0, phys1 * 16, &full[s],
                                  l2_policy);
@@ -365,7 +401,7 @@ __global__ void __launch_bounds__(kDecodeThreads)
             nblk = nx_pn - pr;
             L = nx_L;
             t = nx_t;
-            skip = nx_off;
+            skip = SCORED ? set_range(r, t, L) : nx_off;
             nent = (L + (1 << sh) - 1) >> sh;
             win_r = r;
             win_base = entry_of(skip);
@@ -377,7 +413,7 @@ __global__ void __launch_bounds__(kDecodeThreads)
             } while (nblk == 0);
             L = __ldg(p.seq_lens + r);
             t = __ldg(p.qsl + r);
-            skip = chunk_off(r);
+            skip = SCORED ? set_range(r, t, L) : chunk_off(r);
             nent = (L + (1 << sh) - 1) >> sh;
           }
           prefetch_next();
@@ -406,6 +442,9 @@ __global__ void __launch_bounds__(kDecodeThreads)
   float2 o2[GW][4];  // unnormalised output, logical heads, dims li*8 .. li*8+7
   float m_run = -INFINITY, l_run = 0.f;  // for head hm of this lane
   const uint32_t RS = lay.row_bytes;    // bytes between stage rows
+  // SCORED: bias per key of distance and cap, both for base-2 scores
+  const float slope2 = SCORED && p.score.slopes ? __ldg(p.score.slopes + vg * GW + hm) * kLog2e : 0.f;
+  const float cap2 = SCORED ? p.score.softcap * kLog2e : 0.f;
 
   for (uint32_t s = 0, fph = 0;;) {  // ring slot, parity of its full barrier
     if (!mbar_wait(&full[s], fph)) {
@@ -414,7 +453,8 @@ __global__ void __launch_bounds__(kDecodeThreads)
     }
     const int4 m = meta[s];
     if (m.x & kEnd) break;
-    const int flags = m.x, nvalid = m.y, row = m.z, out_base = m.w;
+    const int flags = m.x, nvalid = SCORED ? (m.x >> 16) & 31 : m.y, row = m.z, out_base = m.w;
+    const int klo = SCORED ? (m.x >> 8) & 31 : 0;  // visible keys of the chunk: [klo, nvalid)
     const unsigned char* stage = base + s * lay.stage_bytes;
     const uint32_t kv_base = smem_u32(stage) + hk_local * D * 2 + li * 16;
 
@@ -461,7 +501,11 @@ __global__ void __launch_bounds__(kDecodeThreads)
 #pragma unroll
     for (int q = 0; q < C::NPL; ++q) {
       const int key = ((perm + q) % C::KPL) * C::KPI + sub;
-      sc[q] = (bvalid && key < nvalid) ? acc[q] : -INFINITY;
+      if constexpr (SCORED) {
+        if (p.score.softcap > 0.f) acc[q] = cap2 * tanh_log2(acc[q]);
+        acc[q] -= slope2 * fabsf(static_cast<float>(m.y - key));
+      }
+      sc[q] = (bvalid && key >= klo && key < nvalid) ? acc[q] : -INFINITY;
       lmax = fmaxf(lmax, sc[q]);
     }
 #pragma unroll
@@ -520,13 +564,13 @@ __global__ void __launch_bounds__(kDecodeThreads)
           for (int e = 0; e < 4; ++e) o2[h][e] = ffma2(p2, v2[e], o2[h][e]);
         }
       };
-      if (bvalid && nvalid == kChunkKeys) {
+      if (bvalid && nvalid == kChunkKeys && klo == 0) {
 #pragma unroll
         for (int j = 0; j < C::KPL; ++j) pv_key(j);
       } else {
 #pragma unroll
         for (int j = 0; j < C::KPL; ++j)
-          if (bvalid && j * C::KPI + sub < nvalid) pv_key(j);
+          if (bvalid && j * C::KPI + sub >= klo && j * C::KPI + sub < nvalid) pv_key(j);
       }
     }
     __syncwarp();
@@ -555,7 +599,7 @@ __global__ void __launch_bounds__(kDecodeThreads)
         for (int h = 0; h < GW; ++h) {
           const float2 ml = scr.hs[h];
           if (slot < 0) {
-            const float inv = 1.f / ml.y;
+            const float inv = SCORED && ml.y == 0.f ? 0.f : 1.f / ml.y;  // no key seen: zeros
             uint4 ov;
             ov.x = pack_bf16x2(o2[h][0].x * inv, o2[h][0].y * inv);
             ov.y = pack_bf16x2(o2[h][1].x * inv, o2[h][1].y * inv);
@@ -677,7 +721,7 @@ __global__ void __launch_bounds__(GW * 32) combine_kernel(const DecodeParams p) 
   }
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, off);
-  const float inv = 1.f / Ls;
+  const float inv = p.scored && Ls == 0.f ? 0.f : 1.f / Ls;  // no key seen: zeros
   const int row = __ldg(p.qsl + r);
   uint16_t* dst =
       p.out + (static_cast<long long>(row) * p.num_q_heads + vg * GW + h) * D + lane * E;
@@ -728,7 +772,7 @@ static size_t decode_smem_bytes(int kh, int vh, int stages, int ctas_per_sm) {
   return used > share ? used : share;
 }
 
-template <int D, int GW, int SH>
+template <int D, int GW, int SH, bool SCORED>
 static std::atomic<unsigned long long> g_decode_attr_done{0};
 
 // Launch shape of one decode instantiation on one device for a slab shape,
@@ -747,8 +791,12 @@ static std::mutex g_decode_prep_mu;
 template <int D, int GW, int SH>
 static cudaError_t decode_prepare(int kh, int vh, int num_sms, long long* splits, int* stages,
                                   size_t* smem) {
-  auto kern = decode_kernel<D, GW, SH>;
-  cudaError_t e = smem_attr_once(kern, 227 * 1024, g_decode_attr_done<D, GW, SH>);
+  auto kern = decode_kernel<D, GW, SH, false>;
+  cudaError_t e = smem_attr_once(kern, 227 * 1024, g_decode_attr_done<D, GW, SH, false>);
+  // the scored variant runs with the plain one's launch shape
+  if (e == cudaSuccess)
+    e = smem_attr_once(decode_kernel<D, GW, SH, true>, 227 * 1024,
+                       g_decode_attr_done<D, GW, SH, true>);
   if (e != cudaSuccess) return e;
   int dev = 0;
   e = cudaGetDevice(&dev);
@@ -791,7 +839,8 @@ static cudaError_t launch_decode_t(const DecodeParams& p, const CUtensorMap& kv_
   cudaError_t e = decode_prepare<D, GW, SH>(p.slab_kh, p.slab_vh, num_sms, nullptr, &q.stages, &smem);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(p.splits), static_cast<unsigned>(p.virt_heads / p.slab_vh));
-  e = launch_pdl(decode_kernel<D, GW, SH>, grid, dim3((p.slab_vh + 1) * 32), smem, stream, kv_map, q);
+  auto kern = p.scored ? decode_kernel<D, GW, SH, true> : decode_kernel<D, GW, SH, false>;
+  e = launch_pdl(kern, grid, dim3((p.slab_vh + 1) * 32), smem, stream, kv_map, q);
   if (e == cudaSuccess && trace) e = cudaEventRecord(static_cast<cudaEvent_t>(trace[3]), stream);
   if (e != cudaSuccess) return e;
   return launch_pdl(combine_kernel<D, GW>,
@@ -860,7 +909,10 @@ cudaError_t launch_decode(const AttnArgs& a, const AttnWorkspace& ws, const CUte
   p.virt_heads = a.num_kv_heads * p.head_groups;
   decode_slab(a.num_kv_heads, group, &p.slab_vh, &p.slab_kh);
   p.splits = splits;
-  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.scale_log2 = a.scale * kLog2e;
+  p.scored = a.scored;
+  p.score = a.score;
+  if (a.score.softcap > 0.f) p.scale_log2 = 2.f * kLog2e * (a.scale / a.score.softcap);
   p.dec_prefix = ws.dec_prefix;
   p.hdr = ws.hdr;
   p.part_ml = ws.part_ml;

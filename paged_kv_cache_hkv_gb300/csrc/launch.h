@@ -7,6 +7,8 @@
 
 #include <atomic>
 
+#include "common.cuh"
+
 namespace pkv {
 
 // Header words at the start of the attention workspace (written by the plan
@@ -56,6 +58,8 @@ struct AttnArgs {
   int shared_len, shared_first, shared_num;
   int shared_pieces, shared_tpp;
   long long decode_splits;  // CTAs along the decode stream (C)
+  bool scored;         // some field of score is in use: the kernels' scored variants run
+  ScoreParams score;
 };
 
 // Key pieces of the shared-prefix items: enough items to fill the device

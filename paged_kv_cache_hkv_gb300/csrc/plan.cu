@@ -75,7 +75,10 @@ __device__ __forceinline__ Int3 plan_counts(const AttnArgs& a, const AttnWorkspa
   } else if (n == 1) {
     v.a = static_cast<int>(nblk);
     const int i = r - a.shared_first;
-    if (a.shared_num > 0 && i >= 0 && i < a.shared_num && ws.casc_use[i])
+    const bool shared = a.shared_num > 0 && i >= 0 && i < a.shared_num && ws.casc_use[i];
+    if (a.scored)
+      v.a = range_chunks(row_keys(a.score, q0, c, L, shared ? a.shared_len : 0));
+    else if (shared)
       v.a -= a.shared_len / kChunkKeys;
   } else if (n > 1) {
     v.b = 1;

@@ -176,13 +176,26 @@ struct PrefillLayout {
   // then the item prefix int [kMetaReqs + 1]
   static constexpr uint32_t kMeta = kV + kVStages * kTileKV;
   static constexpr uint32_t kBar = kMeta + kMetaReqs * 16 + (kMetaReqs + 1) * 4 + 124;
-  static constexpr uint32_t kBytes = kBar + 512;
+  static constexpr uint32_t kBad = kBar + 512;  // BadKeys of three items
+  static constexpr uint32_t kBytes = kBad + 1024;
   static constexpr uint32_t kAlloc = kBytes + 1024;  // room to align the base
   static_assert(kAlloc <= 232448, "shared memory");
 };
 
+// SCORED: keys of an item whose V rows hold an infinity or a NaN and that some
+// of its rows may not see. Weight 0 times such a value is a NaN, so their
+// elements go into the tensor core as zeros and the rows that do see the key
+// get them back in the epilogue.
+constexpr int kMaxBadKeys = 80;
+struct BadKeys {
+  int count;  // above kMaxBadKeys: the list is not complete, every key is looked at
+  int key[kMaxBadKeys];
+};
+static_assert(3 * sizeof(BadKeys) <= 1024, "bad key area");
+
 struct PrefillParams {
   uint16_t* out;
+  const uint16_t* pool;
   const int32_t* block_table;
   int max_blocks;
   const int32_t* seq_lens;
@@ -199,6 +212,10 @@ struct PrefillParams {
   int shared_len, shared_first, shared_num, shared_pieces, shared_tpp;
   float2* shared_ml;
   float* shared_o;
+  // Capped, biased or range-masked scores (the kernel's SCORED variant)
+  ScoreParams score;
+  float cap_z;      // softcap: 2 log2(e) scale / softcap, S to the argument of tanh_log2
+  float post_mul;   // scores in registers to base-2 units: scale_log2, or 1 once capped or biased
 };
 
 // mbarriers. "commit" ones are arrived on by a tcgen05.commit of an MMA thread
@@ -220,6 +237,7 @@ struct PrefillShared {
   uint64_t iq_full[kItemQ];      // item id j published in item_q[j % kItemQ]
   uint64_t iq_free[kItemQ];      // 11 arrivals: every role has read it
   int item_q[kItemQ];
+  int4 item_keys[kItemQ];        // SCORED: TileKeys of the item
   uint32_t tmem;
   int abort;
 };
@@ -249,10 +267,11 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, vo
 // warp): item id number j of this CTA, or -1 after an abort. The calling
 // warp's lane 0 releases the slot once every lane has read it.
 __device__ __forceinline__ int take_item(PrefillShared& sh, int j, volatile int* abort,
-                                         bool whole_warp) {
+                                         bool whole_warp, int4* keys) {
   const int slot = j % kItemQ;
   if (!wait_or_abort(&sh.iq_full[slot], (j / kItemQ) & 1u, abort)) return -1;
   const int item = *reinterpret_cast<volatile int*>(&sh.item_q[slot]);
+  if (keys) *keys = sh.item_keys[slot];
   if (whole_warp) __syncwarp();
   if (!whole_warp || (threadIdx.x & 31) == 0) mbar_arrive(&sh.iq_free[slot]);
   return item;
@@ -270,7 +289,108 @@ struct PrefillItem {
   int kt0;     // first key tile (0, or a shared item's piece start)
   int piece;   // shared items: key piece, else -1
   long long bt_row;  // offset of the request's block table row
+  // SCORED items: first key that any row sees; a tile within [full_lo,
+  // full_hi) is seen by every row
+  int k_lo, full_lo, full_hi;
 };
+
+// Keys of row i of a SCORED item (i < m.n), clipped to what the item attends;
+// `ref` is the position its distances count from (see the decode kernel).
+struct RowKeys {
+  int lo, hi, ref;
+};
+__device__ __forceinline__ RowKeys item_row_keys(const PrefillParams& p, const PrefillItem& m,
+                                                 int i) {
+  RowKeys k{0, 0, 0};
+  if (i >= m.n) return k;
+  int L = m.c + m.n, pos = m.c + i;
+  if (m.piece >= 0) {  // a decode row over the shared prefix
+    L = __ldg(p.seq_lens + p.shared_first + i);
+    pos = L - 1;
+  }
+  const KeyRange r = row_keys(p.score, static_cast<long long>(m.q0) + i, pos, L, 0);
+  k.ref = max(min(pos, r.hi - 1), r.lo);
+  k.hi = m.piece >= 0 ? min(r.hi, p.shared_len) : r.hi;
+  k.lo = r.lo;
+  if (k.lo >= k.hi) k.lo = k.hi = 0;
+  return k;
+}
+
+// The item's keys over all its rows, by a whole warp: {first key that any row
+// sees, past the last one, the largest first key, the smallest end}.
+__device__ __forceinline__ int4 item_keys(const PrefillParams& p, const PrefillItem& m, int QT) {
+  int lo_min = 0x7fffffff, hi_max = 0, lo_max = 0, hi_min = 0x7fffffff;
+  const int i1 = min(m.i0 + QT, m.n);
+  for (int i = m.i0 + (threadIdx.x & 31); i < i1; i += 32) {
+    const RowKeys k = item_row_keys(p, m, i);
+    const bool none = k.lo >= k.hi;
+    lo_min = none ? lo_min : min(lo_min, k.lo);
+    hi_max = max(hi_max, k.hi);
+    lo_max = none ? 0x7fffffff : max(lo_max, k.lo);
+    hi_min = min(hi_min, k.hi);
+  }
+  lo_min = __reduce_min_sync(0xffffffffu, lo_min);
+  hi_max = __reduce_max_sync(0xffffffffu, hi_max);
+  lo_max = __reduce_max_sync(0xffffffffu, lo_max);
+  hi_min = __reduce_min_sync(0xffffffffu, hi_min);
+  return make_int4(hi_max > 0 ? lo_min : 0, hi_max, lo_max, hi_min);
+}
+
+// Zero the infinities and NaNs of 64 bf16 in shared memory; true if there were any.
+__device__ __forceinline__ bool zero_nonfinite(uint4* v4) {
+  // x * 0 is 0 or, for an infinity or a NaN, a NaN
+  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+  __nv_bfloat162 acc = zero;
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    uint4 v = v4[x];
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc = __hfma2(h[e], zero, acc);
+  }
+  if ((*reinterpret_cast<uint32_t*>(&acc) & 0x7fff7fffu) == 0u) return false;
+  for (int x = 0; x < 8; ++x) {
+    uint4 v = v4[x];
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
+      if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0x0000ffffu;
+    }
+    v4[x] = v;
+  }
+  return true;
+}
+
+// Add the infinities and NaNs of V elements d0 .. d0+31 of key j to o.
+__device__ __noinline__ void add_nonfinite(const PrefillParams& p, long long bt_row, int g, int D,
+                                           int j, int d0, uint32_t (&o)[32]) {
+  const int id = __ldg(p.block_table + bt_row + (j >> p.block_shift));
+  if (id < 0 || id >= p.num_blocks) return;
+  const long long r = ((static_cast<long long>(id) * 2 + 1) << p.block_shift) +
+                      (j & ((1 << p.block_shift) - 1));
+  const uint16_t* v = p.pool + (r * p.num_kv_heads + g) * D + d0;
+  for (int x = 0; x < 32; ++x) {
+    const uint32_t b = __ldg(v + x);
+    if ((b & 0x7f80u) == 0x7f80u)
+      o[x] = __float_as_uint(__uint_as_float(o[x]) + __uint_as_float(b << 16));
+  }
+}
+
+// Narrow an item to the key tiles that its rows see (at least one, so that
+// rows without keys are written too); a shared-prefix item keeps its piece's tiles.
+__device__ __forceinline__ void narrow_item(PrefillItem& m, const int4& keys) {
+  m.k_lo = keys.x;
+  m.full_lo = keys.z;
+  m.full_hi = keys.w;
+  if (m.piece >= 0) {
+    m.kv_len = min(m.kv_len, keys.y);
+  } else {
+    m.kv_len = keys.y;
+    m.kt0 = keys.x / kTileN;
+    m.nkv = max(1, (m.kv_len + kTileN - 1) / kTileN - m.kt0);
+  }
+}
 
 // Items of the k-th prefill request are numbered tile-major, longest tile
 // first: local index l -> kv head l % Hkv, tile ntile - 1 - l / Hkv. The
@@ -336,21 +456,31 @@ __device__ __forceinline__ PrefillItem prefill_item(const PrefillParams& p, int 
 
 // Block table entry e of the item's request if it holds keys < kv_len and its
 // id is in the pool, else -1.
+// SCORED: neither are entries in front of the item's first key.
+template <bool SCORED>
+__device__ __forceinline__ bool entry_used(const PrefillParams& p, const PrefillItem& m, int e) {
+  return (e << p.block_shift) < m.kv_len && (!SCORED || ((e + 1) << p.block_shift) > m.k_lo);
+}
+template <bool SCORED>
 __device__ __forceinline__ int entry_id(const PrefillParams& p, const PrefillItem& m, int e) {
-  if ((e << p.block_shift) >= m.kv_len) return -1;
+  if (!entry_used<SCORED>(p, m, e)) return -1;
   const int id = __ldg(p.block_table + m.bt_row + e);
   return (id >= 0 && id < p.num_blocks) ? id : -1;
 }
 
 // Chunk b (keys 16b .. 16b+15) of tile kt holds keys < kv_len, all of them in
-// blocks of the pool.
+// blocks of the pool (SCORED: the keys of [k_lo, kv_len) only).
+template <bool SCORED>
 __device__ __forceinline__ bool chunk_ok(const PrefillParams& p, const PrefillItem& m, int kt, int b) {
   const int k0 = kt * kTileN + b * kChunkKeys;
   if (k0 >= m.kv_len) return false;
   const int bsh = p.block_shift;
-  if (bsh == 4) return entry_id(p, m, k0 >> 4) >= 0;
-  if (bsh == 5) return entry_id(p, m, k0 >> 5) >= 0;
-  return entry_id(p, m, k0 >> 3) >= 0 && (k0 + 8 >= m.kv_len || entry_id(p, m, (k0 >> 3) + 1) >= 0);
+  if (bsh == 4) return entry_id<SCORED>(p, m, k0 >> 4) >= 0;
+  if (bsh == 5) return entry_id<SCORED>(p, m, k0 >> 5) >= 0;
+  const int e = k0 >> 3;
+  if (SCORED && !entry_used<true>(p, m, e)) return entry_id<true>(p, m, e + 1) >= 0;
+  return entry_id<SCORED>(p, m, e) >= 0 &&
+         (k0 + 8 >= m.kv_len || entry_id<SCORED>(p, m, e + 1) >= 0);
 }
 
 // Persistent CTAs; CTA b takes items b, b + gridDim.x, ... (items come
@@ -369,7 +499,13 @@ __device__ __forceinline__ bool chunk_ok(const PrefillParams& p, const PrefillIt
 //   warps 0..7: the softmax of every tile, 16 query rows per warp and half
 //            of each row per thread, and the item's epilogue (each thread
 //            normalises and writes half of its row's output columns).
-template <int D>
+//
+// SCORED: the scores are capped, biased or masked by key ranges
+// (ScoreParams). The K-copy warp finds the keys that an item's rows see and
+// publishes them with the item, so every role walks only those tiles; the
+// softmax warps transform their scores in registers and mask by each row's
+// own range.
+template <int D, bool SCORED>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
                    const PrefillParams p) {
@@ -402,6 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.iq_free[i], 11);
     }
     sh.abort = 0;
+    for (int i = 0; i < 3; ++i) reinterpret_cast<BadKeys*>(gbase + Lay::kBad)[i].count = 0;
     fence_barrier_init();
   }
   if (tid == 32 * 9) {
@@ -464,6 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int q_loads = 0;
     for (int it = 0; ok; ++it) {
       int item;
+      int4 keys = make_int4(0, 0, 0, 0);
       if (!is_v) {
         // the Q buffer is free once the previous item's last S is done; only
         // then is the next item claimed (work counter), so that items go to
@@ -475,17 +613,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int slot = it % kItemQ;
           if (it >= kItemQ) ok = wait_or_abort(&sh.iq_free[slot], ((it - kItemQ) / kItemQ) & 1u, abort_flag);
           if (ok) item = it == 0 ? first_claim : static_cast<int>(atomicAdd(&p.hdr[kHdrPrefillNext], 1u));
-          sh.item_q[slot] = item;
-          mbar_arrive(&sh.iq_full[slot]);
+          if constexpr (!SCORED) {
+            sh.item_q[slot] = item;
+            mbar_arrive(&sh.iq_full[slot]);
+          }
         }
         item = __shfl_sync(0xffffffffu, item, 0);
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if constexpr (SCORED) {  // publish the item with its keys
+          if (ok && valid(item))
+            keys = item_keys(p, prefill_item(p, n_req, item, QT, meta, meta_prefix), QT);
+          if (ln == 0) {
+            sh.item_q[it % kItemQ] = item;
+            sh.item_keys[it % kItemQ] = keys;
+            mbar_arrive(&sh.iq_full[it % kItemQ]);
+          }
+        }
       } else {
-        item = take_item(sh, it, abort_flag, true);
+        item = take_item(sh, it, abort_flag, true, SCORED ? &keys : nullptr);
         if (item < 0) ok = false;
       }
       if (!ok || !valid(item)) break;
-      const PrefillItem m = prefill_item(p, n_req, item, QT, meta, meta_prefix);
+      PrefillItem m = prefill_item(p, n_req, item, QT, meta, meta_prefix);
+      if constexpr (SCORED) narrow_item(m, keys);
       if (!is_v) {
         if (ln == 0) {
           fence_proxy_async_smem();
@@ -512,8 +662,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ka * E + E > win_base + 32) {
           win_base = ka * E;
           const int e = win_base + ln;
-          win_val = entry_id(p, m, e);
-          if (!is_v && (e << bsh) < m.kv_len && win_val < 0)
+          win_val = entry_id<SCORED>(p, m, e);
+          if (!is_v && entry_used<SCORED>(p, m, e) && win_val < 0)
             atomicOr(&g_errors_prefill, kErrBlockRange);
         }
         // lane j < E copies the K (or V) rows of table entry ka*E + j, kv
@@ -551,10 +701,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t T = 0;  // tiles of earlier items
       bool ok = true;
       for (int it = 0; ok; ++it) {
-        const int item = take_item(sh, it, abort_flag, false);
+        int4 keys;
+        const int item = take_item(sh, it, abort_flag, false, SCORED ? &keys : nullptr);
         if (item < 0) ok = false;
         if (!ok || !valid(item)) break;
-        const PrefillItem m = prefill_item(p, n_req, item, QT, meta, meta_prefix);
+        PrefillItem m = prefill_item(p, n_req, item, QT, meta, meta_prefix);
+        if constexpr (SCORED) narrow_item(m, keys);
         const int nkv = m.nkv;
         if (is_s) {
           ok = wait_or_abort(&sh.q_full, it & 1u, abort_flag);
@@ -629,13 +781,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     // chunk validity of tile kt of item m (lanes 0..7), read one tile ahead
     auto load_ids = [&](const PrefillItem& mm, int kt) -> int {
-      return (lane < 8 && kt < mm.nkv && chunk_ok(p, mm, mm.kt0 + kt, lane)) ? 1 : -1;
+      return (lane < 8 && kt < mm.nkv && chunk_ok<SCORED>(p, mm, mm.kt0 + kt, lane)) ? 1 : -1;
     };
-    int item = take_item(sh, 0, abort_flag, true);
+    int4 keys;
+    int item = take_item(sh, 0, abort_flag, true, SCORED ? &keys : nullptr);
     PrefillItem m{};
+    RowKeys rk{0, 0, 0};  // SCORED: the keys of this thread's row
     int next_id = -1;
     if (valid(item)) {
       m = prefill_item(p, n_req, item, QT, meta, meta_prefix);
+      if constexpr (SCORED) {
+        narrow_item(m, keys);
+        rk = item_row_keys(p, m, m.i0 + row / G);
+      }
       next_id = load_ids(m, 0);
     }
     for (int it = 0; ok && valid(item); ++it) {
@@ -643,6 +801,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int qi = m.i0 + row / G;                // query of this row
       const int lim = min(m.c + qi, m.kv_len - 1);  // last key this row may see
       float m_run = -INFINITY, l_run = 0.f;
+      // SCORED: bias per key of distance, base-2 scores
+      const float slope2 =
+          SCORED && p.score.slopes ? __ldg(p.score.slopes + m.g * G + row % G) * kLog2e : 0.f;
+      const float mul = SCORED ? p.post_mul : p.scale_log2;
       for (int kt = 0; kt < nkv; ++kt) {
         const uint32_t Tg = T + kt;
         const uint32_t b = Tg % kSBufs;
@@ -655,22 +817,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         // tile is visible iff j <= lim - 128 ka and its 16-key chunk was
         // loaded (chunk c = keys 16c .. 16c+15)
         const int ka = m.kt0 + kt;  // key tile (keys ka*128 ..)
-        const bool full = ka * kTileN + kTileN - 1 <= m.c + m.i0 && mask == 0xFFu;
+        const bool full =
+            mask == 0xFFu && (SCORED ? ka * kTileN >= m.full_lo && ka * kTileN + kTileN <= m.full_hi
+                                     : ka * kTileN + kTileN - 1 <= m.c + m.i0);
         // this thread's keys 64ch .. 64ch+63 of the tile: sr[0] the first 32
         uint32_t sr[2][32];
         tc::ld_half32<64>(t_s, sr[0]);
         tc::ld_half32<64>(t_s + 32, sr[1]);
         tc::wait32(sr[0]);
         tc::wait32(sr[1]);
+        if constexpr (SCORED) {
+          if (p.score.softcap > 0.f) {
+            const float cap2 = p.score.softcap * kLog2e;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                sr[q][i] = __float_as_uint(cap2 * tanh_log2(__uint_as_float(sr[q][i]) * p.cap_z));
+          } else if (p.score.slopes) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                sr[q][i] = __float_as_uint(__uint_as_float(sr[q][i]) * p.scale_log2);
+          }
+          if (p.score.slopes) {
+            const float d0 = static_cast<float>(ka * kTileN + 64 * ch - rk.ref);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                sr[q][i] = __float_as_uint(__uint_as_float(sr[q][i]) -
+                                           slope2 * fabsf(d0 + static_cast<float>(q * 32 + i)));
+          }
+        }
         if (!full) {  // invisible keys become -inf
-          const int jlim = lim - ka * kTileN - 64 * ch;
+          const int jlim = SCORED ? rk.hi - 1 - ka * kTileN - 64 * ch : lim - ka * kTileN - 64 * ch;
+          const int jlo = SCORED ? rk.lo - ka * kTileN - 64 * ch : 0;
           const uint32_t cm = mask >> (4 * ch);
 #pragma unroll
           for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const int j = q * 32 + i;
-              if (!(((cm >> (j >> 4)) & 1u) && j <= jlim)) sr[q][i] = __float_as_uint(-INFINITY);
+              if (!(((cm >> (j >> 4)) & 1u) && j <= jlim && (!SCORED || j >= jlo)))
+                sr[q][i] = __float_as_uint(-INFINITY);
             }
         }
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -682,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 max3f(mx4[(i >> 1) & 3], __uint_as_float(sr[q][i]), __uint_as_float(sr[q][i + 1]));
         float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         // (scale > 0 keeps the argmax; both threads of the row get the same bits)
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) * p.scale_log2;
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) * mul;
         if (__any_sync(0xffffffffu, mx > m_run + kRescaleLog2)) {
           const float m_new = fmaxf(m_run, mx);
           const float alpha = (m_new == -INFINITY) ? 1.f : exp2f(m_run - m_new);
@@ -711,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float2 ps4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                          make_float2(0.f, 0.f)};
         const float msub = (m_run == -INFINITY) ? 0.f : m_run;
-        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-msub, -msub);
+        const float2 sc2 = make_float2(mul, mul), nm2 = make_float2(-msub, -msub);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t pk[16];
@@ -730,7 +921,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // V rows of keys past kv_len or of chunks not loaded must be zero
         // (0 * NaN): for such a tile wait for its V copy first; thread (row,
         // ch) clears 64-element chunk ch of V row `row`
-        if (ka * kTileN + kTileN > m.kv_len || mask != 0xFFu) {
+        // SCORED: in a tile that some row does not see in full, the V rows that
+        // stay must be finite
+        if (SCORED ? !full : ka * kTileN + kTileN > m.kv_len || mask != 0xFFu) {
           const int slot = static_cast<int>(Tg % kVStages);
           // S(Tg) done only implies PV(Tg-3) done, so the slot's copy
           // barrier may be anywhere from V(Tg-2) pending to V(Tg) landed;
@@ -741,12 +934,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (ok) ok = wait_or_abort(&sh.v_full[slot], (Tg / kVStages) & 1u, abort_flag);
           if (!ok) break;
-          if (ch < DH && (ka * kTileN + row >= m.kv_len || !(mask >> (row >> 4) & 1u))) {
-            uint4* v4 = reinterpret_cast<uint4*>(gbase + Lay::kV + slot * Lay::kTileKV +
-                                                 (row >> 3) * Lay::kGroupBytes + ch * 1024 +
-                                                 (row & 7) * 128);
+          uint4* v4 = reinterpret_cast<uint4*>(gbase + Lay::kV + slot * Lay::kTileKV +
+                                               (row >> 3) * Lay::kGroupBytes + ch * 1024 +
+                                               (row & 7) * 128);
+          if (ch < DH && (ka * kTileN + row >= m.kv_len || !(mask >> (row >> 4) & 1u) ||
+                          (SCORED && ka * kTileN + row < m.k_lo))) {
 #pragma unroll
             for (int x = 0; x < 8; ++x) v4[x] = make_uint4(0, 0, 0, 0);
+          } else if (SCORED && ch < DH && zero_nonfinite(v4)) {
+            BadKeys& bad = reinterpret_cast<BadKeys*>(gbase + Lay::kBad)[it % 3];
+            const int i = atomicAdd(&bad.count, 1);
+            if (i < kMaxBadKeys) bad.key[i] = ka * kTileN + row;
           }
           fence_proxy_async_smem();
         }
@@ -757,7 +955,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---- the next item's id and metadata, while the last PV runs
-      const int item_n = take_item(sh, it + 1, abort_flag, true);
+      const RowKeys rk_cur = rk;
+      const int item_n = take_item(sh, it + 1, abort_flag, true, SCORED ? &keys : nullptr);
       if (item_n < 0) {  // aborted
         ok = false;
         break;
@@ -765,14 +964,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       PrefillItem m_next{};
       if (valid(item_n)) {
         m_next = prefill_item(p, n_req, item_n, QT, meta, meta_prefix);
+        if constexpr (SCORED) {
+          narrow_item(m_next, keys);
+          rk = item_row_keys(p, m_next, m_next.i0 + row / G);
+        }
         next_id = load_ids(m_next, 0);
       }
       // ---- epilogue: this thread's O columns HC*ch .. HC*ch + HC - 1 of its row
       ok = wait_or_abort(&sh.o_full, it & 1u, abort_flag);
       if (!ok) break;
+      int n_bad = 0;
+      BadKeys* bad = reinterpret_cast<BadKeys*>(gbase + Lay::kBad);
+      if constexpr (SCORED) {
+        // the item's bad keys, complete once every thread has published P of
+        // its last tile. Three lists: threads may already fill the next
+        // item's, and the one after it, which no thread reads any more and
+        // none fills before all have passed here, starts empty.
+        const uint32_t Tl = T + nkv - 1;
+        ok = wait_or_abort(&sh.p_ready[Tl % kSBufs], (Tl / kSBufs) & 1u, abort_flag);
+        if (!ok) break;
+        n_bad = *reinterpret_cast<volatile int*>(&bad[it % 3].count);
+        if (tid == 0) bad[(it + 2) % 3].count = 0;
+      }
       tc::fence_after_sync();
       const float l_tot = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
-      const float inv = 1.f / l_tot;
+      const float inv = SCORED && l_tot == 0.f ? 0.f : 1.f / l_tot;  // no key seen: zeros
       const bool store = qi < m.n;
       const int head = m.g * G + row % G;
       // shared-prefix items keep the row's partial (max, sum, unnormalised O)
@@ -787,6 +1003,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::ld_half32<HC>(t_lane + 32 * q, o);
         tc::wait32(o);
         if (!store) continue;
+        if (SCORED && n_bad > 0) {
+          const bool listed = n_bad <= kMaxBadKeys;
+          const int a0 = listed ? 0 : rk_cur.lo, a1 = listed ? n_bad : rk_cur.hi;
+          for (int i = a0; i < a1; ++i) {
+            const int j = listed ? bad[it % 3].key[i] : i;
+            if (j >= rk_cur.lo && j < rk_cur.hi)
+              add_nonfinite(p, m.bt_row, m.g, D, j, HC * ch + 32 * q, o);
+          }
+        }
         if (partial) {
           float4* d4 = reinterpret_cast<float4*>(p.shared_o + pslot * D + HC * ch + 32 * q);
 #pragma unroll
@@ -818,10 +1043,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
+template <int D, bool SCORED>
 static cudaError_t launch_prefill_t(const PrefillParams& p, const CUtensorMap& kv_map,
                                     const CUtensorMap& q_map, int grid, cudaStream_t stream) {
-  auto kern = prefill_kernel<D>;
+  auto kern = prefill_kernel<D, SCORED>;
   const int smem = static_cast<int>(PrefillLayout<D>::kAlloc);
   static std::atomic<unsigned long long> attr_done{0};
   cudaError_t e = smem_attr_once(kern, smem, attr_done);
@@ -834,6 +1059,7 @@ cudaError_t launch_prefill(const AttnArgs& a, const AttnWorkspace& ws, const CUt
                            const CUtensorMap& q_map, int num_sms, cudaStream_t stream) {
   PrefillParams p;
   p.out = a.out;
+  p.pool = static_cast<const uint16_t*>(a.kv_cache);
   p.block_table = a.block_table;
   p.max_blocks = a.max_blocks;
   p.seq_lens = a.seq_lens;
@@ -844,7 +1070,10 @@ cudaError_t launch_prefill(const AttnArgs& a, const AttnWorkspace& ws, const CUt
   p.group = a.num_q_heads / a.num_kv_heads;
   p.num_blocks = a.num_blocks;
   p.block_shift = a.block_shift;
-  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.scale_log2 = a.scale * kLog2e;
+  p.score = a.score;
+  p.cap_z = a.score.softcap > 0.f ? 2.f * kLog2e * (a.scale / a.score.softcap) : 0.f;
+  p.post_mul = a.score.softcap > 0.f || a.score.slopes ? 1.f : p.scale_log2;
   p.hdr = ws.hdr;
   p.pf_req = ws.pf_req;
   p.pf_prefix = ws.pf_prefix;
@@ -867,8 +1096,12 @@ cudaError_t launch_prefill(const AttnArgs& a, const AttnWorkspace& ws, const CUt
     max_items += (a.shared_num + tile_q - 1) / tile_q * a.shared_pieces * a.num_kv_heads;
   const int grid = static_cast<int>(max_items < num_sms ? max_items : num_sms);
   if (grid <= 0) return cudaSuccess;
-  if (a.head_dim == 128) return launch_prefill_t<128>(p, kv_map, q_map, grid, stream);
-  if (a.head_dim == 64) return launch_prefill_t<64>(p, kv_map, q_map, grid, stream);
+  if (a.head_dim == 128)
+    return a.scored ? launch_prefill_t<128, true>(p, kv_map, q_map, grid, stream)
+                    : launch_prefill_t<128, false>(p, kv_map, q_map, grid, stream);
+  if (a.head_dim == 64)
+    return a.scored ? launch_prefill_t<64, true>(p, kv_map, q_map, grid, stream)
+                    : launch_prefill_t<64, false>(p, kv_map, q_map, grid, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -46,14 +46,17 @@ class DeviceStep:
     """One step's inputs on the GPU plus its output buffers."""
 
     def __init__(self, step, device="cuda", decode_splits=None, upload_pool=True,
-                 shared_prefix=None, fused_write=False, write_in_attention=False):
+                 shared_prefix=None, fused_write=False, write_in_attention=False, softcap=0.0,
+                 alibi_slopes=None, key_begin=None, key_end=None):
         """shared_prefix: None, or (shared_prefix_len, shared_first_req,
         shared_num_reqs) for the attention call (see pagedkv.h); "auto" takes
         it from the step's shared prefix when its sharing requests form one
         contiguous run of decodes. fused_write: run() maps the slots and
         writes the rows in one launch (pkv_slot_mapping_and_write);
         write_in_attention: run() is the single call
-        pkv_paged_attention_with_write."""
+        pkv_paged_attention_with_write. softcap, alibi_slopes [Hq],
+        key_begin, key_end [T] (host arrays): capped, biased or range-masked
+        scores."""
         self.step = step
         self.device = torch.device(device)
         dev = self.device
@@ -75,6 +78,12 @@ class DeviceStep:
         if shared_prefix == "auto":
             shared_prefix = shared_prefix_of(step)
         self.shared_prefix = shared_prefix
+        self.scores = dict(
+            softcap=softcap,
+            alibi_slopes=None if alibi_slopes is None else torch.from_numpy(
+                np.ascontiguousarray(alibi_slopes, dtype=np.float32)).to(dev),
+            key_begin=None if key_begin is None else _i32(key_begin, dev),
+            key_end=None if key_end is None else _i32(key_end, dev))
         self.layout = binding.pkv_cache_layout(step.num_blocks, step.block_size,
                                                step.num_kv_heads, step.head_dim)
         nbytes = binding.pkv_attention_workspace_size(step.num_reqs, step.num_q_heads,
@@ -106,7 +115,7 @@ class DeviceStep:
             self.query_start_loc, self.num_computed, max_query_len=s.max_query_len,
             max_seq_len=s.max_seq_len, scale=s.scale, workspace=self.workspace,
             slot_mapping=self.slot_mapping, decode_splits=self.decode_splits,
-            shared_prefix=self.shared_prefix, stream=stream)
+            shared_prefix=self.shared_prefix, stream=stream, **self.scores)
 
     def attend(self, stream=None):
         s = self.step
@@ -114,7 +123,8 @@ class DeviceStep:
             self.out, self.q, self.kv_cache, self.block_table, self.seq_lens,
             self.query_start_loc, self.num_computed, max_query_len=s.max_query_len,
             max_seq_len=s.max_seq_len, scale=s.scale, workspace=self.workspace,
-            decode_splits=self.decode_splits, shared_prefix=self.shared_prefix, stream=stream)
+            decode_splits=self.decode_splits, shared_prefix=self.shared_prefix, stream=stream,
+            **self.scores)
 
     def run(self, stream=None):
         """The whole step: slot mapping, cache write (one launch with
@@ -137,7 +147,8 @@ class DeviceStep:
                 seq_lens=self.seq_lens, max_query_len=s.max_query_len,
                 max_seq_len=s.max_seq_len, scale=s.scale, workspace=self.workspace,
                 decode_splits=self.decode_splits, shared_prefix=self.shared_prefix,
-                fused_write=self.fused_write, write_in_attention=self.write_in_attention)
+                fused_write=self.fused_write, write_in_attention=self.write_in_attention,
+                **self.scores)
             self._calls_bufs = bufs
         return self._calls
 
