@@ -429,6 +429,94 @@ int32_t pkv_paged_attention_static_workspace(
     void* stream);
 
 /*
+ * pkv_build_step_tables -- the metadata of one step, built on the device from
+ * the requests' lengths: new blocks taken from the free queue and entered in
+ * the block tables, the batch's row starts, the sequence lengths and the slot
+ * of every new token ("vllm v1 源码精读（三）" §3.3: allocation pops blocks
+ * from the head of a free queue; §3.4: block table and slot mapping; "vLLM
+ * 架构源码解析（一）" §3.3.2: positions and lengths of the batch). The outputs
+ * are the arguments of pkv_paged_kv_write, pkv_paged_attention and
+ * pkv_paged_attention_with_write, so a step needs no block table from the host.
+ *
+ * Request r with c = num_computed_tokens[r] and n = query_lens[r] holds
+ * ceil(c / B) blocks and needs ceil((c + n) / B). Its new blocks are the next
+ * ones of the queue, in batch order, first come, first served: if the queue
+ * cannot cover what is asked for up to and including request r, then r and
+ * every later request that needs a block get none. Such a request keeps its
+ * rows in the batch but gets seq_lens 0, slots -1 and -1 in the entries asked
+ * for, and PKV_DEVERR_NO_BLOCKS is set; the attention call skips it (its rows
+ * are not written, PKV_DEVERR_LENGTHS).
+ *
+ * block_table      in/out, device int32 [num_reqs][max_blocks_per_req]: the
+ *                  entries [ceil(c / B), ceil((c + n) / B)) of each row are
+ *                  written, no others.
+ * query_start_loc  out, device int32 [num_reqs + 1].
+ * seq_lens         out, device int32 [num_reqs]: c + n.
+ * slot_mapping     out, device int64 [num_tokens], or NULL. Rows at or past
+ *                  query_start_loc[num_reqs] get -1.
+ * num_computed_tokens, query_lens   device int32 [num_reqs]. A negative length
+ *                  or a sequence of more than max_blocks_per_req blocks sets
+ *                  PKV_DEVERR_LENGTHS: the request keeps its rows (a negative
+ *                  query length counts as 0), with seq_lens 0 and slots -1, and
+ *                  takes no block. So does a batch of more than num_tokens
+ *                  rows; the rows past num_tokens have no slot.
+ * free_queue       device int32 [num_blocks], a ring of free block ids.
+ * free_state       device int32 [2]: the ring's head and how many ids it holds.
+ * free_state_out   out, device int32 [2]: the state after the step. May be
+ *                  free_state itself; another buffer leaves the queue as it
+ *                  was until the caller takes the new state over.
+ * ref_cnt          in/out, device int32 [num_blocks], or NULL: the new blocks
+ *                  get 1.
+ * A state or a queue entry out of range hands out nothing (PKV_DEVERR_LENGTHS,
+ * PKV_DEVERR_BLOCK_RANGE); so does -1 in the table where a request goes on in
+ * a block it should have. The call can be recorded into a CUDA graph. Calls
+ * that share a queue, its state, tables or counts must be ordered.
+ */
+int32_t pkv_build_step_tables(int32_t* block_table, int32_t max_blocks_per_req,
+                              int32_t* query_start_loc, int32_t* seq_lens, int64_t* slot_mapping,
+                              const int32_t* num_computed_tokens, const int32_t* query_lens,
+                              int32_t num_reqs, int32_t num_tokens, const int32_t* free_queue,
+                              const int32_t* free_state, int32_t* free_state_out,
+                              int32_t* ref_cnt, int32_t num_blocks, int32_t block_size,
+                              void* stream);
+
+/*
+ * pkv_release_blocks -- give back the blocks of requests that finished or
+ * were preempted ("vLLM 架构源码解析（一）" §4.3.1: a block returns to the pool
+ * when its reference count reaches zero; "vllm v1 源码精读（三）" §3.3: at the
+ * tail of the free queue).
+ *
+ * The rows are released in the order given, each from its last block to its
+ * first, so that the blocks at the head of a sequence, the ones a prefix is
+ * shared by, are reused last. Every entry counts its block down by one, and a
+ * block that reaches zero is appended to the queue at the place of its last
+ * release. The result does not depend on the order in which the device's threads run.
+ *
+ * block_table      device int32 [num_reqs][max_blocks_per_req], read only: the
+ *                  entries of a released row stay as they are.
+ * release_rows     device int32 [num_released]: rows of the table. Several
+ *                  may share blocks; a row may stand in it as often as its
+ *                  blocks are held.
+ * release_tokens   device int32 [num_reqs]: tokens whose blocks row r holds,
+ *                  ceil(release_tokens[r] / B) entries.
+ * free_queue       in/out, free_state in, free_state_out out: as in
+ *                  pkv_build_step_tables.
+ * ref_cnt          in/out, device int32 [num_blocks]: how many rows hold each
+ *                  block.
+ * A row or a length out of range is skipped (PKV_DEVERR_LENGTHS), as is an
+ * entry out of the pool (PKV_DEVERR_BLOCK_RANGE). A block that is released more
+ * often than it is held goes back once (PKV_DEVERR_REF_COUNT). num_released *
+ * max_blocks_per_req must stay below 2^29. The call can be recorded into a
+ * CUDA graph.
+ */
+int32_t pkv_release_blocks(const int32_t* block_table, int32_t max_blocks_per_req,
+                           int32_t num_reqs, const int32_t* release_rows,
+                           const int32_t* release_tokens, int32_t num_released,
+                           int32_t* free_queue, const int32_t* free_state,
+                           int32_t* free_state_out, int32_t* ref_cnt, int32_t num_blocks,
+                           int32_t block_size, void* stream);
+
+/*
  * pkv_get_device_errors -- checked path: synchronise `stream`, then return
  * in *flags the PKV_DEVERR_* bits that kernels on the current device have set
  * since the last clear; clear them when `clear` is nonzero.

@@ -27,3 +27,4 @@ from .paged_oracle import (  # noqa: F401
     combine_partials,
 )
 from .scored_oracle import scored_attention  # noqa: F401
+from .tables_oracle import build_step_tables, release_blocks, ring  # noqa: F401

@@ -79,6 +79,12 @@ _SIGNATURES = {
                 c_void_p, c_i32, c_void_p, c_void_p, c_void_p, c_i32, c_i32, c_i32, c_i32, c_i32,
                 c_float, pkv_cache_layout, c_void_p, c_size_t,
                 ctypes.POINTER(pkv_attention_options), c_void_p]),
+    "pkv_build_step_tables": (
+        c_i32, [c_void_p, c_i32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_i32, c_i32,
+                c_void_p, c_void_p, c_void_p, c_void_p, c_i32, c_i32, c_void_p]),
+    "pkv_release_blocks": (
+        c_i32, [c_void_p, c_i32, c_i32, c_void_p, c_void_p, c_i32, c_void_p, c_void_p, c_void_p,
+                c_void_p, c_i32, c_i32, c_void_p]),
     "pkv_paged_attention_static_workspace": (
         c_i32, [c_void_p, c_void_p, c_i64, c_void_p, c_void_p, c_i32, c_void_p, c_void_p,
                 c_void_p, c_i32, c_i32, c_i32, c_i32, c_i32, c_float, pkv_cache_layout,
@@ -392,6 +398,133 @@ def pkv_paged_attention_static_workspace(out, q, kv_cache, block_table, seq_lens
         _options(decode_splits, None, shared_prefix,
                  _scores(q, softcap, alibi_slopes, key_begin, key_end)), _stream(stream)))
     return out
+
+
+def _table_args(block_table, free_queue, free_state, free_state_out, ref_cnt):
+    """Checks of the arguments that pkv_build_step_tables and
+    pkv_release_blocks share; returns free_state_out (free_state when None)."""
+    if free_state_out is None:
+        free_state_out = free_state
+    for t, n in ((block_table, "block_table"), (free_queue, "free_queue"),
+                 (free_state, "free_state"), (free_state_out, "free_state_out"),
+                 (ref_cnt, "ref_cnt")):
+        if t is None and n == "ref_cnt":
+            continue
+        _require(t, torch.int32, n)
+        if not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [num_reqs, max_blocks]")
+    for t, n in ((free_state, "free_state"), (free_state_out, "free_state_out")):
+        if t.shape != (2,):
+            raise ValueError(f"{n} must be [2]: head and count")
+    if free_queue.dim() != 1 or (ref_cnt is not None and ref_cnt.shape != free_queue.shape):
+        raise ValueError("free_queue and ref_cnt must be [num_blocks]")
+    return free_state_out
+
+
+def _build_args(block_table, query_start_loc, seq_lens, slot_mapping, num_computed_tokens,
+                query_lens, free_queue, free_state, free_state_out, ref_cnt, block_size,
+                num_tokens):
+    free_state_out = _table_args(block_table, free_queue, free_state, free_state_out, ref_cnt)
+    R = block_table.shape[0]
+    for t, n, size in ((query_start_loc, "query_start_loc", R + 1), (seq_lens, "seq_lens", R),
+                       (num_computed_tokens, "num_computed_tokens", R),
+                       (query_lens, "query_lens", R)):
+        _require(t, torch.int32, n)
+        if t.shape != (size,) or not t.is_contiguous():
+            raise ValueError(f"{n} must be a contiguous [{size}] tensor")
+    if slot_mapping is not None:
+        _require(slot_mapping, torch.int64, "slot_mapping")
+        if slot_mapping.dim() != 1 or not slot_mapping.is_contiguous():
+            raise ValueError("slot_mapping must be a contiguous [T] tensor")
+        num_tokens = slot_mapping.shape[0]
+    elif num_tokens is None:
+        raise ValueError("num_tokens is needed without a slot_mapping")
+    return (_ptr(block_table), block_table.shape[1], _ptr(query_start_loc), _ptr(seq_lens),
+            _ptr(slot_mapping), _ptr(num_computed_tokens), _ptr(query_lens), R, int(num_tokens),
+            _ptr(free_queue), _ptr(free_state), _ptr(free_state_out), _ptr(ref_cnt),
+            free_queue.shape[0], int(block_size))
+
+
+def _release_args(block_table, release_rows, release_tokens, free_queue, free_state,
+                  free_state_out, ref_cnt, block_size):
+    if ref_cnt is None:
+        raise ValueError("a release needs ref_cnt")
+    free_state_out = _table_args(block_table, free_queue, free_state, free_state_out, ref_cnt)
+    for t, n in ((release_rows, "release_rows"), (release_tokens, "release_tokens")):
+        _require(t, torch.int32, n)
+        if t.dim() != 1 or not t.is_contiguous():
+            raise ValueError(f"{n} must be a contiguous 1-D tensor")
+    if release_tokens.shape[0] != block_table.shape[0]:
+        raise ValueError("release_tokens must be [num_reqs]")
+    return (_ptr(block_table), block_table.shape[1], block_table.shape[0], _ptr(release_rows),
+            _ptr(release_tokens), release_rows.shape[0], _ptr(free_queue), _ptr(free_state),
+            _ptr(free_state_out), _ptr(ref_cnt), free_queue.shape[0], int(block_size))
+
+
+def pkv_build_step_tables(block_table, query_start_loc, seq_lens, slot_mapping,
+                          num_computed_tokens, query_lens, free_queue, free_state, *,
+                          block_size: int, ref_cnt=None, free_state_out=None, num_tokens=None,
+                          stream=None):
+    """One step's block tables, row starts, lengths and slots from the
+    requests' lengths and the free queue (see pagedkv.h). slot_mapping (int64
+    [T]) may be None when num_tokens is given; free_state_out defaults to
+    free_state (in place)."""
+    _check("pkv_build_step_tables", load().pkv_build_step_tables(
+        *_build_args(block_table, query_start_loc, seq_lens, slot_mapping, num_computed_tokens,
+                     query_lens, free_queue, free_state, free_state_out, ref_cnt, block_size,
+                     num_tokens), _stream(stream)))
+
+
+def pkv_release_blocks(block_table, release_rows, release_tokens, free_queue, free_state, ref_cnt,
+                       *, block_size: int, free_state_out=None, stream=None):
+    """Give back the blocks of the rows release_rows (see pagedkv.h)."""
+    _check("pkv_release_blocks", load().pkv_release_blocks(
+        *_release_args(block_table, release_rows, release_tokens, free_queue, free_state,
+                       free_state_out, ref_cnt, block_size), _stream(stream)))
+
+
+class TableCalls:
+    """pkv_build_step_tables and pkv_release_blocks on buffers that a serving
+    loop keeps, with their arguments checked and marshalled once (as StepCalls
+    does for the step's calls). Pass the arguments of either call or of both."""
+
+    def __init__(self, *, block_table, free_queue, free_state, block_size: int, ref_cnt=None,
+                 free_state_out=None, query_start_loc=None, seq_lens=None, slot_mapping=None,
+                 num_computed_tokens=None, query_lens=None, num_tokens=None, release_rows=None,
+                 release_tokens=None):
+        self.lib = load()
+        self.build_args = self.release_args = None
+        if query_lens is not None:
+            self.build_args = _build_args(
+                block_table, query_start_loc, seq_lens, slot_mapping, num_computed_tokens,
+                query_lens, free_queue, free_state, free_state_out, ref_cnt, block_size,
+                num_tokens)
+        if release_rows is not None:
+            self.release_args = _release_args(block_table, release_rows, release_tokens,
+                                              free_queue, free_state, free_state_out, ref_cnt,
+                                              block_size)
+        if self.build_args is None and self.release_args is None:
+            raise ValueError("pass query_lens (build), release_rows (release) or both")
+        # the tensors stay referenced, so their memory stays valid
+        self._keep = (block_table, free_queue, free_state, ref_cnt, free_state_out,
+                      query_start_loc, seq_lens, slot_mapping, num_computed_tokens, query_lens,
+                      release_rows, release_tokens)
+
+    def build(self, stream=None):
+        if self.build_args is None:
+            raise ValueError("these TableCalls were made without query_lens")
+        status = self.lib.pkv_build_step_tables(*self.build_args, _stream(stream))
+        if status:
+            raise PagedKVError("pkv_build_step_tables", status)
+
+    def release(self, stream=None):
+        if self.release_args is None:
+            raise ValueError("these TableCalls were made without release_rows")
+        status = self.lib.pkv_release_blocks(*self.release_args, _stream(stream))
+        if status:
+            raise PagedKVError("pkv_release_blocks", status)
 
 
 class StepCalls:

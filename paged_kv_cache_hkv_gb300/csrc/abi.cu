@@ -5,6 +5,7 @@
 
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 
@@ -610,6 +611,75 @@ int32_t pkv_paged_attention_with_write(
                         workspace_bytes, options, stream, num_tokens > 0 ? &w : nullptr);
 }
 
+int32_t pkv_build_step_tables(int32_t* block_table, int32_t max_blocks_per_req,
+                              int32_t* query_start_loc, int32_t* seq_lens, int64_t* slot_mapping,
+                              const int32_t* num_computed_tokens, const int32_t* query_lens,
+                              int32_t num_reqs, int32_t num_tokens, const int32_t* free_queue,
+                              const int32_t* free_state, int32_t* free_state_out,
+                              int32_t* ref_cnt, int32_t num_blocks, int32_t block_size,
+                              void* stream) {
+  if (num_tokens < 0 || num_reqs < 0 || max_blocks_per_req < 0 || num_blocks < 1 || block_size < 1)
+    return PKV_ERR_BAD_SHAPE;
+  if (!block_size_ok(block_size)) return PKV_ERR_UNSUPPORTED;
+  if (!query_start_loc || !free_queue || !free_state || !free_state_out)
+    return PKV_ERR_NULL_POINTER;
+  if (num_reqs > 0 && (!seq_lens || !num_computed_tokens || !query_lens ||
+                       (max_blocks_per_req > 0 && !block_table)))
+    return PKV_ERR_NULL_POINTER;
+  for (const void* p : {static_cast<const void*>(block_table),
+                        static_cast<const void*>(query_start_loc),
+                        static_cast<const void*>(seq_lens),
+                        static_cast<const void*>(num_computed_tokens),
+                        static_cast<const void*>(query_lens), static_cast<const void*>(free_queue),
+                        static_cast<const void*>(free_state),
+                        static_cast<const void*>(free_state_out),
+                        static_cast<const void*>(ref_cnt)})
+    if (!aligned4(p)) return PKV_ERR_MISALIGNED;
+  if (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) return PKV_ERR_MISALIGNED;
+  DeviceInfo* d;
+  int32_t st = device_info(&d);
+  if (st != PKV_OK) return st;
+  cudaError_t e = pkv::launch_build_tables(
+      block_table, max_blocks_per_req, query_start_loc, seq_lens, slot_mapping,
+      num_computed_tokens, query_lens, num_reqs, num_tokens, free_queue, free_state,
+      free_state_out, ref_cnt, num_blocks, block_size, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "build_step_tables launch");
+}
+
+int32_t pkv_release_blocks(const int32_t* block_table, int32_t max_blocks_per_req,
+                           int32_t num_reqs, const int32_t* release_rows,
+                           const int32_t* release_tokens, int32_t num_released,
+                           int32_t* free_queue, const int32_t* free_state,
+                           int32_t* free_state_out, int32_t* ref_cnt, int32_t num_blocks,
+                           int32_t block_size, void* stream) {
+  if (num_released < 0 || num_reqs < 0 || max_blocks_per_req < 0 || num_blocks < 1 ||
+      block_size < 1)
+    return PKV_ERR_BAD_SHAPE;
+  // the entries of one call are numbered below 2^29
+  if (static_cast<long long>(num_released) * max_blocks_per_req >= (1ll << 29))
+    return PKV_ERR_BAD_SHAPE;
+  if (!block_size_ok(block_size)) return PKV_ERR_UNSUPPORTED;
+  if (!free_queue || !free_state || !free_state_out || !ref_cnt) return PKV_ERR_NULL_POINTER;
+  if (num_released > 0 && (!release_rows || !release_tokens ||
+                           (num_reqs > 0 && max_blocks_per_req > 0 && !block_table)))
+    return PKV_ERR_NULL_POINTER;
+  for (const void* p : {static_cast<const void*>(block_table),
+                        static_cast<const void*>(release_rows),
+                        static_cast<const void*>(release_tokens),
+                        static_cast<const void*>(free_queue), static_cast<const void*>(free_state),
+                        static_cast<const void*>(free_state_out),
+                        static_cast<const void*>(ref_cnt)})
+    if (!aligned4(p)) return PKV_ERR_MISALIGNED;
+  DeviceInfo* d;
+  int32_t st = device_info(&d);
+  if (st != PKV_OK) return st;
+  cudaError_t e = pkv::launch_release_blocks(
+      block_table, max_blocks_per_req, num_reqs, release_rows, release_tokens, num_released,
+      free_queue, free_state, free_state_out, ref_cnt, num_blocks, block_size,
+      static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "release_blocks launch");
+}
+
 int32_t pkv_get_device_errors(uint32_t* flags, int32_t clear, void* stream) {
   if (!flags) return PKV_ERR_NULL_POINTER;
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
@@ -619,6 +689,7 @@ int32_t pkv_get_device_errors(uint32_t* flags, int32_t clear, void* stream) {
   if (e == cudaSuccess) e = pkv::read_errors_decode(&v, clear != 0);
   if (e == cudaSuccess) e = pkv::read_errors_prefill(&v, clear != 0);
   if (e == cudaSuccess) e = pkv::read_errors_plan(&v, clear != 0);
+  if (e == cudaSuccess) e = pkv::read_errors_tables(&v, clear != 0);
   if (e != cudaSuccess) return cuda_fail(e, "reading device error word");
   *flags = v;
   return PKV_OK;

@@ -170,9 +170,23 @@ cudaError_t launch_decode(const AttnArgs& a, const AttnWorkspace& ws, const CUte
 cudaError_t launch_prefill(const AttnArgs& a, const AttnWorkspace& ws, const CUtensorMap& kv_map,
                            const CUtensorMap& q_map, int num_sms, cudaStream_t stream);
 
+cudaError_t launch_build_tables(int32_t* block_table, int max_blocks, int32_t* qsl,
+                                int32_t* seq_lens, int64_t* slots, const int32_t* num_computed,
+                                const int32_t* query_lens, int num_reqs, int num_tokens,
+                                const int32_t* queue, const int32_t* state, int32_t* state_out,
+                                int32_t* ref_cnt, int num_blocks, int block_size,
+                                cudaStream_t stream);
+
+cudaError_t launch_release_blocks(const int32_t* block_table, int max_blocks, int num_reqs,
+                                  const int32_t* rows, const int32_t* tokens, int num_released,
+                                  int32_t* queue, const int32_t* state, int32_t* state_out,
+                                  int32_t* ref_cnt, int num_blocks, int block_size,
+                                  cudaStream_t stream);
+
 cudaError_t read_errors_kvwrite(uint32_t* out, bool clear);
 cudaError_t read_errors_decode(uint32_t* out, bool clear);
 cudaError_t read_errors_prefill(uint32_t* out, bool clear);
 cudaError_t read_errors_plan(uint32_t* out, bool clear);
+cudaError_t read_errors_tables(uint32_t* out, bool clear);
 
 }  // namespace pkv
