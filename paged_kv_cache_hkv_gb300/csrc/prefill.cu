@@ -176,7 +176,7 @@ struct PrefillLayout {
   // then the item prefix int [kMetaReqs + 1]
   static constexpr uint32_t kMeta = kV + kVStages * kTileKV;
   static constexpr uint32_t kBar = kMeta + kMetaReqs * 16 + (kMetaReqs + 1) * 4 + 124;
-  static constexpr uint32_t kBad = kBar + 512;  // BadKeys of three items
+  static constexpr uint32_t kBad = kBar + 512;  // BadKeys of kBadLists items
   static constexpr uint32_t kBytes = kBad + 1024;
   static constexpr uint32_t kAlloc = kBytes + 1024;  // room to align the base
   static_assert(kAlloc <= 232448, "shared memory");
@@ -186,12 +186,13 @@ struct PrefillLayout {
 // of its rows may not see. Weight 0 times such a value is a NaN, so their
 // elements go into the tensor core as zeros and the rows that do see the key
 // get them back in the epilogue.
-constexpr int kMaxBadKeys = 80;
+constexpr int kMaxBadKeys = 63;
+constexpr int kBadLists = 4;
 struct BadKeys {
   int count;  // above kMaxBadKeys: the list is not complete, every key is looked at
   int key[kMaxBadKeys];
 };
-static_assert(3 * sizeof(BadKeys) <= 1024, "bad key area");
+static_assert(kBadLists * sizeof(BadKeys) <= 1024, "bad key area");
 
 struct PrefillParams {
   uint16_t* out;
@@ -216,7 +217,32 @@ struct PrefillParams {
   ScoreParams score;
   float cap_z;      // softcap: 2 log2(e) scale / softcap, S to the argument of tanh_log2
   float post_mul;   // scores in registers to base-2 units: scale_log2, or 1 once capped or biased
+  // softcap by polynomial (see CapPoly): S up to cap_lim in size, 0 = never
+  float cap_lim;
+  float cap_a[5];
+  bool cap_fixed;   // capped without a bias: the running maximum stays 0 (see below)
 };
+
+// The cap on the tensor core's S without a division or a second exponential:
+// for |u| <= 0.8, u = s * scale / softcap,
+//   tanh(u) = u (c0 + c1 w + c2 w^2 + c3 w^3 + c4 w^4), w = u^2,
+// with the c_i that minimise the largest relative error over that interval
+// (1.0e-6: equal-ripple, found by reweighted least squares). The powers of
+// scale / softcap and the factor softcap * log2(e) go into the coefficients,
+// so a pair of scores takes six packed FMA-pipe instructions; as a whole the
+// prefill of 4 x 2048 rows over 8192 keys went 1828 -> 1298 us with it. A
+// warp that holds a larger |u| takes the exact form (tanh_log2) for its tile.
+constexpr float kCapLim = 0.8f;
+constexpr double kCapPoly[5] = {9.999989943e-01, -3.332537196e-01, 1.323056551e-01, -4.918014086e-02, 1.210013789e-02};
+// The factors above stay normal fp32 numbers, and w^4 finite, for
+// scale / softcap in this range (0.125 / 15 to 0.09 / 1000 in practice).
+constexpr float kCapRatioMin = 1e-4f, kCapRatioMax = 1e4f;
+// A capped score is at most softcap in size, so 2^score needs no maximum
+// taken off it while softcap * log2(e) stays far below fp32's and bf16's
+// exponent range: 2^+-90 leaves 2^37 for the sums over keys. Above this the
+// running maximum is kept as for plain scores.
+constexpr float kCapFixedMax = 90.f;
+
 
 // mbarriers. "commit" ones are arrived on by a tcgen05.commit of an MMA thread
 // (S: s_full, q_free, drain[0]; PV: pv_done, o_full, drain[1]).
@@ -334,6 +360,13 @@ __device__ __forceinline__ int4 item_keys(const PrefillParams& p, const PrefillI
   lo_max = __reduce_max_sync(0xffffffffu, lo_max);
   hi_min = __reduce_min_sync(0xffffffffu, hi_min);
   return make_int4(hi_max > 0 ? lo_min : 0, hi_max, lo_max, hi_min);
+}
+
+// Bits lo .. hi-1 of a word (any lo, hi).
+__device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
+  const uint32_t below_hi = hi >= 32 ? 0xffffffffu : (1u << max(hi, 0)) - 1u;
+  const uint32_t below_lo = lo >= 32 ? 0xffffffffu : (1u << max(lo, 0)) - 1u;
+  return below_hi & ~below_lo;
 }
 
 // Zero the infinities and NaNs of 64 bf16 in shared memory; true if there were any.
@@ -538,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.iq_free[i], 11);
     }
     sh.abort = 0;
-    for (int i = 0; i < 3; ++i) reinterpret_cast<BadKeys*>(gbase + Lay::kBad)[i].count = 0;
+    for (int i = 0; i < kBadLists; ++i) reinterpret_cast<BadKeys*>(gbase + Lay::kBad)[i].count = 0;
     fence_barrier_init();
   }
   if (tid == 32 * 9) {
@@ -599,10 +632,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t T = 0;               // tiles issued so far (all items)
     bool ok = true;
     int q_loads = 0;
+    // SCORED, K: the next item is claimed, and the keys of its rows looked up
+    // (two dependent loads), while the current one's last tiles are still in
+    // flight, and published for every role at once
+    int claimed = n_items;
+    int4 claimed_keys = make_int4(0, 0, 0, 0);
+    auto claim_ahead = [&](int it) {
+      const int slot = it % kItemQ;
+      int item = n_items;
+      if (ln == 0) {
+        if (it >= kItemQ)
+          ok = wait_or_abort(&sh.iq_free[slot], ((it - kItemQ) / kItemQ) & 1u, abort_flag);
+        if (ok) item = it == 0 ? first_claim : static_cast<int>(atomicAdd(&p.hdr[kHdrPrefillNext], 1u));
+      }
+      claimed = __shfl_sync(0xffffffffu, item, 0);
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (valid(claimed))
+        claimed_keys = item_keys(p, prefill_item(p, n_req, claimed, QT, meta, meta_prefix), QT);
+      if (ln == 0) {
+        sh.item_q[slot] = claimed;
+        sh.item_keys[slot] = claimed_keys;
+        mbar_arrive(&sh.iq_full[slot]);
+      }
+    };
+    if (SCORED && !is_v) claim_ahead(0);
     for (int it = 0; ok; ++it) {
       int item;
       int4 keys = make_int4(0, 0, 0, 0);
-      if (!is_v) {
+      if (SCORED && !is_v) {
+        item = claimed;
+        keys = claimed_keys;
+        if (it > 0 && valid(item)) ok = wait_or_abort(&sh.q_free, (it - 1) & 1u, abort_flag);
+      } else if (!is_v) {
         // the Q buffer is free once the previous item's last S is done; only
         // then is the next item claimed (work counter), so that items go to
         // the CTAs that are about to be idle
@@ -613,22 +674,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int slot = it % kItemQ;
           if (it >= kItemQ) ok = wait_or_abort(&sh.iq_free[slot], ((it - kItemQ) / kItemQ) & 1u, abort_flag);
           if (ok) item = it == 0 ? first_claim : static_cast<int>(atomicAdd(&p.hdr[kHdrPrefillNext], 1u));
-          if constexpr (!SCORED) {
-            sh.item_q[slot] = item;
-            mbar_arrive(&sh.iq_full[slot]);
-          }
+          sh.item_q[slot] = item;
+          mbar_arrive(&sh.iq_full[slot]);
         }
         item = __shfl_sync(0xffffffffu, item, 0);
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        if constexpr (SCORED) {  // publish the item with its keys
-          if (ok && valid(item))
-            keys = item_keys(p, prefill_item(p, n_req, item, QT, meta, meta_prefix), QT);
-          if (ln == 0) {
-            sh.item_q[it % kItemQ] = item;
-            sh.item_keys[it % kItemQ] = keys;
-            mbar_arrive(&sh.iq_full[it % kItemQ]);
-          }
-        }
       } else {
         item = take_item(sh, it, abort_flag, true, SCORED ? &keys : nullptr);
         if (item < 0) ok = false;
@@ -683,6 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       ((id * 2 + (is_v ? 1 : 0)) << bsh) >> 3, &full[slot]);
         ++T;
       }
+      if (SCORED && !is_v && ok) claim_ahead(it + 1);
     }
     if (!ok) {  // let the copies in flight land before the shared memory goes away
       for (int s = 0; s < S; ++s)
@@ -783,6 +834,73 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto load_ids = [&](const PrefillItem& mm, int kt) -> int {
       return (lane < 8 && kt < mm.nkv && chunk_ok<SCORED>(p, mm, mm.kt0 + kt, lane)) ? 1 : -1;
     };
+    // The epilogue of item `it` of the CTA, whose last tile is Tl: this
+    // thread's O columns HC*ch .. HC*ch + HC - 1 of its row.
+    auto epilogue = [&](int it, const PrefillItem& m, const RowKeys& rk, float m_run, float l_run,
+                        uint32_t Tl) -> bool {
+      if (!wait_or_abort(&sh.o_full, it & 1u, abort_flag)) return false;
+      int n_bad = 0;
+      BadKeys* bad = reinterpret_cast<BadKeys*>(gbase + Lay::kBad);
+      if constexpr (SCORED) {
+        // the item's bad keys, complete once every thread has published P of
+        // its last tile Tl. Threads may be filling the lists of the next two
+        // items; the third, last read by the epilogue of item it - 1, which
+        // every thread has left (it comes before its P of this item), and
+        // not filled before all threads have passed here, is emptied.
+        if (!wait_or_abort(&sh.p_ready[Tl % kSBufs], (Tl / kSBufs) & 1u, abort_flag)) return false;
+        n_bad = *reinterpret_cast<volatile int*>(&bad[it % kBadLists].count);
+        if (tid == 0) bad[(it + 3) % kBadLists].count = 0;
+      }
+      tc::fence_after_sync();
+      const float l_tot = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
+      const float inv = SCORED && l_tot == 0.f ? 0.f : 1.f / l_tot;  // no key seen: zeros
+      const int qi = m.i0 + row / G;
+      const bool store = qi < m.n;
+      const int head = m.g * G + row % G;
+      // shared-prefix items keep the row's partial (max, sum, unnormalised O)
+      // for the decode of request shared_first + qi: slot of (piece, qi, head)
+      const bool partial = m.piece >= 0;
+      const long long pslot = (static_cast<long long>(m.piece) * p.shared_num + qi) * p.num_q_heads + head;
+      if (partial && store && ch == 0) p.shared_ml[pslot] = make_float2(m_run, l_tot);
+      uint16_t* dst = p.out + (static_cast<long long>(m.q0 + qi) * p.num_q_heads + head) * D + HC * ch;
+#pragma unroll 1
+      for (int q = 0; q < HC / 32; ++q) {
+        uint32_t o[32];
+        tc::ld_half32<HC>(t_lane + 32 * q, o);
+        tc::wait32(o);
+        if (!store) continue;
+        if (SCORED && n_bad > 0) {
+          const bool listed = n_bad <= kMaxBadKeys;
+          const int a0 = listed ? 0 : rk.lo, a1 = listed ? n_bad : rk.hi;
+          uint32_t t[32];  // (a copy, so that o stays in registers otherwise)
+#pragma unroll
+          for (int x = 0; x < 32; ++x) t[x] = o[x];
+          for (int i = a0; i < a1; ++i) {
+            const int j = listed ? bad[it % kBadLists].key[i] : i;
+            if (j >= rk.lo && j < rk.hi)
+              add_nonfinite(p, m.bt_row, m.g, D, j, HC * ch + 32 * q, t);
+          }
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[x] = t[x];
+        }
+        if (partial) {
+          float4* d4 = reinterpret_cast<float4*>(p.shared_o + pslot * D + HC * ch + 32 * q);
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            d4[x] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
+                                __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
+        } else {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            w[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+          uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * q);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) d4[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+        }
+      }
+      return true;
+    };
     int4 keys;
     int item = take_item(sh, 0, abort_flag, true, SCORED ? &keys : nullptr);
     PrefillItem m{};
@@ -796,11 +914,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       next_id = load_ids(m, 0);
     }
-    for (int it = 0; ok && valid(item); ++it) {
+    // SCORED: the previous item, its epilogue still to come
+    bool pend = false;
+    PrefillItem pend_m{};
+    RowKeys pend_rk{0, 0, 0};
+    float pend_max = 0.f, pend_sum = 0.f;
+    int it = 0;
+    for (; ok && valid(item); ++it) {
       const int nkv = m.nkv;
       const int qi = m.i0 + row / G;                // query of this row
       const int lim = min(m.c + qi, m.kv_len - 1);  // last key this row may see
-      float m_run = -INFINITY, l_run = 0.f;
+      float m_run = SCORED && p.cap_fixed ? 0.f : -INFINITY, l_run = 0.f;
       // SCORED: bias per key of distance, base-2 scores
       const float slope2 =
           SCORED && p.score.slopes ? __ldg(p.score.slopes + m.g * G + row % G) * kLog2e : 0.f;
@@ -826,8 +950,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::ld_half32<64>(t_s + 32, sr[1]);
         tc::wait32(sr[0]);
         tc::wait32(sr[1]);
+        uint32_t vis[2] = {0xffffffffu, 0xffffffffu};  // SCORED: visible keys, a bit each
         if constexpr (SCORED) {
-          if (p.score.softcap > 0.f) {
+          if (!full) {
+            const int lo = rk.lo - ka * kTileN - 64 * ch, hi = rk.hi - ka * kTileN - 64 * ch;
+            const uint32_t cm = mask >> (4 * ch);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              vis[q] = bits_between(lo - 32 * q, hi - 32 * q) &
+                       (((cm >> (2 * q)) & 1u ? 0xffffu : 0u) |
+                        ((cm >> (2 * q + 1)) & 1u ? 0xffff0000u : 0u));
+            // what the tensor core made of rows that were not loaded must not
+            // decide which form of the cap is taken
+            if (p.cap_lim > 0.f) {
+#pragma unroll
+              for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (!(vis[q] & (1u << i))) sr[q][i] = 0u;
+            }
+          }
+          bool small = false;
+          if (p.cap_lim > 0.f) {
+            float am[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int i = 0; i < 32; i += 2)
+                am[(i >> 1) & 3] = max3f(am[(i >> 1) & 3], fabsf(__uint_as_float(sr[q][i])),
+                                         fabsf(__uint_as_float(sr[q][i + 1])));
+            small = __all_sync(0xffffffffu,
+                               fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3])) <= p.cap_lim);
+          }
+          if (small) {
+            const float2 a0 = make_float2(p.cap_a[0], p.cap_a[0]), a1 = make_float2(p.cap_a[1], p.cap_a[1]),
+                         a2 = make_float2(p.cap_a[2], p.cap_a[2]), a3 = make_float2(p.cap_a[3], p.cap_a[3]),
+                         a4 = make_float2(p.cap_a[4], p.cap_a[4]);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 x = make_float2(__uint_as_float(sr[q][i]), __uint_as_float(sr[q][i + 1]));
+                const float2 w = fmul2(x, x);
+                const float2 y =
+                    fmul2(x, ffma2(ffma2(ffma2(ffma2(a4, w, a3), w, a2), w, a1), w, a0));
+                sr[q][i] = __float_as_uint(y.x);
+                sr[q][i + 1] = __float_as_uint(y.y);
+              }
+          } else if (p.score.softcap > 0.f) {
             const float cap2 = p.score.softcap * kLog2e;
 #pragma unroll
             for (int q = 0; q < 2; ++q)
@@ -852,18 +1022,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!full) {  // invisible keys become -inf
-          const int jlim = SCORED ? rk.hi - 1 - ka * kTileN - 64 * ch : lim - ka * kTileN - 64 * ch;
-          const int jlo = SCORED ? rk.lo - ka * kTileN - 64 * ch : 0;
+          const int jlim = lim - ka * kTileN - 64 * ch;
           const uint32_t cm = mask >> (4 * ch);
 #pragma unroll
           for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const int j = q * 32 + i;
-              if (!(((cm >> (j >> 4)) & 1u) && j <= jlim && (!SCORED || j >= jlo)))
+              if (SCORED ? !(vis[q] & (1u << i)) : !(((cm >> (j >> 4)) & 1u) && j <= jlim))
                 sr[q][i] = __float_as_uint(-INFINITY);
             }
         }
+        if (!SCORED || !p.cap_fixed) {
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int q = 0; q < 2; ++q)
@@ -895,6 +1065,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc::st_half32<HC>(t_lane + 32 * q, o);
             }
           }
+        }
         }
         // P = 2^(s * scale - m) as bf16 (-inf -> 0) over the S buffer: column
         // c holds keys 2c (low half) and 2c+1, so this thread's keys land in
@@ -942,13 +1113,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int x = 0; x < 8; ++x) v4[x] = make_uint4(0, 0, 0, 0);
           } else if (SCORED && ch < DH && zero_nonfinite(v4)) {
-            BadKeys& bad = reinterpret_cast<BadKeys*>(gbase + Lay::kBad)[it % 3];
+            BadKeys& bad = reinterpret_cast<BadKeys*>(gbase + Lay::kBad)[it % kBadLists];
             const int i = atomicAdd(&bad.count, 1);
             if (i < kMaxBadKeys) bad.key[i] = ka * kTileN + row;
           }
           fence_proxy_async_smem();
         }
         tc::wait_st();
+        if (SCORED && pend) {
+          // O is overwritten once P of this tile is published
+          pend = false;
+          ok = epilogue(it - 1, pend_m, pend_rk, pend_max, pend_sum, T - 1);
+          if (!ok) break;
+        }
         tc::fence_before_sync();
         mbar_arrive(&sh.p_ready[b]);
         next_id = load_ids(m, kt + 1);  // its latency hides under the next S wait
@@ -970,68 +1147,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         next_id = load_ids(m_next, 0);
       }
-      // ---- epilogue: this thread's O columns HC*ch .. HC*ch + HC - 1 of its row
-      ok = wait_or_abort(&sh.o_full, it & 1u, abort_flag);
-      if (!ok) break;
-      int n_bad = 0;
-      BadKeys* bad = reinterpret_cast<BadKeys*>(gbase + Lay::kBad);
       if constexpr (SCORED) {
-        // the item's bad keys, complete once every thread has published P of
-        // its last tile. Three lists: threads may already fill the next
-        // item's, and the one after it, which no thread reads any more and
-        // none fills before all have passed here, starts empty.
-        const uint32_t Tl = T + nkv - 1;
-        ok = wait_or_abort(&sh.p_ready[Tl % kSBufs], (Tl / kSBufs) & 1u, abort_flag);
+        // left until the next item's first tile is in registers (above), so
+        // that its softmax runs while this item's last PV does
+        pend = true;
+        pend_m = m;
+        pend_rk = rk_cur;
+        pend_max = m_run;
+        pend_sum = l_run;
+      } else {
+        ok = epilogue(it, m, rk, m_run, l_run, T + nkv - 1);
         if (!ok) break;
-        n_bad = *reinterpret_cast<volatile int*>(&bad[it % 3].count);
-        if (tid == 0) bad[(it + 2) % 3].count = 0;
-      }
-      tc::fence_after_sync();
-      const float l_tot = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
-      const float inv = SCORED && l_tot == 0.f ? 0.f : 1.f / l_tot;  // no key seen: zeros
-      const bool store = qi < m.n;
-      const int head = m.g * G + row % G;
-      // shared-prefix items keep the row's partial (max, sum, unnormalised O)
-      // for the decode of request shared_first + qi: slot of (piece, qi, head)
-      const bool partial = m.piece >= 0;
-      const long long pslot = (static_cast<long long>(m.piece) * p.shared_num + qi) * p.num_q_heads + head;
-      if (partial && store && ch == 0) p.shared_ml[pslot] = make_float2(m_run, l_tot);
-      uint16_t* dst = p.out + (static_cast<long long>(m.q0 + qi) * p.num_q_heads + head) * D + HC * ch;
-#pragma unroll 1
-      for (int q = 0; q < HC / 32; ++q) {
-        uint32_t o[32];
-        tc::ld_half32<HC>(t_lane + 32 * q, o);
-        tc::wait32(o);
-        if (!store) continue;
-        if (SCORED && n_bad > 0) {
-          const bool listed = n_bad <= kMaxBadKeys;
-          const int a0 = listed ? 0 : rk_cur.lo, a1 = listed ? n_bad : rk_cur.hi;
-          for (int i = a0; i < a1; ++i) {
-            const int j = listed ? bad[it % 3].key[i] : i;
-            if (j >= rk_cur.lo && j < rk_cur.hi)
-              add_nonfinite(p, m.bt_row, m.g, D, j, HC * ch + 32 * q, o);
-          }
-        }
-        if (partial) {
-          float4* d4 = reinterpret_cast<float4*>(p.shared_o + pslot * D + HC * ch + 32 * q);
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            d4[x] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
-                                __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
-        } else {
-          uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            w[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-          uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * q);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) d4[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
-        }
       }
       T += nkv;
       m = m_next;
       item = item_n;
     }
+    if (SCORED && ok && pend) epilogue(it - 1, pend_m, pend_rk, pend_max, pend_sum, T - 1);
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -1073,6 +1205,14 @@ cudaError_t launch_prefill(const AttnArgs& a, const AttnWorkspace& ws, const CUt
   p.scale_log2 = a.scale * kLog2e;
   p.score = a.score;
   p.cap_z = a.score.softcap > 0.f ? 2.f * kLog2e * (a.scale / a.score.softcap) : 0.f;
+  const float ratio = a.score.softcap > 0.f ? a.scale / a.score.softcap : 0.f;
+  const bool poly = ratio >= kCapRatioMin && ratio <= kCapRatioMax;
+  p.cap_lim = poly ? kCapLim / ratio : 0.f;
+  double pw = static_cast<double>(a.score.softcap) * kLog2e * ratio;
+  for (int i = 0; i < 5; ++i, pw *= static_cast<double>(ratio) * ratio)
+    p.cap_a[i] = poly ? static_cast<float>(kCapPoly[i] * pw) : 0.f;
+  p.cap_fixed = a.score.softcap > 0.f && !a.score.slopes &&
+                a.score.softcap * kLog2e <= kCapFixedMax;
   p.post_mul = a.score.softcap > 0.f || a.score.slopes ? 1.f : p.scale_log2;
   p.hdr = ws.hdr;
   p.pf_req = ws.pf_req;
