@@ -120,6 +120,26 @@ __device__ __forceinline__ void ld_half32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr), "n"(OFF));
 }
 
+// The same access shape with 8 columns per thread, loaded and waited for.
+template <int OFF>
+__device__ __forceinline__ void ld_half8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], %9;\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr), "n"(OFF)
+      : "memory");
+}
+
+template <int OFF>
+__device__ __forceinline__ void st_half8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x32bx2.x8.b32 [%0], %1, {%2,%3,%4,%5,%6,%7,%8,%9};" ::"r"(taddr),
+      "n"(OFF), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
+      "r"(v[7])
+      : "memory");
+}
+
 template <int OFF>
 __device__ __forceinline__ void st_half16(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
@@ -160,6 +180,9 @@ constexpr int kItemQ = 4;      // claimed work items in flight between the roles
 constexpr int kMetaReqs = 128;  // prefill requests whose metadata a CTA keeps in shared memory
 constexpr int kThreads = 384;  // 8 softmax warps, S-MMA warp, K-copy warp, V-copy warp, PV-MMA warp
 constexpr float kRescaleLog2 = 8.f;  // lazy rescale threshold (powers of two)
+// Scores of a kernel instance: plain, or key ranges with or without a cap
+// (ScoreParams::softcap) and a bias (ScoreParams::slopes).
+enum : int { kPlain = 0, kRanges = 1, kCap = 2, kBias = 4 };
 
 template <int D>
 struct PrefillLayout {
@@ -186,8 +209,8 @@ struct PrefillLayout {
 // of its rows may not see. Weight 0 times such a value is a NaN, so their
 // elements go into the tensor core as zeros and the rows that do see the key
 // get them back in the epilogue.
-constexpr int kMaxBadKeys = 63;
-constexpr int kBadLists = 4;
+constexpr int kMaxBadKeys = 50;
+constexpr int kBadLists = 5;
 struct BadKeys {
   int count;  // above kMaxBadKeys: the list is not complete, every key is looked at
   int key[kMaxBadKeys];
@@ -216,11 +239,10 @@ struct PrefillParams {
   // Capped, biased or range-masked scores (the kernel's SCORED variant)
   ScoreParams score;
   float cap_z;      // softcap: 2 log2(e) scale / softcap, S to the argument of tanh_log2
-  float post_mul;   // scores in registers to base-2 units: scale_log2, or 1 once capped or biased
   // softcap by polynomial (see CapPoly): S up to cap_lim in size, 0 = never
   float cap_lim;
   float cap_a[5];
-  bool cap_fixed;   // capped without a bias: the running maximum stays 0 (see below)
+  bool out32;       // the output is 32-byte aligned
 };
 
 // The cap on the tensor core's S without a division or a second exponential:
@@ -230,7 +252,7 @@ struct PrefillParams {
 // (1.0e-6: equal-ripple, found by reweighted least squares). The powers of
 // scale / softcap and the factor softcap * log2(e) go into the coefficients,
 // so a pair of scores takes six packed FMA-pipe instructions; as a whole the
-// prefill of 4 x 2048 rows over 8192 keys went 1828 -> 1298 us with it. A
+// prefill of 4 x 2048 rows over 8192 keys went 1828 -> 1218 us with it and without the running maximum. A
 // warp that holds a larger |u| takes the exact form (tanh_log2) for its tile.
 constexpr float kCapLim = 0.8f;
 constexpr double kCapPoly[5] = {9.999989943e-01, -3.332537196e-01, 1.323056551e-01, -4.918014086e-02, 1.210013789e-02};
@@ -239,10 +261,27 @@ constexpr double kCapPoly[5] = {9.999989943e-01, -3.332537196e-01, 1.323056551e-
 constexpr float kCapRatioMin = 1e-4f, kCapRatioMax = 1e4f;
 // A capped score is at most softcap in size, so 2^score needs no maximum
 // taken off it while softcap * log2(e) stays far below fp32's and bf16's
-// exponent range: 2^+-90 leaves 2^37 for the sums over keys. Above this the
-// running maximum is kept as for plain scores.
+// exponent range: 2^+-90 leaves 2^37 for the sums over keys. A wider cap
+// takes the biased instance (without slopes), which keeps the maximum.
 constexpr float kCapFixedMax = 90.f;
 
+
+// One work item: (request, 128-row query tile, kv head).
+struct PrefillItem {
+  int g;       // kv head
+  int c;       // cached tokens of the request
+  int q0;      // batch row of the request's first query
+  int n;       // new tokens of the request
+  int i0;      // first query of the tile (within the request)
+  int kv_len;  // keys the tile's last query sees (shared items: end of the piece)
+  int nkv;     // key tiles
+  int kt0;     // first key tile (0, or a shared item's piece start)
+  int piece;   // shared items: key piece, else -1
+  long long bt_row;  // offset of the request's block table row
+  // SCORED items: first key that any row sees; a tile within [full_lo,
+  // full_hi) is seen by every row
+  int k_lo, full_lo, full_hi;
+};
 
 // mbarriers. "commit" ones are arrived on by a tcgen05.commit of an MMA thread
 // (S: s_full, q_free, drain[0]; PV: pv_done, o_full, drain[1]).
@@ -263,7 +302,7 @@ struct PrefillShared {
   uint64_t iq_full[kItemQ];      // item id j published in item_q[j % kItemQ]
   uint64_t iq_free[kItemQ];      // 11 arrivals: every role has read it
   int item_q[kItemQ];
-  int4 item_keys[kItemQ];        // SCORED: TileKeys of the item
+  PrefillItem item_m[kItemQ];    // SCORED: the item described, for every role
   uint32_t tmem;
   int abort;
 };
@@ -289,55 +328,65 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, vo
   }
 }
 
+// The same with its loop out of line, where the code around it has to stay small.
+__device__ __noinline__ bool wait_loop(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return wait_or_abort(bar, parity, abort);
+}
+__device__ __forceinline__ bool wait_small(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return mbar_try_wait(smem_u32(bar), parity) || wait_loop(bar, parity, abort);
+}
+
 // Consumers of the item queue (the MMA thread, the V-copy warp, each softmax
 // warp): item id number j of this CTA, or -1 after an abort. The calling
 // warp's lane 0 releases the slot once every lane has read it.
 __device__ __forceinline__ int take_item(PrefillShared& sh, int j, volatile int* abort,
-                                         bool whole_warp, int4* keys) {
+                                         bool whole_warp, PrefillItem* m) {
   const int slot = j % kItemQ;
   if (!wait_or_abort(&sh.iq_full[slot], (j / kItemQ) & 1u, abort)) return -1;
   const int item = *reinterpret_cast<volatile int*>(&sh.item_q[slot]);
-  if (keys) *keys = sh.item_keys[slot];
+  if (m) *m = sh.item_m[slot];
   if (whole_warp) __syncwarp();
   if (!whole_warp || (threadIdx.x & 31) == 0) mbar_arrive(&sh.iq_free[slot]);
   return item;
 }
 
-// One work item: (request, 128-row query tile, kv head).
-struct PrefillItem {
-  int g;       // kv head
-  int c;       // cached tokens of the request
-  int q0;      // batch row of the request's first query
-  int n;       // new tokens of the request
-  int i0;      // first query of the tile (within the request)
-  int kv_len;  // keys the tile's last query sees (shared items: end of the piece)
-  int nkv;     // key tiles
-  int kt0;     // first key tile (0, or a shared item's piece start)
-  int piece;   // shared items: key piece, else -1
-  long long bt_row;  // offset of the request's block table row
-  // SCORED items: first key that any row sees; a tile within [full_lo,
-  // full_hi) is seen by every row
-  int k_lo, full_lo, full_hi;
-};
+// The same without the release: the caller takes the item later.
+__device__ __forceinline__ int peek_item(PrefillShared& sh, int j, volatile int* abort,
+                                         PrefillItem* m) {
+  const int slot = j % kItemQ;
+  if (!wait_or_abort(&sh.iq_full[slot], (j / kItemQ) & 1u, abort)) return -1;
+  *m = sh.item_m[slot];
+  return *reinterpret_cast<volatile int*>(&sh.item_q[slot]);
+}
 
 // Keys of row i of a SCORED item (i < m.n), clipped to what the item attends;
 // `ref` is the position its distances count from (see the decode kernel).
+// Loaded and evaluated apart, so that the loads can go out early.
+struct RowRaw {
+  int begin, end, L;
+};
 struct RowKeys {
   int lo, hi, ref;
 };
-__device__ __forceinline__ RowKeys item_row_keys(const PrefillParams& p, const PrefillItem& m,
-                                                 int i) {
-  RowKeys k{0, 0, 0};
-  if (i >= m.n) return k;
-  int L = m.c + m.n, pos = m.c + i;
-  if (m.piece >= 0) {  // a decode row over the shared prefix
-    L = __ldg(p.seq_lens + p.shared_first + i);
-    pos = L - 1;
-  }
-  const KeyRange r = row_keys(p.score, static_cast<long long>(m.q0) + i, pos, L, 0);
-  k.ref = max(min(pos, r.hi - 1), r.lo);
-  k.hi = m.piece >= 0 ? min(r.hi, p.shared_len) : r.hi;
-  k.lo = r.lo;
+__device__ __forceinline__ RowRaw load_row(const PrefillParams& p, const PrefillItem& m, int i) {
+  RowRaw r{0, 0, 0};
+  if (i >= m.n) return r;
+  const long long t = static_cast<long long>(m.q0) + i;
+  // (shared-prefix items: row i is the decode of request shared_first + i)
+  r.L = m.piece >= 0 ? __ldg(p.seq_lens + p.shared_first + i) : m.c + m.n;
+  if (p.score.key_begin) r.begin = __ldg(p.score.key_begin + t);
+  if (p.score.key_end) r.end = __ldg(p.score.key_end + t);
+  return r;
+}
+__device__ __forceinline__ RowKeys row_of(const PrefillParams& p, const PrefillItem& m, int i,
+                                          const RowRaw& r) {
+  if (i >= m.n) return RowKeys{0, 0, 0};
+  const int pos = m.piece >= 0 ? r.L - 1 : m.c + i;
+  RowKeys k;
+  k.lo = max(r.begin, 0);
+  k.hi = min(p.score.key_end ? r.end : pos + 1, r.L);
+  k.ref = max(min(pos, k.hi - 1), k.lo);
+  if (m.piece >= 0) k.hi = min(k.hi, p.shared_len);
   if (k.lo >= k.hi) k.lo = k.hi = 0;
   return k;
 }
@@ -348,7 +397,7 @@ __device__ __forceinline__ int4 item_keys(const PrefillParams& p, const PrefillI
   int lo_min = 0x7fffffff, hi_max = 0, lo_max = 0, hi_min = 0x7fffffff;
   const int i1 = min(m.i0 + QT, m.n);
   for (int i = m.i0 + (threadIdx.x & 31); i < i1; i += 32) {
-    const RowKeys k = item_row_keys(p, m, i);
+    const RowKeys k = row_of(p, m, i, load_row(p, m, i));
     const bool none = k.lo >= k.hi;
     lo_min = none ? lo_min : min(lo_min, k.lo);
     hi_max = max(hi_max, k.hi);
@@ -369,6 +418,13 @@ __device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
   return below_hi & ~below_lo;
 }
 
+// 32-byte store; the address 32-byte aligned.
+__device__ __forceinline__ void st_global_v8(void* dst, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // Zero the infinities and NaNs of 64 bf16 in shared memory; true if there were any.
 __device__ __forceinline__ bool zero_nonfinite(uint4* v4) {
   // x * 0 is 0 or, for an infinity or a NaN, a NaN
@@ -382,6 +438,7 @@ __device__ __forceinline__ bool zero_nonfinite(uint4* v4) {
     for (int e = 0; e < 4; ++e) acc = __hfma2(h[e], zero, acc);
   }
   if ((*reinterpret_cast<uint32_t*>(&acc) & 0x7fff7fffu) == 0u) return false;
+#pragma unroll 1
   for (int x = 0; x < 8; ++x) {
     uint4 v = v4[x];
     uint32_t* w = reinterpret_cast<uint32_t*>(&v);
@@ -395,18 +452,25 @@ __device__ __forceinline__ bool zero_nonfinite(uint4* v4) {
   return true;
 }
 
-// Add the infinities and NaNs of V elements d0 .. d0+31 of key j to o.
+// Add the infinities and NaNs of V elements d0 .. d0+nd-1 of key j to the
+// thread's part of its output row, already stored (bf16, or fp32 partials).
 __device__ __noinline__ void add_nonfinite(const PrefillParams& p, long long bt_row, int g, int D,
-                                           int j, int d0, uint32_t (&o)[32]) {
+                                           int j, int d0, int nd, uint16_t* out, float* partial) {
   const int id = __ldg(p.block_table + bt_row + (j >> p.block_shift));
   if (id < 0 || id >= p.num_blocks) return;
   const long long r = ((static_cast<long long>(id) * 2 + 1) << p.block_shift) +
                       (j & ((1 << p.block_shift) - 1));
   const uint16_t* v = p.pool + (r * p.num_kv_heads + g) * D + d0;
-  for (int x = 0; x < 32; ++x) {
+#pragma unroll 1
+  for (int x = 0; x < nd; ++x) {
     const uint32_t b = __ldg(v + x);
-    if ((b & 0x7f80u) == 0x7f80u)
-      o[x] = __float_as_uint(__uint_as_float(o[x]) + __uint_as_float(b << 16));
+    if ((b & 0x7f80u) != 0x7f80u) continue;
+    const float f = __uint_as_float(b << 16);
+    if (partial)
+      partial[x] += f;
+    else
+      out[x] = static_cast<uint16_t>(
+          pack_bf16x2(__uint_as_float(static_cast<uint32_t>(out[x]) << 16) + f, 0.f));
   }
 }
 
@@ -502,18 +566,427 @@ __device__ __forceinline__ int entry_id(const PrefillParams& p, const PrefillIte
 }
 
 // Chunk b (keys 16b .. 16b+15) of tile kt holds keys < kv_len, all of them in
-// blocks of the pool (SCORED: the keys of [k_lo, kv_len) only).
-template <bool SCORED>
+// blocks of the pool.
 __device__ __forceinline__ bool chunk_ok(const PrefillParams& p, const PrefillItem& m, int kt, int b) {
   const int k0 = kt * kTileN + b * kChunkKeys;
   if (k0 >= m.kv_len) return false;
   const int bsh = p.block_shift;
-  if (bsh == 4) return entry_id<SCORED>(p, m, k0 >> 4) >= 0;
-  if (bsh == 5) return entry_id<SCORED>(p, m, k0 >> 5) >= 0;
-  const int e = k0 >> 3;
-  if (SCORED && !entry_used<true>(p, m, e)) return entry_id<true>(p, m, e + 1) >= 0;
-  return entry_id<SCORED>(p, m, e) >= 0 &&
-         (k0 + 8 >= m.kv_len || entry_id<SCORED>(p, m, e + 1) >= 0);
+  if (bsh == 4) return entry_id<false>(p, m, k0 >> 4) >= 0;
+  if (bsh == 5) return entry_id<false>(p, m, k0 >> 5) >= 0;
+  return entry_id<false>(p, m, k0 >> 3) >= 0 &&
+         (k0 + 8 >= m.kv_len || entry_id<false>(p, m, (k0 >> 3) + 1) >= 0);
+}
+
+// The same for SCORED items, whose keys are [k_lo, kv_len), in two steps: the
+// chunk's table entries (the second for 8-token blocks only), and their check.
+struct ChunkRaw {
+  int a, b;
+};
+__device__ __forceinline__ ChunkRaw load_chunk(const PrefillParams& p, const PrefillItem& m, int kt,
+                                               int b) {
+  const int k0 = kt * kTileN + b * kChunkKeys, e = k0 >> p.block_shift;
+  ChunkRaw c{-1, -1};
+  if (entry_used<true>(p, m, e)) c.a = __ldg(p.block_table + m.bt_row + e);
+  if (p.block_shift == 3 && entry_used<true>(p, m, e + 1))
+    c.b = __ldg(p.block_table + m.bt_row + e + 1);
+  return c;
+}
+__device__ __forceinline__ bool chunk_good(const PrefillParams& p, const PrefillItem& m, int kt,
+                                           int b, const ChunkRaw& c) {
+  const int k0 = kt * kTileN + b * kChunkKeys, e = k0 >> p.block_shift;
+  if (k0 >= m.kv_len) return false;
+  const bool a_ok = c.a >= 0 && c.a < p.num_blocks, b_ok = c.b >= 0 && c.b < p.num_blocks;
+  if (p.block_shift != 3) return a_ok;
+  if (!entry_used<true>(p, m, e)) return b_ok;
+  return a_ok && (k0 + 8 >= m.kv_len || b_ok);
+}
+
+// The softmax warps of a SCORED kernel: the roles and lane map of the plain
+// ones (see the kernel), with the scores transformed in registers, each row
+// masked by its own range, and two things done to keep short items (packed
+// documents, windows: a few key tiles each) from waiting on latency one after
+// the other. What the next tile or item needs from global memory is loaded a
+// tile ahead. And an item's epilogue is left until the next item's first
+// tile has been through the softmax, so that the item's last PV runs
+// meanwhile; only its reads of O come before that tile's P is published (the
+// next PV overwrites O), its stores after.
+template <int D, int SC>
+__device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillShared& sh,
+                                               unsigned char* gbase, uint32_t tmem, int n_items) {
+  constexpr bool CAP = (SC & kCap) != 0, BIAS = (SC & kBias) != 0;
+  constexpr bool FIXED = CAP && !BIAS;  // no running maximum (kCapFixedMax): it stays 0
+  using Lay = PrefillLayout<D>;
+  constexpr int DH = Lay::DH;
+  constexpr int HC = D / 2;  // O columns per thread
+  constexpr int NQ = HC / 32;
+  volatile int* abort_flag = &sh.abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = p.group;
+  const int ch = lane >> 4;  // key half of this thread
+  const int lane0 = 32 * (warp & 3) + 16 * (warp >> 2);
+  const int row = lane0 + (lane & 15);  // query row of this thread (TMEM lane)
+  const uint32_t t_lane = tmem + (static_cast<uint32_t>(lane0) << 16);
+  BadKeys* bad_lists = reinterpret_cast<BadKeys*>(gbase + Lay::kBad);
+  auto valid = [&](int item) { return item >= 0 && item < n_items; };
+  auto chunk = [&](const PrefillItem& m, int kt) -> ChunkRaw {
+    return lane < 8 ? load_chunk(p, m, m.kt0 + kt, lane) : ChunkRaw{-1, -1};
+  };
+  const float mul = CAP || BIAS ? 1.f : p.scale_log2;  // scores in registers to base 2
+  uint32_t T = 0;  // tiles of earlier items
+  bool ok = true;
+
+  // the epilogue of the item before the current one, number it - 1, in two
+  // steps around the publication of P (none before the first)
+  bool pend = false;
+  int pend_qi = -1, pend_q0 = 0, pend_g = 0, pend_piece = -1;  // qi < 0: no row to store
+  int pend_lo = 0, pend_hi = 0;
+  long long pend_bt = 0;
+  float pend_max = 0.f, pend_sum = 0.f;
+  auto epilogue_load = [&](int it, uint32_t Tl, uint32_t (&o)[NQ][32], int& n_bad) -> bool {
+    // the item's bad keys are complete once every thread has published P of
+    // its last tile Tl. Five lists: when a thread is here in item it's
+    // epilogue, every thread has published all P of item it; others may be
+    // storing item it - 1 or filling the lists of the two items after it; no
+    // thread uses that of item it - 2 any more, and none fills it again (as
+    // item it + 3's) before all have passed here.
+    if (!wait_small(&sh.o_full, it & 1u, abort_flag)) return false;
+    if (!wait_small(&sh.p_ready[Tl % kSBufs], (Tl / kSBufs) & 1u, abort_flag)) return false;
+    n_bad = *reinterpret_cast<volatile int*>(&bad_lists[it % kBadLists].count);
+    if (tid == 0) bad_lists[(it + 3) % kBadLists].count = 0;
+    tc::fence_after_sync();
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) tc::ld_half32<HC>(t_lane + 32 * q, o[q]);
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) tc::wait32(o[q]);
+    return true;
+  };
+  auto epilogue_store = [&](int it, const uint32_t (&o)[NQ][32], int n_bad) {
+    const float l_tot = pend_sum + __shfl_xor_sync(0xffffffffu, pend_sum, 16);
+    const float inv = l_tot == 0.f ? 0.f : 1.f / l_tot;  // no key seen: zeros
+    const int qi = pend_qi;
+    if (qi < 0) return;
+    const int head = pend_g * G + row % G;
+    uint16_t* dst =
+        p.out + ((static_cast<long long>(pend_q0) + qi) * p.num_q_heads + head) * D + HC * ch;
+    float* part = nullptr;
+    if (pend_piece >= 0) {
+      // shared-prefix items keep the row's partial (max, sum, unnormalised O)
+      // for the decode of request shared_first + qi: slot of (piece, qi, head)
+      const long long pslot =
+          (static_cast<long long>(pend_piece) * p.shared_num + qi) * p.num_q_heads + head;
+      if (ch == 0) p.shared_ml[pslot] = make_float2(pend_max, l_tot);
+      part = p.shared_o + pslot * D + HC * ch;
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        float4* d4 = reinterpret_cast<float4*>(part + 32 * q);
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          d4[x] = make_float4(__uint_as_float(o[q][4 * x]), __uint_as_float(o[q][4 * x + 1]),
+                              __uint_as_float(o[q][4 * x + 2]), __uint_as_float(o[q][4 * x + 3]));
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          w[e] = pack_bf16x2(__uint_as_float(o[q][2 * e]) * inv, __uint_as_float(o[q][2 * e + 1]) * inv);
+        // each thread writes its own row: whole 32-byte sectors where the
+        // output's alignment allows, so that a row's sector is written once
+        if (p.out32) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) st_global_v8(dst + 32 * q + 16 * x, &w[8 * x]);
+        } else {
+          uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * q);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) d4[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+        }
+      }
+    }
+    if (n_bad > 0) {
+      const BadKeys& bad = bad_lists[it % kBadLists];
+      const bool listed = n_bad <= kMaxBadKeys;
+#pragma unroll 1
+      for (int i = listed ? 0 : pend_lo; i < (listed ? n_bad : pend_hi); ++i) {
+        const int j = listed ? bad.key[i] : i;
+        if (j >= pend_lo && j < pend_hi)
+          add_nonfinite(p, pend_bt, pend_g, D, j, HC * ch, HC, dst, part);
+      }
+    }
+  };
+
+  PrefillItem m{};
+  int item = take_item(sh, 0, abort_flag, true, &m);
+  RowKeys rk{0, 0, 0};  // the keys of this thread's row
+  ChunkRaw ids{-1, -1};
+  if (valid(item)) {
+    ids = chunk(m, 0);
+    rk = row_of(p, m, m.i0 + row / G, load_row(p, m, m.i0 + row / G));
+  }
+  int it = 0;
+#pragma unroll 1
+  for (; valid(item); ++it) {
+    const int nkv = m.nkv;
+    int item_n = -1;
+    RowRaw raw_n{0, 0, 0};
+    float m_run = FIXED ? 0.f : -INFINITY, l_run = 0.f;
+    // bias per key of distance, base-2 scores
+    const float slope2 =
+        BIAS && p.score.slopes ? __ldg(p.score.slopes + m.g * G + row % G) * kLog2e : 0.f;
+#pragma unroll 1
+    for (int kt = 0; kt < nkv; ++kt) {
+      const uint32_t Tg = T + kt;
+      const uint32_t b = Tg % kSBufs;
+      const uint32_t t_s = t_lane + kTmemS + kTileN * b;
+      const uint32_t mask =
+          __ballot_sync(0xffffffffu, lane < 8 && chunk_good(p, m, m.kt0 + kt, lane, ids)) & 0xFFu;
+      // loads for the next tile, or for the next item
+      if (kt + 1 < nkv) {
+        ids = chunk(m, kt + 1);
+      } else {
+        PrefillItem mn;  // (read again once this item is through: fewer registers)
+        item_n = peek_item(sh, it + 1, abort_flag, &mn);
+        if (item_n < 0) return;  // aborted
+        if (valid(item_n)) {
+          ids = chunk(mn, 0);
+          raw_n = load_row(p, mn, mn.i0 + row / G);
+        }
+      }
+      ok = wait_small(&sh.s_full[b], (Tg / kSBufs) & 1u, abort_flag);
+      if (!ok) return;
+      tc::fence_after_sync();
+      // a tile every row sees in full needs no mask
+      const int ka = m.kt0 + kt;  // key tile (keys ka*128 ..)
+      const bool full = mask == 0xFFu && ka * kTileN >= m.full_lo &&
+                        ka * kTileN + kTileN <= m.full_hi;
+      // this thread's keys 64ch .. 64ch+63 of the tile: sr[0] the first 32
+      uint32_t sr[2][32];
+      tc::ld_half32<64>(t_s, sr[0]);
+      tc::ld_half32<64>(t_s + 32, sr[1]);
+      tc::wait32(sr[0]);
+      tc::wait32(sr[1]);
+      uint32_t vis[2] = {0xffffffffu, 0xffffffffu};  // this thread's visible keys, a bit each
+      if (!full) {
+        const int lo = rk.lo - ka * kTileN - 64 * ch, hi = rk.hi - ka * kTileN - 64 * ch;
+        const uint32_t cm = mask >> (4 * ch);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          vis[q] = bits_between(lo - 32 * q, hi - 32 * q) &
+                   (((cm >> (2 * q)) & 1u ? 0xffffu : 0u) |
+                    ((cm >> (2 * q + 1)) & 1u ? 0xffff0000u : 0u));
+      }
+      if constexpr (CAP) {
+        // Rows of the tile that were not loaded, or hold no key yet, must not
+        // decide which form of the cap is taken.
+        if (mask != 0xFFu || ka * kTileN < m.k_lo || ka * kTileN + kTileN > m.kv_len) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!(vis[q] & (1u << i))) sr[q][i] = 0u;
+        }
+        float am[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            am[(i >> 1) & 3] = max3f(am[(i >> 1) & 3], fabsf(__uint_as_float(sr[q][i])),
+                                     fabsf(__uint_as_float(sr[q][i + 1])));
+        const float amax = fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3]));
+        if (__any_sync(0xffffffffu, amax > p.cap_lim)) {
+          // exact form, eight scores at a time, S replaced in tensor memory
+          // (kept small: it is rarely taken)
+          const float cap2 = p.score.softcap * kLog2e;
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 8) {
+            uint32_t x[8];
+            tc::ld_half8<64>(t_s + c, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              x[i] = __float_as_uint(cap2 * tanh_log2(__uint_as_float(x[i]) * p.cap_z));
+            tc::st_half8<64>(t_s + c, x);
+          }
+          tc::wait_st();
+          tc::ld_half32<64>(t_s, sr[0]);
+          tc::ld_half32<64>(t_s + 32, sr[1]);
+          tc::wait32(sr[0]);
+          tc::wait32(sr[1]);
+        } else {
+          const float2 a0 = make_float2(p.cap_a[0], p.cap_a[0]),
+                       a1 = make_float2(p.cap_a[1], p.cap_a[1]),
+                       a2 = make_float2(p.cap_a[2], p.cap_a[2]),
+                       a3 = make_float2(p.cap_a[3], p.cap_a[3]),
+                       a4 = make_float2(p.cap_a[4], p.cap_a[4]);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 x =
+                  make_float2(__uint_as_float(sr[q][i]), __uint_as_float(sr[q][i + 1]));
+              const float2 w = fmul2(x, x);
+              const float2 y =
+                  fmul2(x, ffma2(ffma2(ffma2(ffma2(a4, w, a3), w, a2), w, a1), w, a0));
+              sr[q][i] = __float_as_uint(y.x);
+              sr[q][i + 1] = __float_as_uint(y.y);
+            }
+        }
+      }
+      if constexpr (BIAS) {
+        // score (with a cap already in base 2) - slope2 * |ref - j|
+        const float2 k2 = CAP ? make_float2(1.f, 1.f) : make_float2(p.scale_log2, p.scale_log2);
+        const int d = ka * kTileN + 64 * ch - rk.ref;  // of this thread's first key
+        const float d0 = static_cast<float>(d);
+        if (__all_sync(0xffffffffu, d + 63 <= 0)) {  // every key at or before its row's position
+          const float2 base = make_float2(slope2 * d0, slope2 * d0);
+          const float2 sl = make_float2(slope2, slope2);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 bias = ffma2(
+                  sl, make_float2(static_cast<float>(q * 32 + i), static_cast<float>(q * 32 + i + 1)),
+                  base);
+              const float2 y = ffma2(
+                  make_float2(__uint_as_float(sr[q][i]), __uint_as_float(sr[q][i + 1])), k2, bias);
+              sr[q][i] = __float_as_uint(y.x);
+              sr[q][i + 1] = __float_as_uint(y.y);
+            }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              sr[q][i] = __float_as_uint(__uint_as_float(sr[q][i]) * k2.x -
+                                         slope2 * fabsf(d0 + static_cast<float>(q * 32 + i)));
+        }
+      }
+      if (!full) {  // invisible keys become -inf
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!(vis[q] & (1u << i))) sr[q][i] = __float_as_uint(-INFINITY);
+      }
+      if constexpr (!FIXED) {
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            mx4[(i >> 1) & 3] =
+                max3f(mx4[(i >> 1) & 3], __uint_as_float(sr[q][i]), __uint_as_float(sr[q][i + 1]));
+        float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+        // (scale > 0 keeps the argmax; both threads of the row get the same bits)
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) * mul;
+        if (__any_sync(0xffffffffu, mx > m_run + kRescaleLog2)) {
+          const float m_new = fmaxf(m_run, mx);
+          const float alpha = (m_new == -INFINITY) ? 1.f : exp2f(m_run - m_new);
+          l_run *= alpha;
+          m_run = m_new;
+          if (kt > 0) {
+            // O holds PV of the item's earlier tiles; the last of them is PV(Tg-1)
+            const uint32_t Tp = Tg - 1;
+            ok = wait_small(&sh.pv_done[Tp % kSBufs], (Tp / kSBufs) & 1u, abort_flag);
+            if (!ok) return;
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int q = 0; q < HC / 32; ++q) {  // this thread's O columns HC*ch + 32q ..
+              uint32_t o[32];
+              tc::ld_half32<HC>(t_lane + 32 * q, o);
+              tc::wait32(o);
+#pragma unroll
+              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+              tc::st_half32<HC>(t_lane + 32 * q, o);
+            }
+          }
+        }
+      }
+      // P = 2^(s * scale - m) as bf16 (-inf -> 0) over the S buffer: column
+      // c holds keys 2c (low half) and 2c+1, so this thread's keys land in
+      // columns 32ch .. 32ch+31 (pairs of keys in the packed fp32x2 FMA / add)
+      float2 ps4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                       make_float2(0.f, 0.f)};
+      const float msub = (m_run == -INFINITY) ? 0.f : m_run;
+      const float2 sc2 = make_float2(mul, mul), nm2 = make_float2(-msub, -msub);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          float2 e = make_float2(__uint_as_float(sr[q][2 * j]), __uint_as_float(sr[q][2 * j + 1]));
+          if constexpr (!FIXED) e = ffma2(e, sc2, nm2);
+          const float2 pp = make_float2(exp2f(e.x), exp2f(e.y));
+          pk[j] = pack_bf16x2(pp.x, pp.y);
+          ps4[j & 3] = fadd2(ps4[j & 3], pp);
+        }
+        tc::st_half16<32>(t_s + 16 * q, pk);
+      }
+      l_run += ((ps4[0].x + ps4[1].x) + (ps4[2].x + ps4[3].x)) +
+               ((ps4[0].y + ps4[1].y) + (ps4[2].y + ps4[3].y));
+      // V rows of keys past kv_len or of chunks not loaded must be zero
+      // (0 * NaN): for such a tile wait for its V copy first; thread (row,
+      // ch) clears 64-element chunk ch of V row `row`
+      // in a tile that some row does not see in full, the V rows that
+      // stay must be finite
+      if (!full) {
+        const int slot = static_cast<int>(Tg % kVStages);
+        // S(Tg) done only implies PV(Tg-3) done, so the slot's copy
+        // barrier may be anywhere from V(Tg-2) pending to V(Tg) landed;
+        // once PV(Tg-2) is done (slot released) it is V(Tg) pending or landed
+        if (Tg >= static_cast<uint32_t>(kVStages)) {
+          const uint32_t Tp = Tg - kVStages;
+          ok = wait_small(&sh.pv_done[Tp % kSBufs], (Tp / kSBufs) & 1u, abort_flag);
+        }
+        if (ok) ok = wait_small(&sh.v_full[slot], (Tg / kVStages) & 1u, abort_flag);
+        if (!ok) return;
+        uint4* v4 = reinterpret_cast<uint4*>(gbase + Lay::kV + slot * Lay::kTileKV +
+                                             (row >> 3) * Lay::kGroupBytes + ch * 1024 +
+                                             (row & 7) * 128);
+        if (ch < DH && (ka * kTileN + row >= m.kv_len || !(mask >> (row >> 4) & 1u) ||
+                        ka * kTileN + row < m.k_lo)) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) v4[x] = make_uint4(0, 0, 0, 0);
+        } else if (ch < DH && zero_nonfinite(v4)) {
+          BadKeys& bad = reinterpret_cast<BadKeys*>(gbase + Lay::kBad)[it % kBadLists];
+          const int i = atomicAdd(&bad.count, 1);
+          if (i < kMaxBadKeys) bad.key[i] = ka * kTileN + row;
+        }
+        fence_proxy_async_smem();
+      }
+      tc::wait_st();
+      if (!pend) {
+        tc::fence_before_sync();
+        mbar_arrive(&sh.p_ready[b]);
+      } else {
+        uint32_t o[NQ][32];
+        int n_bad = 0;
+        if (!epilogue_load(it - 1, T - 1, o, n_bad)) return;
+        tc::fence_before_sync();
+        mbar_arrive(&sh.p_ready[b]);
+        epilogue_store(it - 1, o, n_bad);
+        pend = false;
+      }
+    }
+    pend = true;
+    const int qi = m.i0 + row / G;
+    pend_qi = qi < m.n ? qi : -1;
+    pend_q0 = m.q0;
+    pend_g = m.g;
+    pend_piece = m.piece;
+    pend_bt = m.bt_row;
+    pend_lo = rk.lo;
+    pend_hi = rk.hi;
+    pend_max = m_run;
+    pend_sum = l_run;
+    T += nkv;
+    item = take_item(sh, it + 1, abort_flag, true, &m);
+    if (valid(item)) rk = row_of(p, m, m.i0 + row / G, raw_n);
+  }
+  if (pend) {
+    uint32_t o[NQ][32];
+    int n_bad = 0;
+    if (epilogue_load(it - 1, T - 1, o, n_bad)) epilogue_store(it - 1, o, n_bad);
+  }
 }
 
 // Persistent CTAs; CTA b takes items b, b + gridDim.x, ... (items come
@@ -533,17 +1006,21 @@ __device__ __forceinline__ bool chunk_ok(const PrefillParams& p, const PrefillIt
 //            of each row per thread, and the item's epilogue (each thread
 //            normalises and writes half of its row's output columns).
 //
-// SCORED: the scores are capped, biased or masked by key ranges
-// (ScoreParams). The K-copy warp finds the keys that an item's rows see and
-// publishes them with the item, so every role walks only those tiles; the
-// softmax warps transform their scores in registers and mask by each row's
-// own range.
-template <int D, bool SCORED>
+// SCORED (SC other than kPlain): the scores are capped, biased or masked by
+// key ranges (ScoreParams). The K-copy warp finds the keys that an item's rows
+// see and publishes them with the item, so every role walks only those tiles;
+// the softmax warps transform their scores in registers and mask by each
+// row's own range. One instance per combination of cap and bias: with all of
+// it in one, chosen at run time, the kernel's 130 KB of code missed the
+// instruction caches (no_instruction was its largest stall, and 8191 rows of
+// packed documents took 180 us instead of 115).
+template <int D, int SC>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
                    const PrefillParams p) {
   using Lay = PrefillLayout<D>;
   constexpr int DH = Lay::DH;
+  constexpr bool SCORED = SC != kPlain;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -636,7 +1113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (two dependent loads), while the current one's last tiles are still in
     // flight, and published for every role at once
     int claimed = n_items;
-    int4 claimed_keys = make_int4(0, 0, 0, 0);
+    PrefillItem claimed_m{};
     auto claim_ahead = [&](int it) {
       const int slot = it % kItemQ;
       int item = n_items;
@@ -647,22 +1124,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       claimed = __shfl_sync(0xffffffffu, item, 0);
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      if (valid(claimed))
-        claimed_keys = item_keys(p, prefill_item(p, n_req, claimed, QT, meta, meta_prefix), QT);
+      if (valid(claimed)) {
+        claimed_m = prefill_item(p, n_req, claimed, QT, meta, meta_prefix);
+        narrow_item(claimed_m, item_keys(p, claimed_m, QT));
+      }
       if (ln == 0) {
         sh.item_q[slot] = claimed;
-        sh.item_keys[slot] = claimed_keys;
+        sh.item_m[slot] = claimed_m;
         mbar_arrive(&sh.iq_full[slot]);
       }
     };
-    if (SCORED && !is_v) claim_ahead(0);
     for (int it = 0; ok; ++it) {
       int item;
-      int4 keys = make_int4(0, 0, 0, 0);
+      PrefillItem m;
       if (SCORED && !is_v) {
+        claim_ahead(it);
         item = claimed;
-        keys = claimed_keys;
-        if (it > 0 && valid(item)) ok = wait_or_abort(&sh.q_free, (it - 1) & 1u, abort_flag);
+        m = claimed_m;
+        if (it > 0 && ok && valid(item)) ok = wait_or_abort(&sh.q_free, (it - 1) & 1u, abort_flag);
       } else if (!is_v) {
         // the Q buffer is free once the previous item's last S is done; only
         // then is the next item claimed (work counter), so that items go to
@@ -680,12 +1159,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         item = __shfl_sync(0xffffffffu, item, 0);
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       } else {
-        item = take_item(sh, it, abort_flag, true, SCORED ? &keys : nullptr);
+        item = take_item(sh, it, abort_flag, true, SCORED ? &m : nullptr);
         if (item < 0) ok = false;
       }
       if (!ok || !valid(item)) break;
-      PrefillItem m = prefill_item(p, n_req, item, QT, meta, meta_prefix);
-      if constexpr (SCORED) narrow_item(m, keys);
+      if constexpr (!SCORED) m = prefill_item(p, n_req, item, QT, meta, meta_prefix);
       if (!is_v) {
         if (ln == 0) {
           fence_proxy_async_smem();
@@ -733,7 +1211,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                       ((id * 2 + (is_v ? 1 : 0)) << bsh) >> 3, &full[slot]);
         ++T;
       }
-      if (SCORED && !is_v && ok) claim_ahead(it + 1);
     }
     if (!ok) {  // let the copies in flight land before the shared memory goes away
       for (int s = 0; s < S; ++s)
@@ -752,12 +1229,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t T = 0;  // tiles of earlier items
       bool ok = true;
       for (int it = 0; ok; ++it) {
-        int4 keys;
-        const int item = take_item(sh, it, abort_flag, false, SCORED ? &keys : nullptr);
+        PrefillItem m;
+        const int item = take_item(sh, it, abort_flag, false, SCORED ? &m : nullptr);
         if (item < 0) ok = false;
         if (!ok || !valid(item)) break;
-        PrefillItem m = prefill_item(p, n_req, item, QT, meta, meta_prefix);
-        if constexpr (SCORED) narrow_item(m, keys);
+        if constexpr (!SCORED) m = prefill_item(p, n_req, item, QT, meta, meta_prefix);
         const int nkv = m.nkv;
         if (is_s) {
           ok = wait_or_abort(&sh.q_full, it & 1u, abort_flag);
@@ -815,6 +1291,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(&sh.drain[is_s ? 0 : 1], 0, ok ? kWaitLimitNs : kDrainLimitNs);
     }
     __syncwarp();
+  } else if constexpr (SCORED) {
+    scored_softmax<D, SC>(p, sh, gbase, tmem, n_items);
   } else {
     // ================= softmax warps 0..7: every tile of every item. Warp w
     // owns TMEM lanes (query rows) lane0 .. lane0+15 with lane0 = 32*(w%4) +
@@ -832,103 +1310,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     // chunk validity of tile kt of item m (lanes 0..7), read one tile ahead
     auto load_ids = [&](const PrefillItem& mm, int kt) -> int {
-      return (lane < 8 && kt < mm.nkv && chunk_ok<SCORED>(p, mm, mm.kt0 + kt, lane)) ? 1 : -1;
+      return (lane < 8 && kt < mm.nkv && chunk_ok(p, mm, mm.kt0 + kt, lane)) ? 1 : -1;
     };
-    // The epilogue of item `it` of the CTA, whose last tile is Tl: this
-    // thread's O columns HC*ch .. HC*ch + HC - 1 of its row.
-    auto epilogue = [&](int it, const PrefillItem& m, const RowKeys& rk, float m_run, float l_run,
-                        uint32_t Tl) -> bool {
-      if (!wait_or_abort(&sh.o_full, it & 1u, abort_flag)) return false;
-      int n_bad = 0;
-      BadKeys* bad = reinterpret_cast<BadKeys*>(gbase + Lay::kBad);
-      if constexpr (SCORED) {
-        // the item's bad keys, complete once every thread has published P of
-        // its last tile Tl. Threads may be filling the lists of the next two
-        // items; the third, last read by the epilogue of item it - 1, which
-        // every thread has left (it comes before its P of this item), and
-        // not filled before all threads have passed here, is emptied.
-        if (!wait_or_abort(&sh.p_ready[Tl % kSBufs], (Tl / kSBufs) & 1u, abort_flag)) return false;
-        n_bad = *reinterpret_cast<volatile int*>(&bad[it % kBadLists].count);
-        if (tid == 0) bad[(it + 3) % kBadLists].count = 0;
-      }
-      tc::fence_after_sync();
-      const float l_tot = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
-      const float inv = SCORED && l_tot == 0.f ? 0.f : 1.f / l_tot;  // no key seen: zeros
-      const int qi = m.i0 + row / G;
-      const bool store = qi < m.n;
-      const int head = m.g * G + row % G;
-      // shared-prefix items keep the row's partial (max, sum, unnormalised O)
-      // for the decode of request shared_first + qi: slot of (piece, qi, head)
-      const bool partial = m.piece >= 0;
-      const long long pslot = (static_cast<long long>(m.piece) * p.shared_num + qi) * p.num_q_heads + head;
-      if (partial && store && ch == 0) p.shared_ml[pslot] = make_float2(m_run, l_tot);
-      uint16_t* dst = p.out + (static_cast<long long>(m.q0 + qi) * p.num_q_heads + head) * D + HC * ch;
-#pragma unroll 1
-      for (int q = 0; q < HC / 32; ++q) {
-        uint32_t o[32];
-        tc::ld_half32<HC>(t_lane + 32 * q, o);
-        tc::wait32(o);
-        if (!store) continue;
-        if (SCORED && n_bad > 0) {
-          const bool listed = n_bad <= kMaxBadKeys;
-          const int a0 = listed ? 0 : rk.lo, a1 = listed ? n_bad : rk.hi;
-          uint32_t t[32];  // (a copy, so that o stays in registers otherwise)
-#pragma unroll
-          for (int x = 0; x < 32; ++x) t[x] = o[x];
-          for (int i = a0; i < a1; ++i) {
-            const int j = listed ? bad[it % kBadLists].key[i] : i;
-            if (j >= rk.lo && j < rk.hi)
-              add_nonfinite(p, m.bt_row, m.g, D, j, HC * ch + 32 * q, t);
-          }
-#pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] = t[x];
-        }
-        if (partial) {
-          float4* d4 = reinterpret_cast<float4*>(p.shared_o + pslot * D + HC * ch + 32 * q);
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            d4[x] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
-                                __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
-        } else {
-          uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            w[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-          uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * q);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) d4[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
-        }
-      }
-      return true;
-    };
-    int4 keys;
-    int item = take_item(sh, 0, abort_flag, true, SCORED ? &keys : nullptr);
+    int item = take_item(sh, 0, abort_flag, true, nullptr);
     PrefillItem m{};
-    RowKeys rk{0, 0, 0};  // SCORED: the keys of this thread's row
     int next_id = -1;
     if (valid(item)) {
       m = prefill_item(p, n_req, item, QT, meta, meta_prefix);
-      if constexpr (SCORED) {
-        narrow_item(m, keys);
-        rk = item_row_keys(p, m, m.i0 + row / G);
-      }
       next_id = load_ids(m, 0);
     }
-    // SCORED: the previous item, its epilogue still to come
-    bool pend = false;
-    PrefillItem pend_m{};
-    RowKeys pend_rk{0, 0, 0};
-    float pend_max = 0.f, pend_sum = 0.f;
-    int it = 0;
-    for (; ok && valid(item); ++it) {
+    for (int it = 0; ok && valid(item); ++it) {
       const int nkv = m.nkv;
       const int qi = m.i0 + row / G;                // query of this row
       const int lim = min(m.c + qi, m.kv_len - 1);  // last key this row may see
-      float m_run = SCORED && p.cap_fixed ? 0.f : -INFINITY, l_run = 0.f;
-      // SCORED: bias per key of distance, base-2 scores
-      const float slope2 =
-          SCORED && p.score.slopes ? __ldg(p.score.slopes + m.g * G + row % G) * kLog2e : 0.f;
-      const float mul = SCORED ? p.post_mul : p.scale_log2;
+      float m_run = -INFINITY, l_run = 0.f;
       for (int kt = 0; kt < nkv; ++kt) {
         const uint32_t Tg = T + kt;
         const uint32_t b = Tg % kSBufs;
@@ -941,86 +1336,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // tile is visible iff j <= lim - 128 ka and its 16-key chunk was
         // loaded (chunk c = keys 16c .. 16c+15)
         const int ka = m.kt0 + kt;  // key tile (keys ka*128 ..)
-        const bool full =
-            mask == 0xFFu && (SCORED ? ka * kTileN >= m.full_lo && ka * kTileN + kTileN <= m.full_hi
-                                     : ka * kTileN + kTileN - 1 <= m.c + m.i0);
+        const bool full = ka * kTileN + kTileN - 1 <= m.c + m.i0 && mask == 0xFFu;
         // this thread's keys 64ch .. 64ch+63 of the tile: sr[0] the first 32
         uint32_t sr[2][32];
         tc::ld_half32<64>(t_s, sr[0]);
         tc::ld_half32<64>(t_s + 32, sr[1]);
         tc::wait32(sr[0]);
         tc::wait32(sr[1]);
-        uint32_t vis[2] = {0xffffffffu, 0xffffffffu};  // SCORED: visible keys, a bit each
-        if constexpr (SCORED) {
-          if (!full) {
-            const int lo = rk.lo - ka * kTileN - 64 * ch, hi = rk.hi - ka * kTileN - 64 * ch;
-            const uint32_t cm = mask >> (4 * ch);
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-              vis[q] = bits_between(lo - 32 * q, hi - 32 * q) &
-                       (((cm >> (2 * q)) & 1u ? 0xffffu : 0u) |
-                        ((cm >> (2 * q + 1)) & 1u ? 0xffff0000u : 0u));
-            // what the tensor core made of rows that were not loaded must not
-            // decide which form of the cap is taken
-            if (p.cap_lim > 0.f) {
-#pragma unroll
-              for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (!(vis[q] & (1u << i))) sr[q][i] = 0u;
-            }
-          }
-          bool small = false;
-          if (p.cap_lim > 0.f) {
-            float am[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int i = 0; i < 32; i += 2)
-                am[(i >> 1) & 3] = max3f(am[(i >> 1) & 3], fabsf(__uint_as_float(sr[q][i])),
-                                         fabsf(__uint_as_float(sr[q][i + 1])));
-            small = __all_sync(0xffffffffu,
-                               fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3])) <= p.cap_lim);
-          }
-          if (small) {
-            const float2 a0 = make_float2(p.cap_a[0], p.cap_a[0]), a1 = make_float2(p.cap_a[1], p.cap_a[1]),
-                         a2 = make_float2(p.cap_a[2], p.cap_a[2]), a3 = make_float2(p.cap_a[3], p.cap_a[3]),
-                         a4 = make_float2(p.cap_a[4], p.cap_a[4]);
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 x = make_float2(__uint_as_float(sr[q][i]), __uint_as_float(sr[q][i + 1]));
-                const float2 w = fmul2(x, x);
-                const float2 y =
-                    fmul2(x, ffma2(ffma2(ffma2(ffma2(a4, w, a3), w, a2), w, a1), w, a0));
-                sr[q][i] = __float_as_uint(y.x);
-                sr[q][i + 1] = __float_as_uint(y.y);
-              }
-          } else if (p.score.softcap > 0.f) {
-            const float cap2 = p.score.softcap * kLog2e;
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                sr[q][i] = __float_as_uint(cap2 * tanh_log2(__uint_as_float(sr[q][i]) * p.cap_z));
-          } else if (p.score.slopes) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                sr[q][i] = __float_as_uint(__uint_as_float(sr[q][i]) * p.scale_log2);
-          }
-          if (p.score.slopes) {
-            const float d0 = static_cast<float>(ka * kTileN + 64 * ch - rk.ref);
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                sr[q][i] = __float_as_uint(__uint_as_float(sr[q][i]) -
-                                           slope2 * fabsf(d0 + static_cast<float>(q * 32 + i)));
-          }
-        }
         if (!full) {  // invisible keys become -inf
           const int jlim = lim - ka * kTileN - 64 * ch;
           const uint32_t cm = mask >> (4 * ch);
@@ -1029,11 +1351,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const int j = q * 32 + i;
-              if (SCORED ? !(vis[q] & (1u << i)) : !(((cm >> (j >> 4)) & 1u) && j <= jlim))
-                sr[q][i] = __float_as_uint(-INFINITY);
+              if (!(((cm >> (j >> 4)) & 1u) && j <= jlim)) sr[q][i] = __float_as_uint(-INFINITY);
             }
         }
-        if (!SCORED || !p.cap_fixed) {
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int q = 0; q < 2; ++q)
@@ -1043,7 +1363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 max3f(mx4[(i >> 1) & 3], __uint_as_float(sr[q][i]), __uint_as_float(sr[q][i + 1]));
         float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         // (scale > 0 keeps the argmax; both threads of the row get the same bits)
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) * mul;
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) * p.scale_log2;
         if (__any_sync(0xffffffffu, mx > m_run + kRescaleLog2)) {
           const float m_new = fmaxf(m_run, mx);
           const float alpha = (m_new == -INFINITY) ? 1.f : exp2f(m_run - m_new);
@@ -1066,14 +1386,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        }
         // P = 2^(s * scale - m) as bf16 (-inf -> 0) over the S buffer: column
         // c holds keys 2c (low half) and 2c+1, so this thread's keys land in
         // columns 32ch .. 32ch+31 (pairs of keys in the packed fp32x2 FMA / add)
         float2 ps4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                          make_float2(0.f, 0.f)};
         const float msub = (m_run == -INFINITY) ? 0.f : m_run;
-        const float2 sc2 = make_float2(mul, mul), nm2 = make_float2(-msub, -msub);
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-msub, -msub);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t pk[16];
@@ -1092,9 +1411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // V rows of keys past kv_len or of chunks not loaded must be zero
         // (0 * NaN): for such a tile wait for its V copy first; thread (row,
         // ch) clears 64-element chunk ch of V row `row`
-        // SCORED: in a tile that some row does not see in full, the V rows that
-        // stay must be finite
-        if (SCORED ? !full : ka * kTileN + kTileN > m.kv_len || mask != 0xFFu) {
+        if (ka * kTileN + kTileN > m.kv_len || mask != 0xFFu) {
           const int slot = static_cast<int>(Tg % kVStages);
           // S(Tg) done only implies PV(Tg-3) done, so the slot's copy
           // barrier may be anywhere from V(Tg-2) pending to V(Tg) landed;
@@ -1105,35 +1422,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (ok) ok = wait_or_abort(&sh.v_full[slot], (Tg / kVStages) & 1u, abort_flag);
           if (!ok) break;
-          uint4* v4 = reinterpret_cast<uint4*>(gbase + Lay::kV + slot * Lay::kTileKV +
-                                               (row >> 3) * Lay::kGroupBytes + ch * 1024 +
-                                               (row & 7) * 128);
-          if (ch < DH && (ka * kTileN + row >= m.kv_len || !(mask >> (row >> 4) & 1u) ||
-                          (SCORED && ka * kTileN + row < m.k_lo))) {
+          if (ch < DH && (ka * kTileN + row >= m.kv_len || !(mask >> (row >> 4) & 1u))) {
+            uint4* v4 = reinterpret_cast<uint4*>(gbase + Lay::kV + slot * Lay::kTileKV +
+                                                 (row >> 3) * Lay::kGroupBytes + ch * 1024 +
+                                                 (row & 7) * 128);
 #pragma unroll
             for (int x = 0; x < 8; ++x) v4[x] = make_uint4(0, 0, 0, 0);
-          } else if (SCORED && ch < DH && zero_nonfinite(v4)) {
-            BadKeys& bad = reinterpret_cast<BadKeys*>(gbase + Lay::kBad)[it % kBadLists];
-            const int i = atomicAdd(&bad.count, 1);
-            if (i < kMaxBadKeys) bad.key[i] = ka * kTileN + row;
           }
           fence_proxy_async_smem();
         }
         tc::wait_st();
-        if (SCORED && pend) {
-          // O is overwritten once P of this tile is published
-          pend = false;
-          ok = epilogue(it - 1, pend_m, pend_rk, pend_max, pend_sum, T - 1);
-          if (!ok) break;
-        }
         tc::fence_before_sync();
         mbar_arrive(&sh.p_ready[b]);
         next_id = load_ids(m, kt + 1);  // its latency hides under the next S wait
       }
       if (!ok) break;
       // ---- the next item's id and metadata, while the last PV runs
-      const RowKeys rk_cur = rk;
-      const int item_n = take_item(sh, it + 1, abort_flag, true, SCORED ? &keys : nullptr);
+      const int item_n = take_item(sh, it + 1, abort_flag, true, nullptr);
       if (item_n < 0) {  // aborted
         ok = false;
         break;
@@ -1141,29 +1446,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       PrefillItem m_next{};
       if (valid(item_n)) {
         m_next = prefill_item(p, n_req, item_n, QT, meta, meta_prefix);
-        if constexpr (SCORED) {
-          narrow_item(m_next, keys);
-          rk = item_row_keys(p, m_next, m_next.i0 + row / G);
-        }
         next_id = load_ids(m_next, 0);
       }
-      if constexpr (SCORED) {
-        // left until the next item's first tile is in registers (above), so
-        // that its softmax runs while this item's last PV does
-        pend = true;
-        pend_m = m;
-        pend_rk = rk_cur;
-        pend_max = m_run;
-        pend_sum = l_run;
-      } else {
-        ok = epilogue(it, m, rk, m_run, l_run, T + nkv - 1);
-        if (!ok) break;
+      // ---- epilogue: this thread's O columns HC*ch .. HC*ch + HC - 1 of its row
+      ok = wait_or_abort(&sh.o_full, it & 1u, abort_flag);
+      if (!ok) break;
+      tc::fence_after_sync();
+      const float l_tot = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
+      const float inv = 1.f / l_tot;
+      const bool store = qi < m.n;
+      const int head = m.g * G + row % G;
+      // shared-prefix items keep the row's partial (max, sum, unnormalised O)
+      // for the decode of request shared_first + qi: slot of (piece, qi, head)
+      const bool partial = m.piece >= 0;
+      const long long pslot = (static_cast<long long>(m.piece) * p.shared_num + qi) * p.num_q_heads + head;
+      if (partial && store && ch == 0) p.shared_ml[pslot] = make_float2(m_run, l_tot);
+      uint16_t* dst = p.out + (static_cast<long long>(m.q0 + qi) * p.num_q_heads + head) * D + HC * ch;
+#pragma unroll 1
+      for (int q = 0; q < HC / 32; ++q) {
+        uint32_t o[32];
+        tc::ld_half32<HC>(t_lane + 32 * q, o);
+        tc::wait32(o);
+        if (!store) continue;
+        if (partial) {
+          float4* d4 = reinterpret_cast<float4*>(p.shared_o + pslot * D + HC * ch + 32 * q);
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            d4[x] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
+                                __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
+        } else {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            w[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+          uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * q);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) d4[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+        }
       }
       T += nkv;
       m = m_next;
       item = item_n;
     }
-    if (SCORED && ok && pend) epilogue(it - 1, pend_m, pend_rk, pend_max, pend_sum, T - 1);
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -1175,10 +1499,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool SCORED>
+template <int D, int SC>
 static cudaError_t launch_prefill_t(const PrefillParams& p, const CUtensorMap& kv_map,
                                     const CUtensorMap& q_map, int grid, cudaStream_t stream) {
-  auto kern = prefill_kernel<D, SCORED>;
+  auto kern = prefill_kernel<D, SC>;
   const int smem = static_cast<int>(PrefillLayout<D>::kAlloc);
   static std::atomic<unsigned long long> attr_done{0};
   cudaError_t e = smem_attr_once(kern, smem, attr_done);
@@ -1205,15 +1529,14 @@ cudaError_t launch_prefill(const AttnArgs& a, const AttnWorkspace& ws, const CUt
   p.scale_log2 = a.scale * kLog2e;
   p.score = a.score;
   p.cap_z = a.score.softcap > 0.f ? 2.f * kLog2e * (a.scale / a.score.softcap) : 0.f;
+  p.out32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
   const float ratio = a.score.softcap > 0.f ? a.scale / a.score.softcap : 0.f;
   const bool poly = ratio >= kCapRatioMin && ratio <= kCapRatioMax;
   p.cap_lim = poly ? kCapLim / ratio : 0.f;
   double pw = static_cast<double>(a.score.softcap) * kLog2e * ratio;
   for (int i = 0; i < 5; ++i, pw *= static_cast<double>(ratio) * ratio)
     p.cap_a[i] = poly ? static_cast<float>(kCapPoly[i] * pw) : 0.f;
-  p.cap_fixed = a.score.softcap > 0.f && !a.score.slopes &&
-                a.score.softcap * kLog2e <= kCapFixedMax;
-  p.post_mul = a.score.softcap > 0.f || a.score.slopes ? 1.f : p.scale_log2;
+  const bool wide_cap = a.score.softcap * kLog2e > kCapFixedMax;
   p.hdr = ws.hdr;
   p.pf_req = ws.pf_req;
   p.pf_prefix = ws.pf_prefix;
@@ -1236,12 +1559,19 @@ cudaError_t launch_prefill(const AttnArgs& a, const AttnWorkspace& ws, const CUt
     max_items += (a.shared_num + tile_q - 1) / tile_q * a.shared_pieces * a.num_kv_heads;
   const int grid = static_cast<int>(max_items < num_sms ? max_items : num_sms);
   if (grid <= 0) return cudaSuccess;
-  if (a.head_dim == 128)
-    return a.scored ? launch_prefill_t<128, true>(p, kv_map, q_map, grid, stream)
-                    : launch_prefill_t<128, false>(p, kv_map, q_map, grid, stream);
-  if (a.head_dim == 64)
-    return a.scored ? launch_prefill_t<64, true>(p, kv_map, q_map, grid, stream)
-                    : launch_prefill_t<64, false>(p, kv_map, q_map, grid, stream);
+  const int sc = !a.scored ? kPlain
+                           : kRanges | (a.score.softcap > 0.f ? kCap : 0) |
+                                 (a.score.slopes || wide_cap ? kBias : 0);
+#define PKV_PREFILL_CASE(D_, SC_) \
+  if (a.head_dim == D_ && sc == (SC_)) \
+    return launch_prefill_t<D_, (SC_)>(p, kv_map, q_map, grid, stream);
+#define PKV_PREFILL_D(D_)                                                    \
+  PKV_PREFILL_CASE(D_, kPlain) PKV_PREFILL_CASE(D_, kRanges)                 \
+  PKV_PREFILL_CASE(D_, kRanges | kCap) PKV_PREFILL_CASE(D_, kRanges | kBias) \
+  PKV_PREFILL_CASE(D_, kRanges | kCap | kBias)
+  PKV_PREFILL_D(128) PKV_PREFILL_D(64)
+#undef PKV_PREFILL_D
+#undef PKV_PREFILL_CASE
   return cudaErrorInvalidValue;
 }
 

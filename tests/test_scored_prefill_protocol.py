@@ -2,12 +2,13 @@
 
 The roles are those of test_prefill_protocol.py with two differences: the
 K-copy warp claims and publishes the next item before it waits for the Q
-buffer, and a softmax agent leaves an item's epilogue until it has the next
-item's first tile in hand, just before it publishes that tile's P (the
-accumulator is overwritten only after that). Agents also fill a list of bad V
-rows per item; there are four, and agent 0 empties, in the epilogue of item i,
-the list of item i + 3. The model checks that an epilogue finds its item's
-list complete and with nothing else in it.
+buffer, and a softmax agent looks at the next item at the current one's last
+tile (it takes it when that tile is through) and leaves the current one's epilogue until it has the next item's first tile
+in hand: it reads O just before it publishes that tile's P (the accumulator is
+overwritten only after that) and stores the row afterwards. Agents also fill a
+list of bad V rows per item and read it as they store; there are five, and
+agent 0 empties, as it reads O of item i, the list of item i + 3. The model
+checks that a store finds its item's list complete and with nothing else in it.
 """
 
 import random
@@ -44,28 +45,35 @@ def k_warp_ahead(cta):
         item = cta.item_q[it % ITEM_Q]
 
 
-def agent(cta, a, lists=4, reset=3, publish_first=False):
+def agent(cta, a, lists=5, reset=3, publish_first=False):
     rng = random.Random(cta.rng.random())
     if not hasattr(cta, "lists"):
         cta.lists, cta.fills, cta.closed = [0] * lists, {}, set()
     T, it = 0, 0
     pend = None
 
-    def epilogue(i, last):
+    def load(i, last):
         yield ("wait", "o_full", i)
         yield ("wait", f"p_ready{last % S_BUFS}", last // S_BUFS)
-        assert cta.lists[i % lists] == cta.fills.get(i, 0), f"list of item {i}"
         cta.closed.add(i)
+        assert cta.lists[i % lists] == cta.fills.get(i, 0), f"list of item {i}"
         if a == 0:
-            yield ("step", None, None)  # others may run between the read and the reset
             cta.lists[(i + reset) % lists] = 0
         cta.o_read[i] = cta.o_read.get(i, 0) + 1
+
+    def store(i):
+        for _ in range(2):  # others may run between the reads of the list
+            yield ("step", None, None)
+            assert cta.lists[i % lists] == cta.fills.get(i, 0), f"list of item {i}"
 
     item = yield from take(cta, 0, 1)
     while item is not None:
         nkv = cta.items[item]
         for kt in range(nkv):
             Tg = T + kt
+            if kt == nkv - 1:
+                yield ("wait", f"iq_full{(it + 1) % ITEM_Q}", (it + 1) // ITEM_Q)
+                seen = cta.item_q[(it + 1) % ITEM_Q]
             yield ("wait", f"s_full{Tg % S_BUFS}", Tg // S_BUFS)
             cta.s_read[Tg] = cta.s_read.get(Tg, 0) + 1
             if kt > 0 and rng.random() < 0.3:  # the max grew: rescale O
@@ -84,16 +92,20 @@ def agent(cta, a, lists=4, reset=3, publish_first=False):
             if publish_first:
                 yield ("arrive", f"p_ready{Tg % S_BUFS}", 1)
             if pend is not None:
-                yield from epilogue(*pend)
-                pend = None
+                yield from load(*pend)
             if not publish_first:
                 yield ("arrive", f"p_ready{Tg % S_BUFS}", 1)
+            if pend is not None:
+                yield from store(pend[0])
+                pend = None
         pend = (it, T + nkv - 1)
         T += nkv
         it += 1
         item = yield from take(cta, it, 1)
+        assert item == seen
     if pend is not None:
-        yield from epilogue(*pend)
+        yield from load(*pend)
+        yield from store(pend[0])
 
 
 ROLES = {"k": k_warp_ahead, "agent": agent}
@@ -116,8 +128,9 @@ def test_all_one_tile_and_all_long():
 PLANTED = {
     # P published before the previous item's O was read
     "epilogue_after_p": {"k": k_warp_ahead, "agent": lambda c, a: agent(c, a, publish_first=True)},
-    # two lists
-    "two_lists": {"k": k_warp_ahead, "agent": lambda c, a: agent(c, a, lists=2, reset=1)},
+    # fewer lists: the one emptied is still read
+    "three_lists": {"k": k_warp_ahead, "agent": lambda c, a: agent(c, a, lists=3, reset=2)},
+    "four_lists": {"k": k_warp_ahead, "agent": lambda c, a: agent(c, a, lists=4, reset=3)},
     # the list emptied is one that others fill
     "reset_next": {"k": k_warp_ahead, "agent": lambda c, a: agent(c, a, reset=1)},
 }
