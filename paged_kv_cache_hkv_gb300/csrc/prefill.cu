@@ -177,6 +177,8 @@ static_assert(kKStages == kSBufs, "K slot T % 3 is freed by the commit of S buff
 constexpr uint32_t kTmemS = 128;  // TMEM columns: O at [0, D), S buffer b at [128 + 128b, +128)
 constexpr uint32_t kTmemCols = 512;
 constexpr int kItemQ = 4;      // claimed work items in flight between the roles
+constexpr int kMaskRing = 8;   // SCORED: tiles whose chunk masks are kept. K(T+8) is copied
+                               // once S(T+5) is done, so PV(T+2): every reader of mask T is through
 constexpr int kMetaReqs = 128;  // prefill requests whose metadata a CTA keeps in shared memory
 constexpr int kThreads = 384;  // 8 softmax warps, S-MMA warp, K-copy warp, V-copy warp, PV-MMA warp
 constexpr float kRescaleLog2 = 8.f;  // lazy rescale threshold (powers of two)
@@ -199,7 +201,7 @@ struct PrefillLayout {
   // then the item prefix int [kMetaReqs + 1]
   static constexpr uint32_t kMeta = kV + kVStages * kTileKV;
   static constexpr uint32_t kBar = kMeta + kMetaReqs * 16 + (kMetaReqs + 1) * 4 + 124;
-  static constexpr uint32_t kBad = kBar + 512;  // BadKeys of kBadLists items
+  static constexpr uint32_t kBad = kBar + 640;  // BadKeys of kBadLists items
   static constexpr uint32_t kBytes = kBad + 1024;
   static constexpr uint32_t kAlloc = kBytes + 1024;  // room to align the base
   static_assert(kAlloc <= 232448, "shared memory");
@@ -252,7 +254,7 @@ struct PrefillParams {
 // (1.0e-6: equal-ripple, found by reweighted least squares). The powers of
 // scale / softcap and the factor softcap * log2(e) go into the coefficients,
 // so a pair of scores takes six packed FMA-pipe instructions; as a whole the
-// prefill of 4 x 2048 rows over 8192 keys went 1828 -> 1218 us with it and without the running maximum. A
+// prefill of 4 x 2048 rows over 8192 keys went 1828 -> 1116 us with it and without the running maximum. A
 // warp that holds a larger |u| takes the exact form (tanh_log2) for its tile.
 constexpr float kCapLim = 0.8f;
 constexpr double kCapPoly[5] = {9.999989943e-01, -3.332537196e-01, 1.323056551e-01, -4.918014086e-02, 1.210013789e-02};
@@ -303,10 +305,12 @@ struct PrefillShared {
   uint64_t iq_free[kItemQ];      // 11 arrivals: every role has read it
   int item_q[kItemQ];
   PrefillItem item_m[kItemQ];    // SCORED: the item described, for every role
+  uint64_t mask_full[kMaskRing]; // SCORED: tile T's mask published in masks[T % kMaskRing]
+  uint32_t masks[kMaskRing];
   uint32_t tmem;
   int abort;
 };
-static_assert(sizeof(PrefillShared) <= 512, "barrier area");
+static_assert(sizeof(PrefillShared) <= 640, "barrier area");
 
 
 
@@ -577,30 +581,6 @@ __device__ __forceinline__ bool chunk_ok(const PrefillParams& p, const PrefillIt
          (k0 + 8 >= m.kv_len || entry_id<false>(p, m, (k0 >> 3) + 1) >= 0);
 }
 
-// The same for SCORED items, whose keys are [k_lo, kv_len), in two steps: the
-// chunk's table entries (the second for 8-token blocks only), and their check.
-struct ChunkRaw {
-  int a, b;
-};
-__device__ __forceinline__ ChunkRaw load_chunk(const PrefillParams& p, const PrefillItem& m, int kt,
-                                               int b) {
-  const int k0 = kt * kTileN + b * kChunkKeys, e = k0 >> p.block_shift;
-  ChunkRaw c{-1, -1};
-  if (entry_used<true>(p, m, e)) c.a = __ldg(p.block_table + m.bt_row + e);
-  if (p.block_shift == 3 && entry_used<true>(p, m, e + 1))
-    c.b = __ldg(p.block_table + m.bt_row + e + 1);
-  return c;
-}
-__device__ __forceinline__ bool chunk_good(const PrefillParams& p, const PrefillItem& m, int kt,
-                                           int b, const ChunkRaw& c) {
-  const int k0 = kt * kTileN + b * kChunkKeys, e = k0 >> p.block_shift;
-  if (k0 >= m.kv_len) return false;
-  const bool a_ok = c.a >= 0 && c.a < p.num_blocks, b_ok = c.b >= 0 && c.b < p.num_blocks;
-  if (p.block_shift != 3) return a_ok;
-  if (!entry_used<true>(p, m, e)) return b_ok;
-  return a_ok && (k0 + 8 >= m.kv_len || b_ok);
-}
-
 // The softmax warps of a SCORED kernel: the roles and lane map of the plain
 // ones (see the kernel), with the scores transformed in registers, each row
 // masked by its own range, and two things done to keep short items (packed
@@ -628,9 +608,6 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
   const uint32_t t_lane = tmem + (static_cast<uint32_t>(lane0) << 16);
   BadKeys* bad_lists = reinterpret_cast<BadKeys*>(gbase + Lay::kBad);
   auto valid = [&](int item) { return item >= 0 && item < n_items; };
-  auto chunk = [&](const PrefillItem& m, int kt) -> ChunkRaw {
-    return lane < 8 ? load_chunk(p, m, m.kt0 + kt, lane) : ChunkRaw{-1, -1};
-  };
   const float mul = CAP || BIAS ? 1.f : p.scale_log2;  // scores in registers to base 2
   uint32_t T = 0;  // tiles of earlier items
   bool ok = true;
@@ -718,11 +695,7 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
   PrefillItem m{};
   int item = take_item(sh, 0, abort_flag, true, &m);
   RowKeys rk{0, 0, 0};  // the keys of this thread's row
-  ChunkRaw ids{-1, -1};
-  if (valid(item)) {
-    ids = chunk(m, 0);
-    rk = row_of(p, m, m.i0 + row / G, load_row(p, m, m.i0 + row / G));
-  }
+  if (valid(item)) rk = row_of(p, m, m.i0 + row / G, load_row(p, m, m.i0 + row / G));
   int it = 0;
 #pragma unroll 1
   for (; valid(item); ++it) {
@@ -738,20 +711,15 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
       const uint32_t Tg = T + kt;
       const uint32_t b = Tg % kSBufs;
       const uint32_t t_s = t_lane + kTmemS + kTileN * b;
-      const uint32_t mask =
-          __ballot_sync(0xffffffffu, lane < 8 && chunk_good(p, m, m.kt0 + kt, lane, ids)) & 0xFFu;
-      // loads for the next tile, or for the next item
-      if (kt + 1 < nkv) {
-        ids = chunk(m, kt + 1);
-      } else {
+      if (kt + 1 == nkv) {  // the next item's loads go out
         PrefillItem mn;  // (read again once this item is through: fewer registers)
         item_n = peek_item(sh, it + 1, abort_flag, &mn);
         if (item_n < 0) return;  // aborted
-        if (valid(item_n)) {
-          ids = chunk(mn, 0);
-          raw_n = load_row(p, mn, mn.i0 + row / G);
-        }
+        if (valid(item_n)) raw_n = load_row(p, mn, mn.i0 + row / G);
       }
+      ok = wait_small(&sh.mask_full[Tg % kMaskRing], (Tg / kMaskRing) & 1u, abort_flag);
+      if (!ok) return;
+      const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&sh.masks[Tg % kMaskRing]);
       ok = wait_small(&sh.s_full[b], (Tg / kSBufs) & 1u, abort_flag);
       if (!ok) return;
       tc::fence_after_sync();
@@ -792,6 +760,23 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
           for (int i = 0; i < 32; i += 2)
             am[(i >> 1) & 3] = max3f(am[(i >> 1) & 3], fabsf(__uint_as_float(sr[q][i])),
                                      fabsf(__uint_as_float(sr[q][i + 1])));
+        // the polynomial for all of them, and the vote after it: the maximum
+        // and its shuffles then run beside it
+        const float2 a0 = make_float2(p.cap_a[0], p.cap_a[0]),
+                     a1 = make_float2(p.cap_a[1], p.cap_a[1]),
+                     a2 = make_float2(p.cap_a[2], p.cap_a[2]),
+                     a3 = make_float2(p.cap_a[3], p.cap_a[3]),
+                     a4 = make_float2(p.cap_a[4], p.cap_a[4]);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float2 x = make_float2(__uint_as_float(sr[q][i]), __uint_as_float(sr[q][i + 1]));
+            const float2 w = fmul2(x, x);
+            const float2 y = fmul2(x, ffma2(ffma2(ffma2(ffma2(a4, w, a3), w, a2), w, a1), w, a0));
+            sr[q][i] = __float_as_uint(y.x);
+            sr[q][i + 1] = __float_as_uint(y.y);
+          }
         const float amax = fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3]));
         if (__any_sync(0xffffffffu, amax > p.cap_lim)) {
           // exact form, eight scores at a time, S replaced in tensor memory
@@ -811,24 +796,6 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
           tc::ld_half32<64>(t_s + 32, sr[1]);
           tc::wait32(sr[0]);
           tc::wait32(sr[1]);
-        } else {
-          const float2 a0 = make_float2(p.cap_a[0], p.cap_a[0]),
-                       a1 = make_float2(p.cap_a[1], p.cap_a[1]),
-                       a2 = make_float2(p.cap_a[2], p.cap_a[2]),
-                       a3 = make_float2(p.cap_a[3], p.cap_a[3]),
-                       a4 = make_float2(p.cap_a[4], p.cap_a[4]);
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 x =
-                  make_float2(__uint_as_float(sr[q][i]), __uint_as_float(sr[q][i + 1]));
-              const float2 w = fmul2(x, x);
-              const float2 y =
-                  fmul2(x, ffma2(ffma2(ffma2(ffma2(a4, w, a3), w, a2), w, a1), w, a0));
-              sr[q][i] = __float_as_uint(y.x);
-              sr[q][i + 1] = __float_as_uint(y.y);
-            }
         }
       }
       if constexpr (BIAS) {
@@ -1043,6 +1010,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh.o_full, 1);
     mbar_init(&sh.drain[0], 1);
     mbar_init(&sh.drain[1], 1);
+    if constexpr (SCORED)
+      for (int i = 0; i < kMaskRing; ++i) mbar_init(&sh.mask_full[i], 1);
     for (int i = 0; i < kItemQ; ++i) {
       mbar_init(&sh.iq_full[i], 1);
       mbar_init(&sh.iq_free[i], 11);
@@ -1199,6 +1168,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (block * 2 + k|v) * B
         const int id = __shfl_sync(0xffffffffu, win_val, (ka * E + (ln & (E - 1)) - win_base) & 31);
         const bool mine = ln < E && id >= 0;
+        if constexpr (SCORED) {
+          if (!is_v) {
+            // the tile's chunks without a used entry out of the pool, a bit
+            // each (unused entries lie outside every row's range)
+            const uint32_t bad =
+                __ballot_sync(0xffffffffu, ln < E && id < 0 && entry_used<true>(p, m, ka * E + ln));
+            if (ln == 0) {
+              uint32_t ok8 = 0xffu;
+              for (uint32_t w = bad; w; w &= w - 1) {
+                const int e = __ffs(w) - 1;  // entry: chunk e, 2e and 2e+1, or e/2
+                ok8 &= ~(bsh == 5 ? 3u << (2 * e) : bsh == 4 ? 1u << e : 1u << (e >> 1));
+              }
+              sh.masks[T % kMaskRing] = ok8;
+              mbar_arrive(&sh.mask_full[T % kMaskRing]);
+            }
+          }
+        }
         const uint32_t box = static_cast<uint32_t>(Lay::kGroupBytes) << (bsh - 3);
         const uint32_t tx = __reduce_add_sync(0xffffffffu, mine ? box : 0u);
         if (ln == 0) {

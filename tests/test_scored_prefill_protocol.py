@@ -9,17 +9,22 @@ overwritten only after that) and stores the row afterwards. Agents also fill a
 list of bad V rows per item and read it as they store; there are five, and
 agent 0 empties, as it reads O of item i, the list of item i + 3. The model
 checks that a store finds its item's list complete and with nothing else in it.
+The K-copy warp publishes a mask per tile in a ring of eight; the model checks
+that each agent finds its own tile's.
 """
 
 import random
 
 import pytest
 
-from test_prefill_protocol import ITEM_Q, K_STAGES, N_SOFTMAX, S_BUFS, V_STAGES, run, take
+from test_prefill_protocol import Barrier, ITEM_Q, K_STAGES, N_SOFTMAX, S_BUFS, V_STAGES, run, take
 
 
-def k_warp_ahead(cta):
+def k_warp_ahead(cta, ring=8):
     T, it = 0, 0
+    cta.masks = [None] * ring
+    for i in range(ring):
+        cta.b[f"mask_full{i}"] = Barrier(f"mask_full{i}", 1)
 
     def claim(j):
         slot = j % ITEM_Q
@@ -38,6 +43,8 @@ def k_warp_ahead(cta):
             if T >= K_STAGES:
                 Tp = T - K_STAGES
                 yield ("wait", f"s_full{Tp % S_BUFS}", Tp // S_BUFS)
+            cta.masks[T % len(cta.masks)] = T
+            yield ("arrive", f"mask_full{T % len(cta.masks)}", 1)
             yield ("tma", f"k_full{T % K_STAGES}")
             T += 1
         it += 1
@@ -74,6 +81,9 @@ def agent(cta, a, lists=5, reset=3, publish_first=False):
             if kt == nkv - 1:
                 yield ("wait", f"iq_full{(it + 1) % ITEM_Q}", (it + 1) // ITEM_Q)
                 seen = cta.item_q[(it + 1) % ITEM_Q]
+            ring = len(cta.masks)
+            yield ("wait", f"mask_full{Tg % ring}", Tg // ring)
+            assert cta.masks[Tg % ring] == Tg
             yield ("wait", f"s_full{Tg % S_BUFS}", Tg // S_BUFS)
             cta.s_read[Tg] = cta.s_read.get(Tg, 0) + 1
             if kt > 0 and rng.random() < 0.3:  # the max grew: rescale O
@@ -131,6 +141,8 @@ PLANTED = {
     # fewer lists: the one emptied is still read
     "three_lists": {"k": k_warp_ahead, "agent": lambda c, a: agent(c, a, lists=3, reset=2)},
     "four_lists": {"k": k_warp_ahead, "agent": lambda c, a: agent(c, a, lists=4, reset=3)},
+    # a ring of masks as short as the K ring
+    "three_masks": {"k": lambda c: k_warp_ahead(c, ring=3), "agent": agent},
     # the list emptied is one that others fill
     "reset_next": {"k": k_warp_ahead, "agent": lambda c, a: agent(c, a, reset=1)},
 }
