@@ -172,6 +172,13 @@ constexpr int kTileM = 128;    // query rows (query x head) per tile
 constexpr int kTileN = 128;    // keys per tile (8 chunks of 16)
 constexpr int kKStages = 3;    // K ring: global tile T uses slot T % 3
 constexpr int kVStages = 2;    // V ring: global tile T uses slot T % 2
+// The scored kernels split the same memory the other way. S(T) is issued as
+// soon as PV(T-3) is done, well before K could run short; V(T) with two slots
+// is copied only after PV(T-2), which in items of a few tiles left the softmax
+// (it looks at the V rows of partly seen tiles) and the PV waiting for the
+// copy's ~1 us.
+constexpr int kScoredKStages = 2, kScoredVStages = 3;
+static_assert(kScoredKStages + kScoredVStages == kKStages + kVStages, "one ring area");
 constexpr int kSBufs = 3;      // S (then P) buffers in TMEM: global tile T uses buffer T % 3
 static_assert(kKStages == kSBufs, "K slot T % 3 is freed by the commit of S buffer T % 3");
 constexpr uint32_t kTmemS = 128;  // TMEM columns: O at [0, D), S buffer b at [128 + 128b, +128)
@@ -185,6 +192,14 @@ constexpr float kRescaleLog2 = 8.f;  // lazy rescale threshold (powers of two)
 // Scores of a kernel instance: plain, or key ranges with or without a cap
 // (ScoreParams::softcap) and a bias (ScoreParams::slopes).
 enum : int { kPlain = 0, kRanges = 1, kCap = 2, kBias = 4 };
+// Order of an item's key tiles, the kt-th of nkv. With a bias that falls with
+// distance the nearest keys weigh most: taken last to first, the running
+// maximum is found in the first tile, where the other way round a steep slope
+// moves it (and rescales O, after a wait for the last PV) in every tile.
+template <int SC>
+__device__ __forceinline__ int tile_at(int kt0, int nkv, int kt) {
+  return kt0 + ((SC & kBias) ? nkv - 1 - kt : kt);
+}
 
 template <int D>
 struct PrefillLayout {
@@ -254,7 +269,7 @@ struct PrefillParams {
 // (1.0e-6: equal-ripple, found by reweighted least squares). The powers of
 // scale / softcap and the factor softcap * log2(e) go into the coefficients,
 // so a pair of scores takes six packed FMA-pipe instructions; as a whole the
-// prefill of 4 x 2048 rows over 8192 keys went 1828 -> 1116 us with it and without the running maximum. A
+// prefill of 4 x 2048 rows over 8192 keys went 1828 -> 1104 us with it and without the running maximum. A
 // warp that holds a larger |u| takes the exact form (tanh_log2) for its tile.
 constexpr float kCapLim = 0.8f;
 constexpr double kCapPoly[5] = {9.999989943e-01, -3.332537196e-01, 1.323056551e-01, -4.918014086e-02, 1.210013789e-02};
@@ -290,8 +305,8 @@ struct PrefillItem {
 struct PrefillShared {
   uint64_t q_full;               // Q tile of the item landed (TMA)
   uint64_t q_free;               // commit: the item's last S read Q
-  uint64_t k_full[kKStages];     // K tile landed (TMA)
-  uint64_t v_full[kVStages];     // V tile landed (TMA)
+  uint64_t k_full[3];            // K tile landed (TMA); one per slot of the ring
+  uint64_t v_full[3];            // V tile landed (TMA)
   uint64_t s_full[kSBufs];       // commit: S of the buffer's tile in TMEM (and the
                                  // K slot of the same index free: both rings have 3)
   uint64_t pv_done[kSBufs];      // commit: PV of the buffer's tile done (its P read,
@@ -423,9 +438,9 @@ __device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
 }
 
 // 32-byte store; the address 32-byte aligned.
-__device__ __forceinline__ void st_global_v8(void* dst, const uint32_t* v) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
-               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+__device__ __forceinline__ void st_global_v8(void* dst, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a.x),
+               "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
                : "memory");
 }
 
@@ -581,6 +596,16 @@ __device__ __forceinline__ bool chunk_ok(const PrefillParams& p, const PrefillIt
          (k0 + 8 >= m.kv_len || entry_id<false>(p, m, (k0 >> 3) + 1) >= 0);
 }
 
+// cap2 * tanh(u) for z = 2 log2(e) u, cap2 = softcap * log2(e). 1 - 2 / (2^z + 1)
+// is off by a few 2^-24 however small u is, so by a few 2^-24 cap2 in the
+// exponent of a weight: 2^-15 at most where cap2 <= kCapFixedMax. Wider caps
+// need tanh_log2's relative form.
+template <bool FIXED>
+__device__ __forceinline__ float exact_cap(float z, float cap2) {
+  if constexpr (!FIXED) return cap2 * tanh_log2(z);
+  return fmaf(-2.f * cap2, __fdividef(1.f, exp2f(z) + 1.f), cap2);
+}
+
 // The softmax warps of a SCORED kernel: the roles and lane map of the plain
 // ones (see the kernel), with the scores transformed in registers, each row
 // masked by its own range, and two things done to keep short items (packed
@@ -599,9 +624,10 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
   constexpr int DH = Lay::DH;
   constexpr int HC = D / 2;  // O columns per thread
   constexpr int NQ = HC / 32;
+  constexpr uint32_t kRingV = Lay::kK + kScoredKStages * Lay::kTileKV;
   volatile int* abort_flag = &sh.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = p.group;
+  const int G = p.group, gsh = 31 - __clz(G);  // G is 1, 2, 4 or 8
   const int ch = lane >> 4;  // key half of this thread
   const int lane0 = 32 * (warp & 3) + 16 * (warp >> 2);
   const int row = lane0 + (lane & 15);  // query row of this thread (TMEM lane)
@@ -615,7 +641,7 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
   // the epilogue of the item before the current one, number it - 1, in two
   // steps around the publication of P (none before the first)
   bool pend = false;
-  int pend_qi = -1, pend_q0 = 0, pend_g = 0, pend_piece = -1;  // qi < 0: no row to store
+  int pend_i0 = 0, pend_n = 0, pend_q0 = 0, pend_g = 0, pend_piece = -1;
   int pend_lo = 0, pend_hi = 0;
   long long pend_bt = 0;
   float pend_max = 0.f, pend_sum = 0.f;
@@ -640,9 +666,9 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
   auto epilogue_store = [&](int it, const uint32_t (&o)[NQ][32], int n_bad) {
     const float l_tot = pend_sum + __shfl_xor_sync(0xffffffffu, pend_sum, 16);
     const float inv = l_tot == 0.f ? 0.f : 1.f / l_tot;  // no key seen: zeros
-    const int qi = pend_qi;
-    if (qi < 0) return;
-    const int head = pend_g * G + row % G;
+    const int qi = pend_i0 + (row >> gsh);
+    const bool mine = qi < pend_n;
+    const int head = pend_g * G + (row & (G - 1));
     uint16_t* dst =
         p.out + ((static_cast<long long>(pend_q0) + qi) * p.num_q_heads + head) * D + HC * ch;
     float* part = nullptr;
@@ -651,35 +677,45 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
       // for the decode of request shared_first + qi: slot of (piece, qi, head)
       const long long pslot =
           (static_cast<long long>(pend_piece) * p.shared_num + qi) * p.num_q_heads + head;
-      if (ch == 0) p.shared_ml[pslot] = make_float2(pend_max, l_tot);
       part = p.shared_o + pslot * D + HC * ch;
+      if (mine) {
+        if (ch == 0) p.shared_ml[pslot] = make_float2(pend_max, l_tot);
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        float4* d4 = reinterpret_cast<float4*>(part + 32 * q);
+        for (int q = 0; q < NQ; ++q) {
+          float4* d4 = reinterpret_cast<float4*>(part + 32 * q);
 #pragma unroll
-        for (int x = 0; x < 8; ++x)
-          d4[x] = make_float4(__uint_as_float(o[q][4 * x]), __uint_as_float(o[q][4 * x + 1]),
-                              __uint_as_float(o[q][4 * x + 2]), __uint_as_float(o[q][4 * x + 3]));
+          for (int x = 0; x < 8; ++x)
+            d4[x] = make_float4(__uint_as_float(o[q][4 * x]), __uint_as_float(o[q][4 * x + 1]),
+                                __uint_as_float(o[q][4 * x + 2]), __uint_as_float(o[q][4 * x + 3]));
+        }
       }
-    } else {
+    } else if (mine) {
+      // straight from the thread that holds the half row, in whole 32-byte
+      // sectors where the output's alignment allows (turning the rows in
+      // shared memory first, for stores of whole rows, was slower: 117
+      // instead of 107 us on 8191 rows of packed documents)
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
-        uint32_t w[16];
+        uint4 w[4];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          w[e] = pack_bf16x2(__uint_as_float(o[q][2 * e]) * inv, __uint_as_float(o[q][2 * e + 1]) * inv);
-        // each thread writes its own row: whole 32-byte sectors where the
-        // output's alignment allows, so that a row's sector is written once
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t* v = &o[q][8 * x];
+          w[x].x = pack_bf16x2(__uint_as_float(v[0]) * inv, __uint_as_float(v[1]) * inv);
+          w[x].y = pack_bf16x2(__uint_as_float(v[2]) * inv, __uint_as_float(v[3]) * inv);
+          w[x].z = pack_bf16x2(__uint_as_float(v[4]) * inv, __uint_as_float(v[5]) * inv);
+          w[x].w = pack_bf16x2(__uint_as_float(v[6]) * inv, __uint_as_float(v[7]) * inv);
+        }
         if (p.out32) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) st_global_v8(dst + 32 * q + 16 * x, &w[8 * x]);
+          st_global_v8(dst + 32 * q, w[0], w[1]);
+          st_global_v8(dst + 32 * q + 16, w[2], w[3]);
         } else {
           uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * q);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) d4[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+          for (int x = 0; x < 4; ++x) d4[x] = w[x];
         }
       }
     }
+    if (!mine) return;
     if (n_bad > 0) {
       const BadKeys& bad = bad_lists[it % kBadLists];
       const bool listed = n_bad <= kMaxBadKeys;
@@ -695,7 +731,7 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
   PrefillItem m{};
   int item = take_item(sh, 0, abort_flag, true, &m);
   RowKeys rk{0, 0, 0};  // the keys of this thread's row
-  if (valid(item)) rk = row_of(p, m, m.i0 + row / G, load_row(p, m, m.i0 + row / G));
+  if (valid(item)) rk = row_of(p, m, m.i0 + (row >> gsh), load_row(p, m, m.i0 + (row >> gsh)));
   int it = 0;
 #pragma unroll 1
   for (; valid(item); ++it) {
@@ -705,7 +741,7 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
     float m_run = FIXED ? 0.f : -INFINITY, l_run = 0.f;
     // bias per key of distance, base-2 scores
     const float slope2 =
-        BIAS && p.score.slopes ? __ldg(p.score.slopes + m.g * G + row % G) * kLog2e : 0.f;
+        BIAS && p.score.slopes ? __ldg(p.score.slopes + m.g * G + (row & (G - 1))) * kLog2e : 0.f;
 #pragma unroll 1
     for (int kt = 0; kt < nkv; ++kt) {
       const uint32_t Tg = T + kt;
@@ -715,7 +751,7 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
         PrefillItem mn;  // (read again once this item is through: fewer registers)
         item_n = peek_item(sh, it + 1, abort_flag, &mn);
         if (item_n < 0) return;  // aborted
-        if (valid(item_n)) raw_n = load_row(p, mn, mn.i0 + row / G);
+        if (valid(item_n)) raw_n = load_row(p, mn, mn.i0 + (row >> gsh));
       }
       ok = wait_small(&sh.mask_full[Tg % kMaskRing], (Tg / kMaskRing) & 1u, abort_flag);
       if (!ok) return;
@@ -724,7 +760,7 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
       if (!ok) return;
       tc::fence_after_sync();
       // a tile every row sees in full needs no mask
-      const int ka = m.kt0 + kt;  // key tile (keys ka*128 ..)
+      const int ka = tile_at<SC>(m.kt0, nkv, kt);  // key tile (keys ka*128 ..)
       const bool full = mask == 0xFFu && ka * kTileN >= m.full_lo &&
                         ka * kTileN + kTileN <= m.full_hi;
       // this thread's keys 64ch .. 64ch+63 of the tile: sr[0] the first 32
@@ -780,7 +816,9 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
         const float amax = fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3]));
         if (__any_sync(0xffffffffu, amax > p.cap_lim)) {
           // exact form, eight scores at a time, S replaced in tensor memory
-          // (kept small: it is rarely taken)
+          // (all 64 in registers took 1782 instead of 1937 us where every tile
+          // needs it, but 1437 instead of 1296 where one in eight does: more
+          // code in the way of the polynomial)
           const float cap2 = p.score.softcap * kLog2e;
 #pragma unroll 1
           for (int c = 0; c < 64; c += 8) {
@@ -788,7 +826,7 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
             tc::ld_half8<64>(t_s + c, x);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              x[i] = __float_as_uint(cap2 * tanh_log2(__uint_as_float(x[i]) * p.cap_z));
+              x[i] = __float_as_uint(exact_cap<FIXED>(__uint_as_float(x[i]) * p.cap_z, cap2));
             tc::st_half8<64>(t_s + c, x);
           }
           tc::wait_st();
@@ -896,17 +934,12 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
       // in a tile that some row does not see in full, the V rows that
       // stay must be finite
       if (!full) {
-        const int slot = static_cast<int>(Tg % kVStages);
-        // S(Tg) done only implies PV(Tg-3) done, so the slot's copy
-        // barrier may be anywhere from V(Tg-2) pending to V(Tg) landed;
-        // once PV(Tg-2) is done (slot released) it is V(Tg) pending or landed
-        if (Tg >= static_cast<uint32_t>(kVStages)) {
-          const uint32_t Tp = Tg - kVStages;
-          ok = wait_small(&sh.pv_done[Tp % kSBufs], (Tp / kSBufs) & 1u, abort_flag);
-        }
-        if (ok) ok = wait_small(&sh.v_full[slot], (Tg / kVStages) & 1u, abort_flag);
+        // S(Tg) done implies PV(Tg-3) done, so the slot's barrier is at V(Tg),
+        // pending or landed
+        const int slot = static_cast<int>(Tg % kScoredVStages);
+        ok = wait_small(&sh.v_full[slot], (Tg / kScoredVStages) & 1u, abort_flag);
         if (!ok) return;
-        uint4* v4 = reinterpret_cast<uint4*>(gbase + Lay::kV + slot * Lay::kTileKV +
+        uint4* v4 = reinterpret_cast<uint4*>(gbase + kRingV + slot * Lay::kTileKV +
                                              (row >> 3) * Lay::kGroupBytes + ch * 1024 +
                                              (row & 7) * 128);
         if (ch < DH && (ka * kTileN + row >= m.kv_len || !(mask >> (row >> 4) & 1u) ||
@@ -935,8 +968,8 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
       }
     }
     pend = true;
-    const int qi = m.i0 + row / G;
-    pend_qi = qi < m.n ? qi : -1;
+    pend_i0 = m.i0;
+    pend_n = m.n;
     pend_q0 = m.q0;
     pend_g = m.g;
     pend_piece = m.piece;
@@ -947,7 +980,7 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
     pend_sum = l_run;
     T += nkv;
     item = take_item(sh, it + 1, abort_flag, true, &m);
-    if (valid(item)) rk = row_of(p, m, m.i0 + row / G, raw_n);
+    if (valid(item)) rk = row_of(p, m, m.i0 + (row >> gsh), raw_n);
   }
   if (pend) {
     uint32_t o[NQ][32];
@@ -988,6 +1021,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   using Lay = PrefillLayout<D>;
   constexpr int DH = Lay::DH;
   constexpr bool SCORED = SC != kPlain;
+  constexpr int KST = SCORED ? kScoredKStages : kKStages;
+  constexpr int VST = SCORED ? kScoredVStages : kVStages;
+  constexpr uint32_t kRingV = Lay::kK + KST * Lay::kTileKV;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -1000,8 +1036,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_free, 1);
-    for (int i = 0; i < kKStages; ++i) mbar_init(&sh.k_full[i], 1);
-    for (int i = 0; i < kVStages; ++i) mbar_init(&sh.v_full[i], 1);
+    for (int i = 0; i < KST; ++i) mbar_init(&sh.k_full[i], 1);
+    for (int i = 0; i < VST; ++i) mbar_init(&sh.v_full[i], 1);
     for (int i = 0; i < kSBufs; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.pv_done[i], 1);
@@ -1070,9 +1106,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // block table sit in the lanes' registers.
     const int ln = tid & 31;
     const bool is_v = warp == 10;
-    const int S = is_v ? kVStages : kKStages;
+    const int S = is_v ? VST : KST;
     uint64_t* full = is_v ? sh.v_full : sh.k_full;
-    const uint32_t ring = is_v ? Lay::kV : Lay::kK;
+    const uint32_t ring = is_v ? kRingV : Lay::kK;
     const int bsh = p.block_shift;
     const int E = kTileN >> bsh;  // table entries per tile
     uint32_t T = 0;               // tiles issued so far (all items)
@@ -1155,9 +1191,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     : wait_or_abort(&sh.s_full[Tp % kSBufs], (Tp / kSBufs) & 1u, abort_flag);
           if (!ok) break;
         }
-        const int ka = m.kt0 + kt;  // key tile (keys ka*128 ..)
-        if (ka * E + E > win_base + 32) {
-          win_base = ka * E;
+        const int ka = tile_at<SC>(m.kt0, m.nkv, kt);  // key tile (keys ka*128 ..)
+        if (ka * E + E > win_base + 32 || ((SC & kBias) && ka * E < win_base)) {
+          // 32 entries from this tile's on (last to first: up to this tile's)
+          win_base = (SC & kBias) ? max(0, ka * E + E - 32) : ka * E;
           const int e = win_base + ln;
           win_val = entry_id<SCORED>(p, m, e);
           if (!is_v && entry_used<SCORED>(p, m, e) && win_val < 0)
@@ -1230,7 +1267,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t b = Tk % kSBufs;
             if (Tk >= static_cast<uint32_t>(kSBufs))
               ok = wait_or_abort(&sh.pv_done[b], ((Tk - kSBufs) / kSBufs) & 1u, abort_flag);
-            if (ok) ok = wait_or_abort(&sh.k_full[b], (Tk / kKStages) & 1u, abort_flag);
+            const uint32_t ks = SCORED ? Tk % KST : b;
+            if (ok) ok = wait_or_abort(&sh.k_full[ks], (Tk / KST) & 1u, abort_flag);
             if (!ok) break;
             tc::fence_after_sync();
 #pragma unroll
@@ -1238,7 +1276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t sub = (kk & 3) * 32;  // 16 elements within the 64-element half
               const uint64_t a = tc::sw128_desc(base + Lay::kQ + (kk >> 2) * Lay::kChunk + sub, 16, 1024);
               const uint64_t bd = tc::sw128_desc(
-                  base + Lay::kK + b * Lay::kTileKV + (kk >> 2) * 1024 + sub, 16, Lay::kGroupBytes);
+                  base + Lay::kK + ks * Lay::kTileKV + (kk >> 2) * 1024 + sub, 16, Lay::kGroupBytes);
               tc::mma_bf16(tmem + kTmemS + kTileN * b, a, bd, idesc_qk, kk > 0);
             }
             tc::commit(&sh.s_full[b]);  // S in TMEM, and the K slot free
@@ -1252,12 +1290,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             // read O.
             const uint32_t Tg = T + kt;
             const uint32_t b = Tg % kSBufs;
-            const int slot = static_cast<int>(Tg % kVStages);
+            const int slot = static_cast<int>(Tg % VST);
             ok = wait_or_abort(&sh.p_ready[b], (Tg / kSBufs) & 1u, abort_flag);
-            if (ok) ok = wait_or_abort(&sh.v_full[slot], (Tg / kVStages) & 1u, abort_flag);
+            if (ok) ok = wait_or_abort(&sh.v_full[slot], (Tg / VST) & 1u, abort_flag);
             if (!ok) break;
             tc::fence_after_sync();
-            const uint32_t vbase = base + Lay::kV + slot * Lay::kTileKV;
+            const uint32_t vbase = base + kRingV + slot * Lay::kTileKV;
 #pragma unroll
             for (int kk = 0; kk < kTileN / 16; ++kk) {
               // keys 16kk .. 16kk+15: two 8-key groups (SBO), d halves 1 KB apart (LBO)

@@ -1,6 +1,7 @@
 """Model check of the scored prefill kernel's barrier protocol, on the CPU.
 
-The roles are those of test_prefill_protocol.py with two differences: the
+The roles are those of test_prefill_protocol.py with the K ring of two slots
+and the V ring of three, and these differences: the
 K-copy warp claims and publishes the next item before it waits for the Q
 buffer, and a softmax agent looks at the next item at the current one's last
 tile (it takes it when that tile is through) and leaves the current one's epilogue until it has the next item's first tile
@@ -17,7 +18,16 @@ import random
 
 import pytest
 
-from test_prefill_protocol import Barrier, ITEM_Q, K_STAGES, N_SOFTMAX, S_BUFS, V_STAGES, run, take
+import test_prefill_protocol as plain
+from test_prefill_protocol import Barrier, ITEM_Q, N_SOFTMAX, S_BUFS, run, take
+
+K_STAGES, V_STAGES = 2, 3
+
+
+@pytest.fixture(autouse=True)
+def _rings(monkeypatch):
+    monkeypatch.setattr(plain, "K_STAGES", K_STAGES)
+    monkeypatch.setattr(plain, "V_STAGES", V_STAGES)
 
 
 def k_warp_ahead(cta, ring=8):
@@ -91,9 +101,6 @@ def agent(cta, a, lists=5, reset=3, publish_first=False):
                 yield ("wait", f"pv_done{Tp % S_BUFS}", Tp // S_BUFS)
                 assert Tp in cta.pv_done and Tg not in cta.pv_issued
             if rng.random() < 0.5:  # a partly seen tile: look at its V rows
-                if Tg >= V_STAGES:
-                    Tp = Tg - V_STAGES
-                    yield ("wait", f"pv_done{Tp % S_BUFS}", Tp // S_BUFS)
                 yield ("wait", f"v_full{Tg % V_STAGES}", Tg // V_STAGES)
                 if rng.random() < 0.7:
                     assert it not in cta.closed
