@@ -503,6 +503,9 @@ int32_t pkv_build_step_tables(int32_t* block_table, int32_t max_blocks_per_req,
  *                  pkv_build_step_tables.
  * ref_cnt          in/out, device int32 [num_blocks]: how many rows hold each
  *                  block.
+ * workspace        device buffer of at least pkv_release_workspace_size()
+ *                  bytes, 256-byte aligned, private to this call while it
+ *                  runs (no zeroing needed); may be NULL where that is 0.
  * A row or a length out of range is skipped (PKV_DEVERR_LENGTHS), as is an
  * entry out of the pool (PKV_DEVERR_BLOCK_RANGE). A block that is released more
  * often than it is held goes back once (PKV_DEVERR_REF_COUNT). num_released *
@@ -514,7 +517,16 @@ int32_t pkv_release_blocks(const int32_t* block_table, int32_t max_blocks_per_re
                            const int32_t* release_tokens, int32_t num_released,
                            int32_t* free_queue, const int32_t* free_state,
                            int32_t* free_state_out, int32_t* ref_cnt, int32_t num_blocks,
-                           int32_t block_size, void* stream);
+                           int32_t block_size, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * pkv_release_workspace_size -- bytes of device workspace that
+ * pkv_release_blocks needs for num_released rows of a table of that width (0
+ * for small releases). Returns a negative status on bad arguments. Needs no
+ * device.
+ */
+int64_t pkv_release_workspace_size(int32_t num_released, int32_t max_blocks_per_req);
 
 /*
  * pkv_get_device_errors -- checked path: synchronise `stream`, then return

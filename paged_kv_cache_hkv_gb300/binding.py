@@ -84,7 +84,8 @@ _SIGNATURES = {
                 c_void_p, c_void_p, c_void_p, c_void_p, c_i32, c_i32, c_void_p]),
     "pkv_release_blocks": (
         c_i32, [c_void_p, c_i32, c_i32, c_void_p, c_void_p, c_i32, c_void_p, c_void_p, c_void_p,
-                c_void_p, c_i32, c_i32, c_void_p]),
+                c_void_p, c_i32, c_i32, c_void_p, c_size_t, c_void_p]),
+    "pkv_release_workspace_size": (c_i64, [c_i32, c_i32]),
     "pkv_paged_attention_static_workspace": (
         c_i32, [c_void_p, c_void_p, c_i64, c_void_p, c_void_p, c_i32, c_void_p, c_void_p,
                 c_void_p, c_i32, c_i32, c_i32, c_i32, c_i32, c_float, pkv_cache_layout,
@@ -447,8 +448,16 @@ def _build_args(block_table, query_start_loc, seq_lens, slot_mapping, num_comput
             free_queue.shape[0], int(block_size))
 
 
+def pkv_release_workspace_size(num_released: int, max_blocks_per_req: int) -> int:
+    """Workspace bytes for pkv_release_blocks (0 for small releases)."""
+    n = load().pkv_release_workspace_size(num_released, max_blocks_per_req)
+    if n < 0:
+        raise PagedKVError("pkv_release_workspace_size", int(n))
+    return int(n)
+
+
 def _release_args(block_table, release_rows, release_tokens, free_queue, free_state,
-                  free_state_out, ref_cnt, block_size):
+                  free_state_out, ref_cnt, block_size, workspace):
     if ref_cnt is None:
         raise ValueError("a release needs ref_cnt")
     free_state_out = _table_args(block_table, free_queue, free_state, free_state_out, ref_cnt)
@@ -460,7 +469,8 @@ def _release_args(block_table, release_rows, release_tokens, free_queue, free_st
         raise ValueError("release_tokens must be [num_reqs]")
     return (_ptr(block_table), block_table.shape[1], block_table.shape[0], _ptr(release_rows),
             _ptr(release_tokens), release_rows.shape[0], _ptr(free_queue), _ptr(free_state),
-            _ptr(free_state_out), _ptr(ref_cnt), free_queue.shape[0], int(block_size))
+            _ptr(free_state_out), _ptr(ref_cnt), free_queue.shape[0], int(block_size),
+            _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
 
 
 def pkv_build_step_tables(block_table, query_start_loc, seq_lens, slot_mapping,
@@ -478,17 +488,19 @@ def pkv_build_step_tables(block_table, query_start_loc, seq_lens, slot_mapping,
 
 
 def pkv_release_blocks(block_table, release_rows, release_tokens, free_queue, free_state, ref_cnt,
-                       *, block_size: int, free_state_out=None, stream=None):
-    """Give back the blocks of the rows release_rows (see pagedkv.h)."""
+                       *, block_size: int, workspace=None, free_state_out=None, stream=None):
+    """Give back the blocks of the rows release_rows (see pagedkv.h). workspace:
+    pkv_release_workspace_size() bytes, None where that is 0."""
     _check("pkv_release_blocks", load().pkv_release_blocks(
         *_release_args(block_table, release_rows, release_tokens, free_queue, free_state,
-                       free_state_out, ref_cnt, block_size), _stream(stream)))
+                       free_state_out, ref_cnt, block_size, workspace), _stream(stream)))
 
 
 class TableCalls:
     """pkv_build_step_tables and pkv_release_blocks on buffers that a serving
     loop keeps, with their arguments checked and marshalled once (as StepCalls
-    does for the step's calls). Pass the arguments of either call or of both."""
+    does for the step's calls). Pass the arguments of either call or of both; the
+    release's workspace is made here."""
 
     def __init__(self, *, block_table, free_queue, free_state, block_size: int, ref_cnt=None,
                  free_state_out=None, query_start_loc=None, seq_lens=None, slot_mapping=None,
@@ -501,16 +513,20 @@ class TableCalls:
                 block_table, query_start_loc, seq_lens, slot_mapping, num_computed_tokens,
                 query_lens, free_queue, free_state, free_state_out, ref_cnt, block_size,
                 num_tokens)
+        workspace = None
         if release_rows is not None:
+            nbytes = pkv_release_workspace_size(release_rows.shape[0], block_table.shape[1])
+            if nbytes:
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=block_table.device)
             self.release_args = _release_args(block_table, release_rows, release_tokens,
                                               free_queue, free_state, free_state_out, ref_cnt,
-                                              block_size)
+                                              block_size, workspace)
         if self.build_args is None and self.release_args is None:
             raise ValueError("pass query_lens (build), release_rows (release) or both")
         # the tensors stay referenced, so their memory stays valid
         self._keep = (block_table, free_queue, free_state, ref_cnt, free_state_out,
                       query_start_loc, seq_lens, slot_mapping, num_computed_tokens, query_lens,
-                      release_rows, release_tokens)
+                      release_rows, release_tokens, workspace)
 
     def build(self, stream=None):
         if self.build_args is None:

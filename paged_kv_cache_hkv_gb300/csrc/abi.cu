@@ -642,8 +642,16 @@ int32_t pkv_build_step_tables(int32_t* block_table, int32_t max_blocks_per_req,
   cudaError_t e = pkv::launch_build_tables(
       block_table, max_blocks_per_req, query_start_loc, seq_lens, slot_mapping,
       num_computed_tokens, query_lens, num_reqs, num_tokens, free_queue, free_state,
-      free_state_out, ref_cnt, num_blocks, block_size, static_cast<cudaStream_t>(stream));
+      free_state_out, ref_cnt, num_blocks, block_size, d->num_sms,
+      static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PKV_OK : cuda_fail(e, "build_step_tables launch");
+}
+
+int64_t pkv_release_workspace_size(int32_t num_released, int32_t max_blocks_per_req) {
+  if (num_released < 0 || max_blocks_per_req < 0 ||
+      static_cast<long long>(num_released) * max_blocks_per_req >= (1ll << 29))
+    return PKV_ERR_BAD_SHAPE;
+  return static_cast<int64_t>(pkv::release_workspace_bytes(num_released, max_blocks_per_req));
 }
 
 int32_t pkv_release_blocks(const int32_t* block_table, int32_t max_blocks_per_req,
@@ -651,7 +659,8 @@ int32_t pkv_release_blocks(const int32_t* block_table, int32_t max_blocks_per_re
                            const int32_t* release_tokens, int32_t num_released,
                            int32_t* free_queue, const int32_t* free_state,
                            int32_t* free_state_out, int32_t* ref_cnt, int32_t num_blocks,
-                           int32_t block_size, void* stream) {
+                           int32_t block_size, void* workspace, size_t workspace_bytes,
+                           void* stream) {
   if (num_released < 0 || num_reqs < 0 || max_blocks_per_req < 0 || num_blocks < 1 ||
       block_size < 1)
     return PKV_ERR_BAD_SHAPE;
@@ -670,13 +679,17 @@ int32_t pkv_release_blocks(const int32_t* block_table, int32_t max_blocks_per_re
                         static_cast<const void*>(free_state_out),
                         static_cast<const void*>(ref_cnt)})
     if (!aligned4(p)) return PKV_ERR_MISALIGNED;
+  const size_t need = pkv::release_workspace_bytes(num_released, max_blocks_per_req);
+  if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+                   workspace_bytes < need))
+    return PKV_ERR_WORKSPACE;
   DeviceInfo* d;
   int32_t st = device_info(&d);
   if (st != PKV_OK) return st;
   cudaError_t e = pkv::launch_release_blocks(
       block_table, max_blocks_per_req, num_reqs, release_rows, release_tokens, num_released,
-      free_queue, free_state, free_state_out, ref_cnt, num_blocks, block_size,
-      static_cast<cudaStream_t>(stream));
+      free_queue, free_state, free_state_out, ref_cnt, num_blocks, block_size, workspace,
+      d->num_sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PKV_OK : cuda_fail(e, "release_blocks launch");
 }
 

@@ -174,14 +174,17 @@ cudaError_t launch_build_tables(int32_t* block_table, int max_blocks, int32_t* q
                                 int32_t* seq_lens, int64_t* slots, const int32_t* num_computed,
                                 const int32_t* query_lens, int num_reqs, int num_tokens,
                                 const int32_t* queue, const int32_t* state, int32_t* state_out,
-                                int32_t* ref_cnt, int num_blocks, int block_size,
+                                int32_t* ref_cnt, int num_blocks, int block_size, int num_sms,
                                 cudaStream_t stream);
 
 cudaError_t launch_release_blocks(const int32_t* block_table, int max_blocks, int num_reqs,
                                   const int32_t* rows, const int32_t* tokens, int num_released,
                                   int32_t* queue, const int32_t* state, int32_t* state_out,
                                   int32_t* ref_cnt, int num_blocks, int block_size,
-                                  cudaStream_t stream);
+                                  void* workspace, int num_sms, cudaStream_t stream);
+
+// Scratch of a release (0: it needs none).
+size_t release_workspace_bytes(int num_released, int max_blocks);
 
 cudaError_t read_errors_kvwrite(uint32_t* out, bool clear);
 cudaError_t read_errors_decode(uint32_t* out, bool clear);

@@ -3,19 +3,18 @@
 // (sm_103a).
 //
 // Both calls move integers: a few words per request, one table entry per new
-// block, one slot per new token. What they cost is latency -- the launch,
+// block, one slot per new token. What they cost is latency -- the launches,
 // the dependent loads from a request's lengths to its blocks, and the
-// barriers between phases -- so each is a single launch of one thread-block
-// cluster: its hardware barrier orders the phases, and the free queue's state
-// can be read by every CTA before one of them replaces it in place.
+// barriers between phases -- and, where thousands of requests are released,
+// the rate at which an SM issues scattered atomics.
 //
 // Every CTA scans the lengths of all requests for itself (thread i takes the
 // run of requests [i * per, (i + 1) * per)), which costs a few loads per
 // thread and needs no exchange; the prefix sums of the 1024 runs stay in
-// shared memory. Flat indexes (new tokens, new blocks, released entries) are
-// then spread evenly over the cluster's threads, each of which finds its
-// request by a binary search of the runs and a walk through one run, so that
-// one very long prompt is as evenly spread as thousands of decodes.
+// shared memory. Work is then spread evenly over the grid, one very long
+// prompt as evenly as thousands of decodes: whoever gets a place of a flat
+// index (new tokens, released entries) finds its request by a binary search of
+// the runs and a walk through one run.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -29,57 +28,54 @@ namespace cg = cooperative_groups;
 
 constexpr int kTableThreads = 1024;
 
-// Prefix sums of two counters over the runs of all threads (start[i] = sum
-// before run i, start[kTableThreads] = total).
+// Exclusive prefix sums of N counters over the block's threads: start[c][i] =
+// sum of counter c before thread i, start[c][kTableThreads] = total.
+template <typename T, int N>
 struct RunStarts {
-  long long a[kTableThreads + 1], b[kTableThreads + 1];
+  T start[N][kTableThreads + 1];
+  T warp_sum[N][32];
 };
 
-__device__ __forceinline__ void scan_runs(RunStarts& s, long long a, long long b) {
-  __shared__ long long warp_a[32], warp_b[32];
+template <typename T, int N>
+__device__ __forceinline__ void scan_runs(RunStarts<T, N>& s, const T (&v)[N]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long ia = a, ib = b;
+  T inc[N];
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const long long ua = __shfl_up_sync(0xffffffffu, ia, off);
-    const long long ub = __shfl_up_sync(0xffffffffu, ib, off);
-    if (lane >= off) {
-      ia += ua;
-      ib += ub;
+  for (int c = 0; c < N; ++c) inc[c] = v[c];
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1)
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+      const T u = __shfl_up_sync(0xffffffffu, inc[c], off);
+      if (lane >= off) inc[c] += u;
     }
-  }
-  if (lane == 31) {
-    warp_a[warp] = ia;
-    warp_b[warp] = ib;
-  }
+  if (lane == 31)
+#pragma unroll
+    for (int c = 0; c < N; ++c) s.warp_sum[c][warp] = inc[c];
   __syncthreads();
   if (warp == 0) {
-    const long long wa = warp_a[lane], wb = warp_b[lane];
-    long long ja = wa, jb = wb;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const long long ua = __shfl_up_sync(0xffffffffu, ja, off);
-      const long long ub = __shfl_up_sync(0xffffffffu, jb, off);
-      if (lane >= off) {
-        ja += ua;
-        jb += ub;
+    for (int c = 0; c < N; ++c) {
+      const T w = s.warp_sum[c][lane];
+      T j = w;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const T u = __shfl_up_sync(0xffffffffu, j, off);
+        if (lane >= off) j += u;
       }
-    }
-    warp_a[lane] = ja - wa;
-    warp_b[lane] = jb - wb;
-    if (lane == 31) {
-      s.a[kTableThreads] = ja;
-      s.b[kTableThreads] = jb;
+      s.warp_sum[c][lane] = j - w;
+      if (lane == 31) s.start[c][kTableThreads] = j;
     }
   }
   __syncthreads();
-  s.a[threadIdx.x] = warp_a[warp] + ia - a;
-  s.b[threadIdx.x] = warp_b[warp] + ib - b;
+#pragma unroll
+  for (int c = 0; c < N; ++c) s.start[c][threadIdx.x] = s.warp_sum[c][warp] + inc[c] - v[c];
   __syncthreads();
 }
 
-// The run that holds flat index x < start[kTableThreads].
-__device__ __forceinline__ int run_of(const long long* start, long long x) {
+// The last run that starts at or before x.
+template <typename T>
+__device__ __forceinline__ int run_of(const T* start, T x) {
   int lo = 0;
 #pragma unroll
   for (int step = kTableThreads / 2; step >= 1; step >>= 1)
@@ -124,138 +120,174 @@ __device__ __forceinline__ Ask ask_of(const BuildArgs& a, int r) {
   return k;
 }
 
-__global__ void __launch_bounds__(kTableThreads) build_tables_kernel(const BuildArgs a) {
-  __shared__ RunStarts s;
-  __shared__ long long taken_s;
+// Requests of more new tokens than this are spread over warps, token by
+// token; the others are done by one thread each (a decode is one token).
+constexpr int kShortRows = 8;
+constexpr int kChunkRows = 128;  // consecutive tokens of long requests per warp and turn
+
+// The state of the queue after the step: what leaves it is the largest sum of
+// asks that it covers. One thread, with the sums before each run of requests.
+__device__ __forceinline__ void write_state(const BuildArgs& a, const long long* need_start, int per,
+                                            int head, int count, bool state_ok) {
+  int h = head, c = count;
+  if (state_ok) {
+    const long long n = count;
+    const int run = run_of(need_start, n);
+    long long taken = need_start[run];
+    for (int r = run * per; r < min(a.num_reqs, (run + 1) * per); ++r) {
+      const long long through = taken + ask_of(a, r).need;
+      if (through > n) break;
+      taken = through;
+    }
+    h = static_cast<int>((head + taken) % a.num_blocks);
+    c = static_cast<int>(n - taken);
+  }
+  a.state_out[0] = h;
+  a.state_out[1] = c;
+}
+
+__device__ __forceinline__ bool state_valid(int head, int count, int num_blocks) {
+  return head >= 0 && head < num_blocks && count >= 0 && count <= num_blocks;
+}
+
+__global__ void __launch_bounds__(kTableThreads) build_tables_kernel(const BuildArgs a,
+                                                                     const bool state_here) {
+  __shared__ RunStarts<long long, 3> s;  // batch rows, new blocks, rows of long requests
   pdl_trigger();
   pdl_wait();
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = static_cast<int>(cluster.block_rank());
-  const int nctas = static_cast<int>(cluster.num_blocks());
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int R = a.num_reqs;
-  int head = a.state[0], count = a.state[1];
-  const bool state_ok = head >= 0 && head < a.num_blocks && count >= 0 && count <= a.num_blocks;
-  const int head_in = head, count_in = count;
-  if (!state_ok) head = count = 0;  // nothing to hand out
+  const int head_in = a.state[0], count_in = a.state[1];
+  const bool state_ok = state_valid(head_in, count_in, a.num_blocks);
+  const int head = state_ok ? head_in : 0, count = state_ok ? count_in : 0;  // bad: nothing to hand out
   uint32_t err = state_ok ? 0u : kErrLengths;
 
-  // ---- every CTA: batch rows and new blocks before each run of requests
-  const int per = (R + kTableThreads - 1) / kTableThreads;
-  const int r0 = min(R, tid * per), r1 = min(R, r0 + per);
-  long long rows = 0, need = 0;
-  for (int r = r0; r < r1; ++r) {
-    const Ask k = ask_of(a, r);
-    rows += k.rows;
-    need += k.need;
-  }
-  if (tid == 0) taken_s = 0;
-  scan_runs(s, rows, need);
-  const long long total_rows = s.a[kTableThreads], total_need = s.b[kTableThreads];
-  if (total_rows > a.num_tokens) err |= kErrLengths;
+  // rows of a request in the flat index of long requests. Lengths out of
+  // range can be anything: no more than the batch's rows are looked at.
+  auto long_rows = [&](const Ask& k) -> int {
+    return k.rows <= kShortRows ? 0 : k.bad ? min(k.rows, a.num_tokens) : k.rows;
+  };
 
-  // ---- requests: starts and lengths, first come, first served. A request is
-  // granted its blocks if all that is asked for up to and including it is
-  // there; the largest such sum is what leaves the queue.
+  // ---- every CTA: the sums before each run of requests
+  const int per = (R + kTableThreads - 1) / kTableThreads;
   {
-    long long at = s.a[tid], through = s.b[tid], taken = 0;
-    const bool mine = tid % nctas == rank;
+    const int r0 = min(R, tid * per), r1 = min(R, r0 + per);
+    long long sum[3] = {0, 0, 0};
     for (int r = r0; r < r1; ++r) {
       const Ask k = ask_of(a, r);
-      through += k.need;
-      const bool granted = k.need == 0 || through <= count;
-      if (through <= count) taken = through;
-      if (mine) {
-        a.qsl[r] = static_cast<int32_t>(at < 0x7fffffffll ? at : 0x7fffffffll);
-        a.seq_lens[r] = k.bad || !granted ? 0 : k.c + k.rows;
-        if (k.bad) err |= kErrLengths;
-        if (!granted) err |= kErrNoBlocks;
-      }
-      at += k.rows;
+      sum[0] += k.rows;
+      sum[1] += k.need;
+      sum[2] += long_rows(k);
     }
-    if (rank == 0) {
-      if (tid == 0)
-        a.qsl[R] = static_cast<int32_t>(total_rows < 0x7fffffffll ? total_rows : 0x7fffffffll);
-      if (taken > 0) atomicMax(&taken_s, taken);
-    }
+    scan_runs(s, sum);
   }
+  const long long total_rows = s.start[0][kTableThreads], total_long = s.start[2][kTableThreads];
+  if (total_rows > a.num_tokens) err |= kErrLengths;
 
-  const long long stride = static_cast<long long>(nctas) * kTableThreads;
-  const long long first = static_cast<long long>(rank) * kTableThreads + tid;
-  // place x of the queue, counted from its head
+  // place x of the queue, counted from its head, if it is a block of the pool
   auto popped = [&](long long x) -> int {
     long long i = head + x;
     if (i >= a.num_blocks) i -= a.num_blocks;
-    return __ldg(a.queue + i);
+    const int id = __ldg(a.queue + i);
+    if (id >= 0 && id < a.num_blocks) return id;
+    err |= kErrBlockRange;
+    return -1;
+  };
+  // The i-th new token of request r (its first row `at`, `before` new blocks
+  // asked for by earlier requests): its slot, and, where it is the first
+  // token of a new block, the block's table entry and count. First come,
+  // first served: a request is granted its blocks if all that is asked for up
+  // to and including it is there.
+  auto token = [&](int r, const Ask& k, long long at, long long before, int i) {
+    const bool granted = k.need == 0 || before + k.need <= count;
+    long long slot = -1;
+    if (!k.bad) {
+      const int pos = k.c + i, lb = pos >> a.shift, off = pos & ((1 << a.shift) - 1);
+      int32_t* entry = a.block_table + static_cast<long long>(r) * a.max_blocks + lb;
+      int id = -1;
+      if (lb < k.have)
+        id = granted ? *entry : -1;
+      else if (granted)
+        id = popped(before + lb - k.have);
+      if (lb >= k.have && off == 0) {
+        *entry = id;
+        if (id >= 0 && a.ref_cnt) a.ref_cnt[id] = 1;
+      }
+      if (id >= 0 && id < a.num_blocks)
+        slot = (static_cast<long long>(id) << a.shift) + off;
+      else if (granted)
+        err |= kErrBlockRange;
+    }
+    if (a.slots && at + i < a.num_tokens) a.slots[at + i] = slot;
   };
 
-  // ---- new blocks: table entries and reference counts
-  for (long long x = first; x < total_need; x += stride) {
-    const int run = run_of(s.b, x);
-    int r = run * per;
-    long long before = s.b[run];
-    Ask k = ask_of(a, r);
-    while (before + k.need <= x && r + 1 < R) {
+  const long long first = static_cast<long long>(blockIdx.x) * kTableThreads + tid;
+  const long long stride = static_cast<long long>(gridDim.x) * kTableThreads;
+
+  // ---- a thread per request: start, length, and a short request's tokens
+  for (long long x = first; x < R; x += stride) {
+    const int r = static_cast<int>(x), run = r / per;
+    long long at = s.start[0][run], before = s.start[1][run];
+    for (int j = run * per; j < r; ++j) {
+      const Ask k = ask_of(a, j);
+      at += k.rows;
       before += k.need;
-      k = ask_of(a, ++r);
     }
-    // (lengths that change under the call must not lead outside the table)
-    const long long entry = k.have + (x - before);
-    if (entry >= a.max_blocks) continue;
-    int id = -1;
-    if (before + k.need <= count) {
-      id = popped(x);
-      if (id < 0 || id >= a.num_blocks) {
-        err |= kErrBlockRange;
-        id = -1;
-      } else if (a.ref_cnt) {
-        a.ref_cnt[id] = 1;
-      }
-    }
-    a.block_table[static_cast<long long>(r) * a.max_blocks + entry] = id;
+    const Ask k = ask_of(a, r);
+    const bool granted = k.need == 0 || before + k.need <= count;
+    a.qsl[r] = static_cast<int32_t>(at < 0x7fffffffll ? at : 0x7fffffffll);
+    a.seq_lens[r] = k.bad || !granted ? 0 : k.c + k.rows;
+    if (k.bad) err |= kErrLengths;
+    if (!granted) err |= kErrNoBlocks;
+    if (k.rows <= kShortRows)
+      for (int i = 0; i < k.rows; ++i) token(r, k, at, before, i);
   }
 
-  // ---- new tokens: slots
-  if (a.slots) {
-    for (long long t = first; t < a.num_tokens; t += stride) {
-      long long slot = -1;
-      if (t < total_rows) {
-        const int run = run_of(s.a, t);
-        int r = run * per;
-        long long at = s.a[run], before = s.b[run];
-        Ask k = ask_of(a, r);
-        while (at + k.rows <= t && r + 1 < R) {
-          at += k.rows;
-          before += k.need;
-          k = ask_of(a, ++r);
-        }
-        if (!k.bad && t - at < k.rows && (k.need == 0 || before + k.need <= count)) {
-          const int pos = k.c + static_cast<int>(t - at);
-          const int lb = pos >> a.shift;
-          const int id = lb < k.have
-                             ? a.block_table[static_cast<long long>(r) * a.max_blocks + lb]
-                             : popped(before + lb - k.have);
-          if (id >= 0 && id < a.num_blocks)
-            slot = (static_cast<long long>(id) << a.shift) + (pos & ((1 << a.shift) - 1));
-          else
-            err |= kErrBlockRange;
-        }
+  // ---- long requests: a warp takes kChunkRows tokens in a row. Its lanes
+  // start from the request of the first of them and walk on.
+  const long long warps = stride / 32;
+  for (long long x0 = first / 32 * kChunkRows; x0 < total_long; x0 += warps * kChunkRows) {
+    const int run = run_of(s.start[2], x0);
+    int r = run * per;
+    long long at = s.start[0][run], before = s.start[1][run], flat = s.start[2][run];
+    Ask k = ask_of(a, r);
+    for (int i = lane; i < kChunkRows && x0 + i < total_long; i += 32) {
+      // (lengths that change under the call must not lead past the last request)
+      while (flat + long_rows(k) <= x0 + i && r + 1 < R) {
+        at += k.rows;
+        before += k.need;
+        flat += long_rows(k);
+        k = ask_of(a, ++r);
       }
-      a.slots[t] = slot;
+      const long long in = x0 + i - flat;
+      if (in < k.rows) token(r, k, at, before, static_cast<int>(in));
     }
   }
+
+  // ---- rows behind the last request
+  if (a.slots)
+    for (long long t = total_rows + first; t < a.num_tokens; t += stride) a.slots[t] = -1;
   if (err) atomicOr(&g_errors_tables, err);
 
-  // every CTA has read the state (it may be replaced in place)
-  cluster.sync();
-  if (rank == 0 && tid == 0) {
-    int h = head_in, c = count_in;
-    if (state_ok) {
-      h = static_cast<int>((head + taken_s) % a.num_blocks);
-      c = static_cast<int>(count - taken_s);
-    }
-    a.state_out[0] = h;
-    a.state_out[1] = c;
+  if (blockIdx.x == 0 && tid == 0) {
+    a.qsl[R] = static_cast<int32_t>(total_rows < 0x7fffffffll ? total_rows : 0x7fffffffll);
+    if (state_here) write_state(a, s.start[1], per, head_in, count_in, state_ok);
+  }
+}
+
+// The queue's state replaced in place, after every CTA of the build has read it.
+__global__ void __launch_bounds__(kTableThreads) commit_state_kernel(const BuildArgs a) {
+  __shared__ RunStarts<long long, 1> s;
+  pdl_trigger();
+  pdl_wait();
+  const int per = (a.num_reqs + kTableThreads - 1) / kTableThreads;
+  const int r0 = min(a.num_reqs, static_cast<int>(threadIdx.x) * per), r1 = min(a.num_reqs, r0 + per);
+  long long need[1] = {0};
+  for (int r = r0; r < r1; ++r) need[0] += ask_of(a, r).need;
+  scan_runs(s, need);
+  if (threadIdx.x == 0) {
+    const int head = a.state[0], count = a.state[1];
+    write_state(a, s.start[0], per, head, count, state_valid(head, count, a.num_blocks));
   }
 }
 
@@ -271,6 +303,11 @@ struct ReleaseArgs {
   int32_t* state_out;
   int32_t* ref_cnt;
   int num_blocks, shift;
+  // large releases: which flat entries free a block (a bit each), how many do
+  // in each tile of kTableThreads, and the queue's state before the call
+  uint32_t* bits;
+  int32_t* tile_freed;
+  int32_t* state_copy;
 };
 
 // Reference counts double as the scratch that finds each freed block's place.
@@ -297,10 +334,206 @@ __device__ __forceinline__ int entries_of(const ReleaseArgs& a, int i, int* row,
   return static_cast<int>(e);
 }
 
-__global__ void __launch_bounds__(kTableThreads) release_blocks_kernel(const ReleaseArgs a) {
-  __shared__ RunStarts s;
-  __shared__ int counts[32];   // owners per warp
-  __shared__ int cta_owners;   // freed blocks of this CTA's segment
+// The released entries as a flat index, the sums before each run of rows in
+// shared memory.
+struct ReleaseRuns {
+  RunStarts<int, 1> s;
+  int row[kTableThreads], entries[kTableThreads];  // of runs of one row
+};
+
+__device__ __forceinline__ int release_per(const ReleaseArgs& a) {
+  return (a.num_released + kTableThreads - 1) / kTableThreads;
+}
+
+// Fills the runs; returns the number of entries (0 under a bad state).
+__device__ __forceinline__ int scan_runs_released(const ReleaseArgs& a, ReleaseRuns& v,
+                                                  uint32_t* err, bool state_ok) {
+  const int per = release_per(a), tid = threadIdx.x;
+  const int i0 = min(a.num_released, tid * per), i1 = min(a.num_released, i0 + per);
+  int sum[1] = {0}, row = 0, e = 0;
+  for (int i = i0; i < i1; ++i) {
+    e = entries_of(a, i, &row, err);
+    sum[0] += e;
+  }
+  v.row[tid] = row;
+  v.entries[tid] = e;
+  scan_runs(v.s, sum);
+  if (state_ok) return v.s.start[0][kTableThreads];
+  *err |= kErrLengths;
+  return 0;
+}
+__device__ __forceinline__ int scan_released(const ReleaseArgs& a, ReleaseRuns& v, uint32_t* err) {
+  return scan_runs_released(a, v, err, state_valid(a.state[0], a.state[1], a.num_blocks));
+}
+
+// Block of flat entry x (rows in the order given, each from its last entry),
+// -1 if it is out of the pool.
+__device__ __forceinline__ int block_of(const ReleaseArgs& a, const ReleaseRuns& v, int x) {
+  const int* start = v.s.start[0];
+  const int run = run_of(start, x), per = release_per(a);
+  int at = start[run], r = v.row[run], e = v.entries[run];
+  if (per > 1) {
+    int i = run * per;
+    uint32_t ignore = 0;
+    e = entries_of(a, i, &r, &ignore);
+    while (at + e <= x && i + 1 < a.num_released) {
+      at += e;
+      e = entries_of(a, ++i, &r, &ignore);
+    }
+  }
+  // (lengths that change under the call must not lead outside the table)
+  if (x - at >= e) return -1;
+  const int b = __ldg(a.block_table + static_cast<long long>(r) * a.max_blocks + (e - 1 - (x - at)));
+  return b >= 0 && b < a.num_blocks ? b : -1;
+}
+
+// Count block b down; the release that reaches zero marks it. One too many is
+// undone and flagged (sums commute, so the marks do not depend on the order
+// of the releases).
+__device__ __forceinline__ void count_down(const ReleaseArgs& a, int b, uint32_t* err) {
+  const int old = atomicSub(a.ref_cnt + b, 1);
+  if (old == 1) {
+    atomicAdd(a.ref_cnt + b, kFreed);
+  } else if (old <= 0) {
+    atomicAdd(a.ref_cnt + b, 1);
+    *err |= kErrRefCount;
+  }
+}
+
+// A freed block's place is its last release's.
+__device__ __forceinline__ void claim_place(const ReleaseArgs& a, int b, int x) {
+  if (__ldcg(a.ref_cnt + b) < kFreedTop) atomicMax(a.ref_cnt + b, kFreed + 1 + x);
+}
+
+// Block b to its place, counted from the queue's head.
+__device__ __forceinline__ void append_block(const ReleaseArgs& a, int b, int head, long long place,
+                                             uint32_t* err) {
+  if (b < 0) return;
+  a.ref_cnt[b] = 0;
+  if (place >= a.num_blocks) {
+    *err |= kErrRefCount;  // more blocks than the pool has: the state was wrong
+    return;
+  }
+  long long q = head + place;
+  if (q >= a.num_blocks) q -= a.num_blocks;
+  a.queue[q] = b;
+}
+
+// Large releases run over the whole device, a launch per phase: what bounds
+// them is the rate of scattered accesses per SM (1024 rows of 160 blocks took
+// 54 us with the last phase, and 90 with all of them, in one cluster of 8).
+__global__ void __launch_bounds__(kTableThreads) release_count_kernel(const ReleaseArgs a) {
+  __shared__ ReleaseRuns v;
+  pdl_trigger();
+  pdl_wait();
+  uint32_t err = 0;
+  const int total = scan_released(a, v, &err);
+  for (long long x = static_cast<long long>(blockIdx.x) * kTableThreads + threadIdx.x; x < total;
+       x += static_cast<long long>(gridDim.x) * kTableThreads) {
+    const int b = block_of(a, v, static_cast<int>(x));
+    if (b >= 0)
+      count_down(a, b, &err);
+    else
+      err |= kErrBlockRange;
+  }
+  if (err) atomicOr(&g_errors_tables, err);
+}
+
+__global__ void __launch_bounds__(kTableThreads) release_claim_kernel(const ReleaseArgs a) {
+  __shared__ ReleaseRuns v;
+  pdl_trigger();
+  pdl_wait();
+  uint32_t err = 0;
+  const int total = scan_released(a, v, &err);
+  for (long long x = static_cast<long long>(blockIdx.x) * kTableThreads + threadIdx.x; x < total;
+       x += static_cast<long long>(gridDim.x) * kTableThreads) {
+    const int b = block_of(a, v, static_cast<int>(x));
+    if (b >= 0) claim_place(a, b, static_cast<int>(x));
+  }
+}
+
+// Which entries free a block: every claim is in.
+__global__ void __launch_bounds__(kTableThreads) release_flag_kernel(const ReleaseArgs a) {
+  __shared__ ReleaseRuns v;
+  pdl_trigger();
+  pdl_wait();
+  uint32_t err = 0;
+  const int total = scan_released(a, v, &err);
+  if (blockIdx.x == 0 && threadIdx.x < 2) a.state_copy[threadIdx.x] = a.state[threadIdx.x];
+  const int tiles = (total + kTableThreads - 1) / kTableThreads;
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const int x = t * kTableThreads + threadIdx.x;
+    const int b = x < total ? block_of(a, v, x) : -1;
+    const bool own = b >= 0 && __ldcg(a.ref_cnt + b) == kFreed + 1 + x;
+    const uint32_t m = __ballot_sync(0xffffffffu, own);
+    if ((threadIdx.x & 31) == 0) a.bits[x >> 5] = m;
+    const int n = __syncthreads_count(own);
+    if (threadIdx.x == 0) a.tile_freed[t] = n;
+  }
+}
+
+// Freed blocks to their places behind the queue's tail, counts back to zero.
+__global__ void __launch_bounds__(kTableThreads) release_append_kernel(const ReleaseArgs a) {
+  __shared__ ReleaseRuns v;
+  __shared__ int warp_n[32], before_s, all_s;
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t err = 0;
+  const int head = a.state_copy[0], count = a.state_copy[1];
+  const bool state_ok = state_valid(head, count, a.num_blocks);
+  // (the state itself may be replaced by now: only the copy counts)
+  const int total = scan_runs_released(a, v, &err, state_ok);
+  const int tiles = (total + kTableThreads - 1) / kTableThreads;
+  // this CTA's tiles in a row; freed blocks before them, and in all
+  const int t0 = static_cast<int>(static_cast<long long>(tiles) * blockIdx.x / gridDim.x);
+  const int t1 = static_cast<int>(static_cast<long long>(tiles) * (blockIdx.x + 1) / gridDim.x);
+  if (tid == 0) before_s = all_s = 0;
+  __syncthreads();
+  int sum = 0, upto = 0;
+  for (int t = tid; t < tiles; t += kTableThreads) {
+    const int n = __ldcg(a.tile_freed + t);
+    sum += n;
+    if (t < t0) upto += n;
+  }
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  upto = __reduce_add_sync(0xffffffffu, upto);
+  if (lane == 0 && sum) atomicAdd(&all_s, sum);
+  if (lane == 0 && upto) atomicAdd(&before_s, upto);
+  __syncthreads();
+  long long place0 = static_cast<long long>(count) + before_s;
+  for (int t = t0; t < t1; ++t) {
+    const int x = t * kTableThreads + tid;
+    const uint32_t m = __ldcg(a.bits + (x >> 5));
+    if (lane == 0) warp_n[warp] = __popc(m);
+    __syncthreads();
+    const int c = warp_n[lane];
+    const int below = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
+    const int tile = __reduce_add_sync(0xffffffffu, c);
+    if (m >> lane & 1u) {
+      append_block(a, block_of(a, v, x), head, place0 + below + __popc(m & ((1u << lane) - 1u)), &err);
+    }
+    place0 += tile;
+    __syncthreads();
+  }
+  if (err) atomicOr(&g_errors_tables, err);
+  if (blockIdx.x == 0 && tid == 0) {
+    a.state_out[0] = head;
+    a.state_out[1] = state_ok ? min(count + all_s, a.num_blocks) : count;
+  }
+}
+
+// Small releases in one launch of one cluster, its barrier between the
+// phases. The entries of a CTA's share: block ids, kept in shared memory from
+// the first phase on.
+constexpr int kStash = 16 * 1024;
+constexpr int kBatch = 4;  // entries per thread whose loads go out together
+
+__global__ void __launch_bounds__(kTableThreads) release_small_kernel(const ReleaseArgs a) {
+  extern __shared__ int32_t stash[];
+  __shared__ ReleaseRuns v;
+  __shared__ int tile_scan[32];
+  __shared__ int cta_freed;  // freed blocks of this CTA's share
   pdl_trigger();
   pdl_wait();
   cg::cluster_group cluster = cg::this_cluster();
@@ -308,116 +541,78 @@ __global__ void __launch_bounds__(kTableThreads) release_blocks_kernel(const Rel
   const int nctas = static_cast<int>(cluster.num_blocks());
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int head_in = a.state[0], count_in = a.state[1];
-  const bool state_ok =
-      head_in >= 0 && head_in < a.num_blocks && count_in >= 0 && count_in <= a.num_blocks;
-  uint32_t err = state_ok ? 0u : kErrLengths;
+  const bool state_ok = state_valid(head_in, count_in, a.num_blocks);
+  uint32_t err = 0;
+  const int total = scan_runs_released(a, v, &err, state_ok);
 
-  const int per = (a.num_released + kTableThreads - 1) / kTableThreads;
-  const int i0 = min(a.num_released, tid * per), i1 = min(a.num_released, i0 + per);
-  long long sum = 0;
-  int row;
-  for (int i = i0; i < i1; ++i) sum += entries_of(a, i, &row, &err);
-  scan_runs(s, sum, 0);
-  // a bad state releases nothing
-  const int total = state_ok ? static_cast<int>(s.a[kTableThreads]) : 0;
-
-  // this CTA's segment of the flat entries, in whole tiles of the block
+  // this CTA's share of the flat entries, in whole tiles of the block; entry
+  // x0 + n is thread n % kTableThreads's (at most kStash entries in all)
   const int tiles = (total + kTableThreads - 1) / kTableThreads;
   const int x0 = static_cast<int>(static_cast<long long>(tiles) * rank / nctas) * kTableThreads;
   const int x1 = min(total, static_cast<int>(static_cast<long long>(tiles) * (rank + 1) / nctas) *
                                 kTableThreads);
-  // block of flat entry x: rows in the order given, each from its last entry
-  auto block_of = [&](int x) -> int {
-    const int run = run_of(s.a, x);
-    int i = run * per, r;
-    uint32_t ignore = 0;
-    long long at = s.a[run];
-    int e = entries_of(a, i, &r, &ignore);
-    while (at + e <= x && i + 1 < a.num_released) {
-      at += e;
-      e = entries_of(a, ++i, &r, &ignore);
-    }
-    // (lengths that change under the call must not lead outside the table)
-    if (x - at >= e) return -1;
-    return __ldg(a.block_table + static_cast<long long>(r) * a.max_blocks +
-                 (e - 1 - static_cast<int>(x - at)));
-  };
-  auto in_pool = [&](int b) { return b >= 0 && b < a.num_blocks; };
+  const int share = max(0, x1 - x0);
 
-  // ---- count down; the release that reaches zero marks the block. One too
-  // many is undone and flagged (sums commute, so the marks do not depend on
-  // the order of the releases).
-  for (int x = x0 + tid; x < x1; x += kTableThreads) {
-    const int b = block_of(x);
-    if (!in_pool(b)) {
-      err |= kErrBlockRange;
-      continue;
+  for (int n0 = tid; n0 < share; n0 += kBatch * kTableThreads) {
+    int b[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int n = n0 + u * kTableThreads;
+      if (n >= share) {
+        b[u] = -1;
+        continue;
+      }
+      b[u] = block_of(a, v, x0 + n);
+      if (b[u] < 0) err |= kErrBlockRange;
+      stash[n] = b[u];
     }
-    const int old = atomicSub(a.ref_cnt + b, 1);
-    if (old == 1) {
-      atomicAdd(a.ref_cnt + b, kFreed);
-    } else if (old <= 0) {
-      atomicAdd(a.ref_cnt + b, 1);
-      err |= kErrRefCount;
-    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (b[u] >= 0) count_down(a, b[u], &err);
   }
   cluster.sync();
-  // ---- a freed block's place is its last release's
-  for (int x = x0 + tid; x < x1; x += kTableThreads) {
-    const int b = block_of(x);
-    if (in_pool(b) && __ldcg(a.ref_cnt + b) < kFreedTop) atomicMax(a.ref_cnt + b, kFreed + 1 + x);
-  }
+  for (int n = tid; n < share; n += kTableThreads)
+    if (stash[n] >= 0) claim_place(a, stash[n], x0 + n);
   cluster.sync();
-  auto owner = [&](int x, int* b) -> bool {
-    if (x >= x1) return false;
-    *b = block_of(x);
-    return in_pool(*b) && __ldcg(a.ref_cnt + *b) == kFreed + 1 + x;
-  };
-  // ---- freed blocks of the segment, then of the segments before it
-  int mine = 0, b = 0;
-  for (int x = x0; x < x1; x += kTableThreads) mine += owner(x + tid, &b);
+  // ---- how many places this share fills; the stash keeps only their blocks
+  int mine = 0;
+  for (int n = tid; n < share; n += kTableThreads) {
+    const int b = stash[n];
+    const bool own = b >= 0 && __ldcg(a.ref_cnt + b) == kFreed + 1 + x0 + n;
+    mine += own;
+    if (!own) stash[n] = -1;
+  }
   mine = __reduce_add_sync(0xffffffffu, mine);
-  if (lane == 0) counts[warp] = mine;
+  if (lane == 0) tile_scan[warp] = mine;
   __syncthreads();
   if (warp == 0) {
-    const int n = __reduce_add_sync(0xffffffffu, counts[lane]);
-    if (lane == 0) cta_owners = n;
+    const int n = __reduce_add_sync(0xffffffffu, tile_scan[lane]);
+    if (lane == 0) cta_freed = n;
   }
   cluster.sync();
   int before = 0, all = 0;
   for (int k = 0; k < nctas; ++k) {
-    const int n = *cluster.map_shared_rank(&cta_owners, k);
+    const int n = *cluster.map_shared_rank(&cta_freed, k);
     if (k < rank) before += n;
     all += n;
   }
-  // ---- append in order
-  for (int x = x0; x < x1; x += kTableThreads) {
-    const bool own = owner(x + tid, &b);
-    const unsigned m = __ballot_sync(0xffffffffu, own);
+  // ---- append in order, a tile at a time
+  long long place0 = static_cast<long long>(count_in) + before;
+  for (int n0 = 0; n0 < share; n0 += kTableThreads) {
+    const int n = n0 + tid;
+    const int b = n < share ? stash[n] : -1;
+    const unsigned m = __ballot_sync(0xffffffffu, b >= 0);
     __syncthreads();
-    if (lane == 0) counts[warp] = __popc(m);
+    if (lane == 0) tile_scan[warp] = __popc(m);
     __syncthreads();
-    int upto = 0, tile = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) upto += counts[w];
-      tile += counts[w];
-    }
-    if (own) {
-      const long long place = static_cast<long long>(count_in) + before + upto +
-                              __popc(m & ((1u << lane) - 1u));
-      a.ref_cnt[b] = 0;
-      if (place < a.num_blocks) {
-        long long q = head_in + place;
-        if (q >= a.num_blocks) q -= a.num_blocks;
-        a.queue[q] = b;
-      } else {
-        err |= kErrRefCount;  // more blocks than the pool has: the state was wrong
-      }
-    }
-    before += tile;
+    const int c = tile_scan[lane];
+    const int below = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
+    const int tile = __reduce_add_sync(0xffffffffu, c);
+    if (b >= 0) append_block(a, b, head_in, place0 + below + __popc(m & ((1u << lane) - 1u)), &err);
+    place0 += tile;
   }
   if (err) atomicOr(&g_errors_tables, err);
-  // no CTA leaves while another reads its count
+  // no CTA leaves while another reads its count; all have read the state
   cluster.sync();
   if (rank == 0 && tid == 0) {
     a.state_out[0] = head_in;
@@ -427,21 +622,29 @@ __global__ void __launch_bounds__(kTableThreads) release_blocks_kernel(const Rel
 
 // ------------------------------------------------------------------ host
 // CTAs of the cluster: one per kEntriesPerCta flat entries (one CTA needs no
-// cluster barrier), at most the portable size.
-constexpr long long kEntriesPerCta = 2048;
+// barrier between CTAs), at most kMaxCtas, the portable size.
+constexpr long long kEntriesPerCta = 1024;
+constexpr int kMaxCtas = 8;
 
 static int cluster_ctas(long long entries) {
   int n = 1;
-  while (n < 8 && entries > n * kEntriesPerCta) n *= 2;
+  while (n < kMaxCtas && entries > n * kEntriesPerCta) n *= 2;
   return n;
 }
 
+// Releases of up to this many table entries (rows x table width, an upper
+// bound: the lengths are on the device) are one launch. 8 rows of 245 entries
+// take 9.6 us so, and took 12 in several launches; 64 rows of 252 entries take
+// 11.9 us in one, 64 rows of 260 entries 13.8 us in four.
+constexpr long long kSmallEntries = kStash;
+
 template <typename Args>
-static cudaError_t launch_cluster(void (*kern)(Args), int ctas, cudaStream_t stream,
+static cudaError_t launch_cluster(void (*kern)(Args), int ctas, size_t smem, cudaStream_t stream,
                                   const Args& args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kTableThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -459,26 +662,61 @@ cudaError_t launch_build_tables(int32_t* block_table, int max_blocks, int32_t* q
                                 int32_t* seq_lens, int64_t* slots, const int32_t* num_computed,
                                 const int32_t* query_lens, int num_reqs, int num_tokens,
                                 const int32_t* queue, const int32_t* state, int32_t* state_out,
-                                int32_t* ref_cnt, int num_blocks, int block_size,
+                                int32_t* ref_cnt, int num_blocks, int block_size, int num_sms,
                                 cudaStream_t stream) {
   const BuildArgs a{block_table, max_blocks, qsl,   seq_lens,  slots,   num_computed,
                     query_lens,  num_reqs,   num_tokens, queue, state, state_out,
                     ref_cnt,     num_blocks,
                     static_cast<int>(__builtin_ctz(static_cast<unsigned>(block_size)))};
-  return launch_cluster(build_tables_kernel,
-                        cluster_ctas(num_tokens > num_reqs ? num_tokens : num_reqs), stream, a);
+  // a CTA per 1024 requests or tokens, at most one per SM. The state is
+  // replaced by the build itself unless that would be in place with other
+  // CTAs still to read it.
+  const long long work = num_tokens > num_reqs ? num_tokens : num_reqs;
+  const long long want = (work + kTableThreads - 1) / kTableThreads;
+  const int grid = static_cast<int>(want < 1 ? 1 : want < num_sms ? want : num_sms);
+  const bool apart = state_out + 2 <= state || state + 2 <= state_out;
+  const bool state_here = grid == 1 || apart;
+  cudaError_t e = launch_pdl(build_tables_kernel, dim3(grid), dim3(kTableThreads), 0, stream, a,
+                             state_here);
+  if (e != cudaSuccess || state_here) return e;
+  return launch_pdl(commit_state_kernel, dim3(1), dim3(kTableThreads), 0, stream, a);
 }
 
 cudaError_t launch_release_blocks(const int32_t* block_table, int max_blocks, int num_reqs,
                                   const int32_t* rows, const int32_t* tokens, int num_released,
                                   int32_t* queue, const int32_t* state, int32_t* state_out,
                                   int32_t* ref_cnt, int num_blocks, int block_size,
-                                  cudaStream_t stream) {
-  const ReleaseArgs a{block_table, max_blocks, num_reqs, rows,    tokens,     num_released,
-                      queue,       state,      state_out, ref_cnt, num_blocks,
-                      static_cast<int>(__builtin_ctz(static_cast<unsigned>(block_size)))};
-  return launch_cluster(release_blocks_kernel,
-                        cluster_ctas(static_cast<long long>(num_released) * max_blocks), stream, a);
+                                  void* workspace, int num_sms, cudaStream_t stream) {
+  ReleaseArgs a{block_table, max_blocks, num_reqs,  rows,    tokens,     num_released,
+                queue,       state,      state_out, ref_cnt, num_blocks,
+                static_cast<int>(__builtin_ctz(static_cast<unsigned>(block_size))),
+                nullptr,     nullptr,    nullptr};
+  const long long bound = static_cast<long long>(num_released) * max_blocks;
+  if (bound <= kSmallEntries) {
+    static std::atomic<unsigned long long> attr_done{0};
+    const int smem = kStash * static_cast<int>(sizeof(int32_t));
+    cudaError_t e = smem_attr_once(release_small_kernel, smem, attr_done);
+    if (e != cudaSuccess) return e;
+    return launch_cluster(release_small_kernel, cluster_ctas(bound), smem, stream, a);
+  }
+  char* ws = static_cast<char*>(workspace);
+  const long long tiles = (bound + kTableThreads - 1) / kTableThreads;
+  a.state_copy = reinterpret_cast<int32_t*>(ws);
+  a.tile_freed = reinterpret_cast<int32_t*>(ws + 256);
+  a.bits = reinterpret_cast<uint32_t*>(ws + 256 + (tiles * 4 + 255) / 256 * 256);
+  const dim3 grid(static_cast<unsigned>(tiles < num_sms ? tiles : num_sms)), block(kTableThreads);
+  cudaError_t e = launch_pdl(release_count_kernel, grid, block, 0, stream, a);
+  if (e == cudaSuccess) e = launch_pdl(release_claim_kernel, grid, block, 0, stream, a);
+  if (e == cudaSuccess) e = launch_pdl(release_flag_kernel, grid, block, 0, stream, a);
+  if (e == cudaSuccess) e = launch_pdl(release_append_kernel, grid, block, 0, stream, a);
+  return e;
+}
+
+size_t release_workspace_bytes(int num_released, int max_blocks) {
+  const long long bound = static_cast<long long>(num_released) * max_blocks;
+  if (bound <= kSmallEntries) return 0;
+  const long long tiles = (bound + kTableThreads - 1) / kTableThreads;
+  return static_cast<size_t>(256 + (tiles * 4 + 255) / 256 * 256 + tiles * (kTableThreads / 8));
 }
 
 cudaError_t read_errors_tables(uint32_t* out, bool clear) {

@@ -30,6 +30,13 @@ def dev(a):
     return torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()
 
 
+def release_workspace(n, width):
+    nbytes = binding.pkv_release_workspace_size(n, width)
+    if not nbytes:
+        return None
+    return torch.full((nbytes,), 0xa5, dtype=torch.uint8, device="cuda")
+
+
 class Device:
     """The buffers of a serving loop."""
 
@@ -53,7 +60,8 @@ class Device:
 
     def release(self, rows, tokens):
         binding.pkv_release_blocks(self.table, dev(rows), dev(tokens), self.queue, self.state,
-                                   self.ref, block_size=self.B, free_state_out=self.state_out)
+                                   self.ref, block_size=self.B, free_state_out=self.state_out,
+                                   workspace=release_workspace(len(rows), self.table.shape[1]))
         torch.cuda.synchronize()
 
     def check_build(self, want):
@@ -403,14 +411,14 @@ def test_two_pools_on_two_streams_at_once():
         d = Device(table, ref, queue, state, 16)
         R, T = len(c), int(n.sum())
         args = (dev(np.zeros(R + 1)), dev(np.zeros(R)), torch.zeros(T, dtype=torch.int64, device="cuda"),
-                dev(c), dev(n), dev(rows))
+                dev(c), dev(n), dev(rows), release_workspace(2000, table.shape[1]))
         runs.append((d, args, torch.cuda.Stream(), after))
     torch.cuda.synchronize()
-    for d, (qsl, lens, slots, c, n, rows), s, _ in runs:
+    for d, (qsl, lens, slots, c, n, rows, ws), s, _ in runs:
         binding.pkv_build_step_tables(d.table, qsl, lens, slots, c, n, d.queue, d.state,
                                       block_size=16, ref_cnt=d.ref, stream=s)
         binding.pkv_release_blocks(d.table, rows, lens, d.queue, d.state, d.ref, block_size=16,
-                                   stream=s)
+                                   workspace=ws, stream=s)
     torch.cuda.synchronize()
     for d, _, _, after in runs:
         d.check_release(after)

@@ -31,10 +31,11 @@ def _build(lib, **kw):
 
 def _release(lib, **kw):
     a = dict(bt=FAKE, mb=8, R=2, rows=FAKE, tok=FAKE, n=2, q=FAKE, st=FAKE, so=FAKE, ref=FAKE, nb=64,
-             B=16)
+             B=16, ws=None, wsb=0)
     a.update(kw)
     return lib.pkv_release_blocks(a["bt"], a["mb"], a["R"], a["rows"], a["tok"], a["n"], a["q"],
-                                  a["st"], a["so"], a["ref"], a["nb"], a["B"], None)
+                                  a["st"], a["so"], a["ref"], a["nb"], a["B"], a["ws"], a["wsb"],
+                                  None)
 
 
 ODD8 = ctypes.c_void_p(0x10004)
@@ -65,13 +66,25 @@ def test_release_refusals(lib):
         assert _release(lib, **{k: ctypes.c_void_p(0x10002)}) == E("PKV_ERR_MISALIGNED"), k
 
 
+def test_release_workspace(lib):
+    size = lib.pkv_release_workspace_size
+    assert size(0, 100) == 0 and size(8, 300) == 0
+    assert size(-1, 4) < 0 and size(4, -1) < 0 and size(1 << 16, 1 << 13) < 0
+    big = size(1000, 400)
+    assert big > 0
+    kw = dict(n=1000, mb=400, R=1000)
+    assert _release(lib, **kw) == E("PKV_ERR_WORKSPACE")
+    assert _release(lib, ws=FAKE, wsb=big - 1, **kw) == E("PKV_ERR_WORKSPACE")
+    assert _release(lib, ws=ctypes.c_void_p(0x10010), wsb=big, **kw) == E("PKV_ERR_WORKSPACE")
+
+
 def test_binding_checks():
     torch = pytest.importorskip("torch")
     i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
     with pytest.raises(ValueError, match="CUDA"):
         binding.pkv_release_blocks(i32(2, 4), i32(1), i32(2), i32(8), i32(2), i32(8), block_size=16)
     with pytest.raises(ValueError, match="ref_cnt"):
-        binding._release_args(i32(2, 4), i32(1), i32(2), i32(8), i32(2), None, None, 16)
+        binding._release_args(i32(2, 4), i32(1), i32(2), i32(8), i32(2), None, None, 16, None)
     with pytest.raises(ValueError, match="query_lens"):
         binding.TableCalls(block_table=i32(2, 4), free_queue=i32(8), free_state=i32(2), block_size=16)
 
