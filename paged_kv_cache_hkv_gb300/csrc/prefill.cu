@@ -269,7 +269,7 @@ struct PrefillParams {
 // (1.0e-6: equal-ripple, found by reweighted least squares). The powers of
 // scale / softcap and the factor softcap * log2(e) go into the coefficients,
 // so a pair of scores takes six packed FMA-pipe instructions; as a whole the
-// prefill of 4 x 2048 rows over 8192 keys went 1828 -> 1104 us with it and without the running maximum. A
+// prefill of 4 x 2048 rows over 8192 keys went 1828 -> 1049 us with it and without the running maximum. A
 // warp that holds a larger |u| takes the exact form (tanh_log2) for its tile.
 constexpr float kCapLim = 0.8f;
 constexpr double kCapPoly[5] = {9.999989943e-01, -3.332537196e-01, 1.323056551e-01, -4.918014086e-02, 1.210013789e-02};
@@ -759,10 +759,18 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
       ok = wait_small(&sh.s_full[b], (Tg / kSBufs) & 1u, abort_flag);
       if (!ok) return;
       tc::fence_after_sync();
-      // a tile every row sees in full needs no mask
       const int ka = tile_at<SC>(m.kt0, nkv, kt);  // key tile (keys ka*128 ..)
+      // `full`: every row of the item sees the whole tile. Masks go by warp,
+      // whose 16 rows are a few neighbouring queries: `wfull`.
       const bool full = mask == 0xFFu && ka * kTileN >= m.full_lo &&
                         ka * kTileN + kTileN <= m.full_hi;
+      bool wfull = full;
+      if (!full) {
+        const int k0 = ka * kTileN;
+        const bool no_row = m.i0 + (row >> gsh) >= m.n;
+        wfull = mask == 0xFFu &&
+                __all_sync(0xffffffffu, no_row || (rk.lo <= k0 && rk.hi >= k0 + kTileN));
+      }
       // this thread's keys 64ch .. 64ch+63 of the tile: sr[0] the first 32
       uint32_t sr[2][32];
       tc::ld_half32<64>(t_s, sr[0]);
@@ -770,7 +778,7 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
       tc::wait32(sr[0]);
       tc::wait32(sr[1]);
       uint32_t vis[2] = {0xffffffffu, 0xffffffffu};  // this thread's visible keys, a bit each
-      if (!full) {
+      if (!wfull) {
         const int lo = rk.lo - ka * kTileN - 64 * ch, hi = rk.hi - ka * kTileN - 64 * ch;
         const uint32_t cm = mask >> (4 * ch);
 #pragma unroll
@@ -782,7 +790,7 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
       if constexpr (CAP) {
         // Rows of the tile that were not loaded, or hold no key yet, must not
         // decide which form of the cap is taken.
-        if (mask != 0xFFu || ka * kTileN < m.k_lo || ka * kTileN + kTileN > m.kv_len) {
+        if (!wfull && (mask != 0xFFu || ka * kTileN < m.k_lo || ka * kTileN + kTileN > m.kv_len)) {
 #pragma unroll
           for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -865,7 +873,7 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
                                          slope2 * fabsf(d0 + static_cast<float>(q * 32 + i)));
         }
       }
-      if (!full) {  // invisible keys become -inf
+      if (!wfull) {  // invisible keys become -inf
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
