@@ -638,6 +638,8 @@ __global__ void __launch_bounds__(kDecodeThreads)
 // row; the boundary CTAs leave those requests to them.
 // Lanes first read the (m, l) of up to 32 pieces at once, then every lane
 // sums its dims over the pieces with independent loads.
+constexpr int kCombineLoads = 32;
+
 template <int D, int GW>
 __global__ void __launch_bounds__(GW * 32) combine_kernel(const DecodeParams p) {
   const long long c = blockIdx.x;
@@ -699,24 +701,38 @@ __global__ void __launch_bounds__(GW * 32) combine_kernel(const DecodeParams p) 
     const float2 ml = piece_ml(j0 + lane);
     const float wgt = (ml.x == -INFINITY) ? 0.f : exp2f(ml.x - M);
     Ls += wgt * ml.y;
+    const float* mine = piece_o(wgt == 0.f || j0 + lane >= npieces ? 0 : j0 + lane);
     const int cnt = min(32, npieces - j0);
-    // 8 pieces' loads in flight per lane; a piece of weight 0 (an empty
-    // range, which wrote no partial) reads piece 0's slot and adds nothing
-#pragma unroll 8
-    for (int j = 0; j < cnt; ++j) {
-      const float wj = __shfl_sync(0xffffffffu, wgt, j);
-      const float* src = piece_o(wj == 0.f ? 0 : j0 + j) + lane * E;
-      if constexpr (E == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        acc[0] += wj * v.x;
-        acc[1] += wj * v.y;
-        acc[2] += wj * v.z;
-        acc[3] += wj * v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        acc[0] += wj * v.x;
-        acc[1] += wj * v.y;
+    // kCombineLoads pieces' loads go out before the first is used (one after
+    // the other, a decode of 131071 keys in 152 pieces spent 60 us here; so,
+    // 10; the sums keep their order). A piece of weight 0 (an empty range,
+    // which wrote no partial) reads piece 0's slot and adds nothing.
+    for (int i0 = 0; i0 < cnt; i0 += kCombineLoads) {
+      float vals[kCombineLoads][E], wj[kCombineLoads];
+#pragma unroll
+      for (int i = 0; i < kCombineLoads; ++i) {
+        wj[i] = __shfl_sync(0xffffffffu, wgt, (i0 + i) & 31);
+        const float* src = reinterpret_cast<const float*>(__shfl_sync(
+                               0xffffffffu, reinterpret_cast<unsigned long long>(mine), (i0 + i) & 31)) +
+                           lane * E;
+        if constexpr (E == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          vals[i][0] = v.x;
+          vals[i][1] = v.y;
+          vals[i][2] = v.z;
+          vals[i][3] = v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          vals[i][0] = v.x;
+          vals[i][1] = v.y;
+        }
       }
+#pragma unroll
+      for (int i = 0; i < kCombineLoads; ++i)
+        if (i0 + i < cnt) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] += wj[i] * vals[i][e];
+        }
     }
   }
 #pragma unroll
