@@ -82,6 +82,7 @@ struct DecodeParams {
   // a cap, scale_log2 holds 2 log2(e) scale / softcap instead.
   bool scored;
   ScoreParams score;
+  bool deep_combine;  // requests have many pieces each (see the combine kernel)
 };
 
 // CTA that owns position x of the decode stream: ranges start at floor(c * N / C).
@@ -638,9 +639,14 @@ __global__ void __launch_bounds__(kDecodeThreads)
 // row; the boundary CTAs leave those requests to them.
 // Lanes first read the (m, l) of up to 32 pieces at once, then every lane
 // sums its dims over the pieces with independent loads.
+//
+// DEEP: for requests of many pieces (kDeepPieces), many loads in flight per
+// lane, in the same order of sums. It costs registers and, for a few pieces,
+// empty loads: the combine of 128 requests of some 5 pieces took 18 us with
+// it and 10.6 without; that of one request of 152 pieces 10 and 60.
 constexpr int kCombineLoads = 32;
 
-template <int D, int GW>
+template <int D, int GW, bool DEEP>
 __global__ void __launch_bounds__(GW * 32) combine_kernel(const DecodeParams p) {
   const long long c = blockIdx.x;
   const int vg = blockIdx.y;
@@ -701,38 +707,58 @@ __global__ void __launch_bounds__(GW * 32) combine_kernel(const DecodeParams p) 
     const float2 ml = piece_ml(j0 + lane);
     const float wgt = (ml.x == -INFINITY) ? 0.f : exp2f(ml.x - M);
     Ls += wgt * ml.y;
-    const float* mine = piece_o(wgt == 0.f || j0 + lane >= npieces ? 0 : j0 + lane);
     const int cnt = min(32, npieces - j0);
-    // kCombineLoads pieces' loads go out before the first is used (one after
-    // the other, a decode of 131071 keys in 152 pieces spent 60 us here; so,
-    // 10; the sums keep their order). A piece of weight 0 (an empty range,
-    // which wrote no partial) reads piece 0's slot and adds nothing.
-    for (int i0 = 0; i0 < cnt; i0 += kCombineLoads) {
-      float vals[kCombineLoads][E], wj[kCombineLoads];
+    if constexpr (DEEP) {
+      const float* mine = piece_o(wgt == 0.f || j0 + lane >= npieces ? 0 : j0 + lane);
+      // kCombineLoads pieces' loads go out before the first is used. A piece of
+      // weight 0 (an empty range, which wrote no partial) reads piece 0's slot
+      // and adds nothing.
+      for (int i0 = 0; i0 < cnt; i0 += kCombineLoads) {
+        float vals[kCombineLoads][E], wj[kCombineLoads];
 #pragma unroll
-      for (int i = 0; i < kCombineLoads; ++i) {
-        wj[i] = __shfl_sync(0xffffffffu, wgt, (i0 + i) & 31);
-        const float* src = reinterpret_cast<const float*>(__shfl_sync(
-                               0xffffffffu, reinterpret_cast<unsigned long long>(mine), (i0 + i) & 31)) +
-                           lane * E;
+        for (int i = 0; i < kCombineLoads; ++i) {
+          wj[i] = __shfl_sync(0xffffffffu, wgt, (i0 + i) & 31);
+          const float* src = reinterpret_cast<const float*>(__shfl_sync(
+                                 0xffffffffu, reinterpret_cast<unsigned long long>(mine), (i0 + i) & 31)) +
+                             lane * E;
+          if constexpr (E == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            vals[i][0] = v.x;
+            vals[i][1] = v.y;
+            vals[i][2] = v.z;
+            vals[i][3] = v.w;
+          } else {
+            const float2 v = *reinterpret_cast<const float2*>(src);
+            vals[i][0] = v.x;
+            vals[i][1] = v.y;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kCombineLoads; ++i)
+          if (i0 + i < cnt) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += wj[i] * vals[i][e];
+          }
+      }
+    } else {
+      // 8 pieces' loads in flight per lane; a piece of weight 0 (an empty
+      // range, which wrote no partial) reads piece 0's slot and adds nothing
+#pragma unroll 8
+      for (int j = 0; j < cnt; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, wgt, j);
+        const float* src = piece_o(wj == 0.f ? 0 : j0 + j) + lane * E;
         if constexpr (E == 4) {
           const float4 v = *reinterpret_cast<const float4*>(src);
-          vals[i][0] = v.x;
-          vals[i][1] = v.y;
-          vals[i][2] = v.z;
-          vals[i][3] = v.w;
+          acc[0] += wj * v.x;
+          acc[1] += wj * v.y;
+          acc[2] += wj * v.z;
+          acc[3] += wj * v.w;
         } else {
           const float2 v = *reinterpret_cast<const float2*>(src);
-          vals[i][0] = v.x;
-          vals[i][1] = v.y;
+          acc[0] += wj * v.x;
+          acc[1] += wj * v.y;
         }
       }
-#pragma unroll
-      for (int i = 0; i < kCombineLoads; ++i)
-        if (i0 + i < cnt) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] += wj[i] * vals[i][e];
-        }
     }
   }
 #pragma unroll
@@ -761,6 +787,13 @@ __global__ void __launch_bounds__(GW * 32) combine_kernel(const DecodeParams p) 
 // 64 KB took the mixed-step decode from 830 to 788 us)
 constexpr int kDecodeMinStages = 2;
 constexpr int kDecodeMaxStages = PKV_DECODE_MAX_STAGES;
+
+// Splits per request from which the combine's DEEP variant is launched (one
+// decode of 250 keys, 16 pieces: 11.4 us a step with it, 16.4 without). Not in
+// a plain step with prefill rows: such a step's requests are mostly not
+// decodes, and where none is the DEEP kernel's registers only make its idle
+// launch longer (31.5 instead of 31.0 us for the mixed step's prefill rows).
+constexpr long long kDeepPieces = 8;
 
 // Consumer warps per SM the default split aims at (CTAs per SM = this / slab
 // size, at least one): about the count that streamed fastest.
@@ -859,7 +892,7 @@ static cudaError_t launch_decode_t(const DecodeParams& p, const CUtensorMap& kv_
   e = launch_pdl(kern, grid, dim3((p.slab_vh + 1) * 32), smem, stream, kv_map, q);
   if (e == cudaSuccess && trace) e = cudaEventRecord(static_cast<cudaEvent_t>(trace[3]), stream);
   if (e != cudaSuccess) return e;
-  return launch_pdl(combine_kernel<D, GW>,
+  return launch_pdl(p.deep_combine ? combine_kernel<D, GW, true> : combine_kernel<D, GW, false>,
                     dim3(static_cast<unsigned>(p.splits + p.shared_num),
                          static_cast<unsigned>(p.virt_heads)),
                     dim3(GW * 32), 0, stream, p);
@@ -928,6 +961,8 @@ cudaError_t launch_decode(const AttnArgs& a, const AttnWorkspace& ws, const CUte
   p.scale_log2 = a.scale * kLog2e;
   p.scored = a.scored;
   p.score = a.score;
+  p.deep_combine =
+      splits >= kDeepPieces * a.num_reqs && (a.scored || a.max_query_len == 1);
   if (a.score.softcap > 0.f) p.scale_log2 = 2.f * kLog2e * (a.scale / a.score.softcap);
   p.dec_prefix = ws.dec_prefix;
   p.hdr = ws.hdr;

@@ -61,6 +61,8 @@ __device__ __forceinline__ Int3 block_exclusive_scan(Int3 v, Int3* total) {
 // Counts of one request: decode 16-key chunks, is-prefill, prefill work items.
 // A decode request that takes its shared prefix from the shared items
 // streams only the chunks past the prefix.
+// SCORED: it streams the chunks of its row's key range.
+template <bool SCORED>
 __device__ __forceinline__ Int3 plan_counts(const AttnArgs& a, const AttnWorkspace& ws, int r,
                                             int tile_q, bool flag) {
   Int3 v{0, 0, 0};
@@ -75,11 +77,12 @@ __device__ __forceinline__ Int3 plan_counts(const AttnArgs& a, const AttnWorkspa
   } else if (n == 1) {
     v.a = static_cast<int>(nblk);
     const int i = r - a.shared_first;
-    const bool shared = a.shared_num > 0 && i >= 0 && i < a.shared_num && ws.casc_use[i];
-    if (a.scored)
+    if constexpr (SCORED) {
+      const bool shared = a.shared_num > 0 && i >= 0 && i < a.shared_num && ws.casc_use[i];
       v.a = range_chunks(row_keys(a.score, q0, c, L, shared ? a.shared_len : 0));
-    else if (shared)
+    } else if (a.shared_num > 0 && i >= 0 && i < a.shared_num && ws.casc_use[i]) {
       v.a -= a.shared_len / kChunkKeys;
+    }
   } else if (n > 1) {
     v.b = 1;
     v.c = ((n + tile_q - 1) / tile_q) * a.num_kv_heads;
@@ -159,6 +162,7 @@ __device__ int plan_shared(const AttnArgs& a, const AttnWorkspace& ws, int tile_
   return qtiles * a.shared_pieces * a.num_kv_heads;
 }
 
+template <bool SCORED>
 __device__ void plan_block(const AttnArgs& a, const AttnWorkspace& ws, int tile_q) {
   __shared__ Int3 total;
   const int shared_items = a.shared_num > 0 ? plan_shared(a, ws, tile_q) : 0;
@@ -167,7 +171,7 @@ __device__ void plan_block(const AttnArgs& a, const AttnWorkspace& ws, int tile_
   const int r0 = min(R, static_cast<int>(threadIdx.x) * per), r1 = min(R, r0 + per);
   Int3 sum{0, 0, 0};
   for (int r = r0; r < r1; ++r) {
-    const Int3 v = plan_counts(a, ws, r, tile_q, true);
+    const Int3 v = plan_counts<SCORED>(a, ws, r, tile_q, true);
     sum.a += v.a;
     sum.b += v.b;
     sum.c += v.c;
@@ -181,7 +185,7 @@ __device__ void plan_block(const AttnArgs& a, const AttnWorkspace& ws, int tile_
   if (N == 0)
     for (long long c = threadIdx.x; c < C; c += blockDim.x) ws.bound[c] = -1;
   for (int r = r0; r < r1; ++r) {
-    const Int3 v = plan_counts(a, ws, r, tile_q, false);
+    const Int3 v = plan_counts<SCORED>(a, ws, r, tile_q, false);
     if (v.a > 0) {
       const long long c_lo = (static_cast<long long>(run.a) * C + N - 1) / N;
       long long c_hi = ((static_cast<long long>(run.a) + v.a) * C + N - 1) / N;
@@ -214,10 +218,11 @@ __device__ void plan_block(const AttnArgs& a, const AttnWorkspace& ws, int tile_
   }
 }
 
+template <bool SCORED>
 __global__ void __launch_bounds__(1024) plan_kernel(AttnArgs a, AttnWorkspace ws, int tile_q) {
   pdl_trigger();
   pdl_wait();
-  plan_block(a, ws, tile_q);
+  plan_block<SCORED>(a, ws, tile_q);
 }
 
 // The plan and the step's cache write in one launch: CTA 0 plans (it is
@@ -228,12 +233,13 @@ __global__ void __launch_bounds__(1024) plan_kernel(AttnArgs a, AttnWorkspace ws
 // follow wait for both.
 constexpr int kPrologueTokens = 8;
 
+template <bool SCORED>
 __global__ void __launch_bounds__(1024)
     prologue_kernel(AttnArgs a, AttnWorkspace ws, int tile_q, WriteRowsArgs w) {
   pdl_trigger();
   pdl_wait();
   if (blockIdx.x == 0) {
-    plan_block(a, ws, tile_q);
+    plan_block<SCORED>(a, ws, tile_q);
     return;
   }
   const int warp = threadIdx.x >> 5;
@@ -247,10 +253,10 @@ cudaError_t launch_plan(const AttnArgs& a, const AttnWorkspace& ws, cudaStream_t
   const int group = a.num_q_heads / a.num_kv_heads;
   if (write && write->num_tokens > 0) {
     const int write_ctas = (write->num_tokens + kPrologueTokens - 1) / kPrologueTokens;
-    return launch_pdl(prologue_kernel, dim3(1 + write_ctas), dim3(1024), 0, stream, a, ws,
+    return launch_pdl(a.scored ? prologue_kernel<true> : prologue_kernel<false>, dim3(1 + write_ctas), dim3(1024), 0, stream, a, ws,
                       128 / group, *write);
   }
-  return launch_pdl(plan_kernel, dim3(1), dim3(1024), 0, stream, a, ws, 128 / group);
+  return launch_pdl(a.scored ? plan_kernel<true> : plan_kernel<false>, dim3(1), dim3(1024), 0, stream, a, ws, 128 / group);
 }
 
 cudaError_t read_errors_plan(uint32_t* out, bool clear) {

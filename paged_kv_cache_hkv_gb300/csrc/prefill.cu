@@ -30,6 +30,8 @@
 //
 // Every wait is bounded; on a timeout the kernel records
 // PKV_DEVERR_TIMEOUT, drains its copies, frees TMEM and returns.
+#include <type_traits>
+
 #include "common.cuh"
 #include "launch.h"
 
@@ -216,7 +218,7 @@ struct PrefillLayout {
   // then the item prefix int [kMetaReqs + 1]
   static constexpr uint32_t kMeta = kV + kVStages * kTileKV;
   static constexpr uint32_t kBar = kMeta + kMetaReqs * 16 + (kMetaReqs + 1) * 4 + 124;
-  static constexpr uint32_t kBad = kBar + 640;  // BadKeys of kBadLists items
+  static constexpr uint32_t kBad = kBar + 640;  // SCORED: BadKeys of kBadLists items
   static constexpr uint32_t kBytes = kBad + 1024;
   static constexpr uint32_t kAlloc = kBytes + 1024;  // room to align the base
   static_assert(kAlloc <= 232448, "shared memory");
@@ -236,7 +238,6 @@ static_assert(kBadLists * sizeof(BadKeys) <= 1024, "bad key area");
 
 struct PrefillParams {
   uint16_t* out;
-  const uint16_t* pool;
   const int32_t* block_table;
   int max_blocks;
   const int32_t* seq_lens;
@@ -253,7 +254,11 @@ struct PrefillParams {
   int shared_len, shared_first, shared_num, shared_pieces, shared_tpp;
   float2* shared_ml;
   float* shared_o;
-  // Capped, biased or range-masked scores (the kernel's SCORED variant)
+};
+
+// The scored kernels' parameters: capped, biased or range-masked scores.
+struct ScoredParams : PrefillParams {
+  const uint16_t* pool;
   ScoreParams score;
   float cap_z;      // softcap: 2 log2(e) scale / softcap, S to the argument of tanh_log2
   // softcap by polynomial (see CapPoly): S up to cap_lim in size, 0 = never
@@ -387,7 +392,7 @@ struct RowRaw {
 struct RowKeys {
   int lo, hi, ref;
 };
-__device__ __forceinline__ RowRaw load_row(const PrefillParams& p, const PrefillItem& m, int i) {
+__device__ __forceinline__ RowRaw load_row(const ScoredParams& p, const PrefillItem& m, int i) {
   RowRaw r{0, 0, 0};
   if (i >= m.n) return r;
   const long long t = static_cast<long long>(m.q0) + i;
@@ -397,7 +402,7 @@ __device__ __forceinline__ RowRaw load_row(const PrefillParams& p, const Prefill
   if (p.score.key_end) r.end = __ldg(p.score.key_end + t);
   return r;
 }
-__device__ __forceinline__ RowKeys row_of(const PrefillParams& p, const PrefillItem& m, int i,
+__device__ __forceinline__ RowKeys row_of(const ScoredParams& p, const PrefillItem& m, int i,
                                           const RowRaw& r) {
   if (i >= m.n) return RowKeys{0, 0, 0};
   const int pos = m.piece >= 0 ? r.L - 1 : m.c + i;
@@ -412,7 +417,7 @@ __device__ __forceinline__ RowKeys row_of(const PrefillParams& p, const PrefillI
 
 // The item's keys over all its rows, by a whole warp: {first key that any row
 // sees, past the last one, the largest first key, the smallest end}.
-__device__ __forceinline__ int4 item_keys(const PrefillParams& p, const PrefillItem& m, int QT) {
+__device__ __forceinline__ int4 item_keys(const ScoredParams& p, const PrefillItem& m, int QT) {
   int lo_min = 0x7fffffff, hi_max = 0, lo_max = 0, hi_min = 0x7fffffff;
   const int i1 = min(m.i0 + QT, m.n);
   for (int i = m.i0 + (threadIdx.x & 31); i < i1; i += 32) {
@@ -473,7 +478,7 @@ __device__ __forceinline__ bool zero_nonfinite(uint4* v4) {
 
 // Add the infinities and NaNs of V elements d0 .. d0+nd-1 of key j to the
 // thread's part of its output row, already stored (bf16, or fp32 partials).
-__device__ __noinline__ void add_nonfinite(const PrefillParams& p, long long bt_row, int g, int D,
+__device__ __noinline__ void add_nonfinite(const ScoredParams& p, long long bt_row, int g, int D,
                                            int j, int d0, int nd, uint16_t* out, float* partial) {
   const int id = __ldg(p.block_table + bt_row + (j >> p.block_shift));
   if (id < 0 || id >= p.num_blocks) return;
@@ -616,7 +621,7 @@ __device__ __forceinline__ float exact_cap(float z, float cap2) {
 // meanwhile; only its reads of O come before that tile's P is published (the
 // next PV overwrites O), its stores after.
 template <int D, int SC>
-__device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillShared& sh,
+__device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillShared& sh,
                                                unsigned char* gbase, uint32_t tmem, int n_items) {
   constexpr bool CAP = (SC & kCap) != 0, BIAS = (SC & kBias) != 0;
   constexpr bool FIXED = CAP && !BIAS;  // no running maximum (kCapFixedMax): it stays 0
@@ -1025,7 +1030,7 @@ __device__ __forceinline__ void scored_softmax(const PrefillParams& p, PrefillSh
 template <int D, int SC>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
-                   const PrefillParams p) {
+                   const std::conditional_t<SC == kPlain, PrefillParams, ScoredParams> p) {
   using Lay = PrefillLayout<D>;
   constexpr int DH = Lay::DH;
   constexpr bool SCORED = SC != kPlain;
@@ -1139,7 +1144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       if (valid(claimed)) {
         claimed_m = prefill_item(p, n_req, claimed, QT, meta, meta_prefix);
-        narrow_item(claimed_m, item_keys(p, claimed_m, QT));
+        if constexpr (SCORED) narrow_item(claimed_m, item_keys(p, claimed_m, QT));
       }
       if (ln == 0) {
         sh.item_q[slot] = claimed;
@@ -1532,20 +1537,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D, int SC>
-static cudaError_t launch_prefill_t(const PrefillParams& p, const CUtensorMap& kv_map,
+static cudaError_t launch_prefill_t(const ScoredParams& p, const CUtensorMap& kv_map,
                                     const CUtensorMap& q_map, int grid, cudaStream_t stream) {
   auto kern = prefill_kernel<D, SC>;
   const int smem = static_cast<int>(PrefillLayout<D>::kAlloc);
   static std::atomic<unsigned long long> attr_done{0};
   cudaError_t e = smem_attr_once(kern, smem, attr_done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), static_cast<size_t>(smem), stream, kv_map,
-                    q_map, p);
+  if constexpr (SC == kPlain)
+    return launch_pdl(kern, dim3(grid), dim3(kThreads), static_cast<size_t>(smem), stream, kv_map,
+                      q_map, static_cast<const PrefillParams&>(p));
+  else
+    return launch_pdl(kern, dim3(grid), dim3(kThreads), static_cast<size_t>(smem), stream, kv_map,
+                      q_map, p);
 }
 
 cudaError_t launch_prefill(const AttnArgs& a, const AttnWorkspace& ws, const CUtensorMap& kv_map,
                            const CUtensorMap& q_map, int num_sms, cudaStream_t stream) {
-  PrefillParams p;
+  ScoredParams p;
   p.out = a.out;
   p.pool = static_cast<const uint16_t*>(a.kv_cache);
   p.block_table = a.block_table;
