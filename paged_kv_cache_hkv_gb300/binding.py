@@ -138,7 +138,9 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the raw handle: torch.cuda.current_stream() makes an object (3.1 us a
+        # call instead of 0.4, half of a small call's host time)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -235,6 +237,12 @@ def pkv_copy_blocks(dst_pool, src_pool, block_pairs, stream=None):
         _ptr(block_pairs), block_pairs.shape[0], lay, _stream(stream)))
 
 
+def _one_device(first, *tensors):
+    for t in tensors:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device} in one call")
+
+
 def _scores(q, softcap, alibi_slopes, key_begin, key_end):
     """pkv_score_options of a call on q [T, Hq, D] (None when all are off)."""
     softcap = float(softcap or 0.0)
@@ -249,6 +257,7 @@ def _scores(q, softcap, alibi_slopes, key_begin, key_end):
             _require(t, torch.int32, n)
             if t.shape != (q.shape[0],) or not t.is_contiguous():
                 raise ValueError(f"{n} must be a contiguous [T] tensor")
+    _one_device(q, alibi_slopes, key_begin, key_end)
     o = pkv_score_options()
     o.softcap = softcap
     o.alibi_slopes, o.key_begin, o.key_end = _ptr(alibi_slopes), _ptr(key_begin), _ptr(key_end)
@@ -414,6 +423,7 @@ def _table_args(block_table, free_queue, free_state, free_state_out, ref_cnt):
         _require(t, torch.int32, n)
         if not t.is_contiguous():
             raise ValueError(f"{n} must be contiguous")
+    _one_device(block_table, free_queue, free_state, free_state_out, ref_cnt)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [num_reqs, max_blocks]")
     for t, n in ((free_state, "free_state"), (free_state_out, "free_state_out")):
@@ -442,6 +452,8 @@ def _build_args(block_table, query_start_loc, seq_lens, slot_mapping, num_comput
         num_tokens = slot_mapping.shape[0]
     elif num_tokens is None:
         raise ValueError("num_tokens is needed without a slot_mapping")
+    _one_device(block_table, query_start_loc, seq_lens, slot_mapping, num_computed_tokens,
+                query_lens)
     return (_ptr(block_table), block_table.shape[1], _ptr(query_start_loc), _ptr(seq_lens),
             _ptr(slot_mapping), _ptr(num_computed_tokens), _ptr(query_lens), R, int(num_tokens),
             _ptr(free_queue), _ptr(free_state), _ptr(free_state_out), _ptr(ref_cnt),
@@ -467,6 +479,7 @@ def _release_args(block_table, release_rows, release_tokens, free_queue, free_st
             raise ValueError(f"{n} must be a contiguous 1-D tensor")
     if release_tokens.shape[0] != block_table.shape[0]:
         raise ValueError("release_tokens must be [num_reqs]")
+    _one_device(block_table, release_rows, release_tokens, workspace)
     return (_ptr(block_table), block_table.shape[1], block_table.shape[0], _ptr(release_rows),
             _ptr(release_tokens), release_rows.shape[0], _ptr(free_queue), _ptr(free_state),
             _ptr(free_state_out), _ptr(ref_cnt), free_queue.shape[0], int(block_size),
