@@ -274,7 +274,7 @@ struct ScoredParams : PrefillParams {
 // (1.0e-6: equal-ripple, found by reweighted least squares). The powers of
 // scale / softcap and the factor softcap * log2(e) go into the coefficients,
 // so a pair of scores takes six packed FMA-pipe instructions; as a whole the
-// prefill of 4 x 2048 rows over 8192 keys went 1828 -> 1049 us with it and without the running maximum. A
+// prefill of 4 x 2048 rows over 8192 keys went 1828 -> 1068 us with it and without the running maximum. A
 // warp that holds a larger |u| takes the exact form (tanh_log2) for its tile.
 constexpr float kCapLim = 0.8f;
 constexpr double kCapPoly[5] = {9.999989943e-01, -3.332537196e-01, 1.323056551e-01, -4.918014086e-02, 1.210013789e-02};
@@ -744,6 +744,7 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
     int item_n = -1;
     RowRaw raw_n{0, 0, 0};
     float m_run = FIXED ? 0.f : -INFINITY, l_run = 0.f;
+    const bool no_row = m.i0 + (row >> gsh) >= m.n;  // behind the request's rows
     // bias per key of distance, base-2 scores
     const float slope2 =
         BIAS && p.score.slopes ? __ldg(p.score.slopes + m.g * G + (row & (G - 1))) * kLog2e : 0.f;
@@ -772,7 +773,6 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
       bool wfull = full;
       if (!full) {
         const int k0 = ka * kTileN;
-        const bool no_row = m.i0 + (row >> gsh) >= m.n;
         wfull = mask == 0xFFu &&
                 __all_sync(0xffffffffu, no_row || (rk.lo <= k0 && rk.hi >= k0 + kTileN));
       }
@@ -793,9 +793,8 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
                     ((cm >> (2 * q + 1)) & 1u ? 0xffff0000u : 0u));
       }
       if constexpr (CAP) {
-        // Rows of the tile that were not loaded, or hold no key yet, must not
-        // decide which form of the cap is taken.
-        if (!wfull && (mask != 0xFFu || ka * kTileN < m.k_lo || ka * kTileN + kTileN > m.kv_len)) {
+        // What a masked key holds must not decide which form of the cap is taken.
+        if (!wfull) {
 #pragma unroll
           for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -826,7 +825,8 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
             sr[q][i] = __float_as_uint(y.x);
             sr[q][i + 1] = __float_as_uint(y.y);
           }
-        const float amax = fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3]));
+        // (nor what lies in q behind the request's rows)
+        const float amax = no_row ? 0.f : fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3]));
         if (__any_sync(0xffffffffu, amax > p.cap_lim)) {
           // exact form, eight scores at a time, S replaced in tensor memory
           // (all 64 in registers took 1782 instead of 1937 us where every tile

@@ -260,6 +260,50 @@ def test_rows_behind_the_batch_are_left_and_bad_blocks_are_flagged():
     assert (bits_to_f64(ds.out_host()[0]) == 0).all()
 
 
+@pytest.mark.parametrize("mod", ["cap", "small-cap", "cap-alibi", "documents"])
+def test_what_masked_keys_and_padding_rows_hold_changes_no_bit(mod):
+    specs = [RequestSpec(150, 90), RequestSpec(140, 1), RequestSpec(0, 77)]
+    step = make_step(specs, num_q_heads=8, num_kv_heads=2, head_dim=128, seed=31)
+    T = step.num_tokens
+    begin, end = key_ranges(step, "documents", 4)
+    # no row sees the keys 130 and 131 of request 0, nor 60 and 61 of the others
+    q = step.query_start_loc
+    for r, (a, z) in enumerate(((130, 132), (60, 62), (60, 62))):
+        for t in range(q[r], q[r + 1]):
+            if begin[t] < z <= end[t]:
+                begin[t] = z
+            elif begin[t] < z:
+                end[t] = min(end[t], a)
+    scores = scores_for(step, MODS[mod])
+    scores.update(key_begin=begin, key_end=end)
+    outs = []
+    for fill in (0x0000, 0x7F80, 0xFF80, 0x7FC0, 0x7F7F):
+        s = make_step(specs, num_q_heads=8, num_kv_heads=2, head_dim=128, seed=31)
+        for r, keys in enumerate(((130, 131), (60, 61), (60, 61))):
+            for j in keys:
+                c = s.num_computed[r]
+                if j < c:
+                    s.kv_cache[s.block_table[r][j // 16], :, j % 16] = fill
+                else:
+                    s.k[q[r] + j - c] = fill
+                    s.v[q[r] + j - c] = fill
+        # 40 rows behind the batch
+        pad = lambda a: np.concatenate([a, np.full((40,) + a.shape[1:], fill, a.dtype)])  # noqa: E731
+        s.q, s.k, s.v = pad(s.q), pad(s.k), pad(s.v)
+        more = np.zeros(40, np.int32)
+        ds = DeviceStep(s, softcap=scores["softcap"], alibi_slopes=scores.get("alibi_slopes"),
+                        key_begin=np.concatenate([begin, more]), key_end=np.concatenate([end, more]))
+        ds.slot_mapping = torch.empty(T + 40, dtype=torch.int64, device="cuda")
+        ds.out = torch.full((T + 40, 8, 128), 2.0, dtype=torch.bfloat16, device="cuda")
+        ds.run()
+        torch.cuda.synchronize()
+        assert binding.pkv_get_device_errors(clear=True) == 0
+        outs.append(ds.out_host())
+    assert_within(outs[0][:T], *expected(step, **scores))
+    for o in outs[1:]:
+        assert np.array_equal(o, outs[0])
+
+
 def test_every_call_takes_the_scores():
     step = make_step(batch(seed=5), num_q_heads=8, num_kv_heads=2, head_dim=64, seed=21)
     scores = scores_for(step, MODS["cap-alibi-random"])

@@ -398,6 +398,72 @@ def test_graph_replay_advances_the_queue_in_place():
     assert binding.pkv_get_device_errors(clear=True) == 0
 
 
+@pytest.mark.parametrize("rows", [7, 1200])
+def test_a_captured_release_and_build(rows):
+    """Release and build captured together, small and large, replayed over a
+    restored pool; the queue's state in place."""
+    B, R, P = 16, 1300, 4
+    rng = np.random.default_rng(rows)
+    tokens = rng.integers(P * B, 400, R)
+    table, ref, queue, state = pool_state(tokens, tokens, B, prefix_blocks=P, sharers=range(0, R, 2),
+                                          width=40, seed=3)
+    gone = rng.permutation(R)[:rows]
+    d = Device(table, ref, queue, state, B)
+    c, n = np.array([0, 0, 5]), np.array([100, 1, 300])
+    fresh = np.full((3, 40), -1, np.int32)
+    fresh[2, 0] = table[gone[0], 5]  # (any block: request 2 goes on in it)
+    ft, qsl, lens = dev(fresh), dev(np.zeros(4)), dev(np.zeros(3))
+    slots = torch.zeros(401, dtype=torch.int64, device="cuda")
+    rel = binding.TableCalls(block_table=d.table, free_queue=d.queue, free_state=d.state,
+                             ref_cnt=d.ref, block_size=B, release_rows=dev(gone),
+                             release_tokens=dev(tokens))
+    bld = binding.TableCalls(block_table=ft, query_start_loc=qsl, seq_lens=lens, slot_mapping=slots,
+                             num_computed_tokens=dev(c), query_lens=dev(n), free_queue=d.queue,
+                             free_state=d.state, ref_cnt=d.ref, block_size=B)
+    want_r = oracle.release_blocks(table, gone, tokens, queue, state, ref, B)
+    want = oracle.build_step_tables(fresh, c, n, want_r["free_queue"], want_r["free_state"],
+                                    want_r["ref_cnt"], B)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        rel.release()
+        bld.build()
+    for _ in range(3):
+        d.ref.copy_(torch.from_numpy(ref))
+        d.queue.copy_(torch.from_numpy(queue))
+        d.state.copy_(torch.from_numpy(state))
+        ft.copy_(torch.from_numpy(fresh))
+        slots.fill_(-9)
+        g.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(ft.cpu().numpy(), want["block_table"])
+        assert np.array_equal(slots.cpu().numpy(), want["slot_mapping"])
+        assert np.array_equal(d.queue.cpu().numpy(), want_r["free_queue"])
+        assert np.array_equal(d.state.cpu().numpy(), want["free_state"])
+        assert np.array_equal(d.ref.cpu().numpy(), want["ref_cnt"])
+    assert binding.pkv_get_device_errors(clear=True) == 0
+
+
+def test_many_requests():
+    """More than 64 requests per thread of the scan, and a release of as many."""
+    rng = np.random.default_rng(0)
+    R, B = 70001, 16
+    c = rng.integers(0, 40, R)
+    n = np.where(rng.random(R) < 0.01, rng.integers(0, 60, R), rng.integers(0, 2, R))
+    table, ref, queue, state = pool_state(c, c + n, B, seed=0)
+    want = oracle.build_step_tables(table, c, n, queue, state, ref, B)
+    d = Device(table, ref, queue, state, B)
+    d.build(c, n)
+    d.check_build(want)
+    rows = rng.permutation(R)[:65000]
+    want = oracle.release_blocks(want["block_table"], rows, c + n, queue, want["free_state"],
+                                 want["ref_cnt"], B)
+    d.release(rows, c + n)
+    d.check_release(want)
+    assert binding.pkv_get_device_errors(clear=True) == 0
+
+
 def test_two_pools_on_two_streams_at_once():
     rng = np.random.default_rng(1)
     runs = []
