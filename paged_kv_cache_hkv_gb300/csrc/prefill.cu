@@ -299,7 +299,7 @@ struct ScoredParams : PrefillParams {
 // (1.0e-6: equal-ripple, found by reweighted least squares). The powers of
 // scale / softcap and the factor softcap * log2(e) go into the coefficients,
 // so a pair of scores takes six packed FMA-pipe instructions; as a whole the
-// prefill of 4 x 2048 rows over 8192 keys went 1828 -> 1037 us with it and without the running maximum. A
+// prefill of 4 x 2048 rows over 8192 keys went 1828 -> 1003 us with it and without the running maximum. A
 // warp that holds a larger |u| takes the exact form (tanh_log2) for its tile.
 constexpr float kCapLim = 0.8f;
 constexpr double kCapPoly[5] = {9.999989943e-01, -3.332537196e-01, 1.323056551e-01, -4.918014086e-02, 1.210013789e-02};
@@ -350,8 +350,7 @@ struct PrefillShared {
   uint64_t iq_free[kItemQ];      // 11 arrivals: every role has read it
   int item_q[kItemQ];
   PrefillItem item_m[kItemQ];    // SCORED: the item described, for every role
-  uint64_t mask_full[kMaskRing]; // SCORED: tile T's mask published in masks[T % kMaskRing]
-  uint32_t masks[kMaskRing];
+  uint32_t masks[kMaskRing];     // SCORED: chunk mask of tile T in masks[T % kMaskRing]
   uint32_t tmem;
   int abort;
 };
@@ -786,11 +785,9 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
         if (item_n < 0) return;  // aborted
         if (valid(item_n)) raw_n = load_row(p, mn, mn.i0 + (row >> gsh));
       }
-      ok = wait_small(&sh.mask_full[Tg % kMaskRing], (Tg / kMaskRing) & 1u, abort_flag);
-      if (!ok) return;
-      const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&sh.masks[Tg % kMaskRing]);
       ok = wait_small(&sh.s_full[b], (Tg / kSBufs) & 1u, abort_flag);
       if (!ok) return;
+      const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&sh.masks[Tg % kMaskRing]);
       tc::fence_after_sync();
       const int ka = tile_at<SC>(m.kt0, nkv, kt);  // key tile (keys ka*128 ..)
       // `full`: every row of the item sees the whole tile. Masks go by warp,
@@ -1073,15 +1070,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < KST; ++i) mbar_init(&sh.k_full[i], 1);
     for (int i = 0; i < VST; ++i) mbar_init(&sh.v_full[i], 1);
     for (int i = 0; i < kSBufs; ++i) {
-      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.s_full[i], SCORED ? 2 : 1);
       mbar_init(&sh.pv_done[i], 1);
       mbar_init(&sh.p_ready[i], 256);
     }
     mbar_init(&sh.o_full, 1);
     mbar_init(&sh.drain[0], 1);
     mbar_init(&sh.drain[1], 1);
-    if constexpr (SCORED)
-      for (int i = 0; i < kMaskRing; ++i) mbar_init(&sh.mask_full[i], 1);
     for (int i = 0; i < kItemQ; ++i) {
       mbar_init(&sh.iq_full[i], 1);
       mbar_init(&sh.iq_free[i], 11);
@@ -1251,8 +1246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int e = __ffs(w) - 1;  // entry: chunk e, 2e and 2e+1, or e/2
                 ok8 &= ~(bsh == 5 ? 3u << (2 * e) : bsh == 4 ? 1u << e : 1u << (e >> 1));
               }
-              sh.masks[T % kMaskRing] = ok8;
-              mbar_arrive(&sh.mask_full[T % kMaskRing]);
+              sh.masks[T % kMaskRing] = ok8;  // (seen by way of k_full and the S thread)
             }
           }
         }
@@ -1314,6 +1308,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc::mma_bf16(tmem + kTmemS + kTileN * b, a, bd, idesc_qk, kk > 0);
             }
             tc::commit(&sh.s_full[b]);  // S in TMEM, and the K slot free
+            // SCORED: this thread's own arrival, which releases what it has seen
+            // of the K-copy warp's writes (the tile's mask) to the softmax warps
+            if constexpr (SCORED) mbar_arrive(&sh.s_full[b]);
             if (kt == nkv - 1) tc::commit(&sh.q_free);
           }
         } else {

@@ -10,8 +10,10 @@ overwritten only after that) and stores the row afterwards. Agents also fill a
 list of bad V rows per item and read it as they store; there are five, and
 agent 0 empties, as it reads O of item i, the list of item i + 3. The model
 checks that a store finds its item's list complete and with nothing else in it.
-The K-copy warp publishes a mask per tile in a ring of eight; the model checks
-that each agent finds its own tile's.
+The K-copy warp writes a mask per tile into a ring of eight before it copies K;
+the S thread, which waits for that copy, arrives on the tile's S barrier
+itself, next to its commit, so that an agent that has waited for S may read the
+mask. The model checks that each agent finds its own tile's.
 """
 
 import random
@@ -19,7 +21,7 @@ import random
 import pytest
 
 import test_prefill_protocol as plain
-from test_prefill_protocol import Barrier, ITEM_Q, N_SOFTMAX, S_BUFS, run, take
+from test_prefill_protocol import ITEM_Q, N_SOFTMAX, S_BUFS, run, take
 
 K_STAGES, V_STAGES = 2, 3
 
@@ -33,8 +35,8 @@ def _rings(monkeypatch):
 def k_warp_ahead(cta, ring=8):
     T, it = 0, 0
     cta.masks = [None] * ring
-    for i in range(ring):
-        cta.b[f"mask_full{i}"] = Barrier(f"mask_full{i}", 1)
+    for i in range(S_BUFS):
+        cta.b[f"s_full{i}"].count = 2
 
     def claim(j):
         slot = j % ITEM_Q
@@ -54,12 +56,19 @@ def k_warp_ahead(cta, ring=8):
                 Tp = T - K_STAGES
                 yield ("wait", f"s_full{Tp % S_BUFS}", Tp // S_BUFS)
             cta.masks[T % len(cta.masks)] = T
-            yield ("arrive", f"mask_full{T % len(cta.masks)}", 1)
             yield ("tma", f"k_full{T % K_STAGES}")
             T += 1
         it += 1
         yield from claim(it)
         item = cta.item_q[it % ITEM_Q]
+
+
+def s_thread(cta):
+    """The plain S thread with its own arrival next to each S commit."""
+    for op in plain.s_thread(cta):
+        yield op
+        if op[0] == "commit" and op[2].startswith("s_full"):
+            yield ("arrive", op[2], 1)
 
 
 def agent(cta, a, lists=5, reset=3, publish_first=False):
@@ -91,10 +100,8 @@ def agent(cta, a, lists=5, reset=3, publish_first=False):
             if kt == nkv - 1:
                 yield ("wait", f"iq_full{(it + 1) % ITEM_Q}", (it + 1) // ITEM_Q)
                 seen = cta.item_q[(it + 1) % ITEM_Q]
-            ring = len(cta.masks)
-            yield ("wait", f"mask_full{Tg % ring}", Tg // ring)
-            assert cta.masks[Tg % ring] == Tg
             yield ("wait", f"s_full{Tg % S_BUFS}", Tg // S_BUFS)
+            assert cta.masks[Tg % len(cta.masks)] == Tg
             cta.s_read[Tg] = cta.s_read.get(Tg, 0) + 1
             if kt > 0 and rng.random() < 0.3:  # the max grew: rescale O
                 Tp = Tg - 1
@@ -125,7 +132,7 @@ def agent(cta, a, lists=5, reset=3, publish_first=False):
         yield from store(pend[0])
 
 
-ROLES = {"k": k_warp_ahead, "agent": agent}
+ROLES = {"k": k_warp_ahead, "s": s_thread, "agent": agent}
 
 
 @pytest.mark.parametrize("case", range(60))
@@ -144,14 +151,14 @@ def test_all_one_tile_and_all_long():
 
 PLANTED = {
     # P published before the previous item's O was read
-    "epilogue_after_p": {"k": k_warp_ahead, "agent": lambda c, a: agent(c, a, publish_first=True)},
+    "epilogue_after_p": {"k": k_warp_ahead, "s": s_thread, "agent": lambda c, a: agent(c, a, publish_first=True)},
     # fewer lists: the one emptied is still read
-    "three_lists": {"k": k_warp_ahead, "agent": lambda c, a: agent(c, a, lists=3, reset=2)},
-    "four_lists": {"k": k_warp_ahead, "agent": lambda c, a: agent(c, a, lists=4, reset=3)},
+    "three_lists": {"k": k_warp_ahead, "s": s_thread, "agent": lambda c, a: agent(c, a, lists=3, reset=2)},
+    "four_lists": {"k": k_warp_ahead, "s": s_thread, "agent": lambda c, a: agent(c, a, lists=4, reset=3)},
     # a ring of masks as short as the K ring
-    "three_masks": {"k": lambda c: k_warp_ahead(c, ring=3), "agent": agent},
+    "three_masks": {"k": lambda c: k_warp_ahead(c, ring=3), "s": s_thread, "agent": agent},
     # the list emptied is one that others fill
-    "reset_next": {"k": k_warp_ahead, "agent": lambda c, a: agent(c, a, reset=1)},
+    "reset_next": {"k": k_warp_ahead, "s": s_thread, "agent": lambda c, a: agent(c, a, reset=1)},
 }
 
 
