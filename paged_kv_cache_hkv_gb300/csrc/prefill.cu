@@ -147,6 +147,22 @@ __device__ __forceinline__ void ld_half64(uint32_t t0, uint32_t t1, uint32_t (&a
       : "memory");
 }
 
+// One such load and its wait.
+template <int OFF>
+__device__ __forceinline__ void ld_half32_wait(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32], %33;\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr), "n"(OFF)
+      : "memory");
+}
+
 // The same access shape with 8 columns per thread, loaded and waited for.
 template <int OFF>
 __device__ __forceinline__ void ld_half8(uint32_t taddr, uint32_t (&r)[8]) {
@@ -214,11 +230,32 @@ constexpr int kItemQ = 4;      // claimed work items in flight between the roles
 constexpr int kMaskRing = 8;   // SCORED: tiles whose chunk masks are kept. K(T+8) is copied
                                // once S(T+5) is done, so PV(T+2): every reader of mask T is through
 constexpr int kMetaReqs = 128;  // prefill requests whose metadata a CTA keeps in shared memory
-constexpr int kThreads = 384;  // 8 softmax warps, S-MMA warp, K-copy warp, V-copy warp, PV-MMA warp
 constexpr float kRescaleLog2 = 8.f;  // lazy rescale threshold (powers of two)
 // Scores of a kernel instance: plain, or key ranges with or without a cap
 // (ScoreParams::softcap) and a bias (ScoreParams::slopes).
 enum : int { kPlain = 0, kRanges = 1, kCap = 2, kBias = 4 };
+// Softmax warps of an instance; after them the S-MMA warp, the K-copy warp, the
+// V-copy warp and the PV-MMA warp. A capped instance without a bias keeps no
+// running maximum, so the threads of a row need nothing of one another in a
+// tile: four of them take 32 keys each, and sixteen warps hide one another's
+// latencies where eight left the FMA pipe idle half the time (4 x 2048 rows
+// over 8192 keys 1003 -> 954 us). The other instances exchange a row's
+// maximum by a shuffle between two threads of one warp.
+template <int SC>
+__host__ __device__ constexpr int softmax_warps() {
+  return SC == (kRanges | kCap) ? 16 : 8;
+}
+template <int SC>
+__host__ __device__ constexpr int prefill_threads() {
+  return (softmax_warps<SC>() + 4) * 32;
+}
+// TMEM column, from the S buffer's, of P for the kk-th 16 keys (eight columns
+// each). P overwrites only columns whose scores the writing warp holds: with
+// sixteen warps, keys 0..63 and 64..127 are in different ones.
+template <int SC>
+__host__ __device__ constexpr uint32_t p_column(int kk) {
+  return softmax_warps<SC>() == 16 ? (kk >> 2) * 64u + (kk & 3) * 8u : kk * 8u;
+}
 // Order of an item's key tiles, the kt-th of nkv. With a bias that falls with
 // distance the nearest keys weigh most: taken last to first, the running
 // maximum is found in the first tile, where the other way round a steep slope
@@ -244,7 +281,8 @@ struct PrefillLayout {
   static constexpr uint32_t kMeta = kV + kVStages * kTileKV;
   static constexpr uint32_t kBar = kMeta + kMetaReqs * 16 + (kMetaReqs + 1) * 4 + 124;
   static constexpr uint32_t kBad = kBar + 640;  // SCORED: BadKeys of kBadLists items
-  static constexpr uint32_t kBytes = kBad + 1024;
+  static constexpr uint32_t kSums = kBad + 1024;  // 16 softmax warps: row sums [4][2][128]
+  static constexpr uint32_t kBytes = kSums + 4096;
   static constexpr uint32_t kAlloc = kBytes + 1024;  // room to align the base
   static_assert(kAlloc <= 232448, "shared memory");
 };
@@ -473,13 +511,14 @@ __device__ __forceinline__ void st_global_v8(void* dst, const uint4& a, const ui
                : "memory");
 }
 
-// Zero the infinities and NaNs of 64 bf16 in shared memory; true if there were any.
+// Zero the infinities and NaNs of 8 N bf16 in shared memory; true if there were any.
+template <int N>
 __device__ __forceinline__ bool zero_nonfinite(uint4* v4) {
   // x * 0 is 0 or, for an infinity or a NaN, a NaN
   const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
   __nv_bfloat162 acc = zero;
 #pragma unroll
-  for (int x = 0; x < 8; ++x) {
+  for (int x = 0; x < N; ++x) {
     uint4 v = v4[x];
     const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
 #pragma unroll
@@ -487,7 +526,7 @@ __device__ __forceinline__ bool zero_nonfinite(uint4* v4) {
   }
   if ((*reinterpret_cast<uint32_t*>(&acc) & 0x7fff7fffu) == 0u) return false;
 #pragma unroll 1
-  for (int x = 0; x < 8; ++x) {
+  for (int x = 0; x < N; ++x) {
     uint4 v = v4[x];
     uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
@@ -651,14 +690,25 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
   constexpr bool FIXED = CAP && !BIAS;  // no running maximum (kCapFixedMax): it stays 0
   using Lay = PrefillLayout<D>;
   constexpr int DH = Lay::DH;
-  constexpr int HC = D / 2;  // O columns per thread
+  constexpr int NW = softmax_warps<SC>();
+  constexpr int KPT = 512 / NW;  // keys of a tile per thread: 64 or 32
+  constexpr int KQ = KPT / 32;
+  // O columns per thread in the epilogue; with sixteen warps and D = 64 the
+  // first eight hold them all
+  constexpr int HC = NW == 16 && D == 128 ? 32 : D / 2;
   constexpr int NQ = HC / 32;
   constexpr uint32_t kRingV = Lay::kK + kScoredKStages * Lay::kTileKV;
   volatile int* abort_flag = &sh.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.group, gsh = 31 - __clz(G);  // G is 1, 2, 4 or 8
-  const int ch = lane >> 4;  // key half of this thread
-  const int lane0 = 32 * (warp & 3) + 16 * (warp >> 2);
+  const int ch = lane >> 4;      // of the warp's keys (and O columns), this thread's half
+  const int kh = warp >> 3;      // sixteen warps: keys 0..63 or 64..127 of every tile
+  const int lane0 = 32 * (warp & 3) + 16 * ((warp >> 2) & 1);
+  const int key0 = 64 * kh + KPT * ch;        // this thread's first key of a tile
+  const uint32_t scol = 64u * kh;             // the warp's first S (and P) column
+  const bool has_o = HC == 32 && D == 64 && NW == 16 ? kh == 0 : true;
+  const int ocol = HC * (NW == 16 && D == 128 ? 2 * kh + ch : ch);  // its first O column
+  float* sums = reinterpret_cast<float*>(gbase + Lay::kSums);
   const int row = lane0 + (lane & 15);  // query row of this thread (TMEM lane)
   const uint32_t t_lane = tmem + (static_cast<uint32_t>(lane0) << 16);
   BadKeys* bad_lists = reinterpret_cast<BadKeys*>(gbase + Lay::kBad);
@@ -686,31 +736,35 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
     n_bad = *reinterpret_cast<volatile int*>(&bad_lists[it % kBadLists].count);
     if (tid == 0) bad_lists[(it + 3) % kBadLists].count = 0;
     tc::fence_after_sync();
-    if constexpr (NQ == 2) {
+    if constexpr (NQ == 2)
       tc::ld_half64<HC>(t_lane, t_lane + 32, o[0], o[NQ - 1]);
-    } else {
-      tc::ld_half32<HC>(t_lane, o[0]);
-      tc::wait32(o[0]);
-    }
+    else
+      tc::ld_half32_wait<HC>(t_lane + (D == 128 ? scol : 0u), o[0]);
     return true;
   };
   auto epilogue_store = [&](int it, const uint32_t (&o)[NQ][32], int n_bad) {
-    const float l_tot = pend_sum + __shfl_xor_sync(0xffffffffu, pend_sum, 16);
+    float l_tot;
+    if constexpr (NW == 16) {
+      const float* l = sums + (it & 3) * 256 + row;
+      l_tot = l[0] + l[128];
+    } else {
+      l_tot = pend_sum + __shfl_xor_sync(0xffffffffu, pend_sum, 16);
+    }
     const float inv = l_tot == 0.f ? 0.f : 1.f / l_tot;  // no key seen: zeros
     const int qi = pend_i0 + (row >> gsh);
-    const bool mine = qi < pend_n;
+    const bool mine = qi < pend_n && has_o;
     const int head = pend_g * G + (row & (G - 1));
     uint16_t* dst =
-        p.out + ((static_cast<long long>(pend_q0) + qi) * p.num_q_heads + head) * D + HC * ch;
+        p.out + ((static_cast<long long>(pend_q0) + qi) * p.num_q_heads + head) * D + ocol;
     float* part = nullptr;
     if (pend_piece >= 0) {
       // shared-prefix items keep the row's partial (max, sum, unnormalised O)
       // for the decode of request shared_first + qi: slot of (piece, qi, head)
       const long long pslot =
           (static_cast<long long>(pend_piece) * p.shared_num + qi) * p.num_q_heads + head;
-      part = p.shared_o + pslot * D + HC * ch;
+      part = p.shared_o + pslot * D + ocol;
       if (mine) {
-        if (ch == 0) p.shared_ml[pslot] = make_float2(pend_max, l_tot);
+        if (ocol == 0) p.shared_ml[pslot] = make_float2(pend_max, l_tot);
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
           float4* d4 = reinterpret_cast<float4*>(part + 32 * q);
@@ -754,7 +808,7 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
       for (int i = listed ? 0 : pend_lo; i < (listed ? n_bad : pend_hi); ++i) {
         const int j = listed ? bad.key[i] : i;
         if (j >= pend_lo && j < pend_hi)
-          add_nonfinite(p, pend_bt, pend_g, D, j, HC * ch, HC, dst, part);
+          add_nonfinite(p, pend_bt, pend_g, D, j, ocol, HC, dst, part);
       }
     }
   };
@@ -800,15 +854,23 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
         wfull = mask == 0xFFu &&
                 __all_sync(0xffffffffu, no_row || (rk.lo <= k0 && rk.hi >= k0 + kTileN));
       }
-      // this thread's keys 64ch .. 64ch+63 of the tile: sr[0] the first 32
-      uint32_t sr[2][32];
-      tc::ld_half64<64>(t_s, t_s + 32, sr[0], sr[1]);
-      uint32_t vis[2] = {0xffffffffu, 0xffffffffu};  // this thread's visible keys, a bit each
-      if (!wfull) {
-        const int lo = rk.lo - ka * kTileN - 64 * ch, hi = rk.hi - ka * kTileN - 64 * ch;
-        const uint32_t cm = mask >> (4 * ch);
+      // this thread's keys key0 .. key0+KPT-1 of the tile: sr[0] the first 32
+      uint32_t sr[KQ][32];
+      auto load_scores = [&]() {
+        if constexpr (KQ == 2)
+          tc::ld_half64<64>(t_s, t_s + 32, sr[0], sr[KQ - 1]);
+        else
+          tc::ld_half32_wait<32>(t_s + scol, sr[0]);
+      };
+      load_scores();
+      uint32_t vis[KQ];  // this thread's visible keys, a bit each
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+      for (int q = 0; q < KQ; ++q) vis[q] = 0xffffffffu;
+      if (!wfull) {
+        const int lo = rk.lo - ka * kTileN - key0, hi = rk.hi - ka * kTileN - key0;
+        const uint32_t cm = mask >> (key0 >> 4);
+#pragma unroll
+        for (int q = 0; q < KQ; ++q)
           vis[q] = bits_between(lo - 32 * q, hi - 32 * q) &
                    (((cm >> (2 * q)) & 1u ? 0xffffu : 0u) |
                     ((cm >> (2 * q + 1)) & 1u ? 0xffff0000u : 0u));
@@ -817,14 +879,14 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
         // What a masked key holds must not decide which form of the cap is taken.
         if (!wfull) {
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
+          for (int q = 0; q < KQ; ++q)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (!(vis[q] & (1u << i))) sr[q][i] = 0u;
         }
         float am[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+        for (int q = 0; q < KQ; ++q)
 #pragma unroll
           for (int i = 0; i < 32; i += 2)
             am[(i >> 1) & 3] = max3f(am[(i >> 1) & 3], fabsf(__uint_as_float(sr[q][i])),
@@ -837,7 +899,7 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
                      a3 = make_float2(p.cap_a[3], p.cap_a[3]),
                      a4 = make_float2(p.cap_a[4], p.cap_a[4]);
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+        for (int q = 0; q < KQ; ++q)
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             const float2 x = make_float2(__uint_as_float(sr[q][i]), __uint_as_float(sr[q][i + 1]));
@@ -855,28 +917,28 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
           // code in the way of the polynomial)
           const float cap2 = p.score.softcap * kLog2e;
 #pragma unroll 1
-          for (int c = 0; c < 64; c += 8) {
+          for (int c = 0; c < KPT; c += 8) {
             uint32_t x[8];
-            tc::ld_half8<64>(t_s + c, x);
+            tc::ld_half8<KPT>(t_s + scol + c, x);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               x[i] = __float_as_uint(exact_cap<FIXED>(__uint_as_float(x[i]) * p.cap_z, cap2));
-            tc::st_half8<64>(t_s + c, x);
+            tc::st_half8<KPT>(t_s + scol + c, x);
           }
           tc::wait_st();
-          tc::ld_half64<64>(t_s, t_s + 32, sr[0], sr[1]);
+          load_scores();
         }
       }
       if constexpr (BIAS) {
         // score (with a cap already in base 2) - slope2 * |ref - j|
         const float2 k2 = CAP ? make_float2(1.f, 1.f) : make_float2(p.scale_log2, p.scale_log2);
-        const int d = ka * kTileN + 64 * ch - rk.ref;  // of this thread's first key
+        const int d = ka * kTileN + key0 - rk.ref;  // of this thread's first key
         const float d0 = static_cast<float>(d);
-        if (__all_sync(0xffffffffu, d + 63 <= 0)) {  // every key at or before its row's position
+        if (__all_sync(0xffffffffu, d + KPT - 1 <= 0)) {  // every key at or before its row's position
           const float2 base = make_float2(slope2 * d0, slope2 * d0);
           const float2 sl = make_float2(slope2, slope2);
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
+          for (int q = 0; q < KQ; ++q)
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               const float2 bias = ffma2(
@@ -889,7 +951,7 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
             }
         } else {
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
+          for (int q = 0; q < KQ; ++q)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               sr[q][i] = __float_as_uint(__uint_as_float(sr[q][i]) * k2.x -
@@ -898,7 +960,7 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
       }
       if (!wfull) {  // invisible keys become -inf
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+        for (int q = 0; q < KQ; ++q)
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             if (!(vis[q] & (1u << i))) sr[q][i] = __float_as_uint(-INFINITY);
@@ -906,7 +968,7 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
       if constexpr (!FIXED) {
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+        for (int q = 0; q < KQ; ++q)
 #pragma unroll
           for (int i = 0; i < 32; i += 2)
             mx4[(i >> 1) & 3] =
@@ -937,15 +999,14 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
           }
         }
       }
-      // P = 2^(s * scale - m) as bf16 (-inf -> 0) over the S buffer: column
-      // c holds keys 2c (low half) and 2c+1, so this thread's keys land in
-      // columns 32ch .. 32ch+31 (pairs of keys in the packed fp32x2 FMA / add)
+      // P = 2^(s * scale - m) as bf16 (-inf -> 0) over the S buffer, a column
+      // for two keys (the even one in the low half), in the order of p_column
       float2 ps4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                        make_float2(0.f, 0.f)};
       const float msub = (m_run == -INFINITY) ? 0.f : m_run;
       const float2 sc2 = make_float2(mul, mul), nm2 = make_float2(-msub, -msub);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < KQ; ++q) {
         uint32_t pk[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -955,7 +1016,7 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
           pk[j] = pack_bf16x2(pp.x, pp.y);
           ps4[j & 3] = fadd2(ps4[j & 3], pp);
         }
-        tc::st_half16<32>(t_s + 16 * q, pk);
+        tc::st_half16<KPT / 2>(t_s + scol + 16 * q, pk);
       }
       l_run += ((ps4[0].x + ps4[1].x) + (ps4[2].x + ps4[3].x)) +
                ((ps4[0].y + ps4[1].y) + (ps4[2].y + ps4[3].y));
@@ -970,19 +1031,28 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
         const int slot = static_cast<int>(Tg % kScoredVStages);
         ok = wait_small(&sh.v_full[slot], (Tg / kScoredVStages) & 1u, abort_flag);
         if (!ok) return;
+        constexpr int VN = 64 / NW;  // 16-byte units of the V row per thread: 8 or 4
         uint4* v4 = reinterpret_cast<uint4*>(gbase + kRingV + slot * Lay::kTileKV +
                                              (row >> 3) * Lay::kGroupBytes + ch * 1024 +
-                                             (row & 7) * 128);
+                                             (row & 7) * 128) + VN * kh;
         if (ch < DH && (ka * kTileN + row >= m.kv_len || !(mask >> (row >> 4) & 1u) ||
                         ka * kTileN + row < m.k_lo)) {
 #pragma unroll
-          for (int x = 0; x < 8; ++x) v4[x] = make_uint4(0, 0, 0, 0);
-        } else if (ch < DH && zero_nonfinite(v4)) {
+          for (int x = 0; x < VN; ++x) v4[x] = make_uint4(0, 0, 0, 0);
+        } else if (ch < DH && zero_nonfinite<VN>(v4)) {
           BadKeys& bad = reinterpret_cast<BadKeys*>(gbase + Lay::kBad)[it % kBadLists];
           const int i = atomicAdd(&bad.count, 1);
           if (i < kMaxBadKeys) bad.key[i] = ka * kTileN + row;
         }
         fence_proxy_async_smem();
+      }
+      if constexpr (NW == 16) {
+        // the item's row sums, in four places by turns: place it & 3 is
+        // filled again four items later
+        if (kt + 1 == nkv) {
+          const float l2 = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
+          if (ch == 0) sums[(it & 3) * 256 + kh * 128 + row] = l2;
+        }
       }
       tc::wait_st();
       if (!pend) {
@@ -991,10 +1061,14 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
       } else {
         uint32_t o[NQ][32];
         int n_bad = 0;
-        if (!epilogue_load(it - 1, T - 1, o, n_bad)) return;
+        // (warps that hold no O wait all the same: the bad-key lists and row sums
+        // are reused on the strength of it)
+        if (has_o ? !epilogue_load(it - 1, T - 1, o, n_bad)
+                  : !wait_small(&sh.o_full, (it - 1) & 1u, abort_flag))
+          return;
         tc::fence_before_sync();
         mbar_arrive(&sh.p_ready[b]);
-        epilogue_store(it - 1, o, n_bad);
+        if (has_o) epilogue_store(it - 1, o, n_bad);
         pend = false;
       }
     }
@@ -1016,7 +1090,7 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
   if (pend) {
     uint32_t o[NQ][32];
     int n_bad = 0;
-    if (epilogue_load(it - 1, T - 1, o, n_bad)) epilogue_store(it - 1, o, n_bad);
+    if (has_o && epilogue_load(it - 1, T - 1, o, n_bad)) epilogue_store(it - 1, o, n_bad);
   }
 }
 
@@ -1046,12 +1120,13 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
 // instruction caches (no_instruction was its largest stall, and 8191 rows of
 // packed documents took 180 us instead of 115).
 template <int D, int SC>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(prefill_threads<SC>(), 1)
     prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
                    const std::conditional_t<SC == kPlain, PrefillParams, ScoredParams> p) {
   using Lay = PrefillLayout<D>;
   constexpr int DH = Lay::DH;
   constexpr bool SCORED = SC != kPlain;
+  constexpr int NW = softmax_warps<SC>();  // warp NW: S, NW + 1: K, NW + 2: V, NW + 3: PV
   constexpr int KST = SCORED ? kScoredKStages : kKStages;
   constexpr int VST = SCORED ? kScoredVStages : kVStages;
   constexpr uint32_t kRingV = Lay::kK + KST * Lay::kTileKV;
@@ -1072,24 +1147,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kSBufs; ++i) {
       mbar_init(&sh.s_full[i], SCORED ? 2 : 1);
       mbar_init(&sh.pv_done[i], 1);
-      mbar_init(&sh.p_ready[i], 256);
+      mbar_init(&sh.p_ready[i], NW * 32);
     }
     mbar_init(&sh.o_full, 1);
     mbar_init(&sh.drain[0], 1);
     mbar_init(&sh.drain[1], 1);
     for (int i = 0; i < kItemQ; ++i) {
       mbar_init(&sh.iq_full[i], 1);
-      mbar_init(&sh.iq_free[i], 11);
+      mbar_init(&sh.iq_free[i], NW + 3);
     }
     sh.abort = 0;
     for (int i = 0; i < kBadLists; ++i) reinterpret_cast<BadKeys*>(gbase + Lay::kBad)[i].count = 0;
     fence_barrier_init();
   }
-  if (tid == 32 * 9) {
+  if (tid == 32 * (NW + 1)) {
     prefetch_tensormap(&kv_map);
     prefetch_tensormap(&q_map);
   }
-  if (warp == 8) {
+  if (warp == NW) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&sh.tmem)),
                  "r"(kTmemCols)
@@ -1104,7 +1179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int4* meta_s = reinterpret_cast<int4*>(gbase + Lay::kMeta);
   int* meta_prefix_s = reinterpret_cast<int*>(gbase + Lay::kMeta + kMetaReqs * 16);
   if (n_req <= kMetaReqs) {
-    for (int i = tid; i <= n_req; i += kThreads) {
+    for (int i = tid; i <= n_req; i += prefill_threads<SC>()) {
       meta_prefix_s[i] = __ldg(p.pf_prefix + i);
       if (i < n_req) {
         const int r = __ldg(p.pf_req + i);
@@ -1119,7 +1194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // the first work item is claimed while the CTA sets up
   int first_claim = 0;
-  if (tid == 32 * 9) first_claim = static_cast<int>(atomicAdd(&p.hdr[kHdrPrefillNext], 1u));
+  if (tid == 32 * (NW + 1)) first_claim = static_cast<int>(atomicAdd(&p.hdr[kHdrPrefillNext], 1u));
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -1128,13 +1203,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int* meta_prefix = meta_prefix_s;
   auto valid = [&](int item) { return item >= 0 && item < n_items; };
 
-  if (warp == 9 || warp == 10) {
+  if (warp == NW + 1 || warp == NW + 2) {
     // ================= copy warps. Lane (chunk b, d half dh), lanes
     // 0 .. 8*DH-1, issues the copies of that chunk (one of 16 rows, or two of
     // 8 rows for 8-token blocks); the block ids of a 32-entry window of the
     // block table sit in the lanes' registers.
     const int ln = tid & 31;
-    const bool is_v = warp == 10;
+    const bool is_v = warp == NW + 2;
     const int S = is_v ? VST : KST;
     uint64_t* full = is_v ? sh.v_full : sh.k_full;
     const uint32_t ring = is_v ? kRingV : Lay::kK;
@@ -1271,10 +1346,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       if (!is_v && q_loads > 0) mbar_wait(&sh.q_full, (q_loads - 1) & 1u, kDrainLimitNs);
     }
-  } else if (warp == 8 || warp == 11) {
+  } else if (warp == NW || warp == NW + 3) {
     // ================= MMA threads: warp 8 issues every S, warp 11 every PV
     if ((tid & 31) == 0) {
-      const bool is_s = warp == 8;
+      const bool is_s = warp == NW;
       constexpr uint32_t idesc_qk = tc::idesc_bf16(kTileM, kTileN, 0);
       constexpr uint32_t idesc_pv = tc::idesc_bf16(kTileM, D, 1);
       uint32_t T = 0;  // tiles of earlier items
@@ -1331,7 +1406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int kk = 0; kk < kTileN / 16; ++kk) {
               // keys 16kk .. 16kk+15: two 8-key groups (SBO), d halves 1 KB apart (LBO)
               const uint64_t bd = tc::sw128_desc(vbase + kk * 2 * Lay::kGroupBytes, 1024, Lay::kGroupBytes);
-              tc::mma_bf16_ts(tmem, tmem + kTmemS + kTileN * b + kk * 8u, bd, idesc_pv,
+              tc::mma_bf16_ts(tmem, tmem + kTmemS + kTileN * b + p_column<SC>(kk), bd, idesc_pv,
                               (kt > 0 || kk > 0) ? 1u : 0u);
             }
             tc::commit(&sh.pv_done[b]);  // P's buffer and the V slot free
@@ -1546,7 +1621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == NW) {
     tc::fence_after_sync();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(kTmemCols)
@@ -1563,10 +1638,10 @@ static cudaError_t launch_prefill_t(const ScoredParams& p, const CUtensorMap& kv
   cudaError_t e = smem_attr_once(kern, smem, attr_done);
   if (e != cudaSuccess) return e;
   if constexpr (SC == kPlain)
-    return launch_pdl(kern, dim3(grid), dim3(kThreads), static_cast<size_t>(smem), stream, kv_map,
+    return launch_pdl(kern, dim3(grid), dim3(prefill_threads<SC>()), static_cast<size_t>(smem), stream, kv_map,
                       q_map, static_cast<const PrefillParams&>(p));
   else
-    return launch_pdl(kern, dim3(grid), dim3(kThreads), static_cast<size_t>(smem), stream, kv_map,
+    return launch_pdl(kern, dim3(grid), dim3(prefill_threads<SC>()), static_cast<size_t>(smem), stream, kv_map,
                       q_map, p);
 }
 
