@@ -239,7 +239,7 @@ enum : int { kPlain = 0, kRanges = 1, kCap = 2, kBias = 4 };
 // running maximum, so the threads of a row need nothing of one another in a
 // tile: four of them take 32 keys each, and sixteen warps hide one another's
 // latencies where eight left the FMA pipe idle half the time (4 x 2048 rows
-// over 8192 keys 1003 -> 954 us). The other instances exchange a row's
+// over 8192 keys: 1003 -> 954 us). The other instances exchange a row's
 // maximum by a shuffle between two threads of one warp.
 template <int SC>
 __host__ __device__ constexpr int softmax_warps() {
@@ -324,8 +324,8 @@ struct ScoredParams : PrefillParams {
   const uint16_t* pool;
   ScoreParams score;
   float cap_z;      // softcap: 2 log2(e) scale / softcap, S to the argument of tanh_log2
-  // softcap by polynomial (see CapPoly): S up to cap_lim in size, 0 = never
-  float cap_lim;
+  // softcap by polynomial (see kCapPoly): S^2 up to cap_lim2, -1 = never
+  float cap_lim2;
   float cap_a[5];
   bool out32;       // the output is 32-byte aligned
 };
@@ -336,11 +336,14 @@ struct ScoredParams : PrefillParams {
 // with the c_i that minimise the largest relative error over that interval
 // (1.0e-6: equal-ripple, found by reweighted least squares). The powers of
 // scale / softcap and the factor softcap * log2(e) go into the coefficients,
-// so a pair of scores takes six packed FMA-pipe instructions; as a whole the
-// prefill of 4 x 2048 rows over 8192 keys went 1828 -> 1003 us with it and without the running maximum. A
-// warp that holds a larger |u| takes the exact form (tanh_log2) for its tile.
+// so a pair of scores takes six packed FMA-pipe instructions. A warp that holds
+// a larger |u| takes the exact form for its tile: at softcap 50 and N(0, 3^2)
+// scores none does, at 15 one tile in eight. 4 x 2048 rows over 8192 keys take
+// 898 us, 977 so, and 1512 where every tile needs the exact form (plain scores
+// 692; the polynomial's FMA-pipe work is some 300 of the difference).
 constexpr float kCapLim = 0.8f;
-constexpr double kCapPoly[5] = {9.999989943e-01, -3.332537196e-01, 1.323056551e-01, -4.918014086e-02, 1.210013789e-02};
+constexpr double kCapPoly[5] = {9.999989943e-01, -3.332537196e-01, 1.323056551e-01,
+                                -4.918014086e-02, 1.210013789e-02};
 // The factors above stay normal fp32 numbers, and w^4 finite, for
 // scale / softcap in this range (0.125 / 15 to 0.09 / 1000 in practice).
 constexpr float kCapRatioMin = 1e-4f, kCapRatioMax = 1e4f;
@@ -884,13 +887,7 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
             for (int i = 0; i < 32; ++i)
               if (!(vis[q] & (1u << i))) sr[q][i] = 0u;
         }
-        float am[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int q = 0; q < KQ; ++q)
-#pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            am[(i >> 1) & 3] = max3f(am[(i >> 1) & 3], fabsf(__uint_as_float(sr[q][i])),
-                                     fabsf(__uint_as_float(sr[q][i + 1])));
+        float am[4] = {0.f, 0.f, 0.f, 0.f};  // largest w = S^2
         // the polynomial for all of them, and the vote after it: the maximum
         // and its shuffles then run beside it
         const float2 a0 = make_float2(p.cap_a[0], p.cap_a[0]),
@@ -904,17 +901,18 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
           for (int i = 0; i < 32; i += 2) {
             const float2 x = make_float2(__uint_as_float(sr[q][i]), __uint_as_float(sr[q][i + 1]));
             const float2 w = fmul2(x, x);
+            am[(i >> 1) & 3] = max3f(am[(i >> 1) & 3], w.x, w.y);
             const float2 y = fmul2(x, ffma2(ffma2(ffma2(ffma2(a4, w, a3), w, a2), w, a1), w, a0));
             sr[q][i] = __float_as_uint(y.x);
             sr[q][i + 1] = __float_as_uint(y.y);
           }
         // (nor what lies in q behind the request's rows)
         const float amax = no_row ? 0.f : fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3]));
-        if (__any_sync(0xffffffffu, amax > p.cap_lim)) {
+        if (__any_sync(0xffffffffu, amax > p.cap_lim2)) {
           // exact form, eight scores at a time, S replaced in tensor memory
-          // (all 64 in registers took 1782 instead of 1937 us where every tile
-          // needs it, but 1437 instead of 1296 where one in eight does: more
-          // code in the way of the polynomial)
+          // (all in registers, it was 8% faster where every tile needs it and
+          // 11% slower where one in eight does: more code in the way of the
+          // polynomial)
           const float cap2 = p.score.softcap * kLog2e;
 #pragma unroll 1
           for (int c = 0; c < KPT; c += 8) {
@@ -1666,7 +1664,7 @@ cudaError_t launch_prefill(const AttnArgs& a, const AttnWorkspace& ws, const CUt
   p.out32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
   const float ratio = a.score.softcap > 0.f ? a.scale / a.score.softcap : 0.f;
   const bool poly = ratio >= kCapRatioMin && ratio <= kCapRatioMax;
-  p.cap_lim = poly ? kCapLim / ratio : 0.f;
+  p.cap_lim2 = poly ? (kCapLim / ratio) * (kCapLim / ratio) : -1.f;
   double pw = static_cast<double>(a.score.softcap) * kLog2e * ratio;
   for (int i = 0; i < 5; ++i, pw *= static_cast<double>(ratio) * ratio)
     p.cap_a[i] = poly ? static_cast<float>(kCapPoly[i] * pw) : 0.f;
