@@ -37,9 +37,10 @@
  * its writes to be visible -- before reading any buffer. Work the caller
  * queued earlier on the stream is therefore seen as with plain stream order.
  * The write calls (pkv_slot_mapping, pkv_paged_kv_write,
- * pkv_slot_mapping_and_write) and the attention calls that take the caller's
- * workspace (pkv_paged_attention, pkv_paged_attention_with_write) can be
- * recorded into a CUDA graph.
+ * pkv_slot_mapping_and_write), the attention calls that take the caller's
+ * workspace (pkv_paged_attention, pkv_paged_attention_with_write) and the table
+ * calls (pkv_build_step_tables, pkv_release_blocks) can be recorded into a CUDA
+ * graph.
  */
 #ifndef PAGEDKV_H_
 #define PAGEDKV_H_
@@ -444,8 +445,10 @@ int32_t pkv_paged_attention_static_workspace(
  * cannot cover what is asked for up to and including request r, then r and
  * every later request that needs a block get none. Such a request keeps its
  * rows in the batch but gets seq_lens 0, slots -1 and -1 in the entries asked
- * for, and PKV_DEVERR_NO_BLOCKS is set; the attention call skips it (its rows
- * are not written, PKV_DEVERR_LENGTHS).
+ * for, and PKV_DEVERR_NO_BLOCKS is set. The attention calls skip it (its rows
+ * are not written, PKV_DEVERR_LENGTHS), and pkv_paged_kv_write skips its slots;
+ * the calls that map slots themselves write those of its tokens that still fit
+ * into its own last block and set PKV_DEVERR_BLOCK_RANGE for the others.
  *
  * block_table      in/out, device int32 [num_reqs][max_blocks_per_req]: the
  *                  entries [ceil(c / B), ceil((c + n) / B)) of each row are

@@ -1108,6 +1108,7 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
 //   warps 0..7: the softmax of every tile, 16 query rows per warp and half
 //            of each row per thread, and the item's epilogue (each thread
 //            normalises and writes half of its row's output columns).
+//   (A capped instance has sixteen softmax warps, and the others behind them.)
 //
 // SCORED (SC other than kPlain): the scores are capped, biased or masked by
 // key ranges (ScoreParams). The K-copy warp finds the keys that an item's rows
