@@ -277,9 +277,17 @@ __global__ void __launch_bounds__(kDecodeThreads)
         nx_pn = __ldg(p.dec_prefix + r + 2);
         nx_L = __ldg(p.seq_lens + r + 1);
         nx_t = __ldg(p.qsl + r + 1);
-        nx_off = SCORED ? row_keys(p.score, nx_t, nx_L - 1, nx_L, chunk_off(r + 1) * kChunkKeys).lo /
-                              kChunkKeys
-                        : chunk_off(r + 1);
+        if constexpr (SCORED) {
+          // (only a request with chunks has a row of its own in the batch: the
+          // start of one without, or with inconsistent lengths, may lie
+          // behind the rows)
+          nx_off = nx_pn - (pr + nblk) > 0
+                       ? row_keys(p.score, nx_t, nx_L - 1, nx_L, chunk_off(r + 1) * kChunkKeys).lo /
+                             kChunkKeys
+                       : 0;
+        } else {
+          nx_off = chunk_off(r + 1);
+        }
         const int e = entry_of(nx_off) + lane;
         nx_win = e < p.max_blocks
                      ? __ldg(p.block_table + static_cast<long long>(r + 1) * p.max_blocks + e)

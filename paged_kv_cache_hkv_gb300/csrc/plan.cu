@@ -97,8 +97,8 @@ __device__ __forceinline__ Int3 plan_counts(const AttnArgs& a, const AttnWorkspa
 // flagged.
 // The shared-prefix hint, checked: every request of the run starts as a
 // member; one whose table does not begin with the run's first request's
-// entries, or whose context does not reach past the prefix, drops out (it is
-// attended without the hint); one with other than a single new token turns
+// entries, whose context does not reach past the prefix or whose lengths are
+// inconsistent drops out (it is attended without the hint); one with other than a single new token turns
 // the whole run off. Returns the number of shared-prefix work items.
 __device__ int plan_shared(const AttnArgs& a, const AttnWorkspace& ws, int tile_q) {
   __shared__ int run_off, dropped;
@@ -111,8 +111,11 @@ __device__ int plan_shared(const AttnArgs& a, const AttnWorkspace& ws, int tile_
   __syncthreads();
   for (int i = threadIdx.x; i < num; i += blockDim.x) {
     const int r = a.shared_first + i;
-    if (__ldg(a.qsl + r + 1) - __ldg(a.qsl + r) != 1) run_off = 1;
-    if (__ldg(a.seq_lens + r) <= a.shared_len) {
+    const int q0 = __ldg(a.qsl + r), q1 = __ldg(a.qsl + r + 1), L = __ldg(a.seq_lens + r);
+    if (q1 - q0 != 1) run_off = 1;
+    // (a request with inconsistent lengths streams nothing and has no row to
+    // write: as a member its merge would write one all the same)
+    if (L <= a.shared_len || L != __ldg(a.num_computed + r) + 1 || q0 < 0 || q1 > a.num_tokens) {
       ws.casc_use[i] = 0;
       dropped = 1;
     }

@@ -322,6 +322,7 @@ struct PrefillParams {
 // The scored kernels' parameters: capped, biased or range-masked scores.
 struct ScoredParams : PrefillParams {
   const uint16_t* pool;
+  int num_tokens;
   ScoreParams score;
   float cap_z;      // softcap: 2 log2(e) scale / softcap, S to the argument of tanh_log2
   // softcap by polynomial (see kCapPoly): S^2 up to cap_lim2, -1 = never
@@ -461,6 +462,7 @@ __device__ __forceinline__ RowRaw load_row(const ScoredParams& p, const PrefillI
   RowRaw r{0, 0, 0};
   if (i >= m.n) return r;
   const long long t = static_cast<long long>(m.q0) + i;
+  if (t < 0 || t >= p.num_tokens) return r;  // (no row of the batch: it sees no key)
   // (shared-prefix items: row i is the decode of request shared_first + i)
   r.L = m.piece >= 0 ? __ldg(p.seq_lens + p.shared_first + i) : m.c + m.n;
   if (p.score.key_begin) r.begin = __ldg(p.score.key_begin + t);
@@ -1649,6 +1651,7 @@ cudaError_t launch_prefill(const AttnArgs& a, const AttnWorkspace& ws, const CUt
   ScoredParams p;
   p.out = a.out;
   p.pool = static_cast<const uint16_t*>(a.kv_cache);
+  p.num_tokens = a.num_tokens;
   p.block_table = a.block_table;
   p.max_blocks = a.max_blocks;
   p.seq_lens = a.seq_lens;

@@ -142,6 +142,30 @@ def test_bias_keeps_its_precision_where_only_far_keys_are_seen():
     assert_within(run(step, **scores).out_host(), *expected(step, **scores))
 
 
+@pytest.mark.parametrize("mod", [None, "cap-alibi", "random"])
+def test_a_request_of_the_shared_run_with_inconsistent_lengths(mod):
+    """It is flagged and its row left as it was; the others of the run keep
+    their results. Empty requests stand behind the batch."""
+    specs = [RequestSpec(64 + s, 1, shares_prefix=True) for s in (5, 30, 40, 9, 17, 2)]
+    specs += [RequestSpec(70, 1), RequestSpec(30, 0), RequestSpec(0, 0)]
+    step = make_step(specs, num_q_heads=8, num_kv_heads=2, head_dim=64, prefix_tokens=64, seed=6)
+    scores = scores_for(step, MODS[mod], seed=1) if mod else {}
+    ref, bound = expected(step, **scores)
+    ds = DeviceStep(step, shared_prefix=(64, 0, 6), **scores)
+    ds.slot_map()
+    ds.write()
+    ds.out.fill_(7.0)
+    ds.seq_lens[3] += 1
+    ds.attend()
+    torch.cuda.synchronize()
+    assert binding.pkv_get_device_errors(clear=True) == (binding.DEVERR_LENGTHS |
+                                                         binding.DEVERR_SHARED)
+    out = ds.out_host()
+    assert (bits_to_f64(out[3]) == 7.0).all()
+    rest = [0, 1, 2, 4, 5, 6]
+    assert_within(out[rest], ref[rest], bound[rest])
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("poison", ["nan", "inf", "many"])
 def test_masked_keys_never_reach_the_output(d, poison):
