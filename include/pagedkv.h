@@ -472,7 +472,8 @@ int32_t pkv_paged_attention_static_workspace(
  *                  get 1.
  * A state or a queue entry out of range hands out nothing (PKV_DEVERR_LENGTHS,
  * PKV_DEVERR_BLOCK_RANGE); so does -1 in the table where a request goes on in
- * a block it should have. The call can be recorded into a CUDA graph. Calls
+ * a block it should have. Apart from the state, no array that is written may
+ * overlap another one (PKV_ERR_BAD_SHAPE). The call can be recorded into a CUDA graph. Calls
  * that share a queue, its state, tables or counts must be ordered.
  */
 int32_t pkv_build_step_tables(int32_t* block_table, int32_t max_blocks_per_req,
@@ -511,7 +512,8 @@ int32_t pkv_build_step_tables(int32_t* block_table, int32_t max_blocks_per_req,
  *                  runs (no zeroing needed); may be NULL where that is 0.
  * A row or a length out of range is skipped (PKV_DEVERR_LENGTHS), as is an
  * entry out of the pool (PKV_DEVERR_BLOCK_RANGE). A block that is released more
- * often than it is held goes back once (PKV_DEVERR_REF_COUNT). num_released *
+ * often than it is held goes back once (PKV_DEVERR_REF_COUNT). Arrays must not
+ * overlap, as in pkv_build_step_tables. num_released *
  * max_blocks_per_req must stay below 2^29. The call can be recorded into a
  * CUDA graph.
  */

@@ -149,6 +149,27 @@ int32_t shared_hint(const pkv_attention_options* opt, const pkv_cache_layout& l,
   return PKV_OK;
 }
 
+struct Span {
+  const void* p;
+  long long bytes;
+};
+
+// Whether an array that a call writes overlaps one of the others of the list
+// (null arrays overlap nothing).
+bool overlap(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  auto meet = [](const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + b.bytes && y < x + a.bytes;
+  };
+  for (const Span* w = written.begin(); w != written.end(); ++w) {
+    for (const Span* v = w + 1; v != written.end(); ++v)
+      if (meet(*w, *v)) return true;
+    for (const Span& r : read)
+      if (meet(*w, r)) return true;
+  }
+  return false;
+}
+
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // The score options of the call, checked: *scored = some field is in use.
@@ -636,6 +657,14 @@ int32_t pkv_build_step_tables(int32_t* block_table, int32_t max_blocks_per_req,
                         static_cast<const void*>(ref_cnt)})
     if (!aligned4(p)) return PKV_ERR_MISALIGNED;
   if (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) return PKV_ERR_MISALIGNED;
+  // threads read the inputs while others write (the state may be replaced in place)
+  const long long R4 = 4ll * num_reqs;
+  if (overlap({{block_table, R4 * max_blocks_per_req}, {query_start_loc, R4 + 4}, {seq_lens, R4},
+               {slot_mapping, 8ll * num_tokens}, {ref_cnt, 4ll * num_blocks}, {free_state_out, 8}},
+              {{num_computed_tokens, R4}, {query_lens, R4}, {free_queue, 4ll * num_blocks}}) ||
+      overlap({{block_table, R4 * max_blocks_per_req}, {query_start_loc, R4 + 4}, {seq_lens, R4},
+               {slot_mapping, 8ll * num_tokens}, {ref_cnt, 4ll * num_blocks}}, {{free_state, 8}}))
+    return PKV_ERR_BAD_SHAPE;
   DeviceInfo* d;
   int32_t st = device_info(&d);
   if (st != PKV_OK) return st;
@@ -683,6 +712,14 @@ int32_t pkv_release_blocks(const int32_t* block_table, int32_t max_blocks_per_re
   if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
                    workspace_bytes < need))
     return PKV_ERR_WORKSPACE;
+  const long long R4 = 4ll * num_reqs, n4 = 4ll * num_released;
+  const long long ws = static_cast<long long>(need);
+  if (overlap({{free_queue, 4ll * num_blocks}, {ref_cnt, 4ll * num_blocks}, {free_state_out, 8},
+               {workspace, ws}},
+              {{block_table, R4 * max_blocks_per_req}, {release_rows, n4}, {release_tokens, R4}}) ||
+      overlap({{free_queue, 4ll * num_blocks}, {ref_cnt, 4ll * num_blocks}, {workspace, ws}},
+              {{free_state, 8}}))
+    return PKV_ERR_BAD_SHAPE;
   DeviceInfo* d;
   int32_t st = device_info(&d);
   if (st != PKV_OK) return st;

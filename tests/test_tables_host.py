@@ -66,6 +66,35 @@ def test_release_refusals(lib):
         assert _release(lib, **{k: ctypes.c_void_p(0x10002)}) == E("PKV_ERR_MISALIGNED"), k
 
 
+def _apart(names, step=1 << 24):
+    return {n: ctypes.c_void_p((i + 1) * step) for i, n in enumerate(names)}
+
+
+BUILD_ARRAYS = ("bt", "qsl", "sl", "slots", "nc", "ql", "q", "st", "so", "ref")
+RELEASE_ARRAYS = ("bt", "rows", "tok", "q", "st", "so", "ref")
+
+
+def test_overlapping_arrays_are_refused(lib):
+    if pytest.importorskip("torch").cuda.is_available():
+        pytest.skip("the accepted calls of this test must end at the device check: no GPU")
+    ok = lambda s: s not in (E("PKV_ERR_BAD_SHAPE"), E("PKV_OK"))  # noqa: E731
+    a = _apart(BUILD_ARRAYS)
+    assert ok(_build(lib, **a)) and ok(_build(lib, **{**a, "so": a["st"]}))
+    assert ok(_build(lib, **{**a, "ref": None})) and ok(_build(lib, **{**a, "slots": None}))
+    # lengths updated in place, a table inside the queue, the last word of one in another
+    for out, src in (("sl", "nc"), ("sl", "ql"), ("qsl", "ql"), ("bt", "q"), ("ref", "q"),
+                     ("so", "q"), ("sl", "st"), ("ref", "st"), ("bt", "ref"), ("slots", "bt")):
+        assert _build(lib, **{**a, out: a[src]}) == E("PKV_ERR_BAD_SHAPE"), (out, src)
+    inside = ctypes.c_void_p(a["bt"].value + 4 * (2 * 8 - 1))
+    behind = ctypes.c_void_p(a["bt"].value + 4 * 2 * 8)
+    assert _build(lib, **{**a, "nc": inside}) == E("PKV_ERR_BAD_SHAPE")
+    assert ok(_build(lib, **{**a, "nc": behind}))
+    r = _apart(RELEASE_ARRAYS)
+    assert ok(_release(lib, **r)) and ok(_release(lib, **{**r, "so": r["st"]}))
+    for out, src in (("q", "bt"), ("ref", "rows"), ("so", "tok"), ("q", "ref"), ("q", "st")):
+        assert _release(lib, **{**r, out: r[src]}) == E("PKV_ERR_BAD_SHAPE"), (out, src)
+
+
 def test_release_workspace(lib):
     size = lib.pkv_release_workspace_size
     assert size(0, 100) == 0 and size(8, 300) == 0
