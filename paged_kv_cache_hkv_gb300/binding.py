@@ -136,11 +136,20 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
+def _stream(stream, device=None):
+    """The stream's handle. device: index of the device that the call's tensors
+    are on, where that is to be checked: the library launches on the current one."""
     if stream is None:
+        current = torch.cuda.current_device()
+        if device is not None and device != current:
+            raise ValueError(f"tensors on cuda:{device}, the current device is cuda:{current}")
         # the raw handle: torch.cuda.current_stream() makes an object (3.1 us a
         # call instead of 0.4, half of a small call's host time)
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(current))
+    if device is not None and (device != torch.cuda.current_device() or
+                               device != stream.device.index):
+        raise ValueError(f"tensors on cuda:{device}, a stream of {stream.device}, the current "
+                         f"device is cuda:{torch.cuda.current_device()}")
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -243,6 +252,11 @@ def _one_device(first, *tensors):
             raise ValueError(f"tensors on {first.device} and {t.device} in one call")
 
 
+def _scored_device(q, options):
+    """Device index to check a call's stream against: scored calls only."""
+    return q.device.index if options is not None and options.contents.scores else None
+
+
 def _scores(q, softcap, alibi_slopes, key_begin, key_end):
     """pkv_score_options of a call on q [T, Hq, D] (None when all are off)."""
     softcap = float(softcap or 0.0)
@@ -325,13 +339,14 @@ def pkv_paged_attention(out, q, kv_cache, block_table, seq_lens, query_start_loc
     if q.dim() != 3 or q.stride(2) != 1 or q.stride(1) != q.shape[2]:
         raise ValueError("q must be [T, Hq, D] with contiguous rows")
     lay = layout_of(kv_cache)
+    options = _options(decode_splits, trace_events, shared_prefix,
+                       _scores(q, softcap, alibi_slopes, key_begin, key_end))
     _check("pkv_paged_attention", load().pkv_paged_attention(
         _ptr(out), _ptr(q), q.stride(0), _ptr(kv_cache), _ptr(block_table),
         block_table.shape[1], _ptr(seq_lens), _ptr(query_start_loc), _ptr(num_computed_tokens),
         seq_lens.shape[0], q.shape[0], int(max_query_len), int(max_seq_len), q.shape[1],
         float(scale), lay, _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _options(decode_splits, trace_events, shared_prefix,
-                 _scores(q, softcap, alibi_slopes, key_begin, key_end)), _stream(stream)))
+        options, _stream(stream, _scored_device(q, options))))
     return out
 
 
@@ -362,14 +377,15 @@ def pkv_paged_attention_with_write(out, q, kv_cache, key, value, block_table, se
     if key.shape[0] != q.shape[0]:
         raise ValueError("key and q must have the same number of rows")
     lay = layout_of(kv_cache)
+    options = _options(decode_splits, trace_events, shared_prefix,
+                       _scores(q, softcap, alibi_slopes, key_begin, key_end))
     _check("pkv_paged_attention_with_write", load().pkv_paged_attention_with_write(
         _ptr(out), _ptr(q), q.stride(0), _ptr(kv_cache), _ptr(key), _ptr(value), key.stride(0),
         value.stride(0), _ptr(slot_mapping), _ptr(block_table), block_table.shape[1],
         _ptr(seq_lens), _ptr(query_start_loc), _ptr(num_computed_tokens), seq_lens.shape[0],
         q.shape[0], int(max_query_len), int(max_seq_len), q.shape[1], float(scale), lay,
         _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _options(decode_splits, trace_events, shared_prefix,
-                 _scores(q, softcap, alibi_slopes, key_begin, key_end)), _stream(stream)))
+        options, _stream(stream, _scored_device(q, options))))
     return out
 
 
@@ -400,13 +416,14 @@ def pkv_paged_attention_static_workspace(out, q, kv_cache, block_table, seq_lens
         raise ValueError("out and block_table must be contiguous")
     if q.dim() != 3 or q.stride(2) != 1 or q.stride(1) != q.shape[2]:
         raise ValueError("q must be [T, Hq, D] with contiguous rows")
+    options = _options(decode_splits, None, shared_prefix,
+                       _scores(q, softcap, alibi_slopes, key_begin, key_end))
     _check("pkv_paged_attention_static_workspace", load().pkv_paged_attention_static_workspace(
         _ptr(out), _ptr(q), q.stride(0), _ptr(kv_cache), _ptr(block_table),
         block_table.shape[1], _ptr(seq_lens), _ptr(query_start_loc), _ptr(num_computed_tokens),
         seq_lens.shape[0], q.shape[0], int(max_query_len), int(max_seq_len), q.shape[1],
-        float(scale), layout_of(kv_cache),
-        _options(decode_splits, None, shared_prefix,
-                 _scores(q, softcap, alibi_slopes, key_begin, key_end)), _stream(stream)))
+        float(scale), layout_of(kv_cache), options,
+        _stream(stream, _scored_device(q, options))))
     return out
 
 
@@ -497,7 +514,7 @@ def pkv_build_step_tables(block_table, query_start_loc, seq_lens, slot_mapping,
     _check("pkv_build_step_tables", load().pkv_build_step_tables(
         *_build_args(block_table, query_start_loc, seq_lens, slot_mapping, num_computed_tokens,
                      query_lens, free_queue, free_state, free_state_out, ref_cnt, block_size,
-                     num_tokens), _stream(stream)))
+                     num_tokens), _stream(stream, block_table.device.index)))
 
 
 def pkv_release_blocks(block_table, release_rows, release_tokens, free_queue, free_state, ref_cnt,
@@ -506,14 +523,16 @@ def pkv_release_blocks(block_table, release_rows, release_tokens, free_queue, fr
     pkv_release_workspace_size() bytes, None where that is 0."""
     _check("pkv_release_blocks", load().pkv_release_blocks(
         *_release_args(block_table, release_rows, release_tokens, free_queue, free_state,
-                       free_state_out, ref_cnt, block_size, workspace), _stream(stream)))
+                       free_state_out, ref_cnt, block_size, workspace),
+        _stream(stream, block_table.device.index)))
 
 
 class TableCalls:
     """pkv_build_step_tables and pkv_release_blocks on buffers that a serving
     loop keeps, with their arguments checked and marshalled once (as StepCalls
     does for the step's calls). Pass the arguments of either call or of both; the
-    release's workspace is made here."""
+    release's workspace is made here. Like the tensors, it has to live until the
+    last call has finished: keep the object for as long."""
 
     def __init__(self, *, block_table, free_queue, free_state, block_size: int, ref_cnt=None,
                  free_state_out=None, query_start_loc=None, seq_lens=None, slot_mapping=None,
@@ -534,6 +553,7 @@ class TableCalls:
             self.release_args = _release_args(block_table, release_rows, release_tokens,
                                               free_queue, free_state, free_state_out, ref_cnt,
                                               block_size, workspace)
+        self._device = block_table.device.index
         if self.build_args is None and self.release_args is None:
             raise ValueError("pass query_lens (build), release_rows (release) or both")
         # the tensors stay referenced, so their memory stays valid
@@ -544,14 +564,16 @@ class TableCalls:
     def build(self, stream=None):
         if self.build_args is None:
             raise ValueError("these TableCalls were made without query_lens")
-        status = self.lib.pkv_build_step_tables(*self.build_args, _stream(stream))
+        status = self.lib.pkv_build_step_tables(*self.build_args,
+                                                _stream(stream, self._device))
         if status:
             raise PagedKVError("pkv_build_step_tables", status)
 
     def release(self, stream=None):
         if self.release_args is None:
             raise ValueError("these TableCalls were made without release_rows")
-        status = self.lib.pkv_release_blocks(*self.release_args, _stream(stream))
+        status = self.lib.pkv_release_blocks(*self.release_args,
+                                             _stream(stream, self._device))
         if status:
             raise PagedKVError("pkv_release_blocks", status)
 
@@ -590,6 +612,7 @@ class StepCalls:
         self.lib = load()
         self._opts = _options(decode_splits, None, shared_prefix,
                               _scores(q, softcap, alibi_slopes, key_begin, key_end))
+        self._device = _scored_device(q, self._opts)
         self.slot_args = (
             _ptr(slot_mapping), _ptr(block_table), block_table.shape[1], _ptr(query_start_loc),
             _ptr(num_computed_tokens), num_computed_tokens.shape[0], slot_mapping.shape[0],
@@ -638,12 +661,12 @@ class StepCalls:
             raise PagedKVError("pkv_slot_mapping_and_write", status)
 
     def attend(self, stream=None):
-        status = self.lib.pkv_paged_attention(*self.attn_args, _stream(stream))
+        status = self.lib.pkv_paged_attention(*self.attn_args, _stream(stream, self._device))
         if status:
             raise PagedKVError("pkv_paged_attention", status)
 
     def run(self, stream=None):
-        st = _stream(stream)
+        st = _stream(stream, self._device)
         lib = self.lib
         if self.write_in_attention:
             status = lib.pkv_paged_attention_with_write(*self.attn_write_args, st)

@@ -200,3 +200,36 @@ def test_the_kernels_counting_in_any_order(seed):
                              np.random.default_rng(k).permutation(n))
         for name in want:
             assert np.array_equal(got[name], want[name]), name
+
+
+def test_calls_refuse_tensors_of_another_device(monkeypatch):
+    """The library launches on the current device: table calls and scored
+    attention name the device of their tensors, and a stream is made for no other."""
+    from types import SimpleNamespace
+
+    import torch
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0x40 + i, raising=False)
+    assert binding._stream(None).value == 0x40 and binding._stream(None, 0).value == 0x40
+    with pytest.raises(ValueError, match="current device"):
+        binding._stream(None, 1)
+    for index, device, fine in ((0, 0, True), (1, 1, False), (1, 0, False), (0, 1, False)):
+        stream = SimpleNamespace(cuda_stream=0x80, device=torch.device("cuda", index))
+        assert binding._stream(stream).value == 0x80  # plain calls, as ever
+        if fine:
+            assert binding._stream(stream, device).value == 0x80
+        else:
+            with pytest.raises(ValueError, match="current device"):
+                binding._stream(stream, device)
+    # which calls check: those with scores, whatever their other options
+    q = SimpleNamespace(device=torch.device("cuda", 1))
+    assert binding._scored_device(q, None) is None
+    assert binding._scored_device(q, binding._options(4)) is None
+    assert binding._scored_device(q, binding._options(4, None, None, binding.pkv_score_options())) == 1
+    calls = binding.TableCalls.__new__(binding.TableCalls)
+    calls.build_args = calls.release_args = ()
+    calls._device = 1
+    calls.lib = None
+    for call in (calls.build, calls.release):
+        with pytest.raises(ValueError, match="current device"):
+            call()
