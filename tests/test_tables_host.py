@@ -229,7 +229,7 @@ def test_calls_refuse_tensors_of_another_device(monkeypatch):
     calls = binding.TableCalls.__new__(binding.TableCalls)
     calls.build_args = calls.release_args = ()
     calls._device = 1
-    calls.lib = None
+    calls.lib = SimpleNamespace(pkv_build_step_tables=None, pkv_release_blocks=None)  # never reached
     for call in (calls.build, calls.release):
         with pytest.raises(ValueError, match="current device"):
             call()
