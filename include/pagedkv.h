@@ -110,6 +110,10 @@ typedef struct pkv_cache_layout {
  * The cache blocks in front of a row's (or a tile of rows') first key and
  * behind its last one are not read: their table entries may be stale or -1.
  * Masked keys never reach the output, whatever their K and V rows hold.
+ * With a softcap up to 51 and no slopes, requests of several new tokens are
+ * summed without a maximum taken off the scores: where all scores of a row lie
+ * at the cap, values above 2^32 in size may overflow, and those below 2^-30
+ * are accurate to 2^-50 absolute only.
  * Every field is off at zero. The pages name no such scores; the entry points
  * are those of plain attention (pkv_attention_options). */
 typedef struct pkv_score_options {

@@ -350,9 +350,12 @@ constexpr double kCapPoly[5] = {9.999989943e-01, -3.332537196e-01, 1.323056551e-
 constexpr float kCapRatioMin = 1e-4f, kCapRatioMax = 1e4f;
 // A capped score is at most softcap in size, so 2^score needs no maximum
 // taken off it while softcap * log2(e) stays far below fp32's and bf16's
-// exponent range: 2^+-90 leaves 2^37 for the sums over keys. A wider cap
-// takes the biased instance (without slopes), which keeps the maximum.
-constexpr float kCapFixedMax = 90.f;
+// exponent range. 74 covers softcap = 50 (72.1), and even where every score
+// of a row lies at the cap, 2^+-74 leaves 2^53 above for the sum over 2^20
+// keys of values up to 2^32, and 2^52 below for values down to 2^-30 with 22
+// bits to spare. A wider cap takes the biased instance (without slopes),
+// which keeps the maximum.
+constexpr float kCapFixedMax = 74.f;
 
 
 // One work item: (request, 128-row query tile, kv head).

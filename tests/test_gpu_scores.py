@@ -424,3 +424,32 @@ def test_runs_are_bit_identical_and_off_means_plain():
     same = run(step, key_begin=np.full_like(p, -5), key_end=p + 1)
     _, _, ref = oracle_step(step)
     assert np.abs(bits_to_f64(same.out_host()) - ref).max() <= 2e-2
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("softcap,up,down", [(51.0, 32, -30), (60.0, 100, -90)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_and_small_values_under_scores_at_the_cap(d, softcap, up, down, sign):
+    """Every score at +softcap or -softcap, V times a power of two: nothing
+    overflows or underflows, so the output is the same power of two times the
+    output for V of ordinary size, bit for bit."""
+    step = make_step(batch(3), num_q_heads=8, num_kv_heads=2, head_dim=d, seed=8)
+    step.q[...] = 0x40C0                                # 6
+    bits = np.uint16(0x40C0 if sign > 0 else 0xC0C0)    # +-6: |x| >= 288, tanh(x / cap) = +-1
+    step.k[...] = bits
+    step.kv_cache[:, 0] = bits
+
+    def times(v, k):  # bf16 bits times 2^k (tiny ones to zero)
+        e = (v >> 7) & 0xFF
+        return np.where((e > 110) & (e < 140), v.astype(np.int32) + k * 128, 0).astype(np.uint16)
+
+    v0, pool0 = step.v.copy(), step.kv_cache[:, 1].copy()
+    outs = {}
+    for k in (0, up, down):
+        step.v[...] = times(v0, k)
+        step.kv_cache[:, 1] = times(pool0, k)
+        outs[k] = run(step, softcap=softcap).out_host()
+        assert_within(outs[k], *expected(step, softcap=softcap), f"2^{k}")
+    f0 = bits_to_f64(outs[0])
+    for k in (up, down):
+        assert np.array_equal(bits_to_f64(outs[k]), np.ldexp(f0, k))
