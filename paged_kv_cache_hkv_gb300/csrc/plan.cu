@@ -58,6 +58,16 @@ __device__ __forceinline__ Int3 block_exclusive_scan(Int3 v, Int3* total) {
   return Int3{base.a + inc.a - v.a, base.b + inc.b - v.b, base.c + inc.c - v.c};
 }
 
+// Whether request r (rows q0 .. q1-1, L keys, c of them cached) has inconsistent
+// lengths or more keys than its table has entries for: it streams nothing, is in
+// no work item and has no row written, as a member of a shared-prefix run too.
+__device__ __forceinline__ bool lengths_bad(const AttnArgs& a, int r, int q0, int q1, int c, int L) {
+  const long long n = static_cast<long long>(q1) - q0;
+  if (n < 0 || q0 < 0 || q1 > a.num_tokens || c < 0 || L != c + n || (r == 0 && q0 != 0)) return true;
+  const long long nent = (static_cast<long long>(L) + (1 << a.block_shift) - 1) >> a.block_shift;
+  return n > 0 && nent > a.max_blocks;
+}
+
 // Counts of one request: decode 16-key chunks, is-prefill, prefill work items.
 // A decode request that takes its shared prefix from the shared items
 // streams only the chunks past the prefix.
@@ -68,11 +78,8 @@ __device__ __forceinline__ Int3 plan_counts(const AttnArgs& a, const AttnWorkspa
   Int3 v{0, 0, 0};
   const int q0 = __ldg(a.qsl + r), q1 = __ldg(a.qsl + r + 1);
   const int n = q1 - q0, L = __ldg(a.seq_lens + r), c = __ldg(a.num_computed + r);
-  bool bad = n < 0 || q0 < 0 || q1 > a.num_tokens || c < 0 || L != c + n || (r == 0 && q0 != 0);
   const long long nblk = (static_cast<long long>(L) + kChunkKeys - 1) / kChunkKeys;
-  const long long nent = (static_cast<long long>(L) + (1 << a.block_shift) - 1) >> a.block_shift;
-  if (!bad && n > 0 && nent > a.max_blocks) bad = true;
-  if (bad) {
+  if (lengths_bad(a, r, q0, q1, c, L)) {
     if (flag) atomicOr(&g_errors_plan, kErrLengths);
   } else if (n == 1) {
     v.a = static_cast<int>(nblk);
@@ -98,7 +105,7 @@ __device__ __forceinline__ Int3 plan_counts(const AttnArgs& a, const AttnWorkspa
 // The shared-prefix hint, checked: every request of the run starts as a
 // member; one whose table does not begin with the run's first request's
 // entries, whose context does not reach past the prefix or whose lengths are
-// inconsistent drops out (it is attended without the hint); one with other than a single new token turns
+// bad (lengths_bad) drops out; one with other than a single new token turns
 // the whole run off. Returns the number of shared-prefix work items.
 __device__ int plan_shared(const AttnArgs& a, const AttnWorkspace& ws, int tile_q) {
   __shared__ int run_off, dropped;
@@ -113,9 +120,10 @@ __device__ int plan_shared(const AttnArgs& a, const AttnWorkspace& ws, int tile_
     const int r = a.shared_first + i;
     const int q0 = __ldg(a.qsl + r), q1 = __ldg(a.qsl + r + 1), L = __ldg(a.seq_lens + r);
     if (q1 - q0 != 1) run_off = 1;
-    // (a request with inconsistent lengths streams nothing and has no row to
-    // write: as a member its merge would write one all the same)
-    if (L <= a.shared_len || L != __ldg(a.num_computed + r) + 1 || q0 < 0 || q1 > a.num_tokens) {
+    // (a member's merge reads the partials of at least one chunk of its own and
+    // writes its row: every member is a request that plan_counts counts as a
+    // decode)
+    if (L <= a.shared_len || lengths_bad(a, r, q0, q1, __ldg(a.num_computed + r), L)) {
       ws.casc_use[i] = 0;
       dropped = 1;
     }
