@@ -732,6 +732,10 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
   int pend_lo = 0, pend_hi = 0;
   long long pend_bt = 0;
   float pend_max = 0.f, pend_sum = 0.f;
+  auto epilogue_wait = [&](int it, uint32_t Tl) -> bool {
+    return wait_small(&sh.o_full, it & 1u, abort_flag) &&
+           wait_small(&sh.p_ready[Tl % kSBufs], (Tl / kSBufs) & 1u, abort_flag);
+  };
   auto epilogue_load = [&](int it, uint32_t Tl, uint32_t (&o)[NQ][32], int& n_bad) -> bool {
     // the item's bad keys are complete once every thread has published P of
     // its last tile Tl. Five lists: when a thread is here in item it's
@@ -739,8 +743,7 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
     // storing item it - 1 or filling the lists of the two items after it; no
     // thread uses that of item it - 2 any more, and none fills it again (as
     // item it + 3's) before all have passed here.
-    if (!wait_small(&sh.o_full, it & 1u, abort_flag)) return false;
-    if (!wait_small(&sh.p_ready[Tl % kSBufs], (Tl / kSBufs) & 1u, abort_flag)) return false;
+    if (!epilogue_wait(it, Tl)) return false;
     n_bad = *reinterpret_cast<volatile int*>(&bad_lists[it % kBadLists].count);
     if (tid == 0) bad_lists[(it + 3) % kBadLists].count = 0;
     tc::fence_after_sync();
@@ -1064,11 +1067,11 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
       } else {
         uint32_t o[NQ][32];
         int n_bad = 0;
-        // (warps that hold no O wait all the same: the bad-key lists and row sums
-        // are reused on the strength of it)
-        if (has_o ? !epilogue_load(it - 1, T - 1, o, n_bad)
-                  : !wait_small(&sh.o_full, (it - 1) & 1u, abort_flag))
-          return;
+        // warps that hold no O wait all the same: what they add to the bad-key
+        // lists and the row sums has to come after the other warps' reads and
+        // after thread 0's emptying of the list. p_ready, on which every thread
+        // has arrived, orders that; o_full, a commit, only the tensor core's work.
+        if (has_o ? !epilogue_load(it - 1, T - 1, o, n_bad) : !epilogue_wait(it - 1, T - 1)) return;
         tc::fence_before_sync();
         mbar_arrive(&sh.p_ready[b]);
         if (has_o) epilogue_store(it - 1, o, n_bad);
