@@ -30,6 +30,7 @@
 //
 // Every wait is bounded; on a timeout the kernel records
 // PKV_DEVERR_TIMEOUT, drains its copies, frees TMEM and returns.
+#include <cfloat>
 #include <type_traits>
 
 #include "common.cuh"
@@ -345,8 +346,11 @@ struct ScoredParams : PrefillParams {
 constexpr float kCapLim = 0.8f;
 constexpr double kCapPoly[5] = {9.999989943e-01, -3.332537196e-01, 1.323056551e-01,
                                 -4.918014086e-02, 1.210013789e-02};
-// The factors above stay normal fp32 numbers, and w^4 finite, for
-// scale / softcap in this range (0.125 / 15 to 0.09 / 1000 in practice).
+// For scale / softcap in this range (0.125 / 15 to 0.09 / 800 in practice) S^2
+// is a normal fp32 number wherever u matters. The coefficients also carry
+// softcap * log2(e), and leave fp32 at large caps all the same (softcap 1e5
+// under a scale of 1e9): cap_coefficients then says no, and every tile takes
+// the exact form.
 constexpr float kCapRatioMin = 1e-4f, kCapRatioMax = 1e4f;
 // A capped score is at most softcap in size, so 2^score needs no maximum
 // taken off it while softcap * log2(e) stays far below fp32's and bf16's
@@ -1652,6 +1656,22 @@ static cudaError_t launch_prefill_t(const ScoredParams& p, const CUtensorMap& kv
                       q_map, p);
 }
 
+// kCapPoly in terms of S = u / ratio and base-2 scores; false (and zeros) where
+// that is not to be used: ratio outside its range, or a coefficient that is not
+// a normal fp32 number.
+static bool cap_coefficients(float softcap, float ratio, float (&out)[5]) {
+  bool ok = ratio >= kCapRatioMin && ratio <= kCapRatioMax;
+  double f = static_cast<double>(softcap) * kLog2e * ratio;
+  for (int i = 0; i < 5; ++i, f *= static_cast<double>(ratio) * ratio) {
+    const double c = kCapPoly[i] * f, size = c < 0 ? -c : c;
+    ok = ok && size >= FLT_MIN && size <= FLT_MAX;
+    out[i] = ok ? static_cast<float>(c) : 0.f;
+  }
+  if (!ok)
+    for (float& c : out) c = 0.f;
+  return ok;
+}
+
 cudaError_t launch_prefill(const AttnArgs& a, const AttnWorkspace& ws, const CUtensorMap& kv_map,
                            const CUtensorMap& q_map, int num_sms, cudaStream_t stream) {
   ScoredParams p;
@@ -1673,11 +1693,8 @@ cudaError_t launch_prefill(const AttnArgs& a, const AttnWorkspace& ws, const CUt
   p.cap_z = a.score.softcap > 0.f ? 2.f * kLog2e * (a.scale / a.score.softcap) : 0.f;
   p.out32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
   const float ratio = a.score.softcap > 0.f ? a.scale / a.score.softcap : 0.f;
-  const bool poly = ratio >= kCapRatioMin && ratio <= kCapRatioMax;
+  const bool poly = cap_coefficients(a.score.softcap, ratio, p.cap_a);
   p.cap_lim2 = poly ? (kCapLim / ratio) * (kCapLim / ratio) : -1.f;
-  double pw = static_cast<double>(a.score.softcap) * kLog2e * ratio;
-  for (int i = 0; i < 5; ++i, pw *= static_cast<double>(ratio) * ratio)
-    p.cap_a[i] = poly ? static_cast<float>(kCapPoly[i] * pw) : 0.f;
   const bool wide_cap = a.score.softcap * kLog2e > kCapFixedMax;
   p.hdr = ws.hdr;
   p.pf_req = ws.pf_req;

@@ -1,0 +1,55 @@
+"""Scored attention on the GPU at the ends of what its options accept: caps and
+scales whose products leave fp32."""
+
+import numpy as np
+import pytest
+
+from score_cases import batch, slopes_of
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - CPU containers
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+from paged_kv_cache_hkv_gb300 import binding  # noqa: E402
+from paged_kv_cache_hkv_gb300.synth import make_step  # noqa: E402
+from test_gpu_scores import assert_within, expected, run  # noqa: E402
+
+
+@pytest.fixture(autouse=True)
+def _clear_errors():
+    binding.pkv_get_device_errors(clear=True)
+    yield
+
+
+def times_power(bits, k):
+    """bf16 bit patterns times 2^k (zeros stay)."""
+    e = (bits >> 7) & 0xFF
+    assert ((e == 0) | ((e.astype(int) + k > 0) & (e.astype(int) + k < 255))).all()
+    return np.where(e == 0, bits, bits.astype(np.int32) + k * 128).astype(np.uint16)
+
+
+# softcap, scale, power of two on q. The products of softcap and the powers of
+# scale / softcap overflow fp32 in the first three and are subnormal in the
+# fourth; the others are the corners of the accepted range.
+EXTREMES = [(2e4, 2e8, -27), (1e5, 1e9, -30), (1e26, 1e28, -93), (0.5, 5.1e-5, 9),
+            (1e30, 1e30, -100), (5e29, 1.0, 0), (1.0, 1e-30, 0), (1e-29, 1.0, 0), (1.0, 1e30, -100)]
+
+
+@pytest.mark.parametrize("alibi", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("softcap,scale,power", EXTREMES)
+def test_caps_and_scales_whose_products_leave_fp32(softcap, scale, power, d, alibi):
+    """With q times 2^power the scores are of ordinary size (or the cap makes
+    them small), so the oracle's bound is as tight as ever; rows of zeros in q
+    and k give scores of exactly 0."""
+    step = make_step(batch(2), num_q_heads=8, num_kv_heads=2, head_dim=d, seed=d, scale=scale)
+    step.q[...] = times_power(step.q, power)
+    step.q[3::7] = 0
+    step.k[5::9] = 0
+    scores = dict(softcap=softcap)
+    if alibi:
+        scores["alibi_slopes"] = slopes_of(8)
+    assert_within(run(step, **scores).out_host(), *expected(step, **scores))
