@@ -1,5 +1,5 @@
 """Scored attention on the GPU at the ends of what its options accept: caps and
-scales whose products leave fp32."""
+scales whose products leave fp32, caps too wide for a fixed maximum."""
 
 import numpy as np
 import pytest
@@ -52,4 +52,20 @@ def test_caps_and_scales_whose_products_leave_fp32(softcap, scale, power, d, ali
     scores = dict(softcap=softcap)
     if alibi:
         scores["alibi_slopes"] = slopes_of(8)
+    assert_within(run(step, **scores).out_host(), *expected(step, **scores))
+
+
+@pytest.mark.parametrize("power", [0, 5])
+@pytest.mark.parametrize("softcap", [52.0, 60.0, 500.0, 880.0])
+@pytest.mark.parametrize("d", [64, 128])
+def test_caps_that_keep_the_running_maximum(d, softcap, power):
+    """Caps above 51 without slopes: every score within the polynomial's range
+    (power 0), or some tiles beyond it and some not (q of every other request
+    times 32: a score's deviation is 48)."""
+    step = make_step(batch(4), num_q_heads=8, num_kv_heads=4, head_dim=d, seed=d + 1,
+                     scale=1.5 / d ** 0.5)
+    for r in range(0, step.num_reqs, 2):
+        rows = slice(step.query_start_loc[r], step.query_start_loc[r + 1])
+        step.q[rows] = times_power(step.q[rows], power)
+    scores = dict(softcap=softcap)
     assert_within(run(step, **scores).out_host(), *expected(step, **scores))
