@@ -119,7 +119,11 @@ typedef struct pkv_cache_layout {
 typedef struct pkv_score_options {
   float softcap;             /* 0 = off, else softcap and scale / softcap both in
                                 [1e-30, 1e30] (else PKV_ERR_BAD_SHAPE)          */
-  const float* alibi_slopes; /* device fp32 [num_q_heads], finite; NULL = off   */
+  const float* alibi_slopes; /* device fp32 [num_q_heads], finite; NULL = off.
+                                Sizes above 1e28 count as 1e28. The bias is an
+                                fp32 number: 2^-24 of slope * distance is its
+                                rounding, which matters where the farthest keys
+                                weigh most (negative slopes)                    */
   const int32_t* key_begin;  /* device int32 [num_tokens]; NULL = 0; values
                                 below 0 count as 0                              */
   const int32_t* key_end;    /* device int32 [num_tokens]; NULL = p + 1; values

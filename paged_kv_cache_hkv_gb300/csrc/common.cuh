@@ -279,6 +279,15 @@ struct ScoreParams {
   const int32_t* key_end;    // past the last key of each query row, or null (p + 1)
 };
 
+// Bias per key of distance of q head h for base-2 scores, 0 without slopes.
+// Slopes beyond +-kMaxSlope count as that: times log2(e) and a distance below
+// 2^31 the bias stays finite (3e37), where an infinite one times the nearest
+// key's distance 0, or minus a row's infinite maximum, would be a NaN.
+constexpr float kMaxSlope = 1e28f;
+__device__ __forceinline__ float slope_log2(const ScoreParams& s, int h) {
+  return s.slopes ? fminf(fmaxf(__ldg(s.slopes + h), -kMaxSlope), kMaxSlope) * kLog2e : 0.f;
+}
+
 // Keys [lo, hi) that a row sees; lo == hi == 0 for a row that sees none.
 struct KeyRange {
   int lo, hi;

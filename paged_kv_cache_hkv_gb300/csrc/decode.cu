@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kDecodeThreads)
   float m_run = -INFINITY, l_run = 0.f;  // for head hm of this lane
   const uint32_t RS = lay.row_bytes;    // bytes between stage rows
   // SCORED: bias per key of distance and cap, both for base-2 scores
-  const float slope2 = SCORED && p.score.slopes ? __ldg(p.score.slopes + vg * GW + hm) * kLog2e : 0.f;
+  const float slope2 = SCORED ? slope_log2(p.score, vg * GW + hm) : 0.f;
   const float cap2 = SCORED ? p.score.softcap * kLog2e : 0.f;
 
   for (uint32_t s = 0, fph = 0;;) {  // ring slot, parity of its full barrier

@@ -841,8 +841,7 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
     float m_run = FIXED ? 0.f : -INFINITY, l_run = 0.f;
     const bool no_row = m.i0 + (row >> gsh) >= m.n;  // behind the request's rows
     // bias per key of distance, base-2 scores
-    const float slope2 =
-        BIAS && p.score.slopes ? __ldg(p.score.slopes + m.g * G + (row & (G - 1))) * kLog2e : 0.f;
+    const float slope2 = BIAS ? slope_log2(p.score, m.g * G + (row & (G - 1))) : 0.f;
 #pragma unroll 1
     for (int kt = 0; kt < nkv; ++kt) {
       const uint32_t Tg = T + kt;
