@@ -838,8 +838,11 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
     const int nkv = m.nkv;
     int item_n = -1;
     RowRaw raw_n{0, 0, 0};
-    float m_run = FIXED ? 0.f : -INFINITY, l_run = 0.f;
     const bool no_row = m.i0 + (row >> gsh) >= m.n;  // behind the request's rows
+    // A row behind the request's holds another request's q, and its threads
+    // store nothing. From an infinite maximum on it asks for no rescale, which
+    // would move the maxima, and with them the roundings, of its warp's rows.
+    float m_run = FIXED ? 0.f : no_row ? INFINITY : -INFINITY, l_run = 0.f;
     // bias per key of distance, base-2 scores
     const float slope2 = BIAS ? slope_log2(p.score, m.g * G + (row & (G - 1))) : 0.f;
 #pragma unroll 1
