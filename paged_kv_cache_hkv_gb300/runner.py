@@ -91,7 +91,7 @@ class DeviceStep:
                                                       shared_prefix=shared_prefix)
         self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
         self._calls = None
-        self._calls_bufs = ()
+        self._calls_bufs, self._calls_settings = (), None
 
     # -- the three calls of the hot path
     def slot_map(self, stream=None):
@@ -135,10 +135,15 @@ class DeviceStep:
 
     def calls(self) -> "binding.StepCalls":
         """The step's three calls with their arguments marshalled (rebuilt
-        when a buffer was replaced)."""
+        when a buffer, a score tensor, the cap or one of the step's settings was
+        replaced)."""
         bufs = (self.slot_mapping, self.block_table, self.query_start_loc, self.num_computed,
-                self.kv_cache, self.k, self.v, self.out, self.q, self.seq_lens, self.workspace)
-        if self._calls is None or any(a is not b for a, b in zip(bufs, self._calls_bufs)):
+                self.kv_cache, self.k, self.v, self.out, self.q, self.seq_lens, self.workspace,
+                *(self.scores[n] for n in ("alibi_slopes", "key_begin", "key_end")))
+        settings = (self.scores["softcap"], self.decode_splits, self.shared_prefix,
+                    self.fused_write, self.write_in_attention)
+        if (self._calls is None or settings != self._calls_settings or
+                any(a is not b for a, b in zip(bufs, self._calls_bufs))):
             s = self.step
             self._calls = binding.StepCalls(
                 slot_mapping=self.slot_mapping, block_table=self.block_table,
@@ -149,7 +154,7 @@ class DeviceStep:
                 decode_splits=self.decode_splits, shared_prefix=self.shared_prefix,
                 fused_write=self.fused_write, write_in_attention=self.write_in_attention,
                 **self.scores)
-            self._calls_bufs = bufs
+            self._calls_bufs, self._calls_settings = bufs, settings
         return self._calls
 
     # -- host copies
