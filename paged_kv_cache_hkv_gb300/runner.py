@@ -7,6 +7,8 @@ the smoke check and the benchmark drive.
 
 from __future__ import annotations
 
+import operator
+
 import numpy as np
 import torch
 
@@ -137,13 +139,13 @@ class DeviceStep:
         """The step's three calls with their arguments marshalled (rebuilt
         when a buffer, a score tensor, the cap or one of the step's settings was
         replaced)."""
+        sc = self.scores
         bufs = (self.slot_mapping, self.block_table, self.query_start_loc, self.num_computed,
                 self.kv_cache, self.k, self.v, self.out, self.q, self.seq_lens, self.workspace,
-                *(self.scores[n] for n in ("alibi_slopes", "key_begin", "key_end")))
-        settings = (self.scores["softcap"], self.decode_splits, self.shared_prefix,
-                    self.fused_write, self.write_in_attention)
-        if (self._calls is None or settings != self._calls_settings or
-                any(a is not b for a, b in zip(bufs, self._calls_bufs))):
+                sc["alibi_slopes"], sc["key_begin"], sc["key_end"])
+        settings = (sc["softcap"], self.decode_splits, self.shared_prefix, self.fused_write,
+                    self.write_in_attention)
+        if settings != self._calls_settings or not all(map(operator.is_, bufs, self._calls_bufs)):
             s = self.step
             self._calls = binding.StepCalls(
                 slot_mapping=self.slot_mapping, block_table=self.block_table,
