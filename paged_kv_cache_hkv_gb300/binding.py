@@ -252,9 +252,13 @@ def _one_device(first, *tensors):
             raise ValueError(f"tensors on {first.device} and {t.device} in one call")
 
 
-def _scored_device(q, options):
-    """Device index to check a call's stream against: scored calls only."""
-    return q.device.index if options is not None and options.contents.scores else None
+def _scored_device(q, options, *tensors):
+    """Device index to check a call's stream against, its other tensors being on
+    q's device: scored calls only."""
+    if options is None or not options.contents.scores:
+        return None
+    _one_device(q, *tensors)
+    return q.device.index
 
 
 def _scores(q, softcap, alibi_slopes, key_begin, key_end):
@@ -341,12 +345,14 @@ def pkv_paged_attention(out, q, kv_cache, block_table, seq_lens, query_start_loc
     lay = layout_of(kv_cache)
     options = _options(decode_splits, trace_events, shared_prefix,
                        _scores(q, softcap, alibi_slopes, key_begin, key_end))
+    device = _scored_device(q, options, out, kv_cache, block_table, seq_lens, query_start_loc,
+                            num_computed_tokens, workspace)
     _check("pkv_paged_attention", load().pkv_paged_attention(
         _ptr(out), _ptr(q), q.stride(0), _ptr(kv_cache), _ptr(block_table),
         block_table.shape[1], _ptr(seq_lens), _ptr(query_start_loc), _ptr(num_computed_tokens),
         seq_lens.shape[0], q.shape[0], int(max_query_len), int(max_seq_len), q.shape[1],
         float(scale), lay, _ptr(workspace), workspace.numel() * workspace.element_size(),
-        options, _stream(stream, _scored_device(q, options))))
+        options, _stream(stream, device)))
     return out
 
 
@@ -379,13 +385,15 @@ def pkv_paged_attention_with_write(out, q, kv_cache, key, value, block_table, se
     lay = layout_of(kv_cache)
     options = _options(decode_splits, trace_events, shared_prefix,
                        _scores(q, softcap, alibi_slopes, key_begin, key_end))
+    device = _scored_device(q, options, out, kv_cache, key, value, block_table, seq_lens,
+                            query_start_loc, num_computed_tokens, workspace, slot_mapping)
     _check("pkv_paged_attention_with_write", load().pkv_paged_attention_with_write(
         _ptr(out), _ptr(q), q.stride(0), _ptr(kv_cache), _ptr(key), _ptr(value), key.stride(0),
         value.stride(0), _ptr(slot_mapping), _ptr(block_table), block_table.shape[1],
         _ptr(seq_lens), _ptr(query_start_loc), _ptr(num_computed_tokens), seq_lens.shape[0],
         q.shape[0], int(max_query_len), int(max_seq_len), q.shape[1], float(scale), lay,
         _ptr(workspace), workspace.numel() * workspace.element_size(),
-        options, _stream(stream, _scored_device(q, options))))
+        options, _stream(stream, device)))
     return out
 
 
@@ -418,12 +426,14 @@ def pkv_paged_attention_static_workspace(out, q, kv_cache, block_table, seq_lens
         raise ValueError("q must be [T, Hq, D] with contiguous rows")
     options = _options(decode_splits, None, shared_prefix,
                        _scores(q, softcap, alibi_slopes, key_begin, key_end))
+    device = _scored_device(q, options, out, kv_cache, block_table, seq_lens, query_start_loc,
+                            num_computed_tokens)
     _check("pkv_paged_attention_static_workspace", load().pkv_paged_attention_static_workspace(
         _ptr(out), _ptr(q), q.stride(0), _ptr(kv_cache), _ptr(block_table),
         block_table.shape[1], _ptr(seq_lens), _ptr(query_start_loc), _ptr(num_computed_tokens),
         seq_lens.shape[0], q.shape[0], int(max_query_len), int(max_seq_len), q.shape[1],
         float(scale), layout_of(kv_cache), options,
-        _stream(stream, _scored_device(q, options))))
+        _stream(stream, device)))
     return out
 
 
@@ -612,7 +622,9 @@ class StepCalls:
         self.lib = load()
         self._opts = _options(decode_splits, None, shared_prefix,
                               _scores(q, softcap, alibi_slopes, key_begin, key_end))
-        self._device = _scored_device(q, self._opts)
+        self._device = _scored_device(q, self._opts, out, kv_cache, key, value, block_table,
+                                      seq_lens, query_start_loc, num_computed_tokens, workspace,
+                                      slot_mapping)
         self.slot_args = (
             _ptr(slot_mapping), _ptr(block_table), block_table.shape[1], _ptr(query_start_loc),
             _ptr(num_computed_tokens), num_computed_tokens.shape[0], slot_mapping.shape[0],
