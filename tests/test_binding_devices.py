@@ -1,5 +1,6 @@
 """Which tensors the scored attention calls look at before they launch on the
-current device, without a GPU: stand-ins for tensors and for the library."""
+current device, and where the stream comes from, without a GPU: stand-ins for
+tensors and for the library."""
 
 import pytest
 
@@ -102,3 +103,13 @@ def test_every_tensor_of_a_scored_call_is_on_one_device(library, name):
     a["kv_cache"].device = torch.device("cuda", 1)
     call(**a, **sizes)
     assert len(library) == 2
+
+
+def test_the_current_stream_without_torchs_private_call(monkeypatch):
+    from types import SimpleNamespace
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 2)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: SimpleNamespace(cuda_stream=0x70 + d))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0x40 + i, raising=False)
+    assert binding._stream(None).value == 0x42
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    assert binding._stream(None).value == 0x72 and binding._stream(None, 2).value == 0x72
