@@ -510,7 +510,10 @@ int32_t pkv_build_step_tables(int32_t* block_table, int32_t max_blocks_per_req,
  *                  may share blocks; a row may stand in it as often as its
  *                  blocks are held.
  * release_tokens   device int32 [num_reqs]: tokens whose blocks row r holds,
- *                  ceil(release_tokens[r] / B) entries.
+ *                  ceil(release_tokens[r] / B) entries. After
+ *                  pkv_build_step_tables that is seq_lens[r], but
+ *                  num_computed_tokens[r] for a request that got no blocks: its
+ *                  seq_lens is 0, and to release it by that gives nothing back.
  * free_queue       in/out, free_state in, free_state_out out: as in
  *                  pkv_build_step_tables.
  * ref_cnt          in/out, device int32 [num_blocks]: how many rows hold each
