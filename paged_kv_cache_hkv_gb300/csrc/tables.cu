@@ -524,13 +524,19 @@ __global__ void __launch_bounds__(kTableThreads) release_append_kernel(const Rel
 }
 
 // Small releases in one launch of one cluster, its barrier between the
-// phases. The entries of a CTA's share: block ids, kept in shared memory from
-// the first phase on.
-constexpr int kStash = 16 * 1024;
-constexpr int kBatch = 4;  // entries per thread whose loads go out together
+// phases: up to kSmallEntries entries, kPerThread per thread of the largest
+// portable cluster. Their block ids stay in shared memory from the first phase
+// on. 8 rows of some 245 entries take 11.1 us so (2.4 of it the measurement's
+// copy of the counts) and 14.9 in four launches; at 64 rows of 250 the two are
+// even (15.4 us), and a third entry per thread would gain nothing (64 rows of
+// 260: 15.7 in one launch, 15.5 in four).
+constexpr int kMaxCtas = 8;
+constexpr int kPerThread = 2;
+constexpr int kShare = kPerThread * kTableThreads;
+constexpr int kSmallEntries = kMaxCtas * kShare;
 
 __global__ void __launch_bounds__(kTableThreads) release_small_kernel(const ReleaseArgs a) {
-  extern __shared__ int32_t stash[];
+  __shared__ int32_t stash[kShare];
   __shared__ ReleaseRuns v;
   __shared__ int tile_scan[32];
   __shared__ int cta_freed;  // freed blocks of this CTA's share
@@ -545,31 +551,29 @@ __global__ void __launch_bounds__(kTableThreads) release_small_kernel(const Rele
   uint32_t err = 0;
   const int total = scan_runs_released(a, v, &err, state_ok);
 
-  // this CTA's share of the flat entries, in whole tiles of the block; entry
-  // x0 + n is thread n % kTableThreads's (at most kStash entries in all)
+  // this CTA's share of the flat entries, in whole tiles of the block (at most
+  // kPerThread: total <= kSmallEntries, and less than a full cluster is launched
+  // only for one tile per CTA); entry x0 + n is thread n % kTableThreads's
   const int tiles = (total + kTableThreads - 1) / kTableThreads;
   const int x0 = static_cast<int>(static_cast<long long>(tiles) * rank / nctas) * kTableThreads;
   const int x1 = min(total, static_cast<int>(static_cast<long long>(tiles) * (rank + 1) / nctas) *
                                 kTableThreads);
   const int share = max(0, x1 - x0);
 
-  for (int n0 = tid; n0 < share; n0 += kBatch * kTableThreads) {
-    int b[kBatch];
+  int ids[kPerThread];  // the loads of a thread's entries go out together
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int n = n0 + u * kTableThreads;
-      if (n >= share) {
-        b[u] = -1;
-        continue;
-      }
-      b[u] = block_of(a, v, x0 + n);
-      if (b[u] < 0) err |= kErrBlockRange;
-      stash[n] = b[u];
+  for (int u = 0; u < kPerThread; ++u) {
+    const int n = tid + u * kTableThreads;
+    ids[u] = -1;
+    if (n < share) {
+      ids[u] = block_of(a, v, x0 + n);
+      if (ids[u] < 0) err |= kErrBlockRange;
+      stash[n] = ids[u];
     }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u)
-      if (b[u] >= 0) count_down(a, b[u], &err);
   }
+#pragma unroll
+  for (int u = 0; u < kPerThread; ++u)
+    if (ids[u] >= 0) count_down(a, ids[u], &err);
   cluster.sync();
   for (int n = tid; n < share; n += kTableThreads)
     if (stash[n] >= 0) claim_place(a, stash[n], x0 + n);
@@ -621,30 +625,20 @@ __global__ void __launch_bounds__(kTableThreads) release_small_kernel(const Rele
 }
 
 // ------------------------------------------------------------------ host
-// CTAs of the cluster: one per kEntriesPerCta flat entries (one CTA needs no
-// barrier between CTAs), at most kMaxCtas, the portable size.
-constexpr long long kEntriesPerCta = 1024;
-constexpr int kMaxCtas = 8;
-
+// CTAs of the cluster: a power of two, one for each kTableThreads flat entries
+// (one CTA needs no barrier between CTAs) up to kMaxCtas.
 static int cluster_ctas(long long entries) {
   int n = 1;
-  while (n < kMaxCtas && entries > n * kEntriesPerCta) n *= 2;
+  while (n < kMaxCtas && entries > static_cast<long long>(n) * kTableThreads) n *= 2;
   return n;
 }
 
-// Releases of up to this many table entries (rows x table width, an upper
-// bound: the lengths are on the device) are one launch. 8 rows of 245 entries
-// take 9.6 us so, and took 12 in several launches; 64 rows of 252 entries take
-// 11.9 us in one, 64 rows of 260 entries 13.8 us in four.
-constexpr long long kSmallEntries = kStash;
-
 template <typename Args>
-static cudaError_t launch_cluster(void (*kern)(Args), int ctas, size_t smem, cudaStream_t stream,
+static cudaError_t launch_cluster(void (*kern)(Args), int ctas, cudaStream_t stream,
                                   const Args& args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kTableThreads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -692,13 +686,9 @@ cudaError_t launch_release_blocks(const int32_t* block_table, int max_blocks, in
                 static_cast<int>(__builtin_ctz(static_cast<unsigned>(block_size))),
                 nullptr,     nullptr,    nullptr};
   const long long bound = static_cast<long long>(num_released) * max_blocks;
-  if (bound <= kSmallEntries) {
-    static std::atomic<unsigned long long> attr_done{0};
-    const int smem = kStash * static_cast<int>(sizeof(int32_t));
-    cudaError_t e = smem_attr_once(release_small_kernel, smem, attr_done);
-    if (e != cudaSuccess) return e;
-    return launch_cluster(release_small_kernel, cluster_ctas(bound), smem, stream, a);
-  }
+  // (rows x table width, an upper bound: the lengths are on the device)
+  if (bound <= kSmallEntries)
+    return launch_cluster(release_small_kernel, cluster_ctas(bound), stream, a);
   char* ws = static_cast<char*>(workspace);
   const long long tiles = (bound + kTableThreads - 1) / kTableThreads;
   a.state_copy = reinterpret_cast<int32_t*>(ws);
