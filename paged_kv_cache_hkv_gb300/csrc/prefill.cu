@@ -21,7 +21,8 @@
 // tcgen05.ld, applies the causal mask, keeps a base-2 running max (rescaling
 // its half of O in TMEM only when the max grows by more than 2^8) and sum,
 // and writes P as bf16 pairs over the S buffer's columns with tcgen05.st.
-// A K-copy warp (3-slot ring) and a V-copy warp (2-slot ring) stream the
+// A K-copy warp (3-slot ring; the scored instances 2) and a V-copy warp (2-slot
+// ring; 3) stream the
 // tiles by TMA (128-byte swizzle, one copy per cache block and kv head: the
 // fewer and larger the copies, the faster one SM's copy engine goes); one
 // thread issues every S and another every PV. The
@@ -228,8 +229,10 @@ static_assert(kKStages == kSBufs, "K slot T % 3 is freed by the commit of S buff
 constexpr uint32_t kTmemS = 128;  // TMEM columns: O at [0, D), S buffer b at [128 + 128b, +128)
 constexpr uint32_t kTmemCols = 512;
 constexpr int kItemQ = 4;      // claimed work items in flight between the roles
-constexpr int kMaskRing = 8;   // SCORED: tiles whose chunk masks are kept. K(T+8) is copied
-                               // once S(T+5) is done, so PV(T+2): every reader of mask T is through
+// SCORED: tiles whose chunk masks are kept. The K-copy warp writes the mask of
+// T+8 once S(T+6) is done (its ring has two slots), so PV(T+3), so every thread
+// has published P(T+3): each has read the mask of T by then.
+constexpr int kMaskRing = 8;
 constexpr int kMetaReqs = 128;  // prefill requests whose metadata a CTA keeps in shared memory
 constexpr float kRescaleLog2 = 8.f;  // lazy rescale threshold (powers of two)
 // Scores of a kernel instance: plain, or key ranges with or without a cap
@@ -239,9 +242,14 @@ enum : int { kPlain = 0, kRanges = 1, kCap = 2, kBias = 4 };
 // V-copy warp and the PV-MMA warp. A capped instance without a bias keeps no
 // running maximum, so the threads of a row need nothing of one another in a
 // tile: four of them take 32 keys each, and sixteen warps hide one another's
-// latencies where eight left the FMA pipe idle half the time (4 x 2048 rows
-// over 8192 keys: 1003 -> 954 us). The other instances exchange a row's
-// maximum by a shuffle between two threads of one warp.
+// latencies where eight left the FMA pipe idle half the time. 4 x 2048 rows over
+// 8192 keys, D = 128, us with sixteen and with eight warps: softcap 50 (every
+// tile by the polynomial) 914 and 990, 15 (one tile in eight exact) 991 and 1163,
+// 5 (all exact) 1528 and 1798. At D = 64 half of the sixteen hold no column of O
+// and 424 bytes a thread are spilled: 989 and 967, 1072 and 1186, 1531 and 1781,
+// and 8191 rows of short documents 122 and 109. Sixteen there too: a cap is for
+// scores that reach it. The other instances exchange a row's maximum by a
+// shuffle between two threads of one warp.
 template <int SC>
 __host__ __device__ constexpr int softmax_warps() {
   return SC == (kRanges | kCap) ? 16 : 8;
@@ -340,9 +348,9 @@ struct ScoredParams : PrefillParams {
 // scale / softcap and the factor softcap * log2(e) go into the coefficients,
 // so a pair of scores takes six packed FMA-pipe instructions. A warp that holds
 // a larger |u| takes the exact form for its tile: at softcap 50 and N(0, 3^2)
-// scores none does, at 15 one tile in eight. 4 x 2048 rows over 8192 keys take
-// 898 us, 977 so, and 1512 where every tile needs the exact form (plain scores
-// 692; the polynomial's FMA-pipe work is some 300 of the difference).
+// scores none does, at 15 one tile in eight, at 5 all do (914, 991 and 1528 us,
+// see softmax_warps; key ranges alone take 715: the polynomial's FMA-pipe work is
+// most of the difference).
 constexpr float kCapLim = 0.8f;
 constexpr double kCapPoly[5] = {9.999989943e-01, -3.332537196e-01, 1.323056551e-01,
                                 -4.918014086e-02, 1.210013789e-02};
@@ -380,23 +388,26 @@ struct PrefillItem {
 };
 
 // mbarriers. "commit" ones are arrived on by a tcgen05.commit of an MMA thread
-// (S: s_full, q_free, drain[0]; PV: pv_done, o_full, drain[1]).
+// (S: s_full, q_free, drain[0]; PV: pv_done, o_full, drain[1]). NW softmax warps:
+// eight, or sixteen in a capped instance. Rings of KST K and VST V slots: 3 and 2,
+// in the scored instances 2 and 3.
 struct PrefillShared {
   uint64_t q_full;               // Q tile of the item landed (TMA)
   uint64_t q_free;               // commit: the item's last S read Q
-  uint64_t k_full[3];            // K tile landed (TMA); one per slot of the ring
-  uint64_t v_full[3];            // V tile landed (TMA)
-  uint64_t s_full[kSBufs];       // commit: S of the buffer's tile in TMEM (and the
-                                 // K slot of the same index free: both rings have 3)
-  uint64_t pv_done[kSBufs];      // commit: PV of the buffer's tile done (its P read,
-                                 // its V slot free, O updated)
-  uint64_t p_ready[kSBufs];      // 256 arrivals: P of the buffer's tile in TMEM, O
+  uint64_t k_full[3];            // K tile landed (TMA); KST used, one per slot of the ring
+  uint64_t v_full[3];            // V tile landed (TMA); VST used
+  uint64_t s_full[kSBufs];       // commit: S of tile T in TMEM, buffer T % 3, and K slot
+                                 // T % KST read; SCORED: and an arrival of the S thread,
+                                 // behind which the tile's mask is
+  uint64_t pv_done[kSBufs];      // commit: PV of tile T done (P in buffer T % 3 and V slot
+                                 // T % VST read, O updated)
+  uint64_t p_ready[kSBufs];      // 32 NW arrivals: P of the buffer's tile in TMEM, O
                                  // rescaled, V cleaned (and, for an item's first tile,
                                  // the previous item's O read)
   uint64_t o_full;               // commit: the item's last PV done
   uint64_t drain[2];             // commit: every MMA of the S / PV thread done (teardown)
   uint64_t iq_full[kItemQ];      // item id j published in item_q[j % kItemQ]
-  uint64_t iq_free[kItemQ];      // 11 arrivals: every role has read it
+  uint64_t iq_free[kItemQ];      // NW + 3 arrivals: every role has read it
   int item_q[kItemQ];
   PrefillItem item_m[kItemQ];    // SCORED: the item described, for every role
   uint32_t masks[kMaskRing];     // SCORED: chunk mask of tile T in masks[T % kMaskRing]
@@ -1106,23 +1117,24 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
   }
 }
 
-// Persistent CTAs; CTA b takes items b, b + gridDim.x, ... (items come
-// longest first within a request). Every role walks that list on its own and
+// Persistent CTAs; each claims its items from a counter (items come longest
+// first within a request). Every role walks that list on its own and
 // the roles meet only at mbarriers, so the next item's Q/K/V copies and first
-// S MMAs overlap the current item's last tiles and epilogue.
-//   warp 9:  Q copy (once the previous item's last S is done) and K tiles
-//            into a 3-slot ring (a slot is refilled once its S is done);
-//   warp 10: V tiles into a 2-slot ring (refilled once its PV is done);
-//   warp 8, lane 0: every MMA, per item in the order S(0), S(1), S(2),
-//            PV(0), S(3), PV(1), S(4), ...: S(kt) = Q K^T into S buffer
-//            (T+kt) % 3, and O += P V with P read from TMEM, where the
+// S MMAs overlap the current item's last tiles and epilogue. With NW softmax
+// warps (eight; sixteen in a capped instance) and rings of KST K and VST V slots
+// (plain 3 and 2, scored 2 and 3):
+//   warp NW + 1: Q copy (once the previous item's last S is done) and K tiles
+//            (slot T % KST is refilled once S(T) is done);
+//   warp NW + 2: V tiles (slot T % VST is refilled once PV(T) is done);
+//   warp NW, lane 0: every S, S(T) = Q K^T into S buffer T % 3 once PV(T-3)
+//            has read the P that the buffer held;
+//   warp NW + 3, lane 0: every PV, O += P V with P read from TMEM, where the
 //            softmax warps wrote it over the tile's S (bf16 pairs, one pair
-//            per 32-bit column). MMAs run in issue order, so S(kt+3)
-//            overwrites P(kt) only after PV(kt) read it.
-//   warps 0..7: the softmax of every tile, 16 query rows per warp and half
-//            of each row per thread, and the item's epilogue (each thread
-//            normalises and writes half of its row's output columns).
-//   (A capped instance has sixteen softmax warps, and the others behind them.)
+//            per 32-bit column);
+//   warps 0..NW-1: the softmax of every tile and the item's epilogue. Of eight,
+//            each has 16 query rows and half of each row per thread (each thread
+//            normalises and writes half of its row's output columns); of sixteen,
+//            two warps share 16 rows.
 //
 // SCORED (SC other than kPlain): the scores are capped, biased or masked by
 // key ranges (ScoreParams). The K-copy warp finds the keys that an item's rows
@@ -1301,8 +1313,7 @@ __global__ void __launch_bounds__(prefill_threads<SC>(), 1)
       for (int kt = 0; kt < m.nkv; ++kt) {
         const int slot = static_cast<int>(T % S);
         if (T >= static_cast<uint32_t>(S)) {
-          // K slot T % 3 is free once S(T-3) is done; V slot T % 2 once
-          // PV(T-2) is done
+          // the K slot is free once S(T-S) is done, the V slot once PV(T-S) is
           const uint32_t Tp = T - S;
           ok = is_v ? wait_or_abort(&sh.pv_done[Tp % kSBufs], (Tp / kSBufs) & 1u, abort_flag)
                     : wait_or_abort(&sh.s_full[Tp % kSBufs], (Tp / kSBufs) & 1u, abort_flag);
@@ -1360,7 +1371,7 @@ __global__ void __launch_bounds__(prefill_threads<SC>(), 1)
       if (!is_v && q_loads > 0) mbar_wait(&sh.q_full, (q_loads - 1) & 1u, kDrainLimitNs);
     }
   } else if (warp == NW || warp == NW + 3) {
-    // ================= MMA threads: warp 8 issues every S, warp 11 every PV
+    // ================= MMA threads: warp NW issues every S, warp NW + 3 every PV
     if ((tid & 31) == 0) {
       const bool is_s = warp == NW;
       constexpr uint32_t idesc_qk = tc::idesc_bf16(kTileM, kTileN, 0);

@@ -11,10 +11,14 @@
 // Every CTA scans the lengths of all requests for itself (thread i takes the
 // run of requests [i * per, (i + 1) * per)), which costs a few loads per
 // thread and needs no exchange; the prefix sums of the 1024 runs stay in
-// shared memory. Work is then spread evenly over the grid, one very long
-// prompt as evenly as thousands of decodes: whoever gets a place of a flat
-// index (new tokens, released entries) finds its request by a binary search of
-// the runs and a walk through one run.
+// shared memory. Work is then spread over the grid by flat indexes (new tokens
+// of long requests, released entries): whoever gets a place of one finds its
+// request by a binary search of the runs and a walk through one run. One very
+// long prompt is so spread as evenly as thousands of decodes. What is not even:
+// the build's warps take 128 tokens of long requests in a row and find the first
+// one's request only, so a warp whose tokens end one long request and begin the
+// next walks over every request that stands between the two in the batch. With
+// 4000 decodes there a step takes 597 us that takes 9.7 with the prompts in front.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -121,7 +125,10 @@ __device__ __forceinline__ Ask ask_of(const BuildArgs& a, int r) {
 }
 
 // Requests of more new tokens than this are spread over warps, token by
-// token; the others are done by one thread each (a decode is one token).
+// token; the others are done by one thread each (a decode is one token). 512
+// requests of 8 tokens take 5.8 us so and 10.3 spread (limit 2); 512 of 32 take 7.9
+// spread and 15.3 by one thread each (limit 32). kChunkRows: 4096 requests with
+// 102,000 new tokens take 9.7 us with 128, 17.3 with 512 and 7.5 with 32.
 constexpr int kShortRows = 8;
 constexpr int kChunkRows = 128;  // consecutive tokens of long requests per warp and turn
 
