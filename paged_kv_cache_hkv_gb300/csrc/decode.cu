@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(GW * 32) combine_kernel(const DecodeParams p) 
       const float* mine = piece_o(wgt == 0.f || j0 + lane >= npieces ? 0 : j0 + lane);
       // kCombineLoads pieces' loads go out before the first is used. A piece of
       // weight 0 (an empty range, which wrote no partial) reads piece 0's slot
-      // and adds nothing.
+      // and is left out of the sum: 0 times an infinity there would be a NaN.
       for (int i0 = 0; i0 < cnt; i0 += kCombineLoads) {
         float vals[kCombineLoads][E], wj[kCombineLoads];
 #pragma unroll
@@ -743,28 +743,31 @@ __global__ void __launch_bounds__(GW * 32) combine_kernel(const DecodeParams p) 
         }
 #pragma unroll
         for (int i = 0; i < kCombineLoads; ++i)
-          if (i0 + i < cnt) {
+          if (wj[i] != 0.f) {  // (nor is there a piece behind the last)
 #pragma unroll
             for (int e = 0; e < E; ++e) acc[e] += wj[i] * vals[i][e];
           }
       }
     } else {
-      // 8 pieces' loads in flight per lane; a piece of weight 0 (an empty
-      // range, which wrote no partial) reads piece 0's slot and adds nothing
+      // 8 pieces' loads in flight per lane; a piece of weight 0 as above
 #pragma unroll 8
       for (int j = 0; j < cnt; ++j) {
         const float wj = __shfl_sync(0xffffffffu, wgt, j);
         const float* src = piece_o(wj == 0.f ? 0 : j0 + j) + lane * E;
         if constexpr (E == 4) {
           const float4 v = *reinterpret_cast<const float4*>(src);
-          acc[0] += wj * v.x;
-          acc[1] += wj * v.y;
-          acc[2] += wj * v.z;
-          acc[3] += wj * v.w;
+          if (wj != 0.f) {
+            acc[0] += wj * v.x;
+            acc[1] += wj * v.y;
+            acc[2] += wj * v.z;
+            acc[3] += wj * v.w;
+          }
         } else {
           const float2 v = *reinterpret_cast<const float2*>(src);
-          acc[0] += wj * v.x;
-          acc[1] += wj * v.y;
+          if (wj != 0.f) {
+            acc[0] += wj * v.x;
+            acc[1] += wj * v.y;
+          }
         }
       }
     }
