@@ -300,11 +300,12 @@ struct PrefillLayout {
 // of its rows may not see. Weight 0 times such a value is a NaN, so their
 // elements go into the tensor core as zeros and the rows that do see the key
 // get them back in the epilogue.
-constexpr int kMaxBadKeys = 50;
+constexpr int kMaxBadKeys = 48;
 constexpr int kBadLists = 5;
 struct BadKeys {
   int count;  // above kMaxBadKeys: the list is not complete, every key is looked at
-  int key[kMaxBadKeys];
+  int k_lo, kv_len;  // of the item, with the first key
+  int key[kMaxBadKeys];  // (a key once for each thread that found a part of its row bad)
 };
 static_assert(kBadLists * sizeof(BadKeys) <= 1024, "bad key area");
 
@@ -562,20 +563,124 @@ __device__ __forceinline__ bool zero_nonfinite(uint4* v4) {
   return true;
 }
 
-// Add the infinities and NaNs of V elements d0 .. d0+nd-1 of key j to the
-// thread's part of its output row, already stored (bf16, or fp32 partials).
-__device__ __noinline__ void add_nonfinite(const ScoredParams& p, long long bt_row, int g, int D,
-                                           int j, int d0, int nd, uint16_t* out, float* partial) {
-  const int id = __ldg(p.block_table + bt_row + (j >> p.block_shift));
-  if (id < 0 || id >= p.num_blocks) return;
-  const long long r = ((static_cast<long long>(id) * 2 + 1) << p.block_shift) +
-                      (j & ((1 << p.block_shift) - 1));
-  const uint16_t* v = p.pool + (r * p.num_kv_heads + g) * D + d0;
+// Which of up to 64 elements of some V rows are a NaN, +infinity and -infinity,
+// a bit each: their sum with a finite value, whatever the order.
+struct Odd {
+  unsigned long long nan, pos, neg;
+};
+
+__device__ __forceinline__ bool has_nonfinite(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  bool any = false;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    any |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+  return any;
+}
+
+// The V row of key j for kv head g, or null if a used entry of its 16-key chunk
+// is out of the pool (the chunk is masked).
+__device__ __forceinline__ const uint4* v_row_of(const ScoredParams& p, const BadKeys& bad,
+                                                 long long bt_row, int g, int D, int j) {
+  const int bsh = p.block_shift, own = j >> bsh;
+  const int e0 = bsh == 3 ? own & ~1 : own, e1 = bsh == 3 ? own | 1 : own;
+  int id = -1;
+  for (int e = e0; e <= e1; ++e) {
+    if ((e << bsh) >= bad.kv_len || ((e + 1) << bsh) <= bad.k_lo) continue;  // not used
+    const int x = __ldg(p.block_table + bt_row + e);
+    if (x < 0 || x >= p.num_blocks) return nullptr;
+    if (e == own) id = x;
+  }
+  if (id < 0) return nullptr;
+  const long long r = ((static_cast<long long>(id) * 2 + 1) << bsh) + (j & ((1 << bsh) - 1));
+  return reinterpret_cast<const uint4*>(p.pool + (r * p.num_kv_heads + g) * D);
+}
+
+// Of nd elements (at most 64).
+__device__ __forceinline__ Odd odd_of(const uint4* v, int nd) {
+  Odd odd{0, 0, 0};
+#pragma unroll 4
+  for (int x = 0; x < nd / 8; ++x) {
+    const uint4 u = __ldg(v + x);
+    if (!has_nonfinite(u)) continue;
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t b = (w[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+      if ((b & 0x7f80u) != 0x7f80u) continue;
+      const unsigned long long bit = 1ull << (8 * x + e);
+      if (b & 0x7fu)
+        odd.nan |= bit;
+      else if (b & 0x8000u)
+        odd.neg |= bit;
+      else
+        odd.pos |= bit;
+    }
+  }
+  return odd;
+}
+
+// Add the infinities and NaNs of the bad keys that a row sees to the thread's
+// part of the row, already stored (bf16, or fp32 partials): V elements d0 ..
+// d0+nd-1 of keys lo .. hi-1. By a whole warp, whose lanes 0-15 and 16-31 hold nd
+// elements next to each other; `mine`: the thread has a part.
+// A lane looks at one key of the list, or, where the list is not complete, at one
+// of all the keys that the warp's rows see, and hands what it finds to all: the
+// other roles wait meanwhile, and waits are limited. Last keys first: rows full of
+// NaN are mostly a step's own, and end the search. (512 rows whose V is all NaN
+// over 32768 clean keys take 0.44 ms, clean ones 0.41; by every thread key after
+// key it was 93 ms, and over a million keys it would outlast the waits.) Keys of tiles that were not cleaned are found too: adding the same infinity or a NaN
+// once more changes nothing.
+__device__ __noinline__ void restore_nonfinite(const ScoredParams& p, const BadKeys& bad, int count,
+                                               long long bt_row, int g, int D, bool mine, int lo,
+                                               int hi, int d0, int nd, uint16_t* out,
+                                               float* partial) {
+  const int lane = threadIdx.x & 31, half = lane >> 4;
+  const bool sees = mine && lo < hi, listed = count <= kMaxBadKeys;
+  const int first = __reduce_min_sync(0xffffffffu, sees ? lo : 0x7fffffff);
+  const int past = __reduce_max_sync(0xffffffffu, sees ? hi : 0);
+  const unsigned long long whole = nd == 64 ? ~0ull : (1ull << nd) - 1ull;
+  Odd odd{0, 0, 0};
+  for (int left = listed ? count : past - first; left > 0; left -= 32) {
+    const int i = left - 1 - lane;
+    const int j = i < 0 ? -1 : listed ? bad.key[i] : first + i;
+    Odd at[2] = {{0, 0, 0}, {0, 0, 0}};  // what lanes 0-15 and lanes 16-31 hold of key j
+    if (j >= first && j < past) {
+      const uint4* v = v_row_of(p, bad, bt_row, g, D, j);
+      if (v) {
+        v += (d0 - half * nd) / 8;
+        at[0] = odd_of(v, nd);
+        at[1] = odd_of(v + nd / 8, nd);
+      }
+    }
+    const bool any = (at[0].nan | at[0].pos | at[0].neg | at[1].nan | at[1].pos | at[1].neg) != 0;
+    for (uint32_t m = __ballot_sync(0xffffffffu, any); m; m &= m - 1) {
+      const int src = __ffs(m) - 1;
+      const int key = __shfl_sync(0xffffffffu, j, src);
+      Odd o[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        o[h].nan = __shfl_sync(0xffffffffu, at[h].nan, src);
+        o[h].pos = __shfl_sync(0xffffffffu, at[h].pos, src);
+        o[h].neg = __shfl_sync(0xffffffffu, at[h].neg, src);
+      }
+      if (!sees || key < lo || key >= hi) continue;
+      odd.nan |= half ? o[1].nan : o[0].nan;
+      odd.pos |= half ? o[1].pos : o[0].pos;
+      odd.neg |= half ? o[1].neg : o[0].neg;
+    }
+    // nothing more can change where every element is a NaN
+    if (__all_sync(0xffffffffu, !sees || (odd.nan | (odd.pos & odd.neg)) == whole)) break;
+  }
+  if (!sees) return;
 #pragma unroll 1
   for (int x = 0; x < nd; ++x) {
-    const uint32_t b = __ldg(v + x);
-    if ((b & 0x7f80u) != 0x7f80u) continue;
-    const float f = __uint_as_float(b << 16);
+    const unsigned long long bit = 1ull << x;
+    if (!((odd.nan | odd.pos | odd.neg) & bit)) continue;
+    const bool pos = odd.pos & bit, neg = odd.neg & bit;
+    const float f = __uint_as_float((odd.nan & bit) || (pos && neg) ? 0x7fc00000u
+                                    : neg                           ? 0xff800000u
+                                                                    : 0x7f800000u);
     if (partial)
       partial[x] += f;
     else
@@ -826,17 +931,9 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
         }
       }
     }
-    if (!mine) return;
-    if (n_bad > 0) {
-      const BadKeys& bad = bad_lists[it % kBadLists];
-      const bool listed = n_bad <= kMaxBadKeys;
-#pragma unroll 1
-      for (int i = listed ? 0 : pend_lo; i < (listed ? n_bad : pend_hi); ++i) {
-        const int j = listed ? bad.key[i] : i;
-        if (j >= pend_lo && j < pend_hi)
-          add_nonfinite(p, pend_bt, pend_g, D, j, ocol, HC, dst, part);
-      }
-    }
+    if (n_bad > 0)
+      restore_nonfinite(p, bad_lists[it % kBadLists], n_bad, pend_bt, pend_g, D, mine, pend_lo,
+                        pend_hi, ocol, HC, dst, part);
   };
 
   PrefillItem m{};
@@ -1065,6 +1162,10 @@ __device__ __forceinline__ void scored_softmax(const ScoredParams& p, PrefillSha
         } else if (ch < DH && zero_nonfinite<VN>(v4)) {
           BadKeys& bad = reinterpret_cast<BadKeys*>(gbase + Lay::kBad)[it % kBadLists];
           const int i = atomicAdd(&bad.count, 1);
+          if (i == 0) {
+            bad.k_lo = m.k_lo;
+            bad.kv_len = m.kv_len;
+          }
           if (i < kMaxBadKeys) bad.key[i] = ka * kTileN + row;
         }
         fence_proxy_async_smem();
