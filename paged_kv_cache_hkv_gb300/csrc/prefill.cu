@@ -246,7 +246,7 @@ enum : int { kPlain = 0, kRanges = 1, kCap = 2, kBias = 4 };
 // 8192 keys, D = 128, us with sixteen and with eight warps: softcap 50 (every
 // tile by the polynomial) 914 and 990, 15 (one tile in eight exact) 991 and 1163,
 // 5 (all exact) 1528 and 1798. At D = 64 half of the sixteen hold no column of O
-// and 424 bytes a thread are spilled: 989 and 967, 1072 and 1186, 1531 and 1781,
+// and 488 bytes a thread are spilled: 989 and 967, 1072 and 1186, 1531 and 1781,
 // and 8191 rows of short documents 122 and 109. Sixteen there too: a cap is for
 // scores that reach it. The other instances exchange a row's maximum by a
 // shuffle between two threads of one warp.
