@@ -38,9 +38,9 @@
  * queued earlier on the stream is therefore seen as with plain stream order.
  * The write calls (pkv_slot_mapping, pkv_paged_kv_write,
  * pkv_slot_mapping_and_write), the attention calls that take the caller's
- * workspace (pkv_paged_attention, pkv_paged_attention_with_write) and the table
- * calls (pkv_build_step_tables, pkv_release_blocks) can be recorded into a CUDA
- * graph.
+ * workspace (pkv_paged_attention, pkv_paged_attention_with_write), the table
+ * calls (pkv_build_step_tables, pkv_release_blocks) and every pkv_quant_ call that
+ * takes a stream can be recorded into a CUDA graph.
  */
 #ifndef PAGEDKV_H_
 #define PAGEDKV_H_
@@ -85,6 +85,9 @@ extern "C" {
                                        held too few blocks for some request      */
 #define PKV_DEVERR_REF_COUNT 0x40u  /* pkv_release_blocks: a block was released
                                        more often than it was held               */
+#define PKV_DEVERR_CHUNK_KEYS 0x80u /* 8-bit pool: the workspace holds too few
+                                       chunk keys for the step; keys were masked
+                                       out                                       */
 
 /* Shape of the physical pool. */
 typedef struct pkv_cache_layout {
@@ -543,6 +546,126 @@ int32_t pkv_release_blocks(const int32_t* block_table, int32_t max_blocks_per_re
  * device.
  */
 int64_t pkv_release_workspace_size(int32_t num_released, int32_t max_blocks_per_req);
+
+/*
+ * The 8-bit pool
+ * --------------
+ * A pool of half the bytes: K and V rows as e4m3 codes, one scale byte per row.
+ * The pages name no such cache; the entry points are the bf16 pool's, with the
+ * same arguments, error bits and options, and `kv_scales` after `kv_cache`:
+ *   kv_cache [num_blocks][2][block_size][num_kv_heads][head_dim], e4m3 codes,
+ *   kv_scales[num_blocks][2][block_size][num_kv_heads], bytes; both contiguous
+ *   and 16-byte aligned.
+ *   value = code * 2^(scale - 127).
+ * A row is the K (or V) of one token and kv head. With a = its largest magnitude,
+ * e the least integer >= -117 with a <= 448 * 2^e: scale = e + 127, and each code
+ * is the e4m3 number nearest to x * 2^-e, ties to even. So a value is kept to
+ * 2^-4 of its size, or to 2^-10 * 2^e where that is more; every value that a pool
+ * holds is a bf16, and rows read back and written again keep their values. A row
+ * with an infinity or a NaN is held as NaN in all its elements (scale 255).
+ * Scale bytes other than 10 .. 247 and 255, and the NaN code in a row whose scale
+ * is not 255, stand in no row that was written by this library; what attention
+ * makes of them is undefined.
+ * Layout limits are the bf16 pool's.
+ */
+
+/* pkv_quant_kv_write -- pkv_paged_kv_write into the 8-bit pool: quantise each new
+ * token's K and V rows and store them at its slot. Two tokens with the same slot
+ * race: the row then holds undefined codes and scale. */
+int32_t pkv_quant_kv_write(void* kv_cache, uint8_t* kv_scales, const void* key, const void* value,
+                           int64_t key_row_stride, int64_t value_row_stride,
+                           const int64_t* slot_mapping, int32_t num_tokens,
+                           pkv_cache_layout layout, void* stream);
+
+/* pkv_quant_slot_mapping_and_write -- pkv_slot_mapping_and_write into the 8-bit
+ * pool: the slot mapping and the quantised write in one launch. */
+int32_t pkv_quant_slot_mapping_and_write(
+    void* kv_cache, uint8_t* kv_scales, const void* key, const void* value, int64_t key_row_stride,
+    int64_t value_row_stride, int64_t* slot_mapping, const int32_t* block_table,
+    int32_t max_blocks_per_req, const int32_t* query_start_loc, const int32_t* num_computed_tokens,
+    int32_t num_reqs, int32_t num_tokens, pkv_cache_layout layout, void* stream);
+
+/* pkv_quant_kv_read -- the inverse of pkv_quant_kv_write: key[t], value[t] = the
+ * values of the rows at slot_mapping[t] (exact: they are bf16 numbers). Rows with
+ * a negative slot stay as they are; so do rows with a slot outside the pool
+ * (PKV_DEVERR_SLOT_RANGE). A slot may stand in the list any number of times.
+ *
+ * key, value    out, device bf16 [num_tokens][num_kv_heads][head_dim], row t at
+ *               key + t * key_row_stride (0 = num_kv_heads * head_dim). */
+int32_t pkv_quant_kv_read(void* key, void* value, int64_t key_row_stride, int64_t value_row_stride,
+                          const void* kv_cache, const uint8_t* kv_scales,
+                          const int64_t* slot_mapping, int32_t num_tokens, pkv_cache_layout layout,
+                          void* stream);
+
+/* pkv_quant_copy_blocks -- pkv_copy_blocks between two 8-bit pools: codes and
+ * scales of every pair's block. Either pool may lie in pinned host memory. */
+int32_t pkv_quant_copy_blocks(void* dst_pool, uint8_t* dst_scales, int32_t dst_num_blocks,
+                              const void* src_pool, const uint8_t* src_scales,
+                              int32_t src_num_blocks, const int32_t* block_pairs,
+                              int32_t num_pairs, pkv_cache_layout layout, void* stream);
+
+/*
+ * pkv_quant_paged_attention -- pkv_paged_attention over the 8-bit pool: the
+ * attention of the bf16 q rows over the values that the pool holds, with the same
+ * options (scores, shared prefix, splits, tracing: the expansion below lies in
+ * bracket [1, 2)).
+ *
+ * Requests of up to pkv_quant_few_rows() new tokens run on the split-KV decode
+ * kernels, so a few guessed tokens of a request are checked at the cost of
+ * reading its keys once. The blocks of the other requests (prompt chunks) and of
+ * a shared prefix are expanded to bf16 in the workspace first, and the tensor-core
+ * prefill kernel runs over those: the results of such rows are bit for bit those
+ * of pkv_paged_attention over the same values.
+ *
+ * workspace      at least pkv_quant_attention_workspace_size() bytes, 256-byte
+ *                aligned, private to this call while it runs. What lies behind the
+ *                part that does not depend on chunk_keys holds the expanded
+ *                blocks. If the step's chunks need more of them than fit,
+ *                keys are masked out and PKV_DEVERR_CHUNK_KEYS is set.
+ */
+int32_t pkv_quant_paged_attention(void* out, const void* q, int64_t q_row_stride,
+                                  const void* kv_cache, const uint8_t* kv_scales,
+                                  const int32_t* block_table, int32_t max_blocks_per_req,
+                                  const int32_t* seq_lens, const int32_t* query_start_loc,
+                                  const int32_t* num_computed_tokens, int32_t num_reqs,
+                                  int32_t num_tokens, int32_t max_query_len, int32_t max_seq_len,
+                                  int32_t num_q_heads, float scale, pkv_cache_layout layout,
+                                  void* workspace, size_t workspace_bytes,
+                                  const pkv_attention_options* options, void* stream);
+
+/* pkv_quant_paged_attention_with_write -- pkv_paged_attention_with_write over the
+ * 8-bit pool: pkv_quant_slot_mapping_and_write in the launch of the attention's
+ * plan, then pkv_quant_paged_attention. */
+int32_t pkv_quant_paged_attention_with_write(
+    void* out, const void* q, int64_t q_row_stride, void* kv_cache, uint8_t* kv_scales,
+    const void* key, const void* value, int64_t key_row_stride, int64_t value_row_stride,
+    int64_t* slot_mapping, const int32_t* block_table, int32_t max_blocks_per_req,
+    const int32_t* seq_lens, const int32_t* query_start_loc, const int32_t* num_computed_tokens,
+    int32_t num_reqs, int32_t num_tokens, int32_t max_query_len, int32_t max_seq_len,
+    int32_t num_q_heads, float scale, pkv_cache_layout layout, void* workspace,
+    size_t workspace_bytes, const pkv_attention_options* options, void* stream);
+
+/* pkv_quant_few_rows -- the most new tokens of a request that a call with this
+ * max_query_len attends on the decode kernels (at least 1): max_query_len itself
+ * while it times the q heads of a kv head is at most 64, else 16 / that many
+ * heads. Needs no device. */
+int32_t pkv_quant_few_rows(int32_t max_query_len, int32_t num_q_heads, int32_t num_kv_heads);
+
+/*
+ * pkv_quant_attention_workspace_size -- bytes of device workspace for
+ * pkv_quant_paged_attention with up to num_reqs requests and tables of that width.
+ * chunk_keys: the most cache tokens that the requests of more than
+ * pkv_quant_few_rows() new tokens hold between them in one step, counted in whole
+ * blocks (the sum of ceil(L / block_size) * block_size); 4 * num_kv_heads *
+ * head_dim bytes each. With key ranges the tokens in front of and behind those
+ * that a request's rows see need not be counted. 0 is enough for steps without such
+ * requests. A shared prefix of the options is counted by itself. Returns a negative
+ * status on bad arguments.
+ */
+int64_t pkv_quant_attention_workspace_size(int32_t num_reqs, int32_t max_blocks_per_req,
+                                           int32_t num_q_heads, pkv_cache_layout layout,
+                                           int64_t chunk_keys,
+                                           const pkv_attention_options* options);
 
 /*
  * pkv_get_device_errors -- checked path: synchronise `stream`, then return

@@ -26,5 +26,13 @@ from .paged_oracle import (  # noqa: F401
     partial_attention,
     combine_partials,
 )
+from .quant_oracle import (  # noqa: F401
+    e4m3_values,
+    quant_pool_bits,
+    quant_read,
+    quant_values,
+    quant_write,
+    quantise_rows,
+)
 from .scored_oracle import scored_attention  # noqa: F401
 from .tables_oracle import build_step_tables, release_blocks, ring  # noqa: F401

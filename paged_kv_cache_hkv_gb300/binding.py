@@ -29,6 +29,7 @@ DEVERR_TIMEOUT = 0x8
 DEVERR_SHARED = 0x10
 DEVERR_NO_BLOCKS = 0x20
 DEVERR_REF_COUNT = 0x40
+DEVERR_CHUNK_KEYS = 0x80
 
 
 class pkv_cache_layout(ctypes.Structure):
@@ -89,6 +90,28 @@ _SIGNATURES = {
     "pkv_paged_attention_static_workspace": (
         c_i32, [c_void_p, c_void_p, c_i64, c_void_p, c_void_p, c_i32, c_void_p, c_void_p,
                 c_void_p, c_i32, c_i32, c_i32, c_i32, c_i32, c_float, pkv_cache_layout,
+                ctypes.POINTER(pkv_attention_options), c_void_p]),
+    "pkv_quant_kv_write": (c_i32, [c_void_p, c_void_p, c_void_p, c_void_p, c_i64, c_i64, c_void_p,
+                                   c_i32, pkv_cache_layout, c_void_p]),
+    "pkv_quant_slot_mapping_and_write": (
+        c_i32, [c_void_p, c_void_p, c_void_p, c_void_p, c_i64, c_i64, c_void_p, c_void_p, c_i32,
+                c_void_p, c_void_p, c_i32, c_i32, pkv_cache_layout, c_void_p]),
+    "pkv_quant_kv_read": (c_i32, [c_void_p, c_void_p, c_i64, c_i64, c_void_p, c_void_p, c_void_p,
+                                  c_i32, pkv_cache_layout, c_void_p]),
+    "pkv_quant_copy_blocks": (c_i32, [c_void_p, c_void_p, c_i32, c_void_p, c_void_p, c_i32,
+                                      c_void_p, c_i32, pkv_cache_layout, c_void_p]),
+    "pkv_quant_few_rows": (c_i32, [c_i32, c_i32, c_i32]),
+    "pkv_quant_attention_workspace_size": (
+        c_i64, [c_i32, c_i32, c_i32, pkv_cache_layout, c_i64,
+                ctypes.POINTER(pkv_attention_options)]),
+    "pkv_quant_paged_attention": (
+        c_i32, [c_void_p, c_void_p, c_i64, c_void_p, c_void_p, c_void_p, c_i32, c_void_p, c_void_p,
+                c_void_p, c_i32, c_i32, c_i32, c_i32, c_i32, c_float, pkv_cache_layout, c_void_p,
+                c_size_t, ctypes.POINTER(pkv_attention_options), c_void_p]),
+    "pkv_quant_paged_attention_with_write": (
+        c_i32, [c_void_p, c_void_p, c_i64, c_void_p, c_void_p, c_void_p, c_void_p, c_i64, c_i64,
+                c_void_p, c_void_p, c_i32, c_void_p, c_void_p, c_void_p, c_i32, c_i32, c_i32,
+                c_i32, c_i32, c_float, pkv_cache_layout, c_void_p, c_size_t,
                 ctypes.POINTER(pkv_attention_options), c_void_p]),
 }
 
@@ -545,6 +568,222 @@ def pkv_release_blocks(block_table, release_rows, release_tokens, free_queue, fr
         _stream(stream, block_table.device.index)))
 
 
+def _quant_pool(kv_cache, kv_scales, names=("kv_cache", "kv_scales"), pinned=False):
+    """Layout of an 8-bit pool: codes [num_blocks, 2, B, Hkv, D] e4m3 and their
+    scales [num_blocks, 2, B, Hkv] uint8."""
+    for t, dtype, n in ((kv_cache, torch.float8_e4m3fn, names[0]),
+                        (kv_scales, torch.uint8, names[1])):
+        if t.dtype != dtype:
+            raise ValueError(f"{n} must be {dtype}, got {t.dtype}")
+        if not (t.is_cuda or (pinned and t.is_pinned())):
+            raise ValueError(f"{n} must be a CUDA tensor" +
+                             (" or pinned host memory" if pinned else ""))
+    lay = layout_of(kv_cache)
+    if kv_scales.shape != kv_cache.shape[:4] or not kv_scales.is_contiguous():
+        raise ValueError(f"{names[1]} must be a contiguous [num_blocks, 2, block_size, Hkv] tensor")
+    return lay
+
+
+def _quant_rows(lay, num_tokens, *rows):
+    """Checks of (tensor, name) rows [T, H, D] bf16, contiguous within a token;
+    heads and dims those of the pool where the name is key or value."""
+    for t, n in rows:
+        _require(t, torch.bfloat16, n)
+        if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]) or (
+                num_tokens > 1 and t.stride(0) < t.shape[1] * t.shape[2]):
+            raise ValueError(f"{n} must be [T, H, D] with contiguous rows")
+        if t.shape[0] != num_tokens or t.shape[2] != lay.head_dim or (
+                n != "q" and t.shape[1] != lay.num_kv_heads):
+            raise ValueError(f"{n} has shape {tuple(t.shape)}: {num_tokens} rows of the pool's "
+                             "heads and dims are wanted")
+
+
+def _row_stride(t):
+    """Row stride argument of rows that _quant_rows has looked at (a single row's
+    stride says nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else 0
+
+
+def _quant_slots(slot_mapping, num_tokens):
+    _require(slot_mapping, torch.int64, "slot_mapping")
+    if slot_mapping.shape != (num_tokens,) or not slot_mapping.is_contiguous():
+        raise ValueError(f"slot_mapping must be a contiguous [{num_tokens}] tensor")
+
+
+def pkv_quant_kv_write(kv_cache, kv_scales, key, value, slot_mapping, stream=None):
+    """Quantise key/value rows ([T, Hkv, D] bf16, row-strided allowed) into the
+    8-bit pool at their slots (see pagedkv.h)."""
+    lay = _quant_pool(kv_cache, kv_scales)
+    T = key.shape[0]
+    _quant_rows(lay, T, (key, "key"), (value, "value"))
+    _quant_slots(slot_mapping, T)
+    _one_device(kv_cache, kv_scales, key, value, slot_mapping)
+    _check("pkv_quant_kv_write", load().pkv_quant_kv_write(
+        _ptr(kv_cache), _ptr(kv_scales), _ptr(key), _ptr(value), _row_stride(key),
+        _row_stride(value), _ptr(slot_mapping), T, lay, _stream(stream, kv_cache.device.index)))
+
+
+def _quant_batch(kv_cache, block_table, query_start_loc, num_computed_tokens, seq_lens=None):
+    for t, n in ((block_table, "block_table"), (query_start_loc, "query_start_loc"),
+                 (num_computed_tokens, "num_computed_tokens"), (seq_lens, "seq_lens")):
+        if t is None and n == "seq_lens":
+            continue
+        _require(t, torch.int32, n)
+        if not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous")
+    R = num_computed_tokens.shape[0]
+    if block_table.dim() != 2 or block_table.shape[0] != R or query_start_loc.shape != (R + 1,) or (
+            num_computed_tokens.dim() != 1 or (seq_lens is not None and seq_lens.shape != (R,))):
+        raise ValueError("block_table, query_start_loc, seq_lens and num_computed_tokens must be "
+                         "[R, max_blocks], [R + 1], [R] and [R]")
+    _one_device(kv_cache, block_table, query_start_loc, num_computed_tokens, seq_lens)
+    return R
+
+
+def pkv_quant_slot_mapping_and_write(kv_cache, kv_scales, key, value, block_table, query_start_loc,
+                                     num_computed_tokens, slot_mapping=None, stream=None):
+    """Slot mapping and quantised cache write in one launch (see pagedkv.h).
+    slot_mapping (int64 [T]) receives the slots when given."""
+    lay = _quant_pool(kv_cache, kv_scales)
+    T = key.shape[0]
+    _quant_rows(lay, T, (key, "key"), (value, "value"))
+    if slot_mapping is not None:
+        _quant_slots(slot_mapping, T)
+    R = _quant_batch(kv_cache, block_table, query_start_loc, num_computed_tokens)
+    _one_device(kv_cache, kv_scales, key, value, slot_mapping)
+    _check("pkv_quant_slot_mapping_and_write", load().pkv_quant_slot_mapping_and_write(
+        _ptr(kv_cache), _ptr(kv_scales), _ptr(key), _ptr(value), _row_stride(key),
+        _row_stride(value), _ptr(slot_mapping), _ptr(block_table), block_table.shape[1], _ptr(query_start_loc),
+        _ptr(num_computed_tokens), R, T, lay, _stream(stream, kv_cache.device.index)))
+    return slot_mapping
+
+
+def pkv_quant_kv_read(key, value, kv_cache, kv_scales, slot_mapping, stream=None):
+    """key, value ([T, Hkv, D] bf16, row-strided allowed) <- the pool's rows at
+    the slots; rows with a negative slot stay as they are (see pagedkv.h)."""
+    lay = _quant_pool(kv_cache, kv_scales)
+    T = key.shape[0]
+    _quant_rows(lay, T, (key, "key"), (value, "value"))
+    _quant_slots(slot_mapping, T)
+    _one_device(kv_cache, kv_scales, key, value, slot_mapping)
+    _check("pkv_quant_kv_read", load().pkv_quant_kv_read(
+        _ptr(key), _ptr(value), _row_stride(key), _row_stride(value), _ptr(kv_cache),
+        _ptr(kv_scales), _ptr(slot_mapping), T, lay, _stream(stream, kv_cache.device.index)))
+
+
+def pkv_quant_copy_blocks(dst_pool, dst_scales, src_pool, src_scales, block_pairs, stream=None):
+    """Codes and scales of dst block d = those of src block s for each (s, d) row
+    of block_pairs (int32 [n, 2] on the device). Pools are CUDA tensors or pinned
+    host tensors."""
+    _quant_pool(dst_pool, dst_scales, ("dst_pool", "dst_scales"), pinned=True)
+    lay = _quant_pool(src_pool, src_scales, ("src_pool", "src_scales"), pinned=True)
+    _require(block_pairs, torch.int32, "block_pairs")
+    if block_pairs.dim() != 2 or block_pairs.shape[1] != 2 or not block_pairs.is_contiguous():
+        raise ValueError("block_pairs must be a contiguous [n, 2] int32 tensor")
+    if dst_pool.shape[1:] != src_pool.shape[1:]:
+        raise ValueError("pools must share the block shape")
+    _one_device(block_pairs, *(t for t in (dst_pool, dst_scales, src_pool, src_scales) if t.is_cuda))
+    _check("pkv_quant_copy_blocks", load().pkv_quant_copy_blocks(
+        _ptr(dst_pool), _ptr(dst_scales), dst_pool.shape[0], _ptr(src_pool), _ptr(src_scales),
+        src_pool.shape[0], _ptr(block_pairs), block_pairs.shape[0], lay,
+        _stream(stream, block_pairs.device.index)))
+
+
+def pkv_quant_few_rows(max_query_len: int, num_q_heads: int, num_kv_heads: int) -> int:
+    """Most new tokens of a request that attention over the 8-bit pool takes on
+    its decode kernels (see pagedkv.h)."""
+    n = load().pkv_quant_few_rows(max_query_len, num_q_heads, num_kv_heads)
+    if n < 0:
+        raise PagedKVError("pkv_quant_few_rows", int(n))
+    return int(n)
+
+
+def quant_chunk_keys(query_lens, seq_lens, group: int, block_size: int) -> int:
+    """chunk_keys of pkv_quant_attention_workspace_size for a step of these (host)
+    lengths; group: q heads per kv head."""
+    few = pkv_quant_few_rows(max(query_lens, default=0), group, 1)
+    return sum(-(-L // block_size) * block_size for n, L in zip(query_lens, seq_lens) if n > few)
+
+
+def pkv_quant_attention_workspace_size(num_reqs: int, num_q_heads: int, kv_cache, *,
+                                       max_blocks_per_req: int, chunk_keys: int,
+                                       decode_splits=None, shared_prefix=None) -> int:
+    """Workspace bytes for pkv_quant_paged_attention (see pagedkv.h; chunk_keys:
+    see quant_chunk_keys); kv_cache is the codes' tensor or a pkv_cache_layout."""
+    lay = kv_cache if isinstance(kv_cache, pkv_cache_layout) else layout_of(kv_cache)
+    n = load().pkv_quant_attention_workspace_size(
+        num_reqs, max_blocks_per_req, num_q_heads, lay, int(chunk_keys),
+        _options(decode_splits, None, shared_prefix))
+    if n < 0:
+        raise PagedKVError("pkv_quant_attention_workspace_size", int(n))
+    return int(n)
+
+
+def _quant_attention_args(out, q, kv_cache, kv_scales, block_table, seq_lens, query_start_loc,
+                          num_computed_tokens, max_query_len, max_seq_len, scale, workspace,
+                          options, write=None):
+    """Checked and marshalled arguments of pkv_quant_paged_attention, or with
+    write = (key, value, slot_mapping) of its _with_write form; all but the stream."""
+    lay = _quant_pool(kv_cache, kv_scales)
+    T = q.shape[0]
+    _quant_rows(lay, T, (q, "q"))
+    _require(out, torch.bfloat16, "out")
+    if out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be contiguous and of q's shape")
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    R = _quant_batch(kv_cache, block_table, query_start_loc, num_computed_tokens, seq_lens)
+    _one_device(kv_cache, kv_scales, out, q, workspace)
+    rows = ()
+    if write is not None:
+        key, value, slot_mapping = write
+        _quant_rows(lay, T, (key, "key"), (value, "value"))
+        if slot_mapping is not None:
+            _quant_slots(slot_mapping, T)
+        _one_device(kv_cache, key, value, slot_mapping)
+        rows = (_ptr(key), _ptr(value), _row_stride(key), _row_stride(value), _ptr(slot_mapping))
+    return (_ptr(out), _ptr(q), _row_stride(q), _ptr(kv_cache), _ptr(kv_scales), *rows,
+            _ptr(block_table), block_table.shape[1], _ptr(seq_lens), _ptr(query_start_loc),
+            _ptr(num_computed_tokens), R, T, int(max_query_len), int(max_seq_len), q.shape[1],
+            float(scale), lay, _ptr(workspace), workspace.numel() * workspace.element_size(),
+            options)
+
+
+def pkv_quant_paged_attention(out, q, kv_cache, kv_scales, block_table, seq_lens, query_start_loc,
+                              num_computed_tokens, *, max_query_len: int, max_seq_len: int,
+                              scale: float, workspace, decode_splits=None, trace_events=None,
+                              shared_prefix=None, softcap=0.0, alibi_slopes=None, key_begin=None,
+                              key_end=None, stream=None):
+    """out [T, Hq, D] bf16 <- attention of one mixed step over the 8-bit pool (see
+    pagedkv.h); options as in pkv_paged_attention."""
+    options = _options(decode_splits, trace_events, shared_prefix,
+                       _scores(q, softcap, alibi_slopes, key_begin, key_end))
+    _check("pkv_quant_paged_attention", load().pkv_quant_paged_attention(
+        *_quant_attention_args(out, q, kv_cache, kv_scales, block_table, seq_lens,
+                               query_start_loc, num_computed_tokens, max_query_len, max_seq_len,
+                               scale, workspace, options), _stream(stream, q.device.index)))
+    return out
+
+
+def pkv_quant_paged_attention_with_write(out, q, kv_cache, kv_scales, key, value, block_table,
+                                         seq_lens, query_start_loc, num_computed_tokens, *,
+                                         max_query_len: int, max_seq_len: int, scale: float,
+                                         workspace, slot_mapping=None, decode_splits=None,
+                                         trace_events=None, shared_prefix=None, softcap=0.0,
+                                         alibi_slopes=None, key_begin=None, key_end=None,
+                                         stream=None):
+    """The step of one layer on the 8-bit pool in one call: slot mapping and
+    quantised write of the new tokens, then attention (see pagedkv.h)."""
+    options = _options(decode_splits, trace_events, shared_prefix,
+                       _scores(q, softcap, alibi_slopes, key_begin, key_end))
+    _check("pkv_quant_paged_attention_with_write", load().pkv_quant_paged_attention_with_write(
+        *_quant_attention_args(out, q, kv_cache, kv_scales, block_table, seq_lens,
+                               query_start_loc, num_computed_tokens, max_query_len, max_seq_len,
+                               scale, workspace, options, (key, value, slot_mapping)),
+        _stream(stream, q.device.index)))
+    return out
+
+
 class TableCalls:
     """pkv_build_step_tables and pkv_release_blocks on buffers that a serving
     loop keeps, with their arguments checked and marshalled once (as StepCalls
@@ -607,13 +846,33 @@ class StepCalls:
     argument checks and the tensor-to-pointer conversion once, not on every
     step; ``run`` then makes the three C calls in a row on the given stream.
     The buffers must stay allocated and keep their shapes while the object is
-    used."""
+    used. With kv_scales the pool is the 8-bit one and the calls are the
+    pkv_quant_ ones."""
 
     def __init__(self, *, slot_mapping, block_table, query_start_loc, num_computed_tokens,
                  kv_cache, key, value, out, q, seq_lens, max_query_len: int,
                  max_seq_len: int, scale: float, workspace, decode_splits=None,
                  shared_prefix=None, fused_write=False, write_in_attention=False, softcap=0.0,
-                 alibi_slopes=None, key_begin=None, key_end=None):
+                 alibi_slopes=None, key_begin=None, key_end=None, kv_scales=None):
+        self.fused_write = bool(fused_write)
+        self.write_in_attention = bool(write_in_attention)
+        self._write, self._mapped_write, self._attend, self._attend_write = (
+            ("pkv_quant_kv_write", "pkv_quant_slot_mapping_and_write",
+             "pkv_quant_paged_attention", "pkv_quant_paged_attention_with_write")
+            if kv_scales is not None else
+            ("pkv_paged_kv_write", "pkv_slot_mapping_and_write", "pkv_paged_attention",
+             "pkv_paged_attention_with_write"))
+        # the tensors stay referenced, so their memory stays valid
+        self._keep = (slot_mapping, block_table, query_start_loc, num_computed_tokens,
+                      kv_cache, key, value, out, q, seq_lens, workspace, kv_scales)
+        self._write_device = None if kv_scales is None else kv_cache.device.index
+        if kv_scales is not None:
+            self._marshal_quant(slot_mapping, block_table, query_start_loc, num_computed_tokens,
+                                kv_cache, kv_scales, key, value, out, q, seq_lens, max_query_len,
+                                max_seq_len, scale, workspace,
+                                _options(decode_splits, None, shared_prefix,
+                                         _scores(q, softcap, alibi_slopes, key_begin, key_end)))
+            return
         _require(slot_mapping, torch.int64, "slot_mapping")
         for t, n in ((block_table, "block_table"), (query_start_loc, "query_start_loc"),
                      (num_computed_tokens, "num_computed_tokens"), (seq_lens, "seq_lens")):
@@ -640,8 +899,6 @@ class StepCalls:
         self.write_args = (
             _ptr(kv_cache), _ptr(key), _ptr(value), key.stride(0), value.stride(0),
             _ptr(slot_mapping), key.shape[0], lay)
-        self.fused_write = bool(fused_write)
-        self.write_in_attention = bool(write_in_attention)
         if self.write_in_attention and key.shape[0] != q.shape[0]:
             raise ValueError("key and q must have the same number of rows")
         self.mapped_write_args = (
@@ -661,49 +918,54 @@ class StepCalls:
             _ptr(num_computed_tokens), seq_lens.shape[0], q.shape[0], int(max_query_len),
             int(max_seq_len), q.shape[1], float(scale), lay, _ptr(workspace),
             workspace.numel() * workspace.element_size(), self._opts)
-        # the tensors stay referenced, so their memory stays valid
-        self._keep = (slot_mapping, block_table, query_start_loc, num_computed_tokens,
-                      kv_cache, key, value, out, q, seq_lens, workspace)
+
+    def _marshal_quant(self, slot_mapping, block_table, query_start_loc, num_computed_tokens,
+                       kv_cache, kv_scales, key, value, out, q, seq_lens, max_query_len,
+                       max_seq_len, scale, workspace, options):
+        """The arguments of the 8-bit pool's calls (kv_scales given)."""
+        self.lib = load()
+        self._opts = options
+        self._device = kv_cache.device.index
+        args = (out, q, kv_cache, kv_scales, block_table, seq_lens, query_start_loc,
+                num_computed_tokens, max_query_len, max_seq_len, scale, workspace, options)
+        self.attn_args = _quant_attention_args(*args)
+        self.attn_write_args = _quant_attention_args(*args, (key, value, slot_mapping))
+        lay, T, R = layout_of(kv_cache), q.shape[0], num_computed_tokens.shape[0]
+        _quant_slots(slot_mapping, T)
+        rows = (_ptr(kv_cache), _ptr(kv_scales), _ptr(key), _ptr(value), _row_stride(key),
+                _row_stride(value), _ptr(slot_mapping))
+        tables = (_ptr(block_table), block_table.shape[1], _ptr(query_start_loc),
+                  _ptr(num_computed_tokens), R, T)
+        self.slot_args = (_ptr(slot_mapping), *tables, lay.num_blocks, lay.block_size)
+        self.write_args = (*rows, T, lay)
+        self.mapped_write_args = (*rows, *tables, lay)
 
     def slot_map(self, stream=None):
-        status = self.lib.pkv_slot_mapping(*self.slot_args, _stream(stream))
+        self._call("pkv_slot_mapping", self.slot_args, _stream(stream, self._write_device))
+
+    def _call(self, name, args, stream):
+        status = getattr(self.lib, name)(*args, stream)
         if status:
-            raise PagedKVError("pkv_slot_mapping", status)
+            raise PagedKVError(name, status)
 
     def write(self, stream=None):
-        status = self.lib.pkv_paged_kv_write(*self.write_args, _stream(stream))
-        if status:
-            raise PagedKVError("pkv_paged_kv_write", status)
+        self._call(self._write, self.write_args, _stream(stream, self._write_device))
 
     def slot_map_and_write(self, stream=None):
-        status = self.lib.pkv_slot_mapping_and_write(*self.mapped_write_args, _stream(stream))
-        if status:
-            raise PagedKVError("pkv_slot_mapping_and_write", status)
+        self._call(self._mapped_write, self.mapped_write_args,
+                   _stream(stream, self._write_device))
 
     def attend(self, stream=None):
-        status = self.lib.pkv_paged_attention(*self.attn_args, _stream(stream, self._device))
-        if status:
-            raise PagedKVError("pkv_paged_attention", status)
+        self._call(self._attend, self.attn_args, _stream(stream, self._device))
 
     def run(self, stream=None):
         st = _stream(stream, self._device)
-        lib = self.lib
         if self.write_in_attention:
-            status = lib.pkv_paged_attention_with_write(*self.attn_write_args, st)
-            if status:
-                raise PagedKVError("pkv_paged_attention_with_write", status)
+            self._call(self._attend_write, self.attn_write_args, st)
             return
         if self.fused_write:
-            status = lib.pkv_slot_mapping_and_write(*self.mapped_write_args, st)
-            if status:
-                raise PagedKVError("pkv_slot_mapping_and_write", status)
+            self._call(self._mapped_write, self.mapped_write_args, st)
         else:
-            status = lib.pkv_slot_mapping(*self.slot_args, st)
-            if status:
-                raise PagedKVError("pkv_slot_mapping", status)
-            status = lib.pkv_paged_kv_write(*self.write_args, st)
-            if status:
-                raise PagedKVError("pkv_paged_kv_write", status)
-        status = lib.pkv_paged_attention(*self.attn_args, st)
-        if status:
-            raise PagedKVError("pkv_paged_attention", status)
+            self._call("pkv_slot_mapping", self.slot_args, st)
+            self._call(self._write, self.write_args, st)
+        self._call(self._attend, self.attn_args, st)

@@ -81,15 +81,16 @@ int32_t encode_fn(EncodeTiledFn* fn) {
   return PKV_OK;
 }
 
-// bf16 map of `rank` dims (dims[0] contiguous); strides[i] is the byte
-// stride of dims[i + 1].
+// bf16 map (or one of another type) of `rank` dims (dims[0] contiguous);
+// strides[i] is the byte stride of dims[i + 1].
 int32_t make_map_n(CUtensorMap* map, const void* base, uint32_t rank, const cuuint64_t* dims,
-                   const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swz) {
+                   const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swz,
+                   CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
   EncodeTiledFn fn;
   int32_t st = encode_fn(&fn);
   if (st != PKV_OK) return st;
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims,
+  CUresult r = fn(map, type, rank, const_cast<void*>(base), dims,
                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
@@ -203,6 +204,8 @@ int32_t score_params(const pkv_attention_options* opt, float scale, pkv::ScorePa
 struct WsLayout {
   size_t hdr, dec_prefix, pf_req, pf_prefix, part_ml, part_o, bound, casc_use, casc_ml, casc_o,
       total;
+  // 8-bit pool; the expanded blocks take what lies behind
+  size_t ex_first, ex_prefix, ex_table, few_ml, few_o, quant_total;
 };
 
 WsLayout ws_layout(int num_reqs, int virt_heads, int gw, int head_dim, long long splits,
@@ -233,6 +236,49 @@ WsLayout ws_layout(int num_reqs, int virt_heads, int gw, int head_dim, long long
   off += round256(shared_rows * head_dim * sizeof(float));
   w.total = off;
   return w;
+}
+
+// The further arrays of a call on the 8-bit pool with at most `few` rows (more
+// than one) of a request on the decode stream.
+void quant_ws_layout(WsLayout* w, int num_reqs, int max_blocks, int num_q_heads, int head_dim,
+                     long long splits, int few) {
+  size_t off = w->total;
+  w->ex_first = off;
+  off += round256((num_reqs + 1) * sizeof(int32_t));
+  w->ex_prefix = off;
+  off += round256((num_reqs + 2) * sizeof(int32_t));
+  w->ex_table = off;
+  off += round256(static_cast<size_t>(num_reqs) * max_blocks * sizeof(int32_t));
+  const size_t rows = static_cast<size_t>(2 * splits) * few * num_q_heads;
+  w->few_ml = off;
+  off += round256(rows * sizeof(float2));
+  w->few_o = off;
+  off += round256(rows * head_dim * sizeof(float));
+  w->quant_total = off;
+}
+
+// bytes of a block expanded to bf16
+size_t expanded_block_bytes(const pkv_cache_layout& l) {
+  return static_cast<size_t>(4) * l.block_size * l.num_kv_heads * l.head_dim;
+}
+
+// One full wave of the 8-bit decode, or the caller's choice.
+int32_t quant_splits_for(DeviceInfo* d, const pkv_cache_layout& l, int group, int max_query_len,
+                         bool scored, const pkv_attention_options* opt, long long* splits) {
+  if (opt) {
+    if (opt->reserved[0] != 0 && opt->reserved[0] != PKV_OPTIONS_SCORES) return PKV_ERR_BAD_SHAPE;
+    for (int i = 1; i < 4; ++i)
+      if (opt->reserved[i] != 0) return PKV_ERR_BAD_SHAPE;
+    if (opt->decode_splits < 0) return PKV_ERR_BAD_SHAPE;
+    if (opt->decode_splits > 0) {
+      *splits = opt->decode_splits;
+      return PKV_OK;
+    }
+  }
+  cudaError_t e = pkv::quant_full_wave_splits(l.head_dim, l.num_kv_heads, group,
+                                              block_shift_of(l.block_size), max_query_len, scored,
+                                              d->num_sms, splits);
+  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "decode occupancy");
 }
 
 // Ranges (CTAs) the decode stream is split into: the caller's choice, else
@@ -424,7 +470,8 @@ int64_t pkv_attention_workspace_size(int32_t num_reqs, int32_t num_q_heads,
 }
 
 // pkv_paged_attention, and with `write` the step's slot mapping and cache
-// write in the plan's launch (pkv_paged_attention_with_write).
+// write in the plan's launch (pkv_paged_attention_with_write). With kv_scales the
+// pool is the 8-bit one (pkv_quant_paged_attention and its _with_write form).
 static int32_t attention_impl(void* out, const void* q, int64_t q_row_stride, const void* kv_cache,
                        const int32_t* block_table, int32_t max_blocks_per_req,
                        const int32_t* seq_lens, const int32_t* query_start_loc,
@@ -432,7 +479,8 @@ static int32_t attention_impl(void* out, const void* q, int64_t q_row_stride, co
                        int32_t max_query_len, int32_t max_seq_len, int32_t num_q_heads,
                        float scale, pkv_cache_layout layout, void* workspace,
                        size_t workspace_bytes, const pkv_attention_options* options, void* stream,
-                       const pkv::WriteRowsArgs* write) {
+                       const pkv::WriteRowsArgs* write, bool quant = false,
+                       const uint8_t* kv_scales = nullptr) {
   int32_t st = check_layout(layout);
   if (st != PKV_OK) return st;
   st = check_group(num_q_heads, layout.num_kv_heads);
@@ -450,16 +498,23 @@ static int32_t attention_impl(void* out, const void* q, int64_t q_row_stride, co
   if (num_reqs == 0 || num_tokens == 0 || max_query_len == 0) {
     // no attention to do; the write (padding rows: slots -1) still runs
     if (!write) return PKV_OK;
-    cudaError_t e = pkv::launch_mapped_write(*write, static_cast<cudaStream_t>(stream));
+    if (quant) {
+      DeviceInfo* d;
+      st = device_info(&d);
+      if (st != PKV_OK) return st;
+    }
+    cudaError_t e = quant ? pkv::launch_quant_mapped_write(*write, static_cast<cudaStream_t>(stream))
+                          : pkv::launch_mapped_write(*write, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PKV_OK : cuda_fail(e, "slot mapping and write launch");
   }
   if (static_cast<long long>(max_seq_len) >
       static_cast<long long>(max_blocks_per_req) * layout.block_size)
     return PKV_ERR_BAD_SHAPE;
   if (!out || !q || !kv_cache || !block_table || !seq_lens || !query_start_loc ||
-      !num_computed_tokens)
+      !num_computed_tokens || (quant && !kv_scales))
     return PKV_ERR_NULL_POINTER;
-  if (!aligned16(out) || !aligned16(q) || !aligned16(kv_cache) || (q_row_stride % 8))
+  if (!aligned16(out) || !aligned16(q) || !aligned16(kv_cache) || !aligned16(kv_scales) ||
+      (q_row_stride % 8))
     return PKV_ERR_MISALIGNED;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return PKV_ERR_WORKSPACE;
 
@@ -468,8 +523,9 @@ static int32_t attention_impl(void* out, const void* q, int64_t q_row_stride, co
   if (st != PKV_OK) return st;
   const int group = num_q_heads / layout.num_kv_heads;
   long long splits = 0;
-  st = decode_splits_for(d, layout.head_dim, layout.num_kv_heads, group, layout.block_size,
-                         options, &splits);
+  st = quant ? quant_splits_for(d, layout, group, max_query_len, a.scored, options, &splits)
+             : decode_splits_for(d, layout.head_dim, layout.num_kv_heads, group,
+                                 layout.block_size, options, &splits);
   if (st != PKV_OK) return st;
   SharedHint sh;
   st = shared_hint(options, layout, group, num_reqs, d->num_sms, &sh);
@@ -479,7 +535,19 @@ static int32_t attention_impl(void* out, const void* q, int64_t q_row_stride, co
     return PKV_ERR_BAD_SHAPE;
   const int gw = pkv::decode_heads_per_warp(group);
   const int virt = layout.num_kv_heads * (group / gw);
-  const WsLayout wl = ws_layout(num_reqs, virt, gw, layout.head_dim, splits, sh, num_q_heads);
+  // (8-bit pool: laid out for the most splits and rows, as its size was asked for)
+  const long long ws_splits =
+      quant && !(options && options->decode_splits > 0)
+          ? pkv::quant_most_splits(layout.num_kv_heads, group, d->num_sms)
+          : splits;
+  WsLayout wl = ws_layout(num_reqs, virt, gw, layout.head_dim, ws_splits, sh, num_q_heads);
+  a.few = 1;
+  if (quant) {
+    a.few = pkv::quant_few_rows(max_query_len, group);
+    quant_ws_layout(&wl, num_reqs, max_blocks_per_req, num_q_heads, layout.head_dim, ws_splits,
+                    pkv::kFewUnits / group);
+    if (workspace_bytes < wl.quant_total + expanded_block_bytes(layout)) return PKV_ERR_WORKSPACE;
+  }
   if (workspace_bytes < wl.total) return PKV_ERR_WORKSPACE;
   // The decode stream holds at most num_reqs * ceil(max_seq_len / 16)
   // chunks: with the default split, never use more ranges than that (a small
@@ -503,11 +571,30 @@ static int32_t attention_impl(void* out, const void* q, int64_t q_row_stride, co
   ws.casc_use = reinterpret_cast<int32_t*>(wsb + wl.casc_use);
   ws.casc_ml = reinterpret_cast<float2*>(wsb + wl.casc_ml);
   ws.casc_o = reinterpret_cast<float*>(wsb + wl.casc_o);
+  if (quant) {
+    ws.ex_first = reinterpret_cast<int32_t*>(wsb + wl.ex_first);
+    ws.ex_prefix = reinterpret_cast<int32_t*>(wsb + wl.ex_prefix);
+    ws.ex_table = reinterpret_cast<int32_t*>(wsb + wl.ex_table);
+    ws.few_ml = reinterpret_cast<float2*>(wsb + wl.few_ml);
+    ws.few_o = reinterpret_cast<float*>(wsb + wl.few_o);
+    ws.ex_pool = reinterpret_cast<uint4*>(wsb + wl.quant_total);
+    const size_t blocks = (workspace_bytes - wl.quant_total) / expanded_block_bytes(layout);
+    // (its rows, like the pool's, are 32-bit TMA coordinates)
+    const size_t most = ((1ull << 31) - 1) / (2u * layout.block_size);
+    ws.ex_capacity = static_cast<int>(blocks < most ? blocks : most);
+  } else {
+    ws.ex_first = ws.ex_prefix = ws.ex_table = nullptr;
+    ws.few_ml = nullptr;
+    ws.few_o = nullptr;
+    ws.ex_pool = nullptr;
+    ws.ex_capacity = 0;
+  }
 
   a.out = static_cast<uint16_t*>(out);
   a.q = static_cast<const uint16_t*>(q);
   a.q_stride = q_row_stride;
   a.kv_cache = kv_cache;
+  a.kv_scales = kv_scales;
   a.block_table = block_table;
   a.max_blocks = max_blocks_per_req;
   a.seq_lens = seq_lens;
@@ -541,8 +628,25 @@ static int32_t attention_impl(void* out, const void* q, int64_t q_row_stride, co
   int slab_vh = 0, slab_kh = 0;
   pkv::decode_slab(Hkv, group, &slab_vh, &slab_kh);
   CUtensorMap kv_map;
-  st = make_map(&kv_map, kv_cache, D, Hkv, pool_rows, static_cast<uint64_t>(D) * 2, row_bytes, D,
-                static_cast<uint32_t>(slab_kh), dec_box, CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (quant) {
+    // codes as {D, row of a block, kv head, block * 2 + k|v}: a copy takes 16 rows
+    // (an 8-token block's 8) of K and V of a CTA's kv heads, and lands them
+    // swizzled as [K|V][kv head][row][D]
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(B),
+                                static_cast<cuuint64_t>(Hkv),
+                                static_cast<cuuint64_t>(layout.num_blocks) * 2};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(Hkv) * D, static_cast<cuuint64_t>(D),
+                                   static_cast<cuuint64_t>(B) * Hkv * D};
+    const cuuint32_t box[4] = {
+        static_cast<cuuint32_t>(D), B < 16 ? 8u : 16u,
+        static_cast<cuuint32_t>(pkv::quant_slab_heads(Hkv, group, max_query_len)), 2};
+    st = make_map_n(&kv_map, kv_cache, 4, dims, strides, box,
+                    D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_DATA_TYPE_UINT8);
+  } else {
+    st = make_map(&kv_map, kv_cache, D, Hkv, pool_rows, static_cast<uint64_t>(D) * 2, row_bytes, D,
+                  static_cast<uint32_t>(slab_kh), dec_box, CU_TENSOR_MAP_SWIZZLE_NONE);
+  }
   if (st != PKV_OK) return st;
 
   a.decode_splits = splits;
@@ -556,7 +660,20 @@ static int32_t attention_impl(void* out, const void* q, int64_t q_row_stride, co
   if (e == cudaSuccess) e = pkv::launch_plan(a, ws, s, write);
   if (e == cudaSuccess) e = mark(1);
   if (e != cudaSuccess) return cuda_fail(e, "plan launch");
-  if (max_query_len > 1 || sh.num > 0) {
+  if (max_query_len > a.few || sh.num > 0) {
+    // the 8-bit pool's prefill runs over its blocks expanded to bf16
+    pkv::AttnArgs pa = a;
+    if (quant) {
+      e = pkv::launch_expand(a,
+                             pkv::ExpandArgs{ws.hdr, ws.pf_req, ws.ex_first, ws.ex_prefix,
+                                             ws.ex_table, ws.ex_pool, ws.ex_capacity},
+                             d->num_sms, s);
+      if (e != cudaSuccess) return cuda_fail(e, "expand launch");
+      pa.kv_cache = ws.ex_pool;
+      pa.block_table = ws.ex_table;
+      pa.num_blocks = ws.ex_capacity;
+    }
+    const uint64_t pf_rows = static_cast<uint64_t>(pa.num_blocks) * 2 * B;
     // pool for the tensor-core path, as {64-element half row, row within an
     // 8-row group, d half, kv head, 8-row group}: one copy takes the K (or V)
     // rows of one block and one kv head, and lands as 128-byte swizzled
@@ -564,23 +681,25 @@ static int32_t attention_impl(void* out, const void* q, int64_t q_row_stride, co
     CUtensorMap kv_map_sw, q_map;
     {
       const cuuint64_t dims[5] = {64, 8, static_cast<cuuint64_t>(D / 64),
-                                  static_cast<cuuint64_t>(Hkv), pool_rows / 8};
+                                  static_cast<cuuint64_t>(Hkv), pf_rows / 8};
       const cuuint64_t strides[4] = {row_bytes, 128, static_cast<uint64_t>(D) * 2, row_bytes * 8};
       const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(D / 64), 1,
                                  static_cast<cuuint32_t>(B / 8)};
-      st = make_map_n(&kv_map_sw, kv_cache, 5, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+      st = make_map_n(&kv_map_sw, pa.kv_cache, 5, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
     }
     if (st != PKV_OK) return st;
     st = make_map(&q_map, q, D, num_q_heads, num_tokens, static_cast<uint64_t>(D) * 2,
                   static_cast<uint64_t>(q_row_stride) * 2, 64, group, 128 / group,
                   CU_TENSOR_MAP_SWIZZLE_128B);
     if (st != PKV_OK) return st;
-    e = pkv::launch_prefill(a, ws, kv_map_sw, q_map, d->num_sms, s);
+    e = pkv::launch_prefill(pa, ws, kv_map_sw, q_map, d->num_sms, s);
     if (e == cudaErrorNotSupported) return PKV_ERR_UNSUPPORTED;
     if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
   }
   e = mark(2);
-  if (e == cudaSuccess) e = pkv::launch_decode(a, ws, kv_map, splits, d->num_sms, s, ev);
+  if (e == cudaSuccess)
+    e = quant ? pkv::launch_quant_decode(a, ws, kv_map, splits, d->num_sms, s, ev)
+              : pkv::launch_decode(a, ws, kv_map, splits, d->num_sms, s, ev);
   if (e == cudaSuccess) e = mark(4);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   return PKV_OK;
@@ -630,6 +749,208 @@ int32_t pkv_paged_attention_with_write(
                         seq_lens, query_start_loc, num_computed_tokens, num_reqs, num_tokens,
                         max_query_len, max_seq_len, num_q_heads, scale, layout, workspace,
                         workspace_bytes, options, stream, num_tokens > 0 ? &w : nullptr);
+}
+
+namespace {
+
+// Checks that the 8-bit pool's row calls share; strides of 0 become the
+// contiguous ones.
+int32_t quant_row_args(const void* kv_cache, const void* kv_scales, const void* key,
+                       const void* value, int64_t* key_row_stride, int64_t* value_row_stride,
+                       int32_t num_tokens, const pkv_cache_layout& layout) {
+  const int64_t row = static_cast<int64_t>(layout.num_kv_heads) * layout.head_dim;
+  if (*key_row_stride == 0) *key_row_stride = row;
+  if (*value_row_stride == 0) *value_row_stride = row;
+  if (*key_row_stride < row || *value_row_stride < row) return PKV_ERR_BAD_SHAPE;
+  if (num_tokens == 0) return PKV_OK;
+  if (!kv_cache || !kv_scales || !key || !value) return PKV_ERR_NULL_POINTER;
+  if (!aligned16(kv_cache) || !aligned16(kv_scales) || !aligned16(key) || !aligned16(value) ||
+      (*key_row_stride % 8) || (*value_row_stride % 8))
+    return PKV_ERR_MISALIGNED;
+  return PKV_OK;
+}
+
+}  // namespace
+
+int32_t pkv_quant_kv_write(void* kv_cache, uint8_t* kv_scales, const void* key, const void* value,
+                           int64_t key_row_stride, int64_t value_row_stride,
+                           const int64_t* slot_mapping, int32_t num_tokens,
+                           pkv_cache_layout layout, void* stream) {
+  int32_t st = check_layout(layout);
+  if (st != PKV_OK) return st;
+  if (num_tokens < 0) return PKV_ERR_BAD_SHAPE;
+  st = quant_row_args(kv_cache, kv_scales, key, value, &key_row_stride, &value_row_stride,
+                      num_tokens, layout);
+  if (st != PKV_OK) return st;
+  if (num_tokens == 0) return PKV_OK;
+  if (!slot_mapping) return PKV_ERR_NULL_POINTER;
+  DeviceInfo* d;
+  st = device_info(&d);
+  if (st != PKV_OK) return st;
+  cudaError_t e = pkv::launch_quant_write(
+      kv_cache, kv_scales, key, value, key_row_stride, value_row_stride, slot_mapping, num_tokens,
+      layout.num_blocks, block_shift_of(layout.block_size), layout.num_kv_heads, layout.head_dim,
+      d->num_sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "quant_write launch");
+}
+
+int32_t pkv_quant_slot_mapping_and_write(
+    void* kv_cache, uint8_t* kv_scales, const void* key, const void* value, int64_t key_row_stride,
+    int64_t value_row_stride, int64_t* slot_mapping, const int32_t* block_table,
+    int32_t max_blocks_per_req, const int32_t* query_start_loc, const int32_t* num_computed_tokens,
+    int32_t num_reqs, int32_t num_tokens, pkv_cache_layout layout, void* stream) {
+  int32_t st = check_layout(layout);
+  if (st != PKV_OK) return st;
+  if (num_tokens < 0 || num_reqs < 0 || max_blocks_per_req < 0) return PKV_ERR_BAD_SHAPE;
+  st = quant_row_args(kv_cache, kv_scales, key, value, &key_row_stride, &value_row_stride,
+                      num_tokens, layout);
+  if (st != PKV_OK) return st;
+  if (num_tokens == 0) return PKV_OK;
+  if (!query_start_loc || (num_reqs > 0 && (!block_table || !num_computed_tokens)))
+    return PKV_ERR_NULL_POINTER;
+  DeviceInfo* d;
+  st = device_info(&d);
+  if (st != PKV_OK) return st;
+  const pkv::WriteRowsArgs w = pkv::write_rows_args(
+      kv_cache, key, value, key_row_stride, value_row_stride, slot_mapping, block_table,
+      max_blocks_per_req, query_start_loc, num_computed_tokens, num_reqs, num_tokens,
+      layout.num_blocks, layout.block_size, layout.num_kv_heads, layout.head_dim, kv_scales);
+  cudaError_t e = pkv::launch_quant_mapped_write(w, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "slot mapping and write launch");
+}
+
+int32_t pkv_quant_kv_read(void* key, void* value, int64_t key_row_stride, int64_t value_row_stride,
+                          const void* kv_cache, const uint8_t* kv_scales,
+                          const int64_t* slot_mapping, int32_t num_tokens, pkv_cache_layout layout,
+                          void* stream) {
+  int32_t st = check_layout(layout);
+  if (st != PKV_OK) return st;
+  if (num_tokens < 0) return PKV_ERR_BAD_SHAPE;
+  st = quant_row_args(kv_cache, kv_scales, key, value, &key_row_stride, &value_row_stride,
+                      num_tokens, layout);
+  if (st != PKV_OK) return st;
+  if (num_tokens == 0) return PKV_OK;
+  if (!slot_mapping) return PKV_ERR_NULL_POINTER;
+  DeviceInfo* d;
+  st = device_info(&d);
+  if (st != PKV_OK) return st;
+  cudaError_t e = pkv::launch_quant_read(
+      key, value, key_row_stride, value_row_stride, kv_cache, kv_scales, slot_mapping, num_tokens,
+      layout.num_blocks, block_shift_of(layout.block_size), layout.num_kv_heads, layout.head_dim,
+      d->num_sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "quant_read launch");
+}
+
+int32_t pkv_quant_copy_blocks(void* dst_pool, uint8_t* dst_scales, int32_t dst_num_blocks,
+                              const void* src_pool, const uint8_t* src_scales,
+                              int32_t src_num_blocks, const int32_t* block_pairs,
+                              int32_t num_pairs, pkv_cache_layout layout, void* stream) {
+  pkv_cache_layout l = layout;
+  l.num_blocks = dst_num_blocks > 0 ? dst_num_blocks : 1;
+  int32_t st = check_layout(l);
+  if (st != PKV_OK) return st;
+  if (dst_num_blocks < 1 || src_num_blocks < 1 || num_pairs < 0) return PKV_ERR_BAD_SHAPE;
+  if (static_cast<long long>(src_num_blocks) * 2 * layout.block_size >= (1ll << 31))
+    return PKV_ERR_BAD_SHAPE;
+  if (num_pairs == 0) return PKV_OK;
+  if (!dst_pool || !dst_scales || !src_pool || !src_scales || !block_pairs)
+    return PKV_ERR_NULL_POINTER;
+  if (!aligned16(dst_pool) || !aligned16(dst_scales) || !aligned16(src_pool) ||
+      !aligned16(src_scales))
+    return PKV_ERR_MISALIGNED;
+  DeviceInfo* d;
+  st = device_info(&d);
+  if (st != PKV_OK) return st;
+  cudaError_t e = pkv::launch_quant_copy(dst_pool, dst_scales, dst_num_blocks, src_pool, src_scales,
+                                         src_num_blocks, block_pairs, num_pairs, layout.block_size,
+                                         layout.num_kv_heads, layout.head_dim, d->num_sms,
+                                         static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "quant_copy launch");
+}
+
+int32_t pkv_quant_few_rows(int32_t max_query_len, int32_t num_q_heads, int32_t num_kv_heads) {
+  if (max_query_len < 0 || num_kv_heads < 1) return PKV_ERR_BAD_SHAPE;
+  const int32_t st = check_group(num_q_heads, num_kv_heads);
+  if (st != PKV_OK) return st;
+  return pkv::quant_few_rows(max_query_len, num_q_heads / num_kv_heads);
+}
+
+int64_t pkv_quant_attention_workspace_size(int32_t num_reqs, int32_t max_blocks_per_req,
+                                           int32_t num_q_heads, pkv_cache_layout layout,
+                                           int64_t chunk_keys,
+                                           const pkv_attention_options* options) {
+  int32_t st = check_layout(layout);
+  if (st != PKV_OK) return st;
+  if (num_reqs < 0 || max_blocks_per_req < 0 || chunk_keys < 0) return PKV_ERR_BAD_SHAPE;
+  if (chunk_keys >= (1ll << 30)) return PKV_ERR_BAD_SHAPE;
+  st = check_group(num_q_heads, layout.num_kv_heads);
+  if (st != PKV_OK) return st;
+  DeviceInfo* d;
+  st = device_info(&d);
+  if (st != PKV_OK) return st;
+  const int group = num_q_heads / layout.num_kv_heads;
+  long long splits = pkv::quant_most_splits(layout.num_kv_heads, group, d->num_sms);
+  if (options) {
+    if (options->reserved[0] != 0 && options->reserved[0] != PKV_OPTIONS_SCORES)
+      return PKV_ERR_BAD_SHAPE;
+    for (int i = 1; i < 4; ++i)
+      if (options->reserved[i] != 0) return PKV_ERR_BAD_SHAPE;
+    if (options->decode_splits < 0) return PKV_ERR_BAD_SHAPE;
+    if (options->decode_splits > 0) splits = options->decode_splits;
+  }
+  SharedHint sh;
+  st = shared_hint(options, layout, group, num_reqs, d->num_sms, &sh);
+  if (st != PKV_OK) return st;
+  const int gw = pkv::decode_heads_per_warp(group);
+  const int virt = layout.num_kv_heads * (group / gw);
+  WsLayout wl = ws_layout(num_reqs, virt, gw, layout.head_dim, splits, sh, num_q_heads);
+  quant_ws_layout(&wl, num_reqs, max_blocks_per_req, num_q_heads, layout.head_dim, splits,
+                  pkv::kFewUnits / group);
+  const int64_t keys = chunk_keys + sh.len;
+  const int64_t blocks = (keys + layout.block_size - 1) / layout.block_size + 1;
+  return static_cast<int64_t>(wl.quant_total + blocks * expanded_block_bytes(layout));
+}
+
+int32_t pkv_quant_paged_attention(void* out, const void* q, int64_t q_row_stride,
+                                  const void* kv_cache, const uint8_t* kv_scales,
+                                  const int32_t* block_table, int32_t max_blocks_per_req,
+                                  const int32_t* seq_lens, const int32_t* query_start_loc,
+                                  const int32_t* num_computed_tokens, int32_t num_reqs,
+                                  int32_t num_tokens, int32_t max_query_len, int32_t max_seq_len,
+                                  int32_t num_q_heads, float scale, pkv_cache_layout layout,
+                                  void* workspace, size_t workspace_bytes,
+                                  const pkv_attention_options* options, void* stream) {
+  return attention_impl(out, q, q_row_stride, kv_cache, block_table, max_blocks_per_req,
+                        seq_lens, query_start_loc, num_computed_tokens, num_reqs, num_tokens,
+                        max_query_len, max_seq_len, num_q_heads, scale, layout, workspace,
+                        workspace_bytes, options, stream, nullptr, true, kv_scales);
+}
+
+int32_t pkv_quant_paged_attention_with_write(
+    void* out, const void* q, int64_t q_row_stride, void* kv_cache, uint8_t* kv_scales,
+    const void* key, const void* value, int64_t key_row_stride, int64_t value_row_stride,
+    int64_t* slot_mapping, const int32_t* block_table, int32_t max_blocks_per_req,
+    const int32_t* seq_lens, const int32_t* query_start_loc, const int32_t* num_computed_tokens,
+    int32_t num_reqs, int32_t num_tokens, int32_t max_query_len, int32_t max_seq_len,
+    int32_t num_q_heads, float scale, pkv_cache_layout layout, void* workspace,
+    size_t workspace_bytes, const pkv_attention_options* options, void* stream) {
+  int32_t st = check_layout(layout);
+  if (st != PKV_OK) return st;
+  if (num_tokens < 0 || num_reqs < 0 || max_blocks_per_req < 0) return PKV_ERR_BAD_SHAPE;
+  st = quant_row_args(kv_cache, kv_scales, key, value, &key_row_stride, &value_row_stride,
+                      num_tokens, layout);
+  if (st != PKV_OK) return st;
+  if (num_tokens > 0 && (!query_start_loc || (num_reqs > 0 && (!block_table || !num_computed_tokens))))
+    return PKV_ERR_NULL_POINTER;
+  const pkv::WriteRowsArgs w = pkv::write_rows_args(
+      kv_cache, key, value, key_row_stride, value_row_stride, slot_mapping, block_table,
+      max_blocks_per_req, query_start_loc, num_computed_tokens, num_reqs, num_tokens,
+      layout.num_blocks, layout.block_size, layout.num_kv_heads, layout.head_dim, kv_scales);
+  return attention_impl(out, q, q_row_stride, kv_cache, block_table, max_blocks_per_req,
+                        seq_lens, query_start_loc, num_computed_tokens, num_reqs, num_tokens,
+                        max_query_len, max_seq_len, num_q_heads, scale, layout, workspace,
+                        workspace_bytes, options, stream, num_tokens > 0 ? &w : nullptr, true,
+                        kv_scales);
 }
 
 int32_t pkv_build_step_tables(int32_t* block_table, int32_t max_blocks_per_req,
@@ -740,6 +1061,8 @@ int32_t pkv_get_device_errors(uint32_t* flags, int32_t clear, void* stream) {
   if (e == cudaSuccess) e = pkv::read_errors_prefill(&v, clear != 0);
   if (e == cudaSuccess) e = pkv::read_errors_plan(&v, clear != 0);
   if (e == cudaSuccess) e = pkv::read_errors_tables(&v, clear != 0);
+  if (e == cudaSuccess) e = pkv::read_errors_quant(&v, clear != 0);
+  if (e == cudaSuccess) e = pkv::read_errors_quant_decode(&v, clear != 0);
   if (e != cudaSuccess) return cuda_fail(e, "reading device error word");
   *flags = v;
   return PKV_OK;

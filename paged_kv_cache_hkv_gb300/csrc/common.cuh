@@ -15,6 +15,7 @@ constexpr uint32_t kErrTimeout = 0x8u;
 constexpr uint32_t kErrShared = 0x10u;
 constexpr uint32_t kErrNoBlocks = 0x20u;
 constexpr uint32_t kErrRefCount = 0x40u;
+constexpr uint32_t kErrChunkKeys = 0x80u;
 
 // The attention kernels move keys in chunks of 16 (one decode stage, one
 // MMA K step). A cache block holds 8, 16 or 32 tokens, so a chunk is two
@@ -302,6 +303,20 @@ __device__ __forceinline__ KeyRange row_keys(const ScoreParams& s, long long t, 
   lo = max(lo, base);
   hi = min(hi, L);
   return lo < hi ? KeyRange{lo, hi} : KeyRange{0, 0};
+}
+
+// From the first key that any of a request's n rows (batch rows t.., positions
+// pos..) sees to past the last one; one row: its range.
+__device__ __forceinline__ KeyRange rows_keys(const ScoreParams& s, long long t, int pos, int n,
+                                              int L, int base) {
+  KeyRange k = row_keys(s, t, pos, L, base);
+  for (int i = 1; i < n; ++i) {
+    const KeyRange y = row_keys(s, t + i, pos + i, L, base);
+    if (y.lo >= y.hi) continue;
+    k.lo = k.lo < k.hi ? min(k.lo, y.lo) : y.lo;
+    k.hi = max(k.hi, y.hi);
+  }
+  return k;
 }
 
 // 16-key chunks that a decode row streams for its range. A row without keys

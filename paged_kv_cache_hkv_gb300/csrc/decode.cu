@@ -1,4 +1,4 @@
-// Split-KV paged decode attention and the split-KV combine (sm_103a).
+// Split-KV paged decode attention (sm_103a); the combine: combine.cu.
 //
 // Decode ("vLLM 架构源码解析（一）" §3.3.3, §4.2; "vllm v1 源码精读（三）" §4.2):
 // a request with one new token attends every one of its L cached keys, read
@@ -32,6 +32,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "decode.cuh"
 #include "launch.h"
 
 namespace pkv {
@@ -49,47 +50,6 @@ static __device__ uint32_t g_errors_decode;
 // per kv head. A request cut by a range boundary leaves one partial per
 // CTA that touched it, in slot (request + c) * V + virtual head; the
 // combine kernel merges them.
-struct DecodeParams {
-  const uint16_t* q;
-  long long q_stride;
-  uint16_t* out;
-  const int32_t* block_table;
-  int max_blocks;
-  const int32_t* seq_lens;
-  const int32_t* qsl;
-  int num_reqs, num_q_heads, num_blocks;
-  int head_groups;  // q-head groups of GW per kv head
-  int virt_heads;   // V = num_kv_heads * head_groups
-  int slab_vh;      // virtual heads per CTA slab (<= 8); slab s = virtual heads [s*slab_vh, ...)
-  int slab_kh;      // kv heads per slab = slab_vh / head_groups
-  long long splits; // C: CTAs along the stream (the grid is C x slabs)
-  int stages;       // depth of the shared-memory ring of K/V chunks (>= 2)
-  float scale_log2;
-  const int32_t* dec_prefix;
-  const uint32_t* hdr;
-  float2* part_ml;
-  float* part_o;
-  const int* bound;  // [C]: request holding the first position of CTA c's range (-1: none)
-  // Shared prefix: request shared_first + i with shared_use[i] streams only
-  // its chunks from shared_chunks on and always leaves partials; the combine
-  // kernel merges them with the shared items' partials of its row
-  // (shared_pieces of them).
-  int shared_first, shared_num, shared_chunks, shared_pieces;
-  const int32_t* shared_use;
-  const float2* shared_ml;
-  const float* shared_o;
-  // Capped, biased or range-masked scores (the kernel's SCORED variant); with
-  // a cap, scale_log2 holds 2 log2(e) scale / softcap instead.
-  bool scored;
-  ScoreParams score;
-  bool deep_combine;  // requests have many pieces each (see the combine kernel)
-};
-
-// CTA that owns position x of the decode stream: ranges start at floor(c * N / C).
-__device__ __forceinline__ long long owner_cta(long long x, long long N, long long C) {
-  return ((x + 1) * C + N - 1) / N - 1;
-}
-
 template <int D, int GW>
 struct DecodeCfg {
   static constexpr int LPK = D / 8;     // lanes per key row (8 bf16 per lane)
@@ -128,8 +88,6 @@ struct DecodeLayout {
   }
 };
 
-enum : int { kFirst = 1, kLast = 2, kInvalid = 4, kEnd = 8 };
-
 // Stage rows of key j (0..15) of a chunk, SH = log2(B). 8-token blocks land
 // as [K 0..7 | V 0..7 | K 8..15 | V 8..15], the others as [K 0..15 | V 0..15].
 template <int SH>
@@ -163,11 +121,6 @@ struct ReduceScatter {
     }
   }
 };
-
-// The running max of a head is only moved (and o, l rescaled) when a chunk's
-// max exceeds it by more than this many powers of two; in between, p may
-// reach 2^8, far inside fp32 range. The result is the same softmax.
-constexpr float kRescaleLog2 = 8.f;
 
 constexpr int kDecodeMaxSlab = 8;                        // virtual heads per CTA at most
 constexpr int kDecodeThreads = (kDecodeMaxSlab + 1) * 32;  // + the producer warp
@@ -635,159 +588,6 @@ __global__ void __launch_bounds__(kDecodeThreads)
   }
 }
 
-// ------------------------------------------------------------------ combine
-// One CTA per (range boundary c of the split, virtual head vg), one warp per
-// q head. A request is split when a boundary falls strictly inside its
-// chunks; the first such boundary is the one right after the CTA that owns
-// the request's first chunk, and that boundary's CTAs merge the request's
-// partials (one per non-empty range that touched it):
-//   M = max_p m_p,  o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
-// CTAs c >= C (one per request of a shared-prefix run) merge such a
-// request's decode partials with the shared-prefix items' partials of its
-// row; the boundary CTAs leave those requests to them.
-// Lanes first read the (m, l) of up to 32 pieces at once, then every lane
-// sums its dims over the pieces with independent loads.
-//
-// DEEP: for requests of many pieces (kDeepPieces), many loads in flight per
-// lane, in the same order of sums. It costs registers and, for a few pieces,
-// empty loads: the combine of 128 requests of some 5 pieces took 18 us with
-// it and 10.6 without; that of one request of 152 pieces 10 and 60.
-constexpr int kCombineLoads = 32;
-
-template <int D, int GW, bool DEEP>
-__global__ void __launch_bounds__(GW * 32) combine_kernel(const DecodeParams p) {
-  const long long c = blockIdx.x;
-  const int vg = blockIdx.y;
-  const int h = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long Cn = p.splits;
-  pdl_trigger();
-  pdl_wait();
-  auto in_shared_run = [&](int rr) -> bool {
-    const int i = rr - p.shared_first;
-    return p.shared_num > 0 && i >= 0 && i < p.shared_num && __ldg(p.shared_use + i);
-  };
-  int r, si = -1;  // si: the request's place in the shared-prefix run, if it has one
-  if (c >= Cn) {
-    si = static_cast<int>(c - Cn);
-    if (si >= p.shared_num || !__ldg(p.shared_use + si)) return;
-    r = p.shared_first + si;
-  } else {
-    if (c < 1) return;
-    r = p.bound[c];
-    if (r < 0) return;
-  }
-  const int pr = __ldg(p.dec_prefix + r);
-  const int nblk = __ldg(p.dec_prefix + r + 1) - pr;
-  const long long N = p.hdr[kHdrDecodeBlocks];
-  const long long cf = owner_cta(pr, N, Cn);
-  if (si < 0 && (cf != c - 1 || in_shared_run(r))) return;
-  // pieces j < nd: the decode partial of CTA cf + j, in slot (r + cf + j) * V
-  // + vg; pieces nd .. nd + ns - 1: the shared-prefix items' partials
-  const int nd = static_cast<int>(owner_cta(pr + nblk - 1, N, Cn) - cf + 1);
-  const int ns = si >= 0 ? p.shared_pieces : 0;
-  const int npieces = nd + ns;
-  const long long srow = static_cast<long long>(si) * p.num_q_heads + vg * GW + h;
-  const long long sstride = static_cast<long long>(p.shared_num) * p.num_q_heads;
-
-  // (m, l) of piece j; empty ranges wrote nothing and weigh zero
-  auto piece_ml = [&](int j) -> float2 {
-    if (j >= npieces) return make_float2(-INFINITY, 0.f);
-    if (j >= nd) return p.shared_ml[srow + (j - nd) * sstride];
-    const long long cc = cf + j;
-    if (cc * N / Cn == (cc + 1) * N / Cn) return make_float2(-INFINITY, 0.f);
-    return p.part_ml[((r + cc) * p.virt_heads + vg) * GW + h];
-  };
-  auto piece_o = [&](int j) -> const float* {
-    if (j >= nd) return p.shared_o + (srow + (j - nd) * sstride) * D;
-    return p.part_o + (((r + cf + j) * p.virt_heads + vg) * GW + h) * D;
-  };
-  float M = -INFINITY;
-  for (int j0 = 0; j0 < npieces; j0 += 32) M = fmaxf(M, piece_ml(j0 + lane).x);
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-
-  constexpr int E = D / 32;  // dims per lane
-  float acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  float Ls = 0.f;
-  for (int j0 = 0; j0 < npieces; j0 += 32) {
-    const float2 ml = piece_ml(j0 + lane);
-    const float wgt = (ml.x == -INFINITY) ? 0.f : exp2f(ml.x - M);
-    Ls += wgt * ml.y;
-    const int cnt = min(32, npieces - j0);
-    if constexpr (DEEP) {
-      const float* mine = piece_o(wgt == 0.f || j0 + lane >= npieces ? 0 : j0 + lane);
-      // kCombineLoads pieces' loads go out before the first is used. A piece of
-      // weight 0 (an empty range, which wrote no partial) reads piece 0's slot
-      // and is left out of the sum: 0 times an infinity there would be a NaN.
-      for (int i0 = 0; i0 < cnt; i0 += kCombineLoads) {
-        float vals[kCombineLoads][E], wj[kCombineLoads];
-#pragma unroll
-        for (int i = 0; i < kCombineLoads; ++i) {
-          wj[i] = __shfl_sync(0xffffffffu, wgt, (i0 + i) & 31);
-          const float* src = reinterpret_cast<const float*>(__shfl_sync(
-                                 0xffffffffu, reinterpret_cast<unsigned long long>(mine), (i0 + i) & 31)) +
-                             lane * E;
-          if constexpr (E == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(src);
-            vals[i][0] = v.x;
-            vals[i][1] = v.y;
-            vals[i][2] = v.z;
-            vals[i][3] = v.w;
-          } else {
-            const float2 v = *reinterpret_cast<const float2*>(src);
-            vals[i][0] = v.x;
-            vals[i][1] = v.y;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kCombineLoads; ++i)
-          if (wj[i] != 0.f) {  // (nor is there a piece behind the last)
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] += wj[i] * vals[i][e];
-          }
-      }
-    } else {
-      // 8 pieces' loads in flight per lane; a piece of weight 0 as above
-#pragma unroll 8
-      for (int j = 0; j < cnt; ++j) {
-        const float wj = __shfl_sync(0xffffffffu, wgt, j);
-        const float* src = piece_o(wj == 0.f ? 0 : j0 + j) + lane * E;
-        if constexpr (E == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(src);
-          if (wj != 0.f) {
-            acc[0] += wj * v.x;
-            acc[1] += wj * v.y;
-            acc[2] += wj * v.z;
-            acc[3] += wj * v.w;
-          }
-        } else {
-          const float2 v = *reinterpret_cast<const float2*>(src);
-          if (wj != 0.f) {
-            acc[0] += wj * v.x;
-            acc[1] += wj * v.y;
-          }
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, off);
-  const float inv = p.scored && Ls == 0.f ? 0.f : 1.f / Ls;  // no key seen: zeros
-  const int row = __ldg(p.qsl + r);
-  uint16_t* dst =
-      p.out + (static_cast<long long>(row) * p.num_q_heads + vg * GW + h) * D + lane * E;
-  if constexpr (E == 4) {
-    uint2 ov;
-    ov.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    ov.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
-    *reinterpret_cast<uint2*>(dst) = ov;
-  } else {
-    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-  }
-}
-
 // ------------------------------------------------------------------ host
 #ifndef PKV_DECODE_MAX_STAGES
 #define PKV_DECODE_MAX_STAGES 6
@@ -798,13 +598,6 @@ __global__ void __launch_bounds__(GW * 32) combine_kernel(const DecodeParams p) 
 // 64 KB took the mixed-step decode from 830 to 788 us)
 constexpr int kDecodeMinStages = 2;
 constexpr int kDecodeMaxStages = PKV_DECODE_MAX_STAGES;
-
-// Splits per request from which the combine's DEEP variant is launched (one
-// decode of 250 keys, 16 pieces: 11.4 us a step with it, 16.4 without). Not in
-// a plain step with prefill rows: such a step's requests are mostly not
-// decodes, and where none is the DEEP kernel's registers only make its idle
-// launch longer (31.5 instead of 31.0 us for the mixed step's prefill rows).
-constexpr long long kDeepPieces = 8;
 
 // Consumer warps per SM the default split aims at (CTAs per SM = this / slab
 // size, at least one): about the count that streamed fastest.
@@ -906,10 +699,7 @@ static cudaError_t launch_decode_t(const DecodeParams& p, const CUtensorMap& kv_
   e = launch_pdl(kern, grid, dim3((p.slab_vh + 1) * 32), smem, stream, kv_map, q);
   if (e == cudaSuccess && trace) e = cudaEventRecord(static_cast<cudaEvent_t>(trace[3]), stream);
   if (e != cudaSuccess) return e;
-  return launch_pdl(p.deep_combine ? combine_kernel<D, GW, true> : combine_kernel<D, GW, false>,
-                    dim3(static_cast<unsigned>(p.splits + p.shared_num),
-                         static_cast<unsigned>(p.virt_heads)),
-                    dim3(GW * 32), 0, stream, p);
+  return launch_combine(p, D, GW, stream);
 }
 
 // Calls F<D, GW, SH>::run(args...) for the instantiated shapes: head_dim 64 or
@@ -955,43 +745,9 @@ cudaError_t decode_full_wave_splits(int head_dim, int num_kv_heads, int group, i
 
 cudaError_t launch_decode(const AttnArgs& a, const AttnWorkspace& ws, const CUtensorMap& kv_map,
                           long long splits, int num_sms, cudaStream_t stream, void** trace) {
-  const int group = a.num_q_heads / a.num_kv_heads;
-  const int gw = decode_heads_per_warp(group);
-  DecodeParams p;
-  p.q = a.q;
-  p.q_stride = a.q_stride;
-  p.out = a.out;
-  p.block_table = a.block_table;
-  p.max_blocks = a.max_blocks;
-  p.seq_lens = a.seq_lens;
-  p.qsl = a.qsl;
-  p.num_reqs = a.num_reqs;
-  p.num_q_heads = a.num_q_heads;
-  p.num_blocks = a.num_blocks;
-  p.head_groups = group / gw;
-  p.virt_heads = a.num_kv_heads * p.head_groups;
-  decode_slab(a.num_kv_heads, group, &p.slab_vh, &p.slab_kh);
-  p.splits = splits;
-  p.scale_log2 = a.scale * kLog2e;
-  p.scored = a.scored;
-  p.score = a.score;
-  p.deep_combine =
-      splits >= kDeepPieces * a.num_reqs && (a.scored || a.max_query_len == 1);
-  if (a.score.softcap > 0.f) p.scale_log2 = 2.f * kLog2e * (a.scale / a.score.softcap);
-  p.dec_prefix = ws.dec_prefix;
-  p.hdr = ws.hdr;
-  p.part_ml = ws.part_ml;
-  p.part_o = ws.part_o;
-  p.bound = ws.bound;
-  p.shared_first = a.shared_first;
-  p.shared_num = a.shared_num;
-  p.shared_chunks = a.shared_len / kChunkKeys;
-  p.shared_pieces = a.shared_pieces;
-  p.shared_use = ws.casc_use;
-  p.shared_ml = ws.casc_ml;
-  p.shared_o = ws.casc_o;
-  return decode_dispatch<LaunchOp>(a.head_dim, gw, a.block_shift, p, kv_map, num_sms, stream,
-                                   trace);
+  const DecodeParams p = decode_params(a, ws, splits);
+  return decode_dispatch<LaunchOp>(a.head_dim, decode_heads_per_warp(a.num_q_heads / a.num_kv_heads),
+                                   a.block_shift, p, kv_map, num_sms, stream, trace);
 }
 
 cudaError_t read_errors_decode(uint32_t* out, bool clear) {

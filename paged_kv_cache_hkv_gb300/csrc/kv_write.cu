@@ -210,7 +210,8 @@ WriteRowsArgs write_rows_args(void* pool, const void* key, const void* value,
                               long long key_stride, long long value_stride, int64_t* slots,
                               const int32_t* block_table, int max_blocks, const int32_t* qsl,
                               const int32_t* num_computed, int num_reqs, int num_tokens,
-                              int num_blocks, int block_size, int num_kv_heads, int head_dim) {
+                              int num_blocks, int block_size, int num_kv_heads, int head_dim,
+                              uint8_t* scales) {
   WriteRowsArgs w;
   w.pool = static_cast<uint4*>(pool);
   w.key = static_cast<const uint4*>(key);
@@ -227,6 +228,8 @@ WriteRowsArgs write_rows_args(void* pool, const void* key, const void* value,
   w.num_blocks = num_blocks;
   w.shift = static_cast<int>(__builtin_ctz(static_cast<unsigned>(block_size)));
   w.vec_per_row = num_kv_heads * head_dim / 8;
+  w.scales = scales;
+  w.vec_per_head = head_dim / 8;
   return w;
 }
 

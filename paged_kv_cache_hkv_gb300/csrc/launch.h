@@ -35,6 +35,17 @@ struct AttnWorkspace {
   int32_t* casc_use;     // [shared_num]: 1 if the request takes its prefix from the shared items
   float2* casc_ml;       // [pieces][shared_num][Hq]: (max in log2 units, sum) of each piece
   float* casc_o;         // [pieces][shared_num][Hq][D]: unnormalised output of each piece
+  // 8-bit pool: the blocks of the prefill requests that are expanded to bf16 (the
+  // k-th prefill request's entries [ex_first[k], ex_first[k] + its count))
+  int32_t* ex_first;     // [R + 1]
+  int32_t* ex_prefix;    // [R + 2]: expanded blocks before the k-th prefill request
+  int32_t* ex_table;     // [R][max_blocks]: scratch block of each expanded entry
+  uint4* ex_pool;        // [ex_capacity] bf16 blocks
+  int ex_capacity;
+  // 8-bit pool: partials of requests with several rows on the decode stream, two
+  // per CTA (the request it goes on with, the one it leaves): [2 C][few][Hq]
+  float2* few_ml;
+  float* few_o;          // [2 C][few][Hq][D]
 };
 
 struct AttnArgs {
@@ -60,6 +71,19 @@ struct AttnArgs {
   long long decode_splits;  // CTAs along the decode stream (C)
   bool scored;         // some field of score is in use: the kernels' scored variants run
   ScoreParams score;
+  const uint8_t* kv_scales;  // 8-bit pool: the codes' scales; null = bf16 pool
+  int few;  // requests of up to this many new tokens are on the decode stream (bf16 pool: 1)
+};
+
+// The blocks that expand_kernel turns into bf16 (AttnWorkspace's ex_ fields).
+struct ExpandArgs {
+  const uint32_t* hdr;
+  const int32_t* req;
+  const int32_t* first;
+  const int32_t* prefix;
+  int32_t* table;
+  uint4* pool;
+  int capacity;
 };
 
 // Key pieces of the shared-prefix items: enough items to fill the device
@@ -141,7 +165,8 @@ WriteRowsArgs write_rows_args(void* pool, const void* key, const void* value,
                               long long key_stride, long long value_stride, int64_t* slots,
                               const int32_t* block_table, int max_blocks, const int32_t* qsl,
                               const int32_t* num_computed, int num_reqs, int num_tokens,
-                              int num_blocks, int block_size, int num_kv_heads, int head_dim);
+                              int num_blocks, int block_size, int num_kv_heads, int head_dim,
+                              uint8_t* scales = nullptr);
 cudaError_t launch_mapped_write(const WriteRowsArgs& w, cudaStream_t stream);
 cudaError_t launch_kv_write(void* pool, const void* key, const void* value, long long key_stride,
                             long long value_stride, const int64_t* slots, int num_tokens,
@@ -186,10 +211,44 @@ cudaError_t launch_release_blocks(const int32_t* block_table, int max_blocks, in
 // Scratch of a release (0: it needs none).
 size_t release_workspace_bytes(int num_released, int max_blocks);
 
+cudaError_t launch_quant_write(void* codes, uint8_t* scales, const void* key, const void* value,
+                               long long key_stride, long long value_stride, const int64_t* slots,
+                               int num_tokens, int num_blocks, int shift, int num_kv_heads,
+                               int head_dim, int num_sms, cudaStream_t stream);
+cudaError_t launch_quant_mapped_write(const WriteRowsArgs& w, cudaStream_t stream);
+cudaError_t launch_quant_read(void* key, void* value, long long key_stride, long long value_stride,
+                              const void* codes, const uint8_t* scales, const int64_t* slots,
+                              int num_tokens, int num_blocks, int shift, int num_kv_heads,
+                              int head_dim, int num_sms, cudaStream_t stream);
+cudaError_t launch_quant_copy(void* dst, uint8_t* dst_scales, int dst_num_blocks, const void* src,
+                              const uint8_t* src_scales, int src_num_blocks, const int32_t* pairs,
+                              int num_pairs, int block_size, int num_kv_heads, int head_dim,
+                              int num_sms, cudaStream_t stream);
+cudaError_t launch_expand(const AttnArgs& a, const ExpandArgs& x, int num_sms,
+                          cudaStream_t stream);
+
+// Query rows x q heads of one kv head that the 8-bit decode holds at most: 8
+// warps of 16.
+constexpr int kFewUnits = 64;
+// Requests of up to this many new tokens are on the 8-bit pool's decode stream
+// (quant_decode.cu).
+int quant_few_rows(int max_query_len, int group);
+// The most splits that quant_full_wave_splits gives for any max_query_len.
+long long quant_most_splits(int num_kv_heads, int group, int num_sms);
+cudaError_t quant_full_wave_splits(int head_dim, int num_kv_heads, int group, int block_shift,
+                                   int max_query_len, bool scored, int num_sms, long long* splits);
+cudaError_t launch_quant_decode(const AttnArgs& a, const AttnWorkspace& ws,
+                                const CUtensorMap& kv_map, long long splits, int num_sms,
+                                cudaStream_t stream, void** trace);
+// kv heads of one CTA of the 8-bit decode
+int quant_slab_heads(int num_kv_heads, int group, int max_query_len);
+
 cudaError_t read_errors_kvwrite(uint32_t* out, bool clear);
 cudaError_t read_errors_decode(uint32_t* out, bool clear);
 cudaError_t read_errors_prefill(uint32_t* out, bool clear);
 cudaError_t read_errors_plan(uint32_t* out, bool clear);
 cudaError_t read_errors_tables(uint32_t* out, bool clear);
+cudaError_t read_errors_quant(uint32_t* out, bool clear);
+cudaError_t read_errors_quant_decode(uint32_t* out, bool clear);
 
 }  // namespace pkv

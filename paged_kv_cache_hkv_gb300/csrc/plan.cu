@@ -68,7 +68,8 @@ __device__ __forceinline__ bool lengths_bad(const AttnArgs& a, int r, int q0, in
   return n > 0 && nent > a.max_blocks;
 }
 
-// Counts of one request: decode 16-key chunks, is-prefill, prefill work items.
+// Counts of one request: decode 16-key chunks (one new token, or up to a.few of
+// them), is-prefill, prefill work items.
 // A decode request that takes its shared prefix from the shared items
 // streams only the chunks past the prefix.
 // SCORED: it streams the chunks of its row's key range.
@@ -81,16 +82,16 @@ __device__ __forceinline__ Int3 plan_counts(const AttnArgs& a, const AttnWorkspa
   const long long nblk = (static_cast<long long>(L) + kChunkKeys - 1) / kChunkKeys;
   if (lengths_bad(a, r, q0, q1, c, L)) {
     if (flag) atomicOr(&g_errors_plan, kErrLengths);
-  } else if (n == 1) {
+  } else if (n >= 1 && n <= a.few) {
     v.a = static_cast<int>(nblk);
     const int i = r - a.shared_first;
     if constexpr (SCORED) {
       const bool shared = a.shared_num > 0 && i >= 0 && i < a.shared_num && ws.casc_use[i];
-      v.a = range_chunks(row_keys(a.score, q0, c, L, shared ? a.shared_len : 0));
+      v.a = range_chunks(rows_keys(a.score, q0, c, n, L, shared ? a.shared_len : 0));
     } else if (a.shared_num > 0 && i >= 0 && i < a.shared_num && ws.casc_use[i]) {
       v.a -= a.shared_len / kChunkKeys;
     }
-  } else if (n > 1) {
+  } else if (n > a.few) {
     v.b = 1;
     v.c = ((n + tile_q - 1) / tile_q) * a.num_kv_heads;
   }
@@ -173,7 +174,103 @@ __device__ int plan_shared(const AttnArgs& a, const AttnWorkspace& ws, int tile_
   return qtiles * a.shared_pieces * a.num_kv_heads;
 }
 
+// The blocks that the 8-bit pool's prefill requests need in bf16: of each
+// request the entries of its L keys, SCORED those between the first and the
+// last key that some row sees. A warp per request; the rows of long requests are
+// looked through by the whole CTA (8191 rows by one warp would be 256 loads one
+// after the other).
+constexpr int kExpandLong = 32, kExpandLongRows = 512;
+
 template <bool SCORED>
+__device__ void plan_expand(const AttnArgs& a, const AttnWorkspace& ws, int nreq) {
+  __shared__ Int3 total;
+  __shared__ int long_k[kExpandLong], long_num, lo_min, hi_max;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) long_num = 0;
+  __syncthreads();  // (and pf_req is written)
+  auto store = [&](int k, int lo, int hi) {
+    const int e0 = lo >> a.block_shift;
+    ws.ex_first[k] = e0;
+    ws.ex_prefix[k] = lo < hi ? ((hi + (1 << a.block_shift) - 1) >> a.block_shift) - e0 : 0;
+  };
+  for (int k = warp; k < nreq; k += 32) {
+    const int r = ws.pf_req[k];
+    if (r < 0) {
+      if (lane == 0) store(k, 0, a.shared_len);
+      continue;
+    }
+    const int q0 = __ldg(a.qsl + r), n = __ldg(a.qsl + r + 1) - q0, L = __ldg(a.seq_lens + r);
+    int lo = 0, hi = L;
+    if constexpr (SCORED) {
+      if (n > kExpandLongRows) {
+        int at = kExpandLong;
+        if (lane == 0) at = atomicAdd(&long_num, 1);
+        at = __shfl_sync(0xffffffffu, at, 0);
+        if (at < kExpandLong) {
+          if (lane == 0) long_k[at] = k;
+          continue;
+        }
+      }
+      lo = 0x7fffffff;
+      hi = 0;
+      for (int i = lane; i < n; i += 32) {
+        const KeyRange y = row_keys(a.score, static_cast<long long>(q0) + i, L - n + i, L, 0);
+        if (y.lo < y.hi) {
+          lo = min(lo, y.lo);
+          hi = max(hi, y.hi);
+        }
+      }
+      lo = __reduce_min_sync(0xffffffffu, lo);
+      hi = __reduce_max_sync(0xffffffffu, hi);
+      if (hi == 0) lo = 0;
+    }
+    if (lane == 0) store(k, lo, hi);
+  }
+  __syncthreads();
+  if constexpr (SCORED) {
+    const int num = min(long_num, kExpandLong);
+    for (int x = 0; x < num; ++x) {
+      if (threadIdx.x == 0) {
+        lo_min = 0x7fffffff;
+        hi_max = 0;
+      }
+      __syncthreads();
+      const int k = long_k[x], r = ws.pf_req[k];
+      const int q0 = __ldg(a.qsl + r), n = __ldg(a.qsl + r + 1) - q0, L = __ldg(a.seq_lens + r);
+      int lo = 0x7fffffff, hi = 0;
+      for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const KeyRange y = row_keys(a.score, static_cast<long long>(q0) + i, L - n + i, L, 0);
+        if (y.lo < y.hi) {
+          lo = min(lo, y.lo);
+          hi = max(hi, y.hi);
+        }
+      }
+      lo = __reduce_min_sync(0xffffffffu, lo);
+      hi = __reduce_max_sync(0xffffffffu, hi);
+      if (lane == 0) {
+        atomicMin(&lo_min, lo);
+        atomicMax(&hi_max, hi);
+      }
+      __syncthreads();
+      if (threadIdx.x == 0) store(k, hi_max > 0 ? lo_min : 0, hi_max);
+      __syncthreads();
+    }
+  }
+  // counts to their exclusive prefix sums
+  const int per = (nreq + 1023) / 1024;
+  const int k0 = min(nreq, static_cast<int>(threadIdx.x) * per), k1 = min(nreq, k0 + per);
+  Int3 sum{0, 0, 0};
+  for (int k = k0; k < k1; ++k) sum.a += ws.ex_prefix[k];
+  Int3 run = block_exclusive_scan(sum, &total);
+  for (int k = k0; k < k1; ++k) {
+    const int n = ws.ex_prefix[k];
+    ws.ex_prefix[k] = run.a;
+    run.a += n;
+  }
+  if (threadIdx.x == 0) ws.ex_prefix[nreq] = total.a;
+}
+
+template <bool SCORED, bool QUANT>
 __device__ void plan_block(const AttnArgs& a, const AttnWorkspace& ws, int tile_q) {
   __shared__ Int3 total;
   const int shared_items = a.shared_num > 0 ? plan_shared(a, ws, tile_q) : 0;
@@ -227,13 +324,16 @@ __device__ void plan_block(const AttnArgs& a, const AttnWorkspace& ws, int tile_
     ws.hdr[kHdrPrefillItems] = static_cast<uint32_t>(nitems);
     ws.hdr[kHdrPrefillNext] = 0u;
   }
+  // (thread 0 may still be about to list the shared-prefix items: plan_expand
+  // starts with a barrier)
+  if constexpr (QUANT) plan_expand<SCORED>(a, ws, total.b + (shared_items > 0 ? 1 : 0));
 }
 
-template <bool SCORED>
+template <bool SCORED, bool QUANT>
 __global__ void __launch_bounds__(1024) plan_kernel(AttnArgs a, AttnWorkspace ws, int tile_q) {
   pdl_trigger();
   pdl_wait();
-  plan_block<SCORED>(a, ws, tile_q);
+  plan_block<SCORED, QUANT>(a, ws, tile_q);
 }
 
 // The plan and the step's cache write in one launch: CTA 0 plans (it is
@@ -244,30 +344,40 @@ __global__ void __launch_bounds__(1024) plan_kernel(AttnArgs a, AttnWorkspace ws
 // follow wait for both.
 constexpr int kPrologueTokens = 8;
 
-template <bool SCORED>
+template <bool SCORED, bool QUANT>
 __global__ void __launch_bounds__(1024)
     prologue_kernel(AttnArgs a, AttnWorkspace ws, int tile_q, WriteRowsArgs w) {
   pdl_trigger();
   pdl_wait();
   if (blockIdx.x == 0) {
-    plan_block<SCORED>(a, ws, tile_q);
+    plan_block<SCORED, QUANT>(a, ws, tile_q);
     return;
   }
   const int warp = threadIdx.x >> 5;
   if (warp >= kPrologueTokens) return;
   const long long t = static_cast<long long>(blockIdx.x - 1) * kPrologueTokens + warp;
-  if (t < w.num_tokens) write_token_rows(w, t, &g_errors_plan);
+  if (t >= w.num_tokens) return;
+  if constexpr (!QUANT)
+    write_token_rows(w, t, &g_errors_plan);
+  else if (w.vec_per_head == 16)
+    quant_token_rows<128>(w, t, &g_errors_plan);
+  else
+    quant_token_rows<64>(w, t, &g_errors_plan);
 }
 
 cudaError_t launch_plan(const AttnArgs& a, const AttnWorkspace& ws, cudaStream_t stream,
                         const WriteRowsArgs* write) {
   const int group = a.num_q_heads / a.num_kv_heads;
+  const bool quant = a.kv_scales != nullptr;
   if (write && write->num_tokens > 0) {
     const int write_ctas = (write->num_tokens + kPrologueTokens - 1) / kPrologueTokens;
-    return launch_pdl(a.scored ? prologue_kernel<true> : prologue_kernel<false>, dim3(1 + write_ctas), dim3(1024), 0, stream, a, ws,
-                      128 / group, *write);
+    auto kern = quant ? (a.scored ? prologue_kernel<true, true> : prologue_kernel<false, true>)
+                      : (a.scored ? prologue_kernel<true, false> : prologue_kernel<false, false>);
+    return launch_pdl(kern, dim3(1 + write_ctas), dim3(1024), 0, stream, a, ws, 128 / group, *write);
   }
-  return launch_pdl(a.scored ? plan_kernel<true> : plan_kernel<false>, dim3(1), dim3(1024), 0, stream, a, ws, 128 / group);
+  auto kern = quant ? (a.scored ? plan_kernel<true, true> : plan_kernel<false, true>)
+                    : (a.scored ? plan_kernel<true, false> : plan_kernel<false, false>);
+  return launch_pdl(kern, dim3(1), dim3(1024), 0, stream, a, ws, 128 / group);
 }
 
 cudaError_t read_errors_plan(uint32_t* out, bool clear) {

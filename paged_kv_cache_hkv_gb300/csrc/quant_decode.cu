@@ -1,0 +1,755 @@
+// Split-KV decode over the 8-bit pool (sm_103a): requests of one new token, and
+// of a few (guessed tokens that are checked at once), over e4m3 codes with a
+// power-of-two scale per row (quant.cuh).
+//
+// The work split is the bf16 decode's (decode.cu): the step's decode stream of
+// (request, 16-key chunk) positions is cut into C equal ranges, a CTA streams its
+// range's chunks through a ring of shared-memory stages that a producer warp
+// fills by TMA, and what a range boundary cuts leaves partials for the combine
+// kernel.
+//
+// The math is on the tensor cores, for half the bytes a key leaves half the time:
+// the bf16 decode's FMAs take 40% of the issue slots at 7 TB/s, and twice the keys
+// a second plus their conversion would be over all of them. A consumer warp holds
+// up to 16 units (query row x q head) of one kv head, eight to a tile:
+//   S [units x keys]: mma.m16n8k32 on the codes as they are. bf16 q's 8
+//     significant bits are two e4m3 numbers of 4: q 2^-e = hi + lo / 16, exactly
+//     but for 2^-23 of the row's largest. The tile's 16 rows are hi of its eight units
+//     and lo of the same; S = (S_hi + S_lo / 16) 2^e times the key's scale.
+//   O^T [dims x units] += V^T P^T: mma.m16n8k16 in bf16. The S tile's registers
+//     are the P^T operand as they stand; V's scale goes into P (fp32, rounded once
+//     to bf16). ldmatrix.trans hands a thread two keys' bytes of two neighbouring
+//     dims, which are the even and odd rows of a V^T tile; a code becomes a bf16
+//     by moving its exponent and mantissa into place and a product with 2^120.
+// K, V and the scales of a chunk are a copy or two each: a 4-D box lands them as
+// [K|V][kv head][16 keys][D], swizzled, so that ldmatrix finds no bank conflict.
+#include <mutex>
+#include <vector>
+
+#include "decode.cuh"
+#include "quant.cuh"
+
+namespace pkv {
+
+static __device__ uint32_t g_errors_quant_decode;
+
+constexpr int kQuantWarps = 8;  // consumer warps of a CTA at most
+constexpr int kQuantDecodeThreads = (kQuantWarps + 1) * 32;
+
+struct QuantDecodeParams : DecodeParams {
+  const uint8_t* scales;
+  int num_kv_heads, group_shift;
+  int slab_heads;      // kv heads of a CTA
+  int warps_per_head;  // consumer warp w: head w / warps_per_head of the slab, its unit
+                       // tiles from (w % warps_per_head) * MT on
+};
+
+// Shared memory of a CTA (bytes from a 1024-aligned base): S stages of the
+// chunk's codes and scales, two words of metadata a stage, the barriers.
+struct QuantLayout {
+  uint32_t kv_bytes, scale_bytes, stage_bytes, meta_off, bar_off, total;
+  __host__ __device__ QuantLayout(int head_dim, int kh, int num_kv_heads, int S) {
+    kv_bytes = 32u * static_cast<uint32_t>(kh) * head_dim;
+    scale_bytes = 32u * static_cast<uint32_t>(num_kv_heads);
+    stage_bytes = (kv_bytes + scale_bytes + 1023u) & ~1023u;
+    meta_off = S * stage_bytes;
+    bar_off = meta_off + S * 32u;
+    total = bar_off + 2u * S * 8u;
+  }
+};
+
+__device__ __forceinline__ void tma_load_4d_hint(void* dst, const CUtensorMap* map, int c0, int c1,
+                                                 int c2, int c3, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar)),
+      "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The codes in bytes 1 and 3 (odd) or 0 and 2 (even) of w as two bf16. Sign,
+// exponent and mantissa moved to bf16's places make the value times 2^-120 (the
+// exponents' biases are 7 and 127), subnormal codes and all; the product puts it right.
+__device__ __forceinline__ uint32_t bf16_of_codes(uint32_t sign_src, uint32_t mag_src) {
+  const uint32_t b = (sign_src & 0x80008000u) | (mag_src & 0x07f007f0u);
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(b), "r"(0x7b807b80u));  // 2^120 twice
+  return r;
+}
+__device__ __forceinline__ uint32_t codes_even(uint32_t w) { return bf16_of_codes(w << 8, w << 4); }
+__device__ __forceinline__ uint32_t codes_odd(uint32_t w) { return bf16_of_codes(w, w >> 4); }
+
+template <int D, int SH, int MT, bool SCORED>
+__global__ void __launch_bounds__(kQuantDecodeThreads)
+    quant_decode_kernel(const __grid_constant__ CUtensorMap kv_map, const QuantDecodeParams p) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int KH = p.slab_heads, WPH = p.warps_per_head, NW = KH * WPH, HKV = p.num_kv_heads;
+  const uint32_t S = static_cast<uint32_t>(p.stages);
+  const QuantLayout lay(D, KH, HKV, p.stages);
+  // of a stage: (flags, first key, out_base, -), and with kFirst (batch row, rows, keys, -)
+  int4* meta = reinterpret_cast<int4*>(base + lay.meta_off);
+  uint64_t* full = reinterpret_cast<uint64_t*>(base + lay.bar_off);
+  uint64_t* empty = full + S;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == NW && lane == 0) prefetch_tensormap(&kv_map);
+  pdl_wait();
+
+  const long long Cn = p.splits, c = blockIdx.x;
+  const int slab = blockIdx.y;
+  const long long N = p.hdr[kHdrDecodeBlocks];
+  const int r_start = __ldg(p.bound + c);  // -1 when the step has no decode chunk
+  const long long x0 = c * N / Cn, x1 = (c + 1) * N / Cn;
+  if (x0 >= x1) return;
+  if (threadIdx.x == 0) {
+    for (uint32_t s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], NW);
+    }
+    fence_barrier_init();
+  }
+  __syncthreads();
+
+  // keys of request r before its first streamed one (its shared prefix)
+  auto key_base = [&](int r) -> int {
+    const int i = r - p.shared_first;
+    return (p.shared_num > 0 && i >= 0 && i < p.shared_num && __ldg(p.shared_use + i))
+               ? p.shared_chunks * kChunkKeys
+               : 0;
+  };
+
+  if (warp == NW) {
+    // ================= producer warp
+    const uint64_t l2_policy = l2_evict_first_policy();
+    // A request, the whole warp alike: its batch rows and keys, the keys [lo, hi)
+    // that its rows see between them, and 32 entries of its block table row.
+    struct Request {
+      int t, n, L, lo, hi, skip, win_base, win;
+    };
+    auto entry_of = [&](int a) -> int { return SH == 4 ? a : (SH == 5 ? a >> 1 : 2 * a); };
+    auto window = [&](int rr, Request& q, int e0) {
+      q.win_base = e0;
+      const int nent = (q.hi + (1 << SH) - 1) >> SH, j = e0 + lane;
+      q.win =
+          j < nent ? __ldg(p.block_table + static_cast<long long>(rr) * p.max_blocks + j) : -1;
+    };
+    auto fetch = [&](int rr, int b) -> Request {  // its chunk b is next
+      Request q;
+      q.t = __ldg(p.qsl + rr);
+      q.n = __ldg(p.qsl + rr + 1) - q.t;
+      q.L = __ldg(p.seq_lens + rr);
+      q.lo = key_base(rr);
+      q.hi = q.L;
+      if constexpr (SCORED) {
+        const int kb = q.lo;
+        int a = 0x7fffffff, z = 0;
+        for (int i = lane; i < q.n; i += 32) {
+          const KeyRange k =
+              row_keys(p.score, static_cast<long long>(q.t) + i, q.L - q.n + i, q.L, kb);
+          if (k.lo < k.hi) {
+            a = min(a, k.lo);
+            z = max(z, k.hi);
+          }
+        }
+        q.hi = __reduce_max_sync(0xffffffffu, z);
+        a = __reduce_min_sync(0xffffffffu, a);
+        q.lo = q.hi > 0 ? a : 0;
+      }
+      q.skip = q.lo / kChunkKeys;
+      window(rr, q, entry_of(b + q.skip));
+      return q;
+    };
+    int r = r_start;
+    int pr = __ldg(p.dec_prefix + r);  // stream position of the request's first chunk
+    int nblk = __ldg(p.dec_prefix + r + 1) - pr;
+    int blk = static_cast<int>(x0 - pr);
+    Request q = fetch(r, blk);
+    // The next request is fetched one ahead, so that a boundary waits on no
+    // load; only one with chunks (the rows of another may lie behind the batch's).
+    int nx_pn = -1;
+    Request nx{};
+    auto fetch_next = [&]() {
+      nx_pn = r + 1 < p.num_reqs ? __ldg(p.dec_prefix + r + 2) : -1;
+      if (nx_pn - (pr + nblk) > 0) nx = fetch(r + 1, 0);
+    };
+    fetch_next();
+    int out_base = -1;
+    bool new_piece = true, ok = true;
+    long long x = x0;
+    uint32_t issued = 0, s = 0, eph = 0;
+    for (;; ++issued) {
+      if (issued >= S && !mbar_wait(&empty[s], eph)) {
+        if (lane == 0) atomicOr(&g_errors_quant_decode, kErrTimeout);
+        ok = false;
+        break;
+      }
+      if (x >= x1) {
+        if (lane == 0) {
+          meta[2 * s] = make_int4(kEnd, 0, 0, 0);
+          mbar_arrive(&full[s]);
+        }
+        ++issued;
+        break;
+      }
+      if (new_piece) {
+        // a request split over several CTAs, or one whose shared prefix is
+        // attended elsewhere, leaves a partial for the combine kernel
+        const long long cf = owner_cta(pr, N, Cn), cl = owner_cta(pr + nblk - 1, N, Cn);
+        out_base = cf == cl && key_base(r) == 0 ? -1
+                   : q.n == 1 ? static_cast<int>((r + c) * p.virt_heads)
+                              : static_cast<int>(2 * c + (pr >= x0 ? 1 : 0));
+      }
+      const int ab = blk + q.skip;  // the chunk's place in the request
+      const int e0 = entry_of(ab), e_hi = SH == 3 ? e0 + 1 : e0;
+      if (e0 < q.win_base || e_hi >= q.win_base + 32) window(r, q, e0);
+      const int phys = __shfl_sync(0xffffffffu, q.win, e0 - q.win_base);
+      const int k0 = ab * kChunkKeys;
+      const bool none = q.lo >= q.hi;  // no row sees a key
+      bool valid = phys >= 0 && phys < p.num_blocks;
+      bool first = true, second = false;  // 8-token blocks: keys 0..7 and 8..15 are wanted
+      int phys1 = -1;
+      if constexpr (SH == 3) {
+        phys1 = __shfl_sync(0xffffffffu, q.win, e_hi - q.win_base);
+        second = q.hi - k0 > 8;
+        first = !SCORED || q.lo - k0 < 8;
+        valid = valid || !first;
+        if (second) valid = valid && phys1 >= 0 && phys1 < p.num_blocks;
+      }
+      if (none) valid = false;
+      if (lane == 0) {
+        const bool last = blk == nblk - 1 || x == x1 - 1;
+        meta[2 * s] = make_int4((new_piece ? kFirst : 0) | (last ? kLast : 0) | (valid ? 0 : kInvalid),
+                                k0, out_base, 0);
+        if (new_piece) meta[2 * s + 1] = make_int4(q.t, q.n, q.L, key_base(r));
+        unsigned char* stage = base + s * lay.stage_bytes;
+        unsigned char* sc = stage + lay.kv_bytes;
+        if (!valid && !none) atomicOr(&g_errors_quant_decode, kErrBlockRange);
+        if (valid) {
+          const bool half = SH == 3 && !(first && second);
+          fence_proxy_async_smem();
+          mbar_arrive_expect_tx(&full[s], (lay.kv_bytes + lay.scale_bytes) >> (half ? 1 : 0));
+          const int hk0 = slab * KH;
+          const uint32_t sb = 32u * HKV;  // scale bytes of 16 rows of K and V
+          if constexpr (SH == 4) {
+            tma_load_4d_hint(stage, &kv_map, 0, 0, hk0, phys * 2, &full[s], l2_policy);
+            bulk_load(sc, p.scales + static_cast<long long>(phys) * sb, sb, &full[s]);
+          } else if constexpr (SH == 5) {  // rows 0..15 or 16..31 of the block's K and V
+            const int row = (ab & 1) * 16;
+            tma_load_4d_hint(stage, &kv_map, 0, row, hk0, phys * 2, &full[s], l2_policy);
+            const uint8_t* src = p.scales + (static_cast<long long>(phys) * 64 + row) * HKV;
+            bulk_load(sc, src, sb / 2, &full[s]);
+            bulk_load(sc + sb / 2, src + 32 * HKV, sb / 2, &full[s]);
+          } else {  // two blocks of 8
+            if (first) {
+              tma_load_4d_hint(stage, &kv_map, 0, 0, hk0, phys * 2, &full[s], l2_policy);
+              bulk_load(sc, p.scales + static_cast<long long>(phys) * (sb / 2), sb / 2, &full[s]);
+            }
+            if (second) {
+              tma_load_4d_hint(stage + lay.kv_bytes / 2, &kv_map, 0, 0, hk0, phys1 * 2, &full[s],
+                               l2_policy);
+              bulk_load(sc + sb / 2, p.scales + static_cast<long long>(phys1) * (sb / 2), sb / 2,
+                        &full[s]);
+            }
+          }
+        } else {
+          mbar_arrive(&full[s]);
+        }
+      }
+      if (++s == S) {  // ring wraps; from the second wrap on, the empty parity flips
+        s = 0;
+        if (issued + 1 > S) eph ^= 1u;
+      }
+      ++x;
+      ++blk;
+      new_piece = false;
+      if (blk == nblk) {
+        blk = 0;
+        new_piece = true;
+        if (x < x1) {
+          pr += nblk;  // empty requests in between add no chunks
+          if (nx_pn - pr > 0) {
+            ++r;
+            nblk = nx_pn - pr;
+            q = nx;
+          } else {
+            do {
+              ++r;
+              nblk = __ldg(p.dec_prefix + r + 1) - pr;
+            } while (nblk == 0);
+            q = fetch(r, 0);
+          }
+          fetch_next();
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      // let every copy in flight land before the shared memory goes away
+      for (uint32_t k = (issued > S ? issued - S : 0); k < issued; ++k)
+        mbar_wait(&full[k % S], (k / S) & 1u, kDrainLimitNs);
+    }
+    return;
+  }
+
+  // ================= consumer warp: unit tiles tile0 .. tile0+MT-1 of kv head hk
+  const int hl = warp / WPH, hk = slab * KH + hl;
+  const int tile0 = (warp - hl * WPH) * MT;
+  const int g = lane >> 2, t4 = lane & 3;
+  const int gsh = p.group_shift, G = 1 << gsh;
+  constexpr int KS = D / 32;  // k steps of S, and pairs of V^T tiles
+  uint32_t qa[MT][KS][4];
+  float o[MT][D / 16][4];
+  float fq[MT], m_run[MT], l_run[MT];  // of unit 8 (tile0 + mt) + g
+  int lim_lo[MT], lim_hi[MT], ref[MT];  // the unit's keys; SCORED: where distances count from
+  float slope2[MT];
+  const float cap2 = SCORED ? p.score.softcap * kLog2e : 0.f;
+  int t = 0, n = 0, my_tiles = 0, hi_all = 0;
+  // this lane's ldmatrix addresses: row lane % 8 of an 8-key group, 16-byte unit
+  // (swizzled by the row) lane / 8 for K, lane / 16 for V, whose lanes 8-15 and
+  // 24-31 take the second group
+  const int row8 = lane & 7, swz = D == 128 ? row8 : row8 >> 1;
+  const uint32_t gstep = SH == 3 ? 16u * KH * D : 8u * D;  // bytes between a head's key groups
+  const uint32_t k_off = (SH == 3 ? 8u : 16u) * hl * D + row8 * D + (((lane >> 3) ^ swz) << 4);
+  const uint32_t v_off = (SH == 3 ? 8u : 16u) * (KH + hl) * D + row8 * D +
+                         ((lane >> 3) & 1 ? gstep : 0u) + (((lane >> 4) ^ swz) << 4);
+
+  for (uint32_t s = 0, fph = 0;;) {  // ring slot, parity of its full barrier
+    if (!mbar_wait(&full[s], fph)) {
+      atomicOr(&g_errors_quant_decode, kErrTimeout);
+      break;
+    }
+    const int4 m = meta[2 * s];
+    if (m.x & kEnd) break;
+    const int flags = m.x, k0 = m.y, out_base = m.z;
+    const unsigned char* stage = base + s * lay.stage_bytes;
+
+    if (flags & kFirst) {
+      const int4 f = meta[2 * s + 1];
+      t = f.x;
+      n = f.y;
+      const int L = f.z;
+      my_tiles = min(MT, max(0, ((n << gsh) + 7) / 8 - tile0));
+      hi_all = L - n + 1;  // keys below it are seen by every row (plain scores)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int u = 8 * (tile0 + mt) + g, i = u >> gsh, h = u & (G - 1);
+        const bool unit = i < n;
+        m_run[mt] = -INFINITY;
+        l_run[mt] = 0.f;
+        lim_lo[mt] = ref[mt] = 0;
+        lim_hi[mt] = 0x7fffffff;  // (a place without a unit masks nothing)
+        slope2[mt] = 0.f;
+        if (unit) {
+          const int pos = L - n + i;
+          lim_hi[mt] = pos + 1;
+          if constexpr (SCORED) {
+            const KeyRange k = row_keys(p.score, static_cast<long long>(t) + i, pos, L, f.w);
+            const KeyRange all = row_keys(p.score, static_cast<long long>(t) + i, pos, L, 0);
+            lim_lo[mt] = k.lo;
+            lim_hi[mt] = k.hi;
+            ref[mt] = max(min(pos, all.hi - 1), all.lo);
+            slope2[mt] = slope_log2(p.score, hk * G + h);
+          }
+        }
+        // the unit's q row: dims 32 ks + 4 t4 .. and 32 ks + 16 + 4 t4 ..
+        uint2 w[2 * KS];
+        const uint16_t* src =
+            p.q + (static_cast<long long>(t) + i) * p.q_stride + (hk * G + h) * D + 4 * t4;
+        uint32_t amax = 0;
+#pragma unroll
+        for (int x = 0; x < 2 * KS; ++x) {
+          w[x] = unit ? __ldg(reinterpret_cast<const uint2*>(src + 16 * x)) : make_uint2(0, 0);
+          amax = max(amax, amax8(make_uint4(w[x].x, w[x].y, 0, 0)));
+        }
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const uint32_t sb = scale_byte(amax);
+        // (a row with an infinity or a NaN makes all its scores NaN)
+        fq[mt] = p.scale_log2 * scale_value(sb);
+        const float inv = __uint_as_float((254u - min(sb, 254u)) << 23);
+#pragma unroll
+        for (int x = 0; x < 2 * KS; ++x) {
+          const float v0 = bf16_lo(w[x].x) * inv, v1 = bf16_hi(w[x].x) * inv;
+          const float v2 = bf16_lo(w[x].y) * inv, v3 = bf16_hi(w[x].y) * inv;
+          const uint32_t h0 = e4m3x2(v0, v1), h1 = e4m3x2(v2, v3);
+          const float2 b0 = e4m3_float2(h0), b1 = e4m3_float2(h1);
+          qa[mt][x >> 1][2 * (x & 1)] = h0 | (h1 << 16);
+          qa[mt][x >> 1][2 * (x & 1) + 1] =
+              e4m3x2((v0 - b0.x) * 16.f, (v1 - b0.y) * 16.f) |
+              (e4m3x2((v2 - b1.x) * 16.f, (v3 - b1.y) * 16.f) << 16);
+        }
+#pragma unroll
+        for (int i2 = 0; i2 < D / 16; ++i2)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[mt][i2][e] = 0.f;
+      }
+    }
+
+    if (!(flags & kInvalid) && my_tiles > 0) {
+      const uint32_t kv = smem_u32(stage);
+      // ---- S of the chunk's two groups of 8 keys
+      float acc[MT][2][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int ng = 0; ng < 2; ++ng)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[mt][ng][e] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < KS / 2; ++kk)
+#pragma unroll
+        for (int ng = 0; ng < 2; ++ng) {
+          uint32_t b[4];
+          ldsm4((kv + k_off + ng * gstep) ^ (kk << 6), b);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            if (MT > 1 && mt >= my_tiles) continue;
+            mma_e4m3(acc[mt][ng], qa[mt][2 * kk], b[0], b[1]);
+            mma_e4m3(acc[mt][ng], qa[mt][2 * kk + 1], b[2], b[3]);
+          }
+        }
+      // scales of this lane's keys 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4
+      float ks[4], vs[4];
+      const unsigned char* sc = stage + lay.kv_bytes + hk;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int j = (x >> 1) * 8 + 2 * t4 + (x & 1);
+        const int kr = SH == 3 ? (j & 7) + (j >> 3) * 16 : j;
+        ks[x] = scale_value(sc[kr * HKV]);
+        vs[x] = scale_value(sc[(kr + (SH == 3 ? 8 : 16)) * HKV]);
+      }
+      // ---- softmax, and P^T times V's scales as the PV operand
+      uint32_t pb[MT][2];
+      bool whole = true;  // every unit sees the whole chunk
+      if constexpr (SCORED) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+          whole = whole && lim_lo[mt] <= k0 && lim_hi[mt] >= k0 + kChunkKeys;
+        whole = __all_sync(0xffffffffu, whole);
+      } else {
+        whole = hi_all >= k0 + kChunkKeys;
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        if (MT > 1 && mt >= my_tiles) continue;
+        float sv[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float a = acc[mt][x >> 1][x & 1], b = acc[mt][x >> 1][2 + (x & 1)];
+          sv[x] = fmaf(b, 0.0625f, a) * (fq[mt] * ks[x]);
+          if constexpr (SCORED) {
+            const int key = k0 + (x >> 1) * 8 + 2 * t4 + (x & 1);
+            if (p.score.softcap > 0.f) sv[x] = cap2 * tanh_log2(sv[x]);
+            if (p.score.slopes) sv[x] -= slope2[mt] * fabsf(static_cast<float>(ref[mt] - key));
+          }
+        }
+        if (!whole) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int key = k0 + (x >> 1) * 8 + 2 * t4 + (x & 1);
+            if (key < lim_lo[mt] || key >= lim_hi[mt]) sv[x] = -INFINITY;
+          }
+        }
+        float lmax = fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3]));
+        if (__any_sync(0xffffffffu, lmax > m_run[mt] + kRescaleLog2)) {
+          lmax = fmaxf(lmax, __shfl_xor_sync(0xffffffffu, lmax, 1));
+          lmax = fmaxf(lmax, __shfl_xor_sync(0xffffffffu, lmax, 2));
+          const float m_new = fmaxf(m_run[mt], lmax);
+          const float alpha = m_new == -INFINITY ? 1.f : exp2f(m_run[mt] - m_new);
+          l_run[mt] *= alpha;
+          m_run[mt] = m_new;
+          // O's columns are units 2 t4 and 2 t4 + 1
+          const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * t4);
+          const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * t4 + 4);
+#pragma unroll
+          for (int i2 = 0; i2 < D / 16; ++i2) {
+            o[mt][i2][0] *= a0;
+            o[mt][i2][1] *= a1;
+            o[mt][i2][2] *= a0;
+            o[mt][i2][3] *= a1;
+          }
+        }
+        const float msub = m_run[mt] == -INFINITY ? 0.f : m_run[mt];
+        float pv[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float e = exp2f(sv[x] - msub);
+          l_run[mt] += e;
+          pv[x] = e * vs[x];
+        }
+        if (!whole) {  // (a masked key's scale may be anything)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (sv[x] == -INFINITY) pv[x] = 0.f;
+        }
+        pb[mt][0] = pack_bf16x2(pv[0], pv[1]);
+        pb[mt][1] = pack_bf16x2(pv[2], pv[3]);
+      }
+      // ---- O^T += V^T P^T
+#pragma unroll
+      for (int i2 = 0; i2 < KS; ++i2) {
+        uint32_t w[4], a[2][4];
+        ldsm4_trans((kv + v_off) ^ (i2 << 5), w);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          a[h][0] = codes_even(w[2 * h]);
+          a[h][1] = codes_odd(w[2 * h]);
+          a[h][2] = codes_even(w[2 * h + 1]);
+          a[h][3] = codes_odd(w[2 * h + 1]);
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          if (MT > 1 && mt >= my_tiles) continue;
+          mma_bf16(o[mt][2 * i2], a[0], pb[mt][0], pb[mt][1]);
+          mma_bf16(o[mt][2 * i2 + 1], a[1], pb[mt][0], pb[mt][1]);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[s]);  // the stage may be refilled
+
+    // ---- end of this CTA's piece of the request
+    if ((flags & kLast) && my_tiles > 0) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        float l = l_run[mt];
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {  // units 2 t4 + j: O's columns in o[..][..][j] and [2 + j]
+          const float lj = __shfl_sync(0xffffffffu, l, 8 * t4 + 4 * j);
+          const float mj = __shfl_sync(0xffffffffu, m_run[mt], 8 * t4 + 4 * j);
+          const int u = 8 * (tile0 + mt) + 2 * t4 + j, i = u >> gsh, h = u & (G - 1);
+          if (i >= n) continue;
+          const int head = hk * G + h;
+          if (out_base < 0) {
+            const float inv = SCORED && lj == 0.f ? 0.f : 1.f / lj;  // no key seen: zeros
+            uint16_t* dst =
+                p.out + ((static_cast<long long>(t) + i) * p.num_q_heads + head) * D + 2 * g;
+#pragma unroll
+            for (int i2 = 0; i2 < D / 16; ++i2)
+              *reinterpret_cast<uint32_t*>(dst + 16 * i2) =
+                  pack_bf16x2(o[mt][i2][j] * inv, o[mt][i2][2 + j] * inv);
+          } else {
+            // n == 1: out_base is (r + c) * V, virtual heads of G or 4 q heads;
+            // several rows: a slot of the few-row partials
+            const long long slot =
+                n == 1 ? static_cast<long long>(out_base) * (p.num_q_heads / p.virt_heads) + head
+                       : (static_cast<long long>(out_base) * p.few + i) * p.num_q_heads + head;
+            float* dst = (n == 1 ? p.part_o : p.few_o) + slot * D + 2 * g;
+            if (g == 0) (n == 1 ? p.part_ml : p.few_ml)[slot] = make_float2(mj, lj);
+#pragma unroll
+            for (int i2 = 0; i2 < D / 16; ++i2)
+              *reinterpret_cast<float2*>(dst + 16 * i2) =
+                  make_float2(o[mt][i2][j], o[mt][i2][2 + j]);
+          }
+        }
+      }
+    }
+    if (++s == S) {
+      s = 0;
+      fph ^= 1u;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host
+constexpr int kQuantMinStages = 2, kQuantMaxStages = 8;
+
+// Unit tiles that the largest request on the stream needs, the tiles of a
+// consumer warp, and the warps of a kv head.
+struct QuantShape {
+  int few, mt, wph;
+};
+
+// Steps whose every request has so few new tokens that their units fit the CTA's
+// warps (kFewUnits) stream all of them; in a step with longer chunks those of up
+// to 16 units do, one warp a head, and the others go to the prefill kernel.
+static QuantShape quant_shape(int max_query_len, int group) {
+  const int units = max_query_len <= kFewUnits / group ? max_query_len * group : 16;
+  const int tiles = (units + 7) / 8;
+  QuantShape s;
+  s.mt = tiles == 1 ? 1 : 2;
+  s.wph = (tiles + s.mt - 1) / s.mt;
+  s.few = max_query_len <= kFewUnits / group ? max_query_len : 16 / group;
+  return s;
+}
+
+int quant_few_rows(int max_query_len, int group) {
+  return max_query_len < 1 ? 1 : quant_shape(max_query_len, group).few;
+}
+
+int quant_slab_heads(int num_kv_heads, int group, int max_query_len) {
+  const int most = kQuantWarps / quant_shape(max_query_len, group).wph;
+  int s = num_kv_heads <= most ? num_kv_heads : most;
+  while (num_kv_heads % s) --s;
+  return s;
+}
+
+// CTAs of nw consumer warps an SM is meant to hold.
+static int quant_ctas(int nw) { return kQuantWarps / nw < 1 ? 1 : kQuantWarps / nw; }
+
+long long quant_most_splits(int num_kv_heads, int group, int num_sms) {
+  int most = 1;
+  for (int n = 1; n <= kFewUnits / group + 1; ++n) {
+    const int nw = quant_slab_heads(num_kv_heads, group, n) * quant_shape(n, group).wph;
+    if (quant_ctas(nw) > most) most = quant_ctas(nw);
+  }
+  return static_cast<long long>(num_sms) * most;
+}
+
+// Launch shape of one instantiation on one device, worked out once.
+struct QuantPrep {
+  int dev, kh, hkv, nw, num_sms, stages;
+  long long splits;
+  size_t smem;
+};
+
+template <int D, int SH, int MT, bool SCORED>
+static std::vector<QuantPrep> g_quant_prep;
+template <int D, int SH, int MT, bool SCORED>
+static std::atomic<unsigned long long> g_quant_attr_done{0};
+static std::mutex g_quant_prep_mu;
+
+template <int D, int SH, int MT, bool SCORED>
+static cudaError_t quant_prepare(int kh, int hkv, int nw, int num_sms, QuantPrep* out) {
+  auto kern = quant_decode_kernel<D, SH, MT, SCORED>;
+  cudaError_t e = smem_attr_once(kern, 227 * 1024, g_quant_attr_done<D, SH, MT, SCORED>);
+  if (e != cudaSuccess) return e;
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(g_quant_prep_mu);
+  for (const QuantPrep& d : g_quant_prep<D, SH, MT, SCORED>)
+    if (d.dev == dev && d.kh == kh && d.hkv == hkv && d.nw == nw && d.num_sms == num_sms) {
+      *out = d;
+      return cudaSuccess;
+    }
+  const int want = quant_ctas(nw);
+  auto bytes = [&](int S) { return QuantLayout(D, kh, hkv, S).total + 1024u; };
+  int fit = 0;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kern, (nw + 1) * 32, bytes(kQuantMinStages));
+  if (e != cudaSuccess) return e;
+  const int ctas = fit < want ? (fit < 1 ? 1 : fit) : want;
+  const size_t budget = 228u * 1024u / ctas - 1024u;
+  int S = kQuantMinStages;
+  while (S < kQuantMaxStages && bytes(S + 1) <= budget) ++S;
+  // more than 1 / (ctas + 1) of the SM's shared memory, see decode_smem_bytes
+  const size_t share = 228u * 1024u / (ctas + 1) + 1024u;
+  const size_t smem = bytes(S) > share ? bytes(S) : share;
+  *out = QuantPrep{dev, kh, hkv, nw, num_sms, S, static_cast<long long>(num_sms) * ctas, smem};
+  g_quant_prep<D, SH, MT, SCORED>.push_back(*out);
+  return cudaSuccess;
+}
+
+// Calls F<D, SH, MT, SCORED>::run(args...) for the instantiated shapes.
+template <template <int, int, int, bool> class F, typename... A>
+static cudaError_t quant_dispatch(int head_dim, int sh, int mt, bool scored, A&&... args) {
+#define PKV_QUANT_CASE(D_, SH_, MT_)                    \
+  if (head_dim == D_ && sh == SH_ && mt == MT_)         \
+    return scored ? F<D_, SH_, MT_, true>::run(args...) \
+                  : F<D_, SH_, MT_, false>::run(args...);
+#define PKV_QUANT_MT(D_, SH_) PKV_QUANT_CASE(D_, SH_, 1) PKV_QUANT_CASE(D_, SH_, 2)
+#define PKV_QUANT_SH(D_) PKV_QUANT_MT(D_, 3) PKV_QUANT_MT(D_, 4) PKV_QUANT_MT(D_, 5)
+  PKV_QUANT_SH(128) PKV_QUANT_SH(64)
+#undef PKV_QUANT_SH
+#undef PKV_QUANT_MT
+#undef PKV_QUANT_CASE
+  return cudaErrorInvalidValue;
+}
+
+template <int D, int SH, int MT, bool SCORED>
+struct QuantPrepareOp {
+  static cudaError_t run(int kh, int hkv, int nw, int sms, long long* splits) {
+    QuantPrep d;
+    const cudaError_t e = quant_prepare<D, SH, MT, SCORED>(kh, hkv, nw, sms, &d);
+    if (e == cudaSuccess) *splits = d.splits;
+    return e;
+  }
+};
+
+template <int D, int SH, int MT, bool SCORED>
+struct QuantLaunchOp {
+  static cudaError_t run(const QuantDecodeParams& p, const CUtensorMap& m, int sms, cudaStream_t s) {
+    QuantPrep d;
+    const int nw = p.slab_heads * p.warps_per_head;
+    cudaError_t e = quant_prepare<D, SH, MT, SCORED>(p.slab_heads, p.num_kv_heads, nw, sms, &d);
+    if (e != cudaSuccess) return e;
+    QuantDecodeParams q = p;
+    q.stages = d.stages;
+    const dim3 grid(static_cast<unsigned>(p.splits),
+                    static_cast<unsigned>(p.num_kv_heads / p.slab_heads));
+    return launch_pdl(quant_decode_kernel<D, SH, MT, SCORED>, grid, dim3((nw + 1) * 32), d.smem, s,
+                      m, q);
+  }
+};
+
+cudaError_t quant_full_wave_splits(int head_dim, int num_kv_heads, int group, int block_shift,
+                                   int max_query_len, bool scored, int num_sms, long long* splits) {
+  const QuantShape q = quant_shape(max_query_len, group);
+  const int kh = quant_slab_heads(num_kv_heads, group, max_query_len);
+  return quant_dispatch<QuantPrepareOp>(head_dim, block_shift, q.mt, scored, kh, num_kv_heads,
+                                        kh * q.wph, num_sms, splits);
+}
+
+cudaError_t launch_quant_decode(const AttnArgs& a, const AttnWorkspace& ws,
+                                const CUtensorMap& kv_map, long long splits, int num_sms,
+                                cudaStream_t stream, void** trace) {
+  const int group = a.num_q_heads / a.num_kv_heads;
+  const QuantShape shape = quant_shape(a.max_query_len, group);
+  QuantDecodeParams p;
+  static_cast<DecodeParams&>(p) = decode_params(a, ws, splits);
+  p.scales = a.kv_scales;
+  p.num_kv_heads = a.num_kv_heads;
+  p.group_shift = __builtin_ctz(static_cast<unsigned>(group));
+  p.slab_heads = quant_slab_heads(a.num_kv_heads, group, a.max_query_len);
+  p.warps_per_head = shape.wph;
+  cudaError_t e = quant_dispatch<QuantLaunchOp>(a.head_dim, a.block_shift, shape.mt, a.scored, p,
+                                                kv_map, num_sms, stream);
+  if (e == cudaSuccess && trace) e = cudaEventRecord(static_cast<cudaEvent_t>(trace[3]), stream);
+  if (e != cudaSuccess) return e;
+  return launch_combine(p, a.head_dim, decode_heads_per_warp(group), stream);
+}
+
+cudaError_t read_errors_quant_decode(uint32_t* out, bool clear) {
+  uint32_t v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_errors_quant_decode, sizeof(v));
+  if (e != cudaSuccess) return e;
+  *out |= v;
+  if (clear) {
+    const uint32_t z = 0;
+    e = cudaMemcpyToSymbol(g_errors_quant_decode, &z, sizeof(z));
+  }
+  return e;
+}
+
+}  // namespace pkv

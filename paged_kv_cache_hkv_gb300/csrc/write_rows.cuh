@@ -9,6 +9,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "quant.cuh"
 
 namespace pkv {
 
@@ -25,31 +26,20 @@ struct WriteRowsArgs {
   int num_reqs, num_tokens, num_blocks;
   int shift;        // log2 of the block size
   int vec_per_row;  // 16-byte words of one K (or V) row: Hkv * D / 8
+  // 8-bit pool (quant_token_rows): `pool` holds codes
+  uint8_t* scales;
+  int vec_per_head;  // D / 8
 };
 
 constexpr int kWritePrefetch = 8;  // 16-byte words per lane loaded before the slot is known
 
-// Token t by one whole warp. The warp issues the loads of the token's K and
-// V rows first (the first kWritePrefetch words per lane of each), finds the
-// token's request with a 32-way search of query_start_loc (non-decreasing),
-// computes the slot and stores the rows. A token that the search puts in no
+// Slot of token t, by one whole warp: its request is found with a 32-way search
+// of query_start_loc (non-decreasing). A token that the search puts in no
 // request (before query_start_loc[0], at or past query_start_loc[num_reqs])
-// or in a request with inconsistent lengths gets slot -1 and is not written;
-// the error bits go to *err.
-__device__ __forceinline__ void write_token_rows(const WriteRowsArgs& w, long long t,
-                                                 uint32_t* err) {
+// or in a request with inconsistent lengths gets -1; the error bits go to *err.
+__device__ __forceinline__ long long token_slot(const WriteRowsArgs& w, long long t,
+                                                uint32_t* err) {
   const int lane = threadIdx.x & 31;
-  const uint4* ksrc = w.key + t * w.key_stride_v;
-  const uint4* vsrc = w.value + t * w.value_stride_v;
-  uint4 kw[kWritePrefetch], vw[kWritePrefetch];
-#pragma unroll
-  for (int i = 0; i < kWritePrefetch; ++i) {
-    const int e = lane + 32 * i;
-    if (e < w.vec_per_row) {
-      kw[i] = __ldg(ksrc + e);
-      vw[i] = __ldg(vsrc + e);
-    }
-  }
   const int tt = static_cast<int>(t);
   long long slot = -1;
   const int qend = __ldg(w.qsl + w.num_reqs), qfirst = __ldg(w.qsl);
@@ -76,6 +66,27 @@ __device__ __forceinline__ void write_token_rows(const WriteRowsArgs& w, long lo
   } else if (tt < qend || qfirst != 0) {  // rows before a non-zero query_start_loc[0]
     if (lane == 0) atomicOr(err, kErrLengths);
   }
+  return slot;
+}
+
+// Token t by one whole warp. The warp issues the loads of the token's K and
+// V rows first (the first kWritePrefetch words per lane of each), finds the
+// token's slot and stores the rows. A token with slot -1 is not written.
+__device__ __forceinline__ void write_token_rows(const WriteRowsArgs& w, long long t,
+                                                 uint32_t* err) {
+  const int lane = threadIdx.x & 31;
+  const uint4* ksrc = w.key + t * w.key_stride_v;
+  const uint4* vsrc = w.value + t * w.value_stride_v;
+  uint4 kw[kWritePrefetch], vw[kWritePrefetch];
+#pragma unroll
+  for (int i = 0; i < kWritePrefetch; ++i) {
+    const int e = lane + 32 * i;
+    if (e < w.vec_per_row) {
+      kw[i] = __ldg(ksrc + e);
+      vw[i] = __ldg(vsrc + e);
+    }
+  }
+  const long long slot = token_slot(w, t, err);
   if (w.slots_out && lane == 0) w.slots_out[t] = slot;
   if (slot < 0) return;
   const long long blk = slot >> w.shift, off = slot & ((1 << w.shift) - 1);
@@ -93,6 +104,49 @@ __device__ __forceinline__ void write_token_rows(const WriteRowsArgs& w, long lo
     kdst[e] = __ldg(ksrc + e);
     vdst[e] = __ldg(vsrc + e);
   }
+}
+
+// The same into the 8-bit pool (quant.cuh): every lane quantises eight values a
+// word, D / 8 neighbouring lanes hold a row of one kv head.
+template <int D>
+__device__ __forceinline__ void quant_token_rows(const WriteRowsArgs& w, long long t,
+                                                 uint32_t* err) {
+  const int lane = threadIdx.x & 31;
+  const uint4* src[2] = {w.key + t * w.key_stride_v, w.value + t * w.value_stride_v};
+  uint4 x[2][kWritePrefetch];
+#pragma unroll
+  for (int i = 0; i < kWritePrefetch; ++i) {
+    const int e = lane + 32 * i;
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+      x[v][i] = e < w.vec_per_row ? __ldg(src[v] + e) : make_uint4(0, 0, 0, 0);
+  }
+  const long long slot = token_slot(w, t, err);
+  if (w.slots_out && lane == 0) w.slots_out[t] = slot;
+  if (slot < 0) return;
+  const long long blk = slot >> w.shift, off = slot & ((1 << w.shift) - 1);
+  // (the whole warp: the row's largest magnitude goes by shuffles)
+  auto store = [&](const uint4& val, int v, int e) {
+    uint32_t m = amax8(val);
+#pragma unroll
+    for (int d = 1; d < D / 8; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (e >= w.vec_per_row) return;
+    const uint32_t s = scale_byte(m);
+    const long long word = (((blk * 2 + v) << w.shift) + off) * w.vec_per_row + e;
+    reinterpret_cast<uint2*>(w.pool)[word] = quant8(val, s);
+    if (e % (D / 8) == 0) w.scales[word / (D / 8)] = static_cast<uint8_t>(s);
+  };
+#pragma unroll
+  for (int i = 0; i < kWritePrefetch; ++i)
+    if (32 * i < w.vec_per_row) {
+      store(x[0][i], 0, lane + 32 * i);
+      store(x[1][i], 1, lane + 32 * i);
+    }
+  for (int e0 = 32 * kWritePrefetch; e0 < w.vec_per_row; e0 += 32)  // rows over 4 KB
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+      store(e0 + lane < w.vec_per_row ? __ldg(src[v] + e0 + lane) : make_uint4(0, 0, 0, 0), v,
+            e0 + lane);
 }
 
 }  // namespace pkv

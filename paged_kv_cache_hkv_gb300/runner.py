@@ -49,7 +49,7 @@ class DeviceStep:
 
     def __init__(self, step, device="cuda", decode_splits=None, upload_pool=True,
                  shared_prefix=None, fused_write=False, write_in_attention=False, softcap=0.0,
-                 alibi_slopes=None, key_begin=None, key_end=None):
+                 alibi_slopes=None, key_begin=None, key_end=None, quantised=False):
         """shared_prefix: None, or (shared_prefix_len, shared_first_req,
         shared_num_reqs) for the attention call (see pagedkv.h); "auto" takes
         it from the step's shared prefix when its sharing requests form one
@@ -58,7 +58,9 @@ class DeviceStep:
         write_in_attention: run() is the single call
         pkv_paged_attention_with_write. softcap, alibi_slopes [Hq],
         key_begin, key_end [T] (host arrays): capped, biased or range-masked
-        scores."""
+        scores. quantised: the step's pool is quantised as it is uploaded, and
+        the calls are those of the 8-bit pool (kv_cache holds codes, kv_scales
+        their scales)."""
         self.step = step
         self.device = torch.device(device)
         dev = self.device
@@ -88,12 +90,39 @@ class DeviceStep:
             key_end=None if key_end is None else _i32(key_end, dev))
         self.layout = binding.pkv_cache_layout(step.num_blocks, step.block_size,
                                                step.num_kv_heads, step.head_dim)
-        nbytes = binding.pkv_attention_workspace_size(step.num_reqs, step.num_q_heads,
-                                                      self.layout, decode_splits=decode_splits,
-                                                      shared_prefix=shared_prefix)
+        self.quantised = quantised
+        self.kv_scales = None
+        if quantised:
+            if not upload_pool:
+                raise ValueError("a quantised step uploads its pool")
+            self._quantise_pool()
+            nbytes = binding.pkv_quant_attention_workspace_size(
+                step.num_reqs, step.num_q_heads, self.layout,
+                max_blocks_per_req=step.max_blocks_per_req,
+                chunk_keys=binding.quant_chunk_keys(
+                    step.query_len.tolist(), step.seq_lens.tolist(),
+                    step.num_q_heads // step.num_kv_heads, step.block_size),
+                decode_splits=decode_splits, shared_prefix=shared_prefix)
+        else:
+            nbytes = binding.pkv_attention_workspace_size(step.num_reqs, step.num_q_heads,
+                                                          self.layout, decode_splits=decode_splits,
+                                                          shared_prefix=shared_prefix)
         self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
         self._calls = None
         self._calls_bufs, self._calls_settings = (), None
+
+    def _quantise_pool(self):
+        """The uploaded bf16 pool's rows written into an 8-bit pool of the same
+        blocks."""
+        s, pool = self.step, self.kv_cache
+        shape = (s.num_blocks, 2, s.block_size, s.num_kv_heads)
+        self.kv_cache = torch.empty((*shape, s.head_dim), dtype=torch.float8_e4m3fn,
+                                    device=self.device)
+        self.kv_scales = torch.empty(shape, dtype=torch.uint8, device=self.device)
+        rows = [pool[:, i].reshape(-1, s.num_kv_heads, s.head_dim) for i in (0, 1)]
+        binding.pkv_quant_kv_write(
+            self.kv_cache, self.kv_scales, *rows,
+            torch.arange(s.num_blocks * s.block_size, dtype=torch.int64, device=self.device))
 
     # -- the three calls of the hot path
     def slot_map(self, stream=None):
@@ -102,18 +131,31 @@ class DeviceStep:
                                  self.num_computed, s.num_blocks, s.block_size, stream=stream)
 
     def write(self, stream=None):
+        if self.quantised:
+            binding.pkv_quant_kv_write(self.kv_cache, self.kv_scales, self.k, self.v,
+                                       self.slot_mapping, stream=stream)
+            return
         binding.pkv_paged_kv_write(self.kv_cache, self.k, self.v, self.slot_mapping,
                                    stream=stream)
 
     def slot_map_and_write(self, stream=None):
+        if self.quantised:
+            binding.pkv_quant_slot_mapping_and_write(
+                self.kv_cache, self.kv_scales, self.k, self.v, self.block_table,
+                self.query_start_loc, self.num_computed, slot_mapping=self.slot_mapping,
+                stream=stream)
+            return
         binding.pkv_slot_mapping_and_write(self.kv_cache, self.k, self.v, self.block_table,
                                            self.query_start_loc, self.num_computed,
                                            slot_mapping=self.slot_mapping, stream=stream)
 
     def attend_with_write(self, stream=None):
         s = self.step
-        binding.pkv_paged_attention_with_write(
-            self.out, self.q, self.kv_cache, self.k, self.v, self.block_table, self.seq_lens,
+        call, pool = ((binding.pkv_quant_paged_attention_with_write,
+                       (self.kv_cache, self.kv_scales)) if self.quantised else
+                      (binding.pkv_paged_attention_with_write, (self.kv_cache,)))
+        call(
+            self.out, self.q, *pool, self.k, self.v, self.block_table, self.seq_lens,
             self.query_start_loc, self.num_computed, max_query_len=s.max_query_len,
             max_seq_len=s.max_seq_len, scale=s.scale, workspace=self.workspace,
             slot_mapping=self.slot_mapping, decode_splits=self.decode_splits,
@@ -121,8 +163,10 @@ class DeviceStep:
 
     def attend(self, stream=None):
         s = self.step
-        binding.pkv_paged_attention(
-            self.out, self.q, self.kv_cache, self.block_table, self.seq_lens,
+        call, pool = ((binding.pkv_quant_paged_attention, (self.kv_cache, self.kv_scales))
+                      if self.quantised else (binding.pkv_paged_attention, (self.kv_cache,)))
+        call(
+            self.out, self.q, *pool, self.block_table, self.seq_lens,
             self.query_start_loc, self.num_computed, max_query_len=s.max_query_len,
             max_seq_len=s.max_seq_len, scale=s.scale, workspace=self.workspace,
             decode_splits=self.decode_splits, shared_prefix=self.shared_prefix, stream=stream,
@@ -141,8 +185,8 @@ class DeviceStep:
         replaced)."""
         sc = self.scores
         bufs = (self.slot_mapping, self.block_table, self.query_start_loc, self.num_computed,
-                self.kv_cache, self.k, self.v, self.out, self.q, self.seq_lens, self.workspace,
-                sc["alibi_slopes"], sc["key_begin"], sc["key_end"])
+                self.kv_cache, self.kv_scales, self.k, self.v, self.out, self.q, self.seq_lens,
+                self.workspace, sc["alibi_slopes"], sc["key_begin"], sc["key_end"])
         settings = (sc["softcap"], self.decode_splits, self.shared_prefix, self.fused_write,
                     self.write_in_attention)
         if settings != self._calls_settings or not all(map(operator.is_, bufs, self._calls_bufs)):
@@ -155,13 +199,17 @@ class DeviceStep:
                 max_seq_len=s.max_seq_len, scale=s.scale, workspace=self.workspace,
                 decode_splits=self.decode_splits, shared_prefix=self.shared_prefix,
                 fused_write=self.fused_write, write_in_attention=self.write_in_attention,
-                **self.scores)
+                kv_scales=self.kv_scales, **self.scores)
             self._calls_bufs, self._calls_settings = bufs, settings
         return self._calls
 
     # -- host copies
     def out_host(self) -> np.ndarray:
         return bf16_to_numpy(self.out)
+
+    def quant_pool_host(self):
+        """(codes, scales) of a quantised step's pool, uint8."""
+        return self.kv_cache.view(torch.uint8).cpu().numpy(), self.kv_scales.cpu().numpy()
 
     def pool_host(self) -> np.ndarray:
         return bf16_to_numpy(self.kv_cache).reshape(self.step.kv_cache.shape)
