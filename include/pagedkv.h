@@ -562,10 +562,10 @@ int64_t pkv_release_workspace_size(int32_t num_released, int32_t max_blocks_per_
  * is the e4m3 number nearest to x * 2^-e, ties to even. So a value is kept to
  * 2^-4 of its size, or to 2^-10 * 2^e where that is more; every value that a pool
  * holds is a bf16, and rows read back and written again keep their values. A row
- * with an infinity or a NaN is held as NaN in all its elements (scale 255).
- * Scale bytes other than 10 .. 247 and 255, and the NaN code in a row whose scale
- * is not 255, stand in no row that was written by this library; what attention
- * makes of them is undefined.
+ * with an infinity or a NaN is held as NaN in all its elements: codes 0 and scale
+ * 255 (0 * 2^128 in fp32). Scale bytes other than 10 .. 247 and 255, and the NaN
+ * codes, stand in no row that was written by this library; what the calls make of
+ * them is undefined.
  * Layout limits are the bf16 pool's.
  */
 
@@ -647,8 +647,8 @@ int32_t pkv_quant_paged_attention_with_write(
 
 /* pkv_quant_few_rows -- the most new tokens of a request that a call with this
  * max_query_len attends on the decode kernels (at least 1): max_query_len itself
- * while it times the q heads of a kv head is at most 64, else 16 / that many
- * heads. Needs no device. */
+ * while it times the q heads of a kv head is at most 64, else 8 / that many heads.
+ * Needs no device. */
 int32_t pkv_quant_few_rows(int32_t max_query_len, int32_t num_q_heads, int32_t num_kv_heads);
 
 /*

@@ -54,13 +54,14 @@ def quantise_rows(bits):
     up, down = MAGNITUDES[hi] - y, y - MAGNITUDES[lo]
     code = np.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
     code = code | np.where(np.signbit(x), 0x80, 0)
-    code = np.where(bad[..., None], 0x7F, code)
+    code = np.where(bad[..., None], 0, code)
     return code.astype(np.uint8), np.where(bad, 255, e + 127).astype(np.uint8)
 
 
 def quant_values(codes, scales):
     """fp64 values of codes [..., D] under scale bytes [...]."""
-    return e4m3_values(codes) * np.exp2(np.asarray(scales, dtype=np.float64) - 127.0)[..., None]
+    s = np.asarray(scales, dtype=np.float64)
+    return e4m3_values(codes) * np.where(s == 255, np.nan, np.exp2(s - 127.0))[..., None]
 
 
 def quant_pool_bits(codes, scales):

@@ -24,16 +24,19 @@ namespace pkv {
 // empty loads: the combine of 128 requests of some 5 pieces took 18 us with
 // it and 10.6 without; that of one request of 152 pieces 10 and 60.
 //
-// FEW: requests of several rows are on the stream (8-bit pool): row i of such a
-// request by the CTAs of blockIdx.z = i, its partials in the slots 2 c (a CTA
-// that goes on with the request) and 2 c + 1 (the CTA that begins it).
+// FEW: requests of several rows are on the stream (8-bit pool), their partials in
+// the slots 2 c (a CTA that goes on with the request) and 2 c + 1 (the CTA that
+// begins it). The (row, q head) pairs of a request go to kFewCombineWarps warps in
+// turn (a CTA per row instead took 31 us where 16 rows were the most and hardly
+// any request had two).
 constexpr int kCombineLoads = 32;
+constexpr int kFewCombineWarps = 8;
 
 template <int D, int GW, bool DEEP, bool FEW>
-__global__ void __launch_bounds__(GW * 32) combine_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__((FEW ? kFewCombineWarps : GW) * 32) combine_kernel(const DecodeParams p) {
   const long long c = blockIdx.x;
   const int vg = blockIdx.y;
-  const int h = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long Cn = p.splits;
   pdl_trigger();
   pdl_wait();
@@ -57,117 +60,119 @@ __global__ void __launch_bounds__(GW * 32) combine_kernel(const DecodeParams p) 
   const long long cf = owner_cta(pr, N, Cn);
   if (si < 0 && (cf != c - 1 || in_shared_run(r))) return;
   const int row = __ldg(p.qsl + r);
-  const int i = FEW ? blockIdx.z : 0;
-  const bool few = FEW && __ldg(p.qsl + r + 1) - row > 1;
-  if (FEW && i >= __ldg(p.qsl + r + 1) - row) return;
+  const int rows = FEW ? __ldg(p.qsl + r + 1) - row : 1;
+  const bool few = FEW && rows > 1;
   // pieces j < nd: the decode partial of CTA cf + j, in slot (r + cf + j) * V
   // + vg; pieces nd .. nd + ns - 1: the shared-prefix items' partials
   const int nd = static_cast<int>(owner_cta(pr + nblk - 1, N, Cn) - cf + 1);
   const int ns = si >= 0 ? p.shared_pieces : 0;
   const int npieces = nd + ns;
-  const long long srow = static_cast<long long>(si) * p.num_q_heads + vg * GW + h;
-  const long long sstride = static_cast<long long>(p.shared_num) * p.num_q_heads;
+  for (int item = warp; item < rows * GW; item += FEW ? kFewCombineWarps : GW) {
+    const int h = item % GW, i = item / GW;
+    const long long srow = static_cast<long long>(si) * p.num_q_heads + vg * GW + h;
+    const long long sstride = static_cast<long long>(p.shared_num) * p.num_q_heads;
 
-  auto few_slot = [&](int j) -> long long {
-    return ((2 * (cf + j) + (j == 0)) * p.few + i) * p.num_q_heads + vg * GW + h;
-  };
-  // (m, l) of piece j; empty ranges wrote nothing and weigh zero
-  auto piece_ml = [&](int j) -> float2 {
-    if (j >= npieces) return make_float2(-INFINITY, 0.f);
-    if (j >= nd) return p.shared_ml[srow + (j - nd) * sstride];
-    const long long cc = cf + j;
-    if (cc * N / Cn == (cc + 1) * N / Cn) return make_float2(-INFINITY, 0.f);
-    if (few) return p.few_ml[few_slot(j)];
-    return p.part_ml[((r + cc) * p.virt_heads + vg) * GW + h];
-  };
-  auto piece_o = [&](int j) -> const float* {
-    if (j >= nd) return p.shared_o + (srow + (j - nd) * sstride) * D;
-    if (few) return p.few_o + few_slot(j) * D;
-    return p.part_o + (((r + cf + j) * p.virt_heads + vg) * GW + h) * D;
-  };
-  float M = -INFINITY;
-  for (int j0 = 0; j0 < npieces; j0 += 32) M = fmaxf(M, piece_ml(j0 + lane).x);
+    auto few_slot = [&](int j) -> long long {
+      return ((2 * (cf + j) + (j == 0)) * p.few + i) * p.num_q_heads + vg * GW + h;
+    };
+    // (m, l) of piece j; empty ranges wrote nothing and weigh zero
+    auto piece_ml = [&](int j) -> float2 {
+      if (j >= npieces) return make_float2(-INFINITY, 0.f);
+      if (j >= nd) return p.shared_ml[srow + (j - nd) * sstride];
+      const long long cc = cf + j;
+      if (cc * N / Cn == (cc + 1) * N / Cn) return make_float2(-INFINITY, 0.f);
+      if (few) return p.few_ml[few_slot(j)];
+      return p.part_ml[((r + cc) * p.virt_heads + vg) * GW + h];
+    };
+    auto piece_o = [&](int j) -> const float* {
+      if (j >= nd) return p.shared_o + (srow + (j - nd) * sstride) * D;
+      if (few) return p.few_o + few_slot(j) * D;
+      return p.part_o + (((r + cf + j) * p.virt_heads + vg) * GW + h) * D;
+    };
+    float M = -INFINITY;
+    for (int j0 = 0; j0 < npieces; j0 += 32) M = fmaxf(M, piece_ml(j0 + lane).x);
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
 
-  constexpr int E = D / 32;  // dims per lane
-  float acc[E];
+    constexpr int E = D / 32;  // dims per lane
+    float acc[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  float Ls = 0.f;
-  for (int j0 = 0; j0 < npieces; j0 += 32) {
-    const float2 ml = piece_ml(j0 + lane);
-    const float wgt = (ml.x == -INFINITY) ? 0.f : exp2f(ml.x - M);
-    Ls += wgt * ml.y;
-    const int cnt = min(32, npieces - j0);
-    if constexpr (DEEP) {
-      const float* mine = piece_o(wgt == 0.f || j0 + lane >= npieces ? 0 : j0 + lane);
-      // kCombineLoads pieces' loads go out before the first is used. A piece of
-      // weight 0 (an empty range, which wrote no partial) reads piece 0's slot
-      // and is left out of the sum: 0 times an infinity there would be a NaN.
-      for (int i0 = 0; i0 < cnt; i0 += kCombineLoads) {
-        float vals[kCombineLoads][E], wj[kCombineLoads];
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    float Ls = 0.f;
+    for (int j0 = 0; j0 < npieces; j0 += 32) {
+      const float2 ml = piece_ml(j0 + lane);
+      const float wgt = (ml.x == -INFINITY) ? 0.f : exp2f(ml.x - M);
+      Ls += wgt * ml.y;
+      const int cnt = min(32, npieces - j0);
+      if constexpr (DEEP) {
+        const float* mine = piece_o(wgt == 0.f || j0 + lane >= npieces ? 0 : j0 + lane);
+        // kCombineLoads pieces' loads go out before the first is used. A piece of
+        // weight 0 (an empty range, which wrote no partial) reads piece 0's slot
+        // and is left out of the sum: 0 times an infinity there would be a NaN.
+        for (int i0 = 0; i0 < cnt; i0 += kCombineLoads) {
+          float vals[kCombineLoads][E], wj[kCombineLoads];
 #pragma unroll
-        for (int i = 0; i < kCombineLoads; ++i) {
-          wj[i] = __shfl_sync(0xffffffffu, wgt, (i0 + i) & 31);
-          const float* src = reinterpret_cast<const float*>(__shfl_sync(
-                                 0xffffffffu, reinterpret_cast<unsigned long long>(mine), (i0 + i) & 31)) +
-                             lane * E;
+          for (int i = 0; i < kCombineLoads; ++i) {
+            wj[i] = __shfl_sync(0xffffffffu, wgt, (i0 + i) & 31);
+            const float* src = reinterpret_cast<const float*>(__shfl_sync(
+                                   0xffffffffu, reinterpret_cast<unsigned long long>(mine), (i0 + i) & 31)) +
+                               lane * E;
+            if constexpr (E == 4) {
+              const float4 v = *reinterpret_cast<const float4*>(src);
+              vals[i][0] = v.x;
+              vals[i][1] = v.y;
+              vals[i][2] = v.z;
+              vals[i][3] = v.w;
+            } else {
+              const float2 v = *reinterpret_cast<const float2*>(src);
+              vals[i][0] = v.x;
+              vals[i][1] = v.y;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kCombineLoads; ++i)
+            if (wj[i] != 0.f) {  // (nor is there a piece behind the last)
+#pragma unroll
+              for (int e = 0; e < E; ++e) acc[e] += wj[i] * vals[i][e];
+            }
+        }
+      } else {
+        // 8 pieces' loads in flight per lane; a piece of weight 0 as above
+#pragma unroll 8
+        for (int j = 0; j < cnt; ++j) {
+          const float wj = __shfl_sync(0xffffffffu, wgt, j);
+          const float* src = piece_o(wj == 0.f ? 0 : j0 + j) + lane * E;
           if constexpr (E == 4) {
             const float4 v = *reinterpret_cast<const float4*>(src);
-            vals[i][0] = v.x;
-            vals[i][1] = v.y;
-            vals[i][2] = v.z;
-            vals[i][3] = v.w;
+            if (wj != 0.f) {
+              acc[0] += wj * v.x;
+              acc[1] += wj * v.y;
+              acc[2] += wj * v.z;
+              acc[3] += wj * v.w;
+            }
           } else {
             const float2 v = *reinterpret_cast<const float2*>(src);
-            vals[i][0] = v.x;
-            vals[i][1] = v.y;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kCombineLoads; ++i)
-          if (wj[i] != 0.f) {  // (nor is there a piece behind the last)
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] += wj[i] * vals[i][e];
-          }
-      }
-    } else {
-      // 8 pieces' loads in flight per lane; a piece of weight 0 as above
-#pragma unroll 8
-      for (int j = 0; j < cnt; ++j) {
-        const float wj = __shfl_sync(0xffffffffu, wgt, j);
-        const float* src = piece_o(wj == 0.f ? 0 : j0 + j) + lane * E;
-        if constexpr (E == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(src);
-          if (wj != 0.f) {
-            acc[0] += wj * v.x;
-            acc[1] += wj * v.y;
-            acc[2] += wj * v.z;
-            acc[3] += wj * v.w;
-          }
-        } else {
-          const float2 v = *reinterpret_cast<const float2*>(src);
-          if (wj != 0.f) {
-            acc[0] += wj * v.x;
-            acc[1] += wj * v.y;
+            if (wj != 0.f) {
+              acc[0] += wj * v.x;
+              acc[1] += wj * v.y;
+            }
           }
         }
       }
     }
-  }
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, off);
-  const float inv = p.scored && Ls == 0.f ? 0.f : 1.f / Ls;  // no key seen: zeros
-  uint16_t* dst =
-      p.out + ((static_cast<long long>(row) + i) * p.num_q_heads + vg * GW + h) * D + lane * E;
-  if constexpr (E == 4) {
-    uint2 ov;
-    ov.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    ov.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
-    *reinterpret_cast<uint2*>(dst) = ov;
-  } else {
-    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    for (int off = 16; off >= 1; off >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, off);
+    const float inv = p.scored && Ls == 0.f ? 0.f : 1.f / Ls;  // no key seen: zeros
+    uint16_t* dst =
+        p.out + ((static_cast<long long>(row) + i) * p.num_q_heads + vg * GW + h) * D + lane * E;
+    if constexpr (E == 4) {
+      uint2 ov;
+      ov.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+      ov.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
+      *reinterpret_cast<uint2*>(dst) = ov;
+    } else {
+      *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    }
   }
 }
 
@@ -187,8 +192,8 @@ static cudaError_t launch_combine_t(const DecodeParams& p, cudaStream_t stream) 
                                           : combine_kernel<D, GW, false, false>);
   return launch_pdl(kern,
                     dim3(static_cast<unsigned>(p.splits + p.shared_num),
-                         static_cast<unsigned>(p.virt_heads), static_cast<unsigned>(p.few)),
-                    dim3(GW * 32), 0, stream, p);
+                         static_cast<unsigned>(p.virt_heads)),
+                    dim3((p.few > 1 ? kFewCombineWarps : GW) * 32), 0, stream, p);
 }
 
 cudaError_t launch_combine(const DecodeParams& p, int head_dim, int gw, cudaStream_t stream) {
@@ -221,7 +226,7 @@ DecodeParams decode_params(const AttnArgs& a, const AttnWorkspace& ws, long long
   p.scored = a.scored;
   p.score = a.score;
   p.deep_combine =
-      splits >= kDeepPieces * a.num_reqs && (a.scored || a.max_query_len == 1);
+      splits >= kDeepPieces * a.num_reqs && (a.scored || a.max_query_len <= a.few);
   if (a.score.softcap > 0.f) p.scale_log2 = 2.f * kLog2e * (a.scale / a.score.softcap);
   p.dec_prefix = ws.dec_prefix;
   p.hdr = ws.hdr;

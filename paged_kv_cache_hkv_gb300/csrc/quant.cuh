@@ -8,7 +8,8 @@
 // the power makes the division exact, and code * 2^e, four significant bits, is
 // exactly a bf16: rows read back are exact, and attention over rows turned into
 // bf16 is attention over what the pool holds. A row with an infinity or a NaN
-// is held as NaN (codes 0x7f, scale 255).
+// is held as NaN: codes 0 and scale 255, 0 times fp32's 2^128, an infinity. (So no
+// code is a NaN, and a weight of 0 leaves nothing of a masked row.)
 #pragma once
 
 #include <cuda_fp16.h>
@@ -19,7 +20,7 @@ namespace pkv {
 
 // 2^-117 times the smallest code, 2^-9, is bf16's (and fp32's) smallest normal number.
 constexpr int kLeastExp = -117;
-constexpr uint32_t kNanScale = 255u, kNanCodes = 0x7f7f7f7fu;
+constexpr uint32_t kNanScale = 255u;
 
 // Scale byte of a row whose largest bf16 magnitude has the bits `amax`
 // (exponent E, mantissa M): 448 = 1.75 * 2^8, so e is E - 127 - 8, plus one where
@@ -34,6 +35,12 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
 __device__ __forceinline__ float scale_value(uint32_t s) {
   const float f = __uint_as_float(s << 23);
   return fmaf(f, 0.f, f);  // an infinity times 0 is a NaN
+}
+
+// scale - 127 as a float, NaN for kNanScale.
+__device__ __forceinline__ float scale_exponent(uint32_t s) {
+  const float e = __uint_as_float(0x4b000000u | s) - 8388735.f;  // (2^23 + s) - (2^23 + 127)
+  return fmaf(__uint_as_float(s << 23), 0.f, e);
 }
 
 // Two floats to two e4m3 codes (a in the low byte), to nearest even; values
@@ -72,7 +79,7 @@ __device__ __forceinline__ float mul_subnormal(float x, float m) {
 
 // Eight bf16 to eight codes under the scale byte s.
 __device__ __forceinline__ uint2 quant8(const uint4& v, uint32_t s) {
-  if (s == kNanScale) return make_uint2(kNanCodes, kNanCodes);
+  if (s == kNanScale) return make_uint2(0u, 0u);
   const float m = __uint_as_float((254u - s) << 23);  // 2^(127 - s)
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t c[4];

@@ -11,18 +11,27 @@
 // The math is on the tensor cores, for half the bytes a key leaves half the time:
 // the bf16 decode's FMAs take 40% of the issue slots at 7 TB/s, and twice the keys
 // a second plus their conversion would be over all of them. A consumer warp holds
-// up to 16 units (query row x q head) of one kv head, eight to a tile:
-//   S [units x keys]: mma.m16n8k32 on the codes as they are. bf16 q's 8
-//     significant bits are two e4m3 numbers of 4: q 2^-e = hi + lo / 16, exactly
-//     but for 2^-23 of the row's largest. The tile's 16 rows are hi of its eight units
-//     and lo of the same; S = (S_hi + S_lo / 16) 2^e times the key's scale.
-//   O^T [dims x units] += V^T P^T: mma.m16n8k16 in bf16. The S tile's registers
-//     are the P^T operand as they stand; V's scale goes into P (fp32, rounded once
-//     to bf16). ldmatrix.trans hands a thread two keys' bytes of two neighbouring
-//     dims, which are the even and odd rows of a V^T tile; a code becomes a bf16
-//     by moving its exponent and mantissa into place and a product with 2^120.
+// MT tiles of 8 units (query row x q head) of one kv head, all in mma.m16n8k16
+// with f16 operands:
+//   S^T [16 keys x 8 units] = K Q^T: codes become f16 by one conversion per two
+//     (exact); a thread's four bytes of a key are its two pairs of a K step, so the
+//     dims need no reordering but q's, which is loaded that way. q 2^-e, e as for
+//     a row of the pool, is an f16 but for what lies below 2^-32 of the row's
+//     largest. The scores are S 2^e times the key's scale.
+//   O^T [16 dims x 8 units] += V^T P^T: ldmatrix.trans hands a thread two keys'
+//     bytes of two neighbouring dims, the even and odd rows of a V^T tile. P^T is
+//     S^T's registers through movmatrix.
+// V's scales 2^v go into the exponent of P: weight 2^(s + v - M), M the running
+// maximum of s + v, in f16 (11 bits; below 2^-14 of the largest weight 2^-25 of
+// it). The sum of weights keeps a running maximum of s of its own, so that rows
+// of tiny or huge V change nothing in it, and O is scaled to it at the end.
+// (mma.m16n8k32 on the codes themselves is no shortcut: the compiler turns each into
+// conversions of both operands and two f16 products, 427 instructions a chunk and
+// warp instead of some 190, and 244 us instead of DECODE_LONG_US on 8 decodes of
+// 32767 to 131071 keys, 32 q and 8 kv heads, D = 128.)
 // K, V and the scales of a chunk are a copy or two each: a 4-D box lands them as
 // [K|V][kv head][16 keys][D], swizzled, so that ldmatrix finds no bank conflict.
+#include <cfloat>
 #include <mutex>
 #include <vector>
 
@@ -45,16 +54,19 @@ struct QuantDecodeParams : DecodeParams {
 };
 
 // Shared memory of a CTA (bytes from a 1024-aligned base): S stages of the
-// chunk's codes and scales, two words of metadata a stage, the barriers.
+// chunk's codes and scales, two words of metadata a stage, the barriers; with two
+// or more unit tiles a warp the warps' q, [tile][K step][lane] of 8 bytes.
 struct QuantLayout {
-  uint32_t kv_bytes, scale_bytes, stage_bytes, meta_off, bar_off, total;
-  __host__ __device__ QuantLayout(int head_dim, int kh, int num_kv_heads, int S) {
+  uint32_t kv_bytes, scale_bytes, stage_bytes, meta_off, bar_off, q_off, q_bytes, total;
+  __host__ __device__ QuantLayout(int head_dim, int kh, int num_kv_heads, int nw, int mt, int S) {
     kv_bytes = 32u * static_cast<uint32_t>(kh) * head_dim;
     scale_bytes = 32u * static_cast<uint32_t>(num_kv_heads);
     stage_bytes = (kv_bytes + scale_bytes + 1023u) & ~1023u;
     meta_off = S * stage_bytes;
     bar_off = meta_off + S * 32u;
-    total = bar_off + 2u * S * 8u;
+    q_off = (bar_off + 2u * S * 8u + 255u) & ~255u;
+    q_bytes = mt > 1 ? static_cast<uint32_t>(mt) * (head_dim / 16) * 256u : 0u;
+    total = q_off + nw * q_bytes;
   }
 };
 
@@ -80,44 +92,44 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// The codes in bytes 1 and 3 (odd) or 0 and 2 (even) of w as two bf16. Sign,
-// exponent and mantissa moved to bf16's places make the value times 2^-120 (the
-// exponents' biases are 7 and 127), subnormal codes and all; the product puts it right.
-__device__ __forceinline__ uint32_t bf16_of_codes(uint32_t sign_src, uint32_t mag_src) {
-  const uint32_t b = (sign_src & 0x80008000u) | (mag_src & 0x07f007f0u);
+// An 8 x 8 tile of 16-bit values, as ldmatrix hands it out, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(b), "r"(0x7b807b80u));  // 2^120 twice
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-__device__ __forceinline__ uint32_t codes_even(uint32_t w) { return bf16_of_codes(w << 8, w << 4); }
-__device__ __forceinline__ uint32_t codes_odd(uint32_t w) { return bf16_of_codes(w, w >> 4); }
+
+// Four codes as two pairs of f16: the bytes 0, 1 and 2, 3.
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 
 template <int D, int SH, int MT, bool SCORED>
-__global__ void __launch_bounds__(kQuantDecodeThreads)
+__global__ void __launch_bounds__(kQuantDecodeThreads, MT == 1 ? 2 : 1)
     quant_decode_kernel(const __grid_constant__ CUtensorMap kv_map, const QuantDecodeParams p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int KH = p.slab_heads, WPH = p.warps_per_head, NW = KH * WPH, HKV = p.num_kv_heads;
   const uint32_t S = static_cast<uint32_t>(p.stages);
-  const QuantLayout lay(D, KH, HKV, p.stages);
-  // of a stage: (flags, first key, out_base, -), and with kFirst (batch row, rows, keys, -)
+  const QuantLayout lay(D, KH, HKV, NW, MT, p.stages);
+  // of a stage: (flags, first key, out_base, which of the 16 keys hold rows that the
+  // request sees: first | end << 8), and with kFirst (batch row, rows, keys, shared keys)
   int4* meta = reinterpret_cast<int4*>(base + lay.meta_off);
   uint64_t* full = reinterpret_cast<uint64_t*>(base + lay.bar_off);
   uint64_t* empty = full + S;
@@ -249,7 +261,8 @@ __global__ void __launch_bounds__(kQuantDecodeThreads)
       if (lane == 0) {
         const bool last = blk == nblk - 1 || x == x1 - 1;
         meta[2 * s] = make_int4((new_piece ? kFirst : 0) | (last ? kLast : 0) | (valid ? 0 : kInvalid),
-                                k0, out_base, 0);
+                                k0, out_base,
+                                max(0, q.lo - k0) | (max(0, min(kChunkKeys, q.hi - k0)) << 8));
         if (new_piece) meta[2 * s + 1] = make_int4(q.t, q.n, q.L, key_base(r));
         unsigned char* stage = base + s * lay.stage_bytes;
         unsigned char* sc = stage + lay.kv_bytes;
@@ -325,22 +338,25 @@ __global__ void __launch_bounds__(kQuantDecodeThreads)
   const int tile0 = (warp - hl * WPH) * MT;
   const int g = lane >> 2, t4 = lane & 3;
   const int gsh = p.group_shift, G = 1 << gsh;
-  constexpr int KS = D / 32;  // k steps of S, and pairs of V^T tiles
-  uint32_t qa[MT][KS][4];
+  // This lane holds S and P of keys g and g + 8, and O of dims 16 i + 2 g and
+  // 16 i + 2 g + 1, for the units 8 (tile0 + mt) + 2 t4 + j, j = 0, 1.
+  // q: in registers with one tile, in shared memory with more (a lane's own values)
+  uint32_t qb[MT == 1 ? D / 16 : 1][2];
+  uint2* qs = reinterpret_cast<uint2*>(base + lay.q_off + warp * lay.q_bytes) + lane;
   float o[MT][D / 16][4];
-  float fq[MT], m_run[MT], l_run[MT];  // of unit 8 (tile0 + mt) + g
-  int lim_lo[MT], lim_hi[MT], ref[MT];  // the unit's keys; SCORED: where distances count from
-  float slope2[MT];
+  float fq[MT][2], m_s[MT][2], m_w[MT][2], l_run[MT][2];
+  // SCORED: the unit's keys, and where its distances count from
+  int lim_lo[MT][2], lim_hi[MT][2], ref[MT][2];
+  float slope2[MT][2];
   const float cap2 = SCORED ? p.score.softcap * kLog2e : 0.f;
   int t = 0, n = 0, my_tiles = 0, hi_all = 0;
-  // this lane's ldmatrix addresses: row lane % 8 of an 8-key group, 16-byte unit
-  // (swizzled by the row) lane / 8 for K, lane / 16 for V, whose lanes 8-15 and
-  // 24-31 take the second group
+  // This lane's ldmatrix address within K: row lane % 8 of an 8-key group, lanes
+  // 8-15 and 24-31 of the second group, 16-byte unit lane / 16 swizzled by the row.
   const int row8 = lane & 7, swz = D == 128 ? row8 : row8 >> 1;
-  const uint32_t gstep = SH == 3 ? 16u * KH * D : 8u * D;  // bytes between a head's key groups
-  const uint32_t k_off = (SH == 3 ? 8u : 16u) * hl * D + row8 * D + (((lane >> 3) ^ swz) << 4);
-  const uint32_t v_off = (SH == 3 ? 8u : 16u) * (KH + hl) * D + row8 * D +
-                         ((lane >> 3) & 1 ? gstep : 0u) + (((lane >> 4) ^ swz) << 4);
+  const uint32_t group_step = SH == 3 ? 16u * KH * D : 8u * D;  // bytes between key groups
+  const uint32_t kv_step = (SH == 3 ? 8u : 16u) * KH * D;       // K to V
+  const uint32_t k_off = (SH == 3 ? 8u : 16u) * hl * D + row8 * D +
+                         ((lane >> 3) & 1 ? group_step : 0u) + (((lane >> 4) ^ swz) << 4);
 
   for (uint32_t s = 0, fph = 0;;) {  // ring slot, parity of its full barrier
     if (!mbar_wait(&full[s], fph)) {
@@ -361,51 +377,55 @@ __global__ void __launch_bounds__(kQuantDecodeThreads)
       hi_all = L - n + 1;  // keys below it are seen by every row (plain scores)
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
+        // q's row of unit 8 (tile0 + mt) + g: dims 16 x + 4 t4 .. + 3
         const int u = 8 * (tile0 + mt) + g, i = u >> gsh, h = u & (G - 1);
-        const bool unit = i < n;
-        m_run[mt] = -INFINITY;
-        l_run[mt] = 0.f;
-        lim_lo[mt] = ref[mt] = 0;
-        lim_hi[mt] = 0x7fffffff;  // (a place without a unit masks nothing)
-        slope2[mt] = 0.f;
-        if (unit) {
-          const int pos = L - n + i;
-          lim_hi[mt] = pos + 1;
-          if constexpr (SCORED) {
-            const KeyRange k = row_keys(p.score, static_cast<long long>(t) + i, pos, L, f.w);
-            const KeyRange all = row_keys(p.score, static_cast<long long>(t) + i, pos, L, 0);
-            lim_lo[mt] = k.lo;
-            lim_hi[mt] = k.hi;
-            ref[mt] = max(min(pos, all.hi - 1), all.lo);
-            slope2[mt] = slope_log2(p.score, hk * G + h);
-          }
-        }
-        // the unit's q row: dims 32 ks + 4 t4 .. and 32 ks + 16 + 4 t4 ..
-        uint2 w[2 * KS];
+        uint2 w[D / 16];
         const uint16_t* src =
             p.q + (static_cast<long long>(t) + i) * p.q_stride + (hk * G + h) * D + 4 * t4;
         uint32_t amax = 0;
 #pragma unroll
-        for (int x = 0; x < 2 * KS; ++x) {
-          w[x] = unit ? __ldg(reinterpret_cast<const uint2*>(src + 16 * x)) : make_uint2(0, 0);
-          amax = max(amax, amax8(make_uint4(w[x].x, w[x].y, 0, 0)));
-        }
+        for (int x = 0; x < D / 16; ++x)
+          w[x] = i < n ? __ldg(reinterpret_cast<const uint2*>(src + 16 * x)) : make_uint2(0, 0);
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) amax = max(amax, amax8(make_uint4(w[x].x, w[x].y, 0, 0)));
         amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         const uint32_t sb = scale_byte(amax);
-        // (a row with an infinity or a NaN makes all its scores NaN)
-        fq[mt] = p.scale_log2 * scale_value(sb);
         const float inv = __uint_as_float((254u - min(sb, 254u)) << 23);
 #pragma unroll
-        for (int x = 0; x < 2 * KS; ++x) {
-          const float v0 = bf16_lo(w[x].x) * inv, v1 = bf16_hi(w[x].x) * inv;
-          const float v2 = bf16_lo(w[x].y) * inv, v3 = bf16_hi(w[x].y) * inv;
-          const uint32_t h0 = e4m3x2(v0, v1), h1 = e4m3x2(v2, v3);
-          const float2 b0 = e4m3_float2(h0), b1 = e4m3_float2(h1);
-          qa[mt][x >> 1][2 * (x & 1)] = h0 | (h1 << 16);
-          qa[mt][x >> 1][2 * (x & 1) + 1] =
-              e4m3x2((v0 - b0.x) * 16.f, (v1 - b0.y) * 16.f) |
-              (e4m3x2((v2 - b1.x) * 16.f, (v3 - b1.y) * 16.f) << 16);
+        for (int x = 0; x < D / 16; ++x) {
+          const uint2 v = make_uint2(pack_f16x2(bf16_lo(w[x].x) * inv, bf16_hi(w[x].x) * inv),
+                                     pack_f16x2(bf16_lo(w[x].y) * inv, bf16_hi(w[x].y) * inv));
+          if constexpr (MT == 1) {
+            qb[x][0] = v.x;
+            qb[x][1] = v.y;
+          } else {
+            qs[(mt * (D / 16) + x) * 32] = v;
+          }
+        }
+        // (a row with an infinity or a NaN makes all its scores NaN)
+        const float f_mine = p.scale_log2 * scale_value(sb);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          fq[mt][j] = __shfl_sync(0xffffffffu, f_mine, 8 * t4 + 4 * j);
+          const int uj = 8 * (tile0 + mt) + 2 * t4 + j, ij = uj >> gsh;
+          m_s[mt][j] = m_w[mt][j] = -FLT_MAX;  // (finite: no difference of infinities)
+          l_run[mt][j] = 0.f;
+          if constexpr (SCORED) {
+            lim_lo[mt][j] = ref[mt][j] = 0;
+            lim_hi[mt][j] = 0x7fffffff;  // (a place without a unit masks nothing)
+            slope2[mt][j] = 0.f;
+            if (ij < n) {
+              const int pos = L - n + ij;
+              const long long row = static_cast<long long>(t) + ij;
+              const KeyRange k = row_keys(p.score, row, pos, L, f.w);
+              const KeyRange all = row_keys(p.score, row, pos, L, 0);
+              lim_lo[mt][j] = k.lo;
+              lim_hi[mt][j] = k.hi;
+              ref[mt][j] = max(min(pos, all.hi - 1), all.lo);
+              slope2[mt][j] = slope_log2(p.score, hk * G + (uj & (G - 1)));
+            }
+          }
         }
 #pragma unroll
         for (int i2 = 0; i2 < D / 16; ++i2)
@@ -415,122 +435,158 @@ __global__ void __launch_bounds__(kQuantDecodeThreads)
     }
 
     if (!(flags & kInvalid) && my_tiles > 0) {
-      const uint32_t kv = smem_u32(stage);
-      // ---- S of the chunk's two groups of 8 keys
-      float acc[MT][2][4];
+      const uint32_t k_addr = smem_u32(stage) + k_off, v_addr = k_addr + kv_step;
+      // ---- S^T
+      float acc[MT][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int ng = 0; ng < 2; ++ng)
+        for (int e = 0; e < 4; ++e) acc[mt][e] = 0.f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[mt][ng][e] = 0.f;
+      for (int kk = 0; kk < D / 32; ++kk) {
+        uint32_t w[4], a[2][4];
+        ldsm4(k_addr ^ (kk << 5), w);
 #pragma unroll
-      for (int kk = 0; kk < KS / 2; ++kk)
+        for (int x = 0; x < 4; ++x) codes_f16(w[x], a[x >> 1][x & 1], a[x >> 1][2 + (x & 1)]);
 #pragma unroll
-        for (int ng = 0; ng < 2; ++ng) {
-          uint32_t b[4];
-          ldsm4((kv + k_off + ng * gstep) ^ (kk << 6), b);
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            if (MT > 1 && mt >= my_tiles) continue;
-            mma_e4m3(acc[mt][ng], qa[mt][2 * kk], b[0], b[1]);
-            mma_e4m3(acc[mt][ng], qa[mt][2 * kk + 1], b[2], b[3]);
+          for (int h = 0; h < 2; ++h) {
+            if constexpr (MT == 1) {
+              mma_f16(acc[mt], a[h], qb[2 * kk + h][0], qb[2 * kk + h][1]);
+            } else {
+              const uint2 v = qs[(mt * (D / 16) + 2 * kk + h) * 32];
+              mma_f16(acc[mt], a[h], v.x, v.y);
+            }
           }
-        }
-      // scales of this lane's keys 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4
-      float ks[4], vs[4];
+      }
+      // ---- scales of keys g and g + 8: K's as a factor, V's as an exponent
+      float ks[2], ve[2];
       const unsigned char* sc = stage + lay.kv_bytes + hk;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int j = (x >> 1) * 8 + 2 * t4 + (x & 1);
-        const int kr = SH == 3 ? (j & 7) + (j >> 3) * 16 : j;
+      for (int x = 0; x < 2; ++x) {
+        const int kr = SH == 3 ? g + 16 * x : g + 8 * x;
         ks[x] = scale_value(sc[kr * HKV]);
-        vs[x] = scale_value(sc[(kr + (SH == 3 ? 8 : 16)) * HKV]);
+        ve[x] = scale_exponent(sc[(kr + (SH == 3 ? 8 : 16)) * HKV]);
       }
-      // ---- softmax, and P^T times V's scales as the PV operand
-      uint32_t pb[MT][2];
       bool whole = true;  // every unit sees the whole chunk
       if constexpr (SCORED) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
-          whole = whole && lim_lo[mt] <= k0 && lim_hi[mt] >= k0 + kChunkKeys;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            whole = whole && lim_lo[mt][j] <= k0 && lim_hi[mt][j] >= k0 + kChunkKeys;
         whole = __all_sync(0xffffffffu, whole);
       } else {
         whole = hi_all >= k0 + kChunkKeys;
       }
+      // ---- softmax: element e is key g + 8 (e / 2), unit j = e % 2
+      float sv[MT][4];
+      bool high = false;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = e & 1, x = e >> 1;
+          float v = acc[mt][e] * (fq[mt][j] * ks[x]);
+          if constexpr (SCORED) {
+            if (p.score.softcap > 0.f) v = cap2 * tanh_log2(v);
+            if (p.score.slopes)
+              v -= slope2[mt][j] * fabsf(static_cast<float>(ref[mt][j] - (k0 + g + 8 * x)));
+          }
+          sv[mt][e] = v;
+        }
+      if (!whole) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = e & 1, key = k0 + g + 8 * (e >> 1);
+            const int unit = 8 * (tile0 + mt) + 2 * t4 + j;
+            if (SCORED ? key < lim_lo[mt][j] || key >= lim_hi[mt][j]
+                       : key >= hi_all + (unit >> gsh))
+              sv[mt][e] = -INFINITY;
+          }
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = e & 1;
+          high = high || sv[mt][e] > m_s[mt][j] + kRescaleLog2 ||
+                 sv[mt][e] + ve[e >> 1] > m_w[mt][j] + kRescaleLog2;
+        }
+      if (__any_sync(0xffffffffu, high)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float a = fmaxf(sv[mt][j], sv[mt][2 + j]);
+            float b = fmaxf(sv[mt][j] + ve[0], sv[mt][2 + j] + ve[1]);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) {
+              a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+              b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, off));
+            }
+            a = fmaxf(a, m_s[mt][j]);
+            b = fmaxf(b, m_w[mt][j]);
+            l_run[mt][j] *= exp2f(m_s[mt][j] - a);
+            const float alpha = exp2f(m_w[mt][j] - b);
+            m_s[mt][j] = a;
+            m_w[mt][j] = b;
+#pragma unroll
+            for (int i2 = 0; i2 < D / 16; ++i2) {
+              o[mt][i2][j] *= alpha;
+              o[mt][i2][2 + j] *= alpha;
+            }
+          }
+      }
+      uint32_t pb[MT][2];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        if (MT > 1 && mt >= my_tiles) continue;
-        float sv[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float a = acc[mt][x >> 1][x & 1], b = acc[mt][x >> 1][2 + (x & 1)];
-          sv[x] = fmaf(b, 0.0625f, a) * (fq[mt] * ks[x]);
-          if constexpr (SCORED) {
-            const int key = k0 + (x >> 1) * 8 + 2 * t4 + (x & 1);
-            if (p.score.softcap > 0.f) sv[x] = cap2 * tanh_log2(sv[x]);
-            if (p.score.slopes) sv[x] -= slope2[mt] * fabsf(static_cast<float>(ref[mt] - key));
-          }
-        }
-        if (!whole) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int key = k0 + (x >> 1) * 8 + 2 * t4 + (x & 1);
-            if (key < lim_lo[mt] || key >= lim_hi[mt]) sv[x] = -INFINITY;
-          }
-        }
-        float lmax = fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3]));
-        if (__any_sync(0xffffffffu, lmax > m_run[mt] + kRescaleLog2)) {
-          lmax = fmaxf(lmax, __shfl_xor_sync(0xffffffffu, lmax, 1));
-          lmax = fmaxf(lmax, __shfl_xor_sync(0xffffffffu, lmax, 2));
-          const float m_new = fmaxf(m_run[mt], lmax);
-          const float alpha = m_new == -INFINITY ? 1.f : exp2f(m_run[mt] - m_new);
-          l_run[mt] *= alpha;
-          m_run[mt] = m_new;
-          // O's columns are units 2 t4 and 2 t4 + 1
-          const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * t4);
-          const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * t4 + 4);
-#pragma unroll
-          for (int i2 = 0; i2 < D / 16; ++i2) {
-            o[mt][i2][0] *= a0;
-            o[mt][i2][1] *= a1;
-            o[mt][i2][2] *= a0;
-            o[mt][i2][3] *= a1;
-          }
-        }
-        const float msub = m_run[mt] == -INFINITY ? 0.f : m_run[mt];
         float pv[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float e = exp2f(sv[x] - msub);
-          l_run[mt] += e;
-          pv[x] = e * vs[x];
+        for (int e = 0; e < 4; ++e) {
+          const int j = e & 1;
+          l_run[mt][j] += exp2f(sv[mt][e] - m_s[mt][j]);
+          pv[e] = exp2f(sv[mt][e] + (ve[e >> 1] - m_w[mt][j]));
         }
-        if (!whole) {  // (a masked key's scale may be anything)
+        if (!whole) {  // (a masked row may be NaN: its exponent is one then)
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (sv[x] == -INFINITY) pv[x] = 0.f;
+          for (int e = 0; e < 4; ++e)
+            if (sv[mt][e] == -INFINITY) pv[e] = 0.f;
         }
-        pb[mt][0] = pack_bf16x2(pv[0], pv[1]);
-        pb[mt][1] = pack_bf16x2(pv[2], pv[3]);
+        pb[mt][0] = transpose8(pack_f16x2(pv[0], pv[1]));
+        pb[mt][1] = transpose8(pack_f16x2(pv[2], pv[3]));
       }
       // ---- O^T += V^T P^T
+      uint32_t keep[2] = {0xffffffffu, 0xffffffffu};  // of keys 2 t4, 2 t4 + 1 and those + 8
+      const bool edge = m.w != (kChunkKeys << 8);
+      if (edge) {
+        // rows that are not the request's may hold NaN codes, which weight 0 does not undo
+        const int a = m.w & 255, z = m.w >> 8;
 #pragma unroll
-      for (int i2 = 0; i2 < KS; ++i2) {
-        uint32_t w[4], a[2][4];
-        ldsm4_trans((kv + v_off) ^ (i2 << 5), w);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          a[h][0] = codes_even(w[2 * h]);
-          a[h][1] = codes_odd(w[2 * h]);
-          a[h][2] = codes_even(w[2 * h + 1]);
-          a[h][3] = codes_odd(w[2 * h + 1]);
+        for (int x = 0; x < 2; ++x) {
+          const int j = 8 * x + 2 * t4;
+          keep[x] = (j >= a && j < z ? 0xffffu : 0u) | (j + 1 >= a && j + 1 < z ? 0xffff0000u : 0u);
         }
+      }
+#pragma unroll
+      for (int i2 = 0; i2 < D / 32; ++i2) {
+        uint32_t w[4], a[2][4];
+        ldsm4_trans(v_addr ^ (i2 << 5), w);
+        if (edge) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) w[x] &= keep[x & 1];
+        }
+        // bytes: (key 2 t4, even dim), (same, odd), (key 2 t4 + 1, even), (same, odd)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          codes_f16(__byte_perm(w[x], 0, 0x3120), a[x >> 1][2 * (x & 1)], a[x >> 1][2 * (x & 1) + 1]);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          if (MT > 1 && mt >= my_tiles) continue;
-          mma_bf16(o[mt][2 * i2], a[0], pb[mt][0], pb[mt][1]);
-          mma_bf16(o[mt][2 * i2 + 1], a[1], pb[mt][0], pb[mt][1]);
+          mma_f16(o[mt][2 * i2], a[0], pb[mt][0], pb[mt][1]);
+          mma_f16(o[mt][2 * i2 + 1], a[1], pb[mt][0], pb[mt][1]);
         }
       }
     }
@@ -541,24 +597,24 @@ __global__ void __launch_bounds__(kQuantDecodeThreads)
     if ((flags & kLast) && my_tiles > 0) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        float l = l_run[mt];
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {  // units 2 t4 + j: O's columns in o[..][..][j] and [2 + j]
-          const float lj = __shfl_sync(0xffffffffu, l, 8 * t4 + 4 * j);
-          const float mj = __shfl_sync(0xffffffffu, m_run[mt], 8 * t4 + 4 * j);
+        for (int j = 0; j < 2; ++j) {
+          float l = l_run[mt][j];
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
           const int u = 8 * (tile0 + mt) + 2 * t4 + j, i = u >> gsh, h = u & (G - 1);
           if (i >= n) continue;
           const int head = hk * G + h;
+          // O's weights are 2^(s + v - m_w): to 2^(s - m_s)
+          float f = exp2f(m_w[mt][j] - m_s[mt][j]);
           if (out_base < 0) {
-            const float inv = SCORED && lj == 0.f ? 0.f : 1.f / lj;  // no key seen: zeros
+            f = SCORED && l == 0.f ? 0.f : f / l;  // no key seen: zeros
             uint16_t* dst =
                 p.out + ((static_cast<long long>(t) + i) * p.num_q_heads + head) * D + 2 * g;
 #pragma unroll
             for (int i2 = 0; i2 < D / 16; ++i2)
               *reinterpret_cast<uint32_t*>(dst + 16 * i2) =
-                  pack_bf16x2(o[mt][i2][j] * inv, o[mt][i2][2 + j] * inv);
+                  pack_bf16x2(o[mt][i2][j] * f, o[mt][i2][2 + j] * f);
           } else {
             // n == 1: out_base is (r + c) * V, virtual heads of G or 4 q heads;
             // several rows: a slot of the few-row partials
@@ -566,11 +622,11 @@ __global__ void __launch_bounds__(kQuantDecodeThreads)
                 n == 1 ? static_cast<long long>(out_base) * (p.num_q_heads / p.virt_heads) + head
                        : (static_cast<long long>(out_base) * p.few + i) * p.num_q_heads + head;
             float* dst = (n == 1 ? p.part_o : p.few_o) + slot * D + 2 * g;
-            if (g == 0) (n == 1 ? p.part_ml : p.few_ml)[slot] = make_float2(mj, lj);
+            if (g == 0) (n == 1 ? p.part_ml : p.few_ml)[slot] = make_float2(m_s[mt][j], l);
 #pragma unroll
             for (int i2 = 0; i2 < D / 16; ++i2)
               *reinterpret_cast<float2*>(dst + 16 * i2) =
-                  make_float2(o[mt][i2][j], o[mt][i2][2 + j]);
+                  make_float2(o[mt][i2][j] * f, o[mt][i2][2 + j] * f);
           }
         }
       }
@@ -585,22 +641,27 @@ __global__ void __launch_bounds__(kQuantDecodeThreads)
 // ------------------------------------------------------------------ host
 constexpr int kQuantMinStages = 2, kQuantMaxStages = 8;
 
-// Unit tiles that the largest request on the stream needs, the tiles of a
-// consumer warp, and the warps of a kv head.
+// Unit tiles of a consumer warp, the warps of a kv head, and the most rows of a
+// request on the stream. At most kQuantTiles tiles, whose O takes 96 registers of
+// a lane at D = 128: nine warps, three on one of the SM's four register files, have
+// 168 each.
 struct QuantShape {
   int few, mt, wph;
 };
+constexpr int kQuantTiles = 3;
 
 // Steps whose every request has so few new tokens that their units fit the CTA's
-// warps (kFewUnits) stream all of them; in a step with longer chunks those of up
-// to 16 units do, one warp a head, and the others go to the prefill kernel.
+// warps (kFewUnits) stream all of them. In a step with longer chunks those of one
+// tile do and the others go to the prefill kernel: most requests of such a step are
+// decodes, and one tile a warp streams them at the copy bandwidth (118 us for 320
+// decodes of 127-2047 keys and three tiles' 156).
 static QuantShape quant_shape(int max_query_len, int group) {
-  const int units = max_query_len <= kFewUnits / group ? max_query_len * group : 16;
-  const int tiles = (units + 7) / 8;
+  const bool all = max_query_len <= kFewUnits / group;
+  const int tiles = all ? (max_query_len * group + 7) / 8 : 1;
   QuantShape s;
-  s.mt = tiles == 1 ? 1 : 2;
-  s.wph = (tiles + s.mt - 1) / s.mt;
-  s.few = max_query_len <= kFewUnits / group ? max_query_len : 16 / group;
+  s.wph = (tiles + kQuantTiles - 1) / kQuantTiles;
+  s.mt = (tiles + s.wph - 1) / s.wph;
+  s.few = all ? max_query_len : 8 / group;
   return s;
 }
 
@@ -615,14 +676,20 @@ int quant_slab_heads(int num_kv_heads, int group, int max_query_len) {
   return s;
 }
 
-// CTAs of nw consumer warps an SM is meant to hold.
-static int quant_ctas(int nw) { return kQuantWarps / nw < 1 ? 1 : kQuantWarps / nw; }
+// CTAs of nw consumer warps an SM is meant to hold: 16 such warps with one tile
+// each (8 decodes of 32767-131071 keys: 202 us, the copies alone 200, with 8 warps
+// 227), 8 with more, for their registers.
+static int quant_ctas(int nw, int mt) {
+  const int warps = mt == 1 ? 2 * kQuantWarps : kQuantWarps;
+  return warps / nw < 1 ? 1 : warps / nw;
+}
 
 long long quant_most_splits(int num_kv_heads, int group, int num_sms) {
   int most = 1;
   for (int n = 1; n <= kFewUnits / group + 1; ++n) {
-    const int nw = quant_slab_heads(num_kv_heads, group, n) * quant_shape(n, group).wph;
-    if (quant_ctas(nw) > most) most = quant_ctas(nw);
+    const QuantShape q = quant_shape(n, group);
+    const int ctas = quant_ctas(quant_slab_heads(num_kv_heads, group, n) * q.wph, q.mt);
+    if (ctas > most) most = ctas;
   }
   return static_cast<long long>(num_sms) * most;
 }
@@ -654,8 +721,8 @@ static cudaError_t quant_prepare(int kh, int hkv, int nw, int num_sms, QuantPrep
       *out = d;
       return cudaSuccess;
     }
-  const int want = quant_ctas(nw);
-  auto bytes = [&](int S) { return QuantLayout(D, kh, hkv, S).total + 1024u; };
+  const int want = quant_ctas(nw, MT);
+  auto bytes = [&](int S) { return QuantLayout(D, kh, hkv, nw, MT, S).total + 1024u; };
   int fit = 0;
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kern, (nw + 1) * 32, bytes(kQuantMinStages));
   if (e != cudaSuccess) return e;
@@ -678,7 +745,8 @@ static cudaError_t quant_dispatch(int head_dim, int sh, int mt, bool scored, A&&
   if (head_dim == D_ && sh == SH_ && mt == MT_)         \
     return scored ? F<D_, SH_, MT_, true>::run(args...) \
                   : F<D_, SH_, MT_, false>::run(args...);
-#define PKV_QUANT_MT(D_, SH_) PKV_QUANT_CASE(D_, SH_, 1) PKV_QUANT_CASE(D_, SH_, 2)
+#define PKV_QUANT_MT(D_, SH_) \
+  PKV_QUANT_CASE(D_, SH_, 1) PKV_QUANT_CASE(D_, SH_, 2) PKV_QUANT_CASE(D_, SH_, 3)
 #define PKV_QUANT_SH(D_) PKV_QUANT_MT(D_, 3) PKV_QUANT_MT(D_, 4) PKV_QUANT_MT(D_, 5)
   PKV_QUANT_SH(128) PKV_QUANT_SH(64)
 #undef PKV_QUANT_SH
