@@ -569,61 +569,68 @@ def pkv_release_blocks(block_table, release_rows, release_tokens, free_queue, fr
 
 
 def _quant_pool(kv_cache, kv_scales, names=("kv_cache", "kv_scales"), pinned=False):
-    """Layout of an 8-bit pool: codes [num_blocks, 2, B, Hkv, D] e4m3 and their
-    scales [num_blocks, 2, B, Hkv] uint8."""
+    """Layout and device index of an 8-bit pool: codes [num_blocks, 2, B, Hkv, D]
+    e4m3 and their scales [num_blocks, 2, B, Hkv] uint8. (The checks of these calls
+    look at each property once: they are most of a small call's host time.)"""
     for t, dtype, n in ((kv_cache, torch.float8_e4m3fn, names[0]),
                         (kv_scales, torch.uint8, names[1])):
         if t.dtype != dtype:
             raise ValueError(f"{n} must be {dtype}, got {t.dtype}")
-        if not (t.is_cuda or (pinned and t.is_pinned())):
+        if not t.is_cuda and not (pinned and t.is_pinned()):
             raise ValueError(f"{n} must be a CUDA tensor" +
                              (" or pinned host memory" if pinned else ""))
-    lay = layout_of(kv_cache)
-    if kv_scales.shape != kv_cache.shape[:4] or not kv_scales.is_contiguous():
+    shape = kv_cache.shape
+    if len(shape) != 5 or shape[1] != 2 or not kv_cache.is_contiguous():
+        raise ValueError(f"{names[0]} must be a contiguous [num_blocks, 2, block_size, Hkv, D] tensor")
+    if kv_scales.shape != shape[:4] or not kv_scales.is_contiguous():
         raise ValueError(f"{names[1]} must be a contiguous [num_blocks, 2, block_size, Hkv] tensor")
-    return lay
+    device = kv_cache.get_device()
+    if kv_scales.get_device() != device:
+        raise ValueError(f"tensors on {kv_cache.device} and {kv_scales.device} in one call")
+    return pkv_cache_layout(shape[0], shape[2], shape[3], shape[4]), device
 
 
-def _quant_rows(lay, num_tokens, *rows):
-    """Checks of (tensor, name) rows [T, H, D] bf16, contiguous within a token;
-    heads and dims those of the pool where the name is key or value."""
-    for t, n in rows:
-        _require(t, torch.bfloat16, n)
-        if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]) or (
-                num_tokens > 1 and t.stride(0) < t.shape[1] * t.shape[2]):
-            raise ValueError(f"{n} must be [T, H, D] with contiguous rows")
-        if t.shape[0] != num_tokens or t.shape[2] != lay.head_dim or (
-                n != "q" and t.shape[1] != lay.num_kv_heads):
-            raise ValueError(f"{n} has shape {tuple(t.shape)}: {num_tokens} rows of the pool's "
-                             "heads and dims are wanted")
+def _quant_rows(t, n, num_tokens, heads, dim, device):
+    """Checks of rows [T, H, D] bf16, contiguous within a token (heads None: any
+    number of them); returns their row stride, 0 for a single row, whose says nothing."""
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{n} must be {torch.bfloat16}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{n} is on {t.device}, the call's pool on cuda:{device}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or stride[2] != 1 or (shape[1] > 1 and stride[1] != shape[2]) or (
+            num_tokens > 1 and stride[0] < shape[1] * shape[2]):
+        raise ValueError(f"{n} must be [T, H, D] with contiguous rows")
+    if shape[0] != num_tokens or shape[2] != dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{n} has shape {tuple(shape)}: {num_tokens} rows of the pool's "
+                         "heads and dims are wanted")
+    return stride[0] if num_tokens > 1 else 0
 
 
-def _row_stride(t):
-    """Row stride argument of rows that _quant_rows has looked at (a single row's
-    stride says nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else 0
-
-
-def _quant_slots(slot_mapping, num_tokens):
-    _require(slot_mapping, torch.int64, "slot_mapping")
+def _quant_slots(slot_mapping, num_tokens, device):
+    if slot_mapping.dtype != torch.int64 or slot_mapping.get_device() != device:
+        raise ValueError(f"slot_mapping must be torch.int64 on cuda:{device}, got "
+                         f"{slot_mapping.dtype} on {slot_mapping.device}")
     if slot_mapping.shape != (num_tokens,) or not slot_mapping.is_contiguous():
         raise ValueError(f"slot_mapping must be a contiguous [{num_tokens}] tensor")
+    return slot_mapping.data_ptr()
 
 
 def pkv_quant_kv_write(kv_cache, kv_scales, key, value, slot_mapping, stream=None):
     """Quantise key/value rows ([T, Hkv, D] bf16, row-strided allowed) into the
     8-bit pool at their slots (see pagedkv.h)."""
-    lay = _quant_pool(kv_cache, kv_scales)
+    lay, device = _quant_pool(kv_cache, kv_scales)
     T = key.shape[0]
-    _quant_rows(lay, T, (key, "key"), (value, "value"))
-    _quant_slots(slot_mapping, T)
-    _one_device(kv_cache, kv_scales, key, value, slot_mapping)
-    _check("pkv_quant_kv_write", load().pkv_quant_kv_write(
-        _ptr(kv_cache), _ptr(kv_scales), _ptr(key), _ptr(value), _row_stride(key),
-        _row_stride(value), _ptr(slot_mapping), T, lay, _stream(stream, kv_cache.device.index)))
+    ks = _quant_rows(key, "key", T, lay.num_kv_heads, lay.head_dim, device)
+    vs = _quant_rows(value, "value", T, lay.num_kv_heads, lay.head_dim, device)
+    status = load().pkv_quant_kv_write(
+        kv_cache.data_ptr(), kv_scales.data_ptr(), key.data_ptr(), value.data_ptr(), ks, vs,
+        _quant_slots(slot_mapping, T, device), T, lay, _stream(stream, device))
+    if status:
+        raise PagedKVError("pkv_quant_kv_write", status)
 
 
-def _quant_batch(kv_cache, block_table, query_start_loc, num_computed_tokens, seq_lens=None):
+def _quant_batch(device, block_table, query_start_loc, num_computed_tokens, seq_lens=None):
     for t, n in ((block_table, "block_table"), (query_start_loc, "query_start_loc"),
                  (num_computed_tokens, "num_computed_tokens"), (seq_lens, "seq_lens")):
         if t is None and n == "seq_lens":
@@ -631,12 +638,13 @@ def _quant_batch(kv_cache, block_table, query_start_loc, num_computed_tokens, se
         _require(t, torch.int32, n)
         if not t.is_contiguous():
             raise ValueError(f"{n} must be contiguous")
+        if t.get_device() != device:
+            raise ValueError(f"{n} is on {t.device}, the call's pool on cuda:{device}")
     R = num_computed_tokens.shape[0]
     if block_table.dim() != 2 or block_table.shape[0] != R or query_start_loc.shape != (R + 1,) or (
             num_computed_tokens.dim() != 1 or (seq_lens is not None and seq_lens.shape != (R,))):
         raise ValueError("block_table, query_start_loc, seq_lens and num_computed_tokens must be "
                          "[R, max_blocks], [R + 1], [R] and [R]")
-    _one_device(kv_cache, block_table, query_start_loc, num_computed_tokens, seq_lens)
     return R
 
 
@@ -644,31 +652,31 @@ def pkv_quant_slot_mapping_and_write(kv_cache, kv_scales, key, value, block_tabl
                                      num_computed_tokens, slot_mapping=None, stream=None):
     """Slot mapping and quantised cache write in one launch (see pagedkv.h).
     slot_mapping (int64 [T]) receives the slots when given."""
-    lay = _quant_pool(kv_cache, kv_scales)
+    lay, device = _quant_pool(kv_cache, kv_scales)
     T = key.shape[0]
-    _quant_rows(lay, T, (key, "key"), (value, "value"))
-    if slot_mapping is not None:
-        _quant_slots(slot_mapping, T)
-    R = _quant_batch(kv_cache, block_table, query_start_loc, num_computed_tokens)
-    _one_device(kv_cache, kv_scales, key, value, slot_mapping)
+    ks = _quant_rows(key, "key", T, lay.num_kv_heads, lay.head_dim, device)
+    vs = _quant_rows(value, "value", T, lay.num_kv_heads, lay.head_dim, device)
+    slots = None if slot_mapping is None else _quant_slots(slot_mapping, T, device)
+    R = _quant_batch(device, block_table, query_start_loc, num_computed_tokens)
     _check("pkv_quant_slot_mapping_and_write", load().pkv_quant_slot_mapping_and_write(
-        _ptr(kv_cache), _ptr(kv_scales), _ptr(key), _ptr(value), _row_stride(key),
-        _row_stride(value), _ptr(slot_mapping), _ptr(block_table), block_table.shape[1], _ptr(query_start_loc),
-        _ptr(num_computed_tokens), R, T, lay, _stream(stream, kv_cache.device.index)))
+        _ptr(kv_cache), _ptr(kv_scales), _ptr(key), _ptr(value), ks, vs, slots, _ptr(block_table),
+        block_table.shape[1], _ptr(query_start_loc), _ptr(num_computed_tokens), R, T, lay,
+        _stream(stream, device)))
     return slot_mapping
 
 
 def pkv_quant_kv_read(key, value, kv_cache, kv_scales, slot_mapping, stream=None):
     """key, value ([T, Hkv, D] bf16, row-strided allowed) <- the pool's rows at
     the slots; rows with a negative slot stay as they are (see pagedkv.h)."""
-    lay = _quant_pool(kv_cache, kv_scales)
+    lay, device = _quant_pool(kv_cache, kv_scales)
     T = key.shape[0]
-    _quant_rows(lay, T, (key, "key"), (value, "value"))
-    _quant_slots(slot_mapping, T)
-    _one_device(kv_cache, kv_scales, key, value, slot_mapping)
-    _check("pkv_quant_kv_read", load().pkv_quant_kv_read(
-        _ptr(key), _ptr(value), _row_stride(key), _row_stride(value), _ptr(kv_cache),
-        _ptr(kv_scales), _ptr(slot_mapping), T, lay, _stream(stream, kv_cache.device.index)))
+    ks = _quant_rows(key, "key", T, lay.num_kv_heads, lay.head_dim, device)
+    vs = _quant_rows(value, "value", T, lay.num_kv_heads, lay.head_dim, device)
+    status = load().pkv_quant_kv_read(
+        key.data_ptr(), value.data_ptr(), ks, vs, kv_cache.data_ptr(), kv_scales.data_ptr(),
+        _quant_slots(slot_mapping, T, device), T, lay, _stream(stream, device))
+    if status:
+        raise PagedKVError("pkv_quant_kv_read", status)
 
 
 def pkv_quant_copy_blocks(dst_pool, dst_scales, src_pool, src_scales, block_pairs, stream=None):
@@ -676,7 +684,7 @@ def pkv_quant_copy_blocks(dst_pool, dst_scales, src_pool, src_scales, block_pair
     of block_pairs (int32 [n, 2] on the device). Pools are CUDA tensors or pinned
     host tensors."""
     _quant_pool(dst_pool, dst_scales, ("dst_pool", "dst_scales"), pinned=True)
-    lay = _quant_pool(src_pool, src_scales, ("src_pool", "src_scales"), pinned=True)
+    lay, _ = _quant_pool(src_pool, src_scales, ("src_pool", "src_scales"), pinned=True)
     _require(block_pairs, torch.int32, "block_pairs")
     if block_pairs.dim() != 2 or block_pairs.shape[1] != 2 or not block_pairs.is_contiguous():
         raise ValueError("block_pairs must be a contiguous [n, 2] int32 tensor")
@@ -724,25 +732,24 @@ def _quant_attention_args(out, q, kv_cache, kv_scales, block_table, seq_lens, qu
                           options, write=None):
     """Checked and marshalled arguments of pkv_quant_paged_attention, or with
     write = (key, value, slot_mapping) of its _with_write form; all but the stream."""
-    lay = _quant_pool(kv_cache, kv_scales)
+    lay, device = _quant_pool(kv_cache, kv_scales)
     T = q.shape[0]
-    _quant_rows(lay, T, (q, "q"))
+    qs = _quant_rows(q, "q", T, None, lay.head_dim, device)
     _require(out, torch.bfloat16, "out")
     if out.shape != q.shape or not out.is_contiguous():
         raise ValueError("out must be contiguous and of q's shape")
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
-    R = _quant_batch(kv_cache, block_table, query_start_loc, num_computed_tokens, seq_lens)
-    _one_device(kv_cache, kv_scales, out, q, workspace)
+    R = _quant_batch(device, block_table, query_start_loc, num_computed_tokens, seq_lens)
+    _one_device(kv_cache, out, workspace)
     rows = ()
     if write is not None:
         key, value, slot_mapping = write
-        _quant_rows(lay, T, (key, "key"), (value, "value"))
-        if slot_mapping is not None:
-            _quant_slots(slot_mapping, T)
-        _one_device(kv_cache, key, value, slot_mapping)
-        rows = (_ptr(key), _ptr(value), _row_stride(key), _row_stride(value), _ptr(slot_mapping))
-    return (_ptr(out), _ptr(q), _row_stride(q), _ptr(kv_cache), _ptr(kv_scales), *rows,
+        ks = _quant_rows(key, "key", T, lay.num_kv_heads, lay.head_dim, device)
+        vs = _quant_rows(value, "value", T, lay.num_kv_heads, lay.head_dim, device)
+        rows = (_ptr(key), _ptr(value), ks, vs,
+                None if slot_mapping is None else _quant_slots(slot_mapping, T, device))
+    return (_ptr(out), _ptr(q), qs, _ptr(kv_cache), _ptr(kv_scales), *rows,
             _ptr(block_table), block_table.shape[1], _ptr(seq_lens), _ptr(query_start_loc),
             _ptr(num_computed_tokens), R, T, int(max_query_len), int(max_seq_len), q.shape[1],
             float(scale), lay, _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -931,9 +938,10 @@ class StepCalls:
         self.attn_args = _quant_attention_args(*args)
         self.attn_write_args = _quant_attention_args(*args, (key, value, slot_mapping))
         lay, T, R = layout_of(kv_cache), q.shape[0], num_computed_tokens.shape[0]
-        _quant_slots(slot_mapping, T)
-        rows = (_ptr(kv_cache), _ptr(kv_scales), _ptr(key), _ptr(value), _row_stride(key),
-                _row_stride(value), _ptr(slot_mapping))
+        ks, vs = (_quant_rows(t, n, T, lay.num_kv_heads, lay.head_dim, self._device)
+                  for t, n in ((key, "key"), (value, "value")))
+        rows = (_ptr(kv_cache), _ptr(kv_scales), _ptr(key), _ptr(value), ks, vs,
+                _quant_slots(slot_mapping, T, self._device))
         tables = (_ptr(block_table), block_table.shape[1], _ptr(query_start_loc),
                   _ptr(num_computed_tokens), R, T)
         self.slot_args = (_ptr(slot_mapping), *tables, lay.num_blocks, lay.block_size)

@@ -790,7 +790,7 @@ int32_t pkv_quant_kv_write(void* kv_cache, uint8_t* kv_scales, const void* key, 
   cudaError_t e = pkv::launch_quant_write(
       kv_cache, kv_scales, key, value, key_row_stride, value_row_stride, slot_mapping, num_tokens,
       layout.num_blocks, block_shift_of(layout.block_size), layout.num_kv_heads, layout.head_dim,
-      d->num_sms, static_cast<cudaStream_t>(stream));
+      static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PKV_OK : cuda_fail(e, "quant_write launch");
 }
 
@@ -837,7 +837,7 @@ int32_t pkv_quant_kv_read(void* key, void* value, int64_t key_row_stride, int64_
   cudaError_t e = pkv::launch_quant_read(
       key, value, key_row_stride, value_row_stride, kv_cache, kv_scales, slot_mapping, num_tokens,
       layout.num_blocks, block_shift_of(layout.block_size), layout.num_kv_heads, layout.head_dim,
-      d->num_sms, static_cast<cudaStream_t>(stream));
+      static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PKV_OK : cuda_fail(e, "quant_read launch");
 }
 

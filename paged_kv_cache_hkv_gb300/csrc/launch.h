@@ -214,12 +214,12 @@ size_t release_workspace_bytes(int num_released, int max_blocks);
 cudaError_t launch_quant_write(void* codes, uint8_t* scales, const void* key, const void* value,
                                long long key_stride, long long value_stride, const int64_t* slots,
                                int num_tokens, int num_blocks, int shift, int num_kv_heads,
-                               int head_dim, int num_sms, cudaStream_t stream);
+                               int head_dim, cudaStream_t stream);
 cudaError_t launch_quant_mapped_write(const WriteRowsArgs& w, cudaStream_t stream);
 cudaError_t launch_quant_read(void* key, void* value, long long key_stride, long long value_stride,
                               const void* codes, const uint8_t* scales, const int64_t* slots,
                               int num_tokens, int num_blocks, int shift, int num_kv_heads,
-                              int head_dim, int num_sms, cudaStream_t stream);
+                              int head_dim, cudaStream_t stream);
 cudaError_t launch_quant_copy(void* dst, uint8_t* dst_scales, int dst_num_blocks, const void* src,
                               const uint8_t* src_scales, int src_num_blocks, const int32_t* pairs,
                               int num_pairs, int block_size, int num_kv_heads, int head_dim,

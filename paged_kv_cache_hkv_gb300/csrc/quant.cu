@@ -13,8 +13,11 @@ static __device__ uint32_t g_errors_quant;
 // the order of the bf16 pool's write: word w = (2 t + kv) * vec_per_row + e. A
 // row of one kv head is D / 8 words in as many neighbouring lanes, which find
 // its largest magnitude by shuffles; the first of them stores the scale. Every
-// thread issues the loads of its kQuantVecs words before it uses the first.
-constexpr int kQuantVecs = 4;
+// thread issues the loads of its kQuantVecs words before it uses the first. A CTA
+// per kQuantVecs * kQuantThreads words, however many: 16001 rows of 8 x 128 take
+// 23.8 us cold (floor 14.2), with four words a thread and two CTAs an SM 26.4; the
+// read of 131072 such rows 125 us (floor 119) and 144.
+constexpr int kQuantVecs = 2;
 constexpr int kQuantThreads = 512;
 
 template <int D>
@@ -89,8 +92,25 @@ __global__ void __launch_bounds__(kQuantMappedWarps * 32)
   if (t < w.num_tokens) quant_token_rows<D>(w, t, &g_errors_quant);
 }
 
+// Sixteen codes times m to bf16; WIDE: by one store, dst being 32-byte aligned.
+// (Stores of half a sector each took the expansion of 32768 rows of 8 x 128 from 33
+// to 44 us and the read of 131072 from 144 to 165.)
+template <bool WIDE>
+__device__ __forceinline__ void store16(uint4* dst, const uint4& codes, float m) {
+  const uint2 a = dequant4(codes.x, m), b = dequant4(codes.y, m), c = dequant4(codes.z, m),
+              d = dequant4(codes.w, m);
+  if constexpr (WIDE) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a.x),
+                 "r"(a.y), "r"(b.x), "r"(b.y), "r"(c.x), "r"(c.y), "r"(d.x), "r"(d.y)
+                 : "memory");
+  } else {
+    dst[0] = make_uint4(a.x, a.y, b.x, b.y);
+    dst[1] = make_uint4(c.x, c.y, d.x, d.y);
+  }
+}
+
 // Rows read back: 16 codes in, 16 bf16 out per thread and word.
-template <int D>
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(kQuantThreads)
     quant_read_kernel(uint4* __restrict__ key, uint4* __restrict__ value, long long key_stride_v,
                       long long value_stride_v, const uint4* __restrict__ codes,
@@ -128,10 +148,7 @@ __global__ void __launch_bounds__(kQuantThreads)
 #pragma unroll
     for (int u = 0; u < kQuantVecs; ++u) {
       if (!dst[u]) continue;
-      const uint2 a = dequant4(val[u].x, m[u]), b = dequant4(val[u].y, m[u]),
-                  c = dequant4(val[u].z, m[u]), d = dequant4(val[u].w, m[u]);
-      dst[u][0] = make_uint4(a.x, a.y, b.x, b.y);
-      dst[u][1] = make_uint4(c.x, c.y, d.x, d.y);
+      store16<WIDE>(dst[u], val[u], m[u]);
     }
   }
 }
@@ -198,30 +215,29 @@ __global__ void __launch_bounds__(kExpandThreads)
     for (int e = threadIdx.x; e < vec_per_block; e += kExpandThreads) {
       const uint4 v = __ldg(from + e);
       const float m = scale_value(__ldg(sc + e / (D / 16)));
-      const uint2 p = dequant4(v.x, m), q = dequant4(v.y, m), s = dequant4(v.z, m),
-                  t = dequant4(v.w, m);
-      to[2 * e] = make_uint4(p.x, p.y, q.x, q.y);
-      to[2 * e + 1] = make_uint4(s.x, s.y, t.x, t.y);
+      store16<true>(to + 2 * e, v, m);
     }
   }
 }
 
 // ------------------------------------------------------------------ host
+static int row_grid(long long words) {
+  const long long need = (words + kQuantThreads * kQuantVecs - 1) / (kQuantThreads * kQuantVecs);
+  return static_cast<int>(need < (1ll << 30) ? need : 1ll << 30);
+}
+
 template <int D>
 static cudaError_t launch_quant_write_t(void* codes, uint8_t* scales, const void* key,
                                         const void* value, long long key_stride,
                                         long long value_stride, const int64_t* slots,
                                         int num_tokens, int num_blocks, int shift,
-                                        int num_kv_heads, int num_sms, cudaStream_t stream) {
+                                        int num_kv_heads, cudaStream_t stream) {
   const int vec_per_row = num_kv_heads * D / 8;
   const long long total = static_cast<long long>(num_tokens) * 2 * vec_per_row;
-  const long long per_cta = static_cast<long long>(kQuantThreads) * kQuantVecs;
-  const long long cap = static_cast<long long>(num_sms) * 2;
-  const long long need = (total + per_cta - 1) / per_cta;
-  const int grid = static_cast<int>(need < cap ? need : cap);
+  const int grid = row_grid(total);
   const long long num_slots = static_cast<long long>(num_blocks) << shift;
   // int indexes while w0 + kQuantVecs * stride stays below 2^31
-  if (total + 2 * static_cast<long long>(grid) * per_cta < (1ll << 31))
+  if (total + 2ll * grid * kQuantThreads * kQuantVecs < (1ll << 31))
     return launch_pdl(quant_write_kernel<D, int>, dim3(grid), dim3(kQuantThreads), 0, stream,
                       static_cast<uint2*>(codes), scales, static_cast<const uint4*>(key),
                       static_cast<const uint4*>(value), key_stride / 8, value_stride / 8, slots,
@@ -235,15 +251,13 @@ static cudaError_t launch_quant_write_t(void* codes, uint8_t* scales, const void
 cudaError_t launch_quant_write(void* codes, uint8_t* scales, const void* key, const void* value,
                                long long key_stride, long long value_stride, const int64_t* slots,
                                int num_tokens, int num_blocks, int shift, int num_kv_heads,
-                               int head_dim, int num_sms, cudaStream_t stream) {
+                               int head_dim, cudaStream_t stream) {
   if (num_tokens == 0) return cudaSuccess;
   return head_dim == 128
              ? launch_quant_write_t<128>(codes, scales, key, value, key_stride, value_stride,
-                                         slots, num_tokens, num_blocks, shift, num_kv_heads,
-                                         num_sms, stream)
+                                         slots, num_tokens, num_blocks, shift, num_kv_heads, stream)
              : launch_quant_write_t<64>(codes, scales, key, value, key_stride, value_stride, slots,
-                                        num_tokens, num_blocks, shift, num_kv_heads, num_sms,
-                                        stream);
+                                        num_tokens, num_blocks, shift, num_kv_heads, stream);
 }
 
 cudaError_t launch_quant_mapped_write(const WriteRowsArgs& w, cudaStream_t stream) {
@@ -257,19 +271,18 @@ cudaError_t launch_quant_mapped_write(const WriteRowsArgs& w, cudaStream_t strea
 cudaError_t launch_quant_read(void* key, void* value, long long key_stride, long long value_stride,
                               const void* codes, const uint8_t* scales, const int64_t* slots,
                               int num_tokens, int num_blocks, int shift, int num_kv_heads,
-                              int head_dim, int num_sms, cudaStream_t stream) {
+                              int head_dim, cudaStream_t stream) {
   if (num_tokens == 0) return cudaSuccess;
   const int vec_per_row = num_kv_heads * head_dim / 16;
   const long long total = static_cast<long long>(num_tokens) * 2 * vec_per_row;
-  const long long per_cta = static_cast<long long>(kQuantThreads) * kQuantVecs;
-  const long long cap = static_cast<long long>(num_sms) * 2;
-  const long long need = (total + per_cta - 1) / per_cta;
-  const int grid = static_cast<int>(need < cap ? need : cap);
-  return launch_pdl(head_dim == 128 ? quant_read_kernel<128> : quant_read_kernel<64>, dim3(grid),
-                    dim3(kQuantThreads), 0, stream, static_cast<uint4*>(key),
-                    static_cast<uint4*>(value), key_stride / 8, value_stride / 8,
-                    static_cast<const uint4*>(codes), scales, slots, total, 2 * vec_per_row,
-                    vec_per_row, shift, static_cast<long long>(num_blocks) << shift);
+  const bool wide = ((reinterpret_cast<uintptr_t>(key) | reinterpret_cast<uintptr_t>(value)) & 31) == 0 &&
+                    key_stride % 16 == 0 && value_stride % 16 == 0;
+  auto kern = head_dim == 128 ? (wide ? quant_read_kernel<128, true> : quant_read_kernel<128, false>)
+                              : (wide ? quant_read_kernel<64, true> : quant_read_kernel<64, false>);
+  return launch_pdl(kern, dim3(row_grid(total)), dim3(kQuantThreads), 0, stream,
+                    static_cast<uint4*>(key), static_cast<uint4*>(value), key_stride / 8,
+                    value_stride / 8, static_cast<const uint4*>(codes), scales, slots, total,
+                    2 * vec_per_row, vec_per_row, shift, static_cast<long long>(num_blocks) << shift);
 }
 
 cudaError_t launch_quant_copy(void* dst, uint8_t* dst_scales, int dst_num_blocks, const void* src,

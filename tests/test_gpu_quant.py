@@ -108,21 +108,22 @@ def test_mapped_write_and_the_step_write_equal_the_two_calls(hq, hkv, d, B):
 
 
 @pytest.mark.parametrize("T,hkv,d,B", ROWS)
-def test_read_is_exact_and_leaves_padding_alone(T, hkv, d, B):
+@pytest.mark.parametrize("gap", [0, 8, 16])  # rows 32-byte aligned, 16-byte aligned, strided
+def test_read_is_exact_and_leaves_padding_alone(T, hkv, d, B, gap):
     nb = -(-T // B) + 3
     codes, scales, c, s = pool_of(nb, B, hkv, d, T)
     slots = random_slots(T, nb * B, T)
     slots[T // 2] = slots[0]  # a row read twice
     row = hkv * d
-    wide = torch.full((T, 2 * row + 8), 5.0, dtype=torch.bfloat16, device="cuda")
-    k, v = wide[:, :row].view(T, hkv, d), wide[:, row + 8:].view(T, hkv, d)
+    wide = torch.full((T, 2 * row + gap), 5.0, dtype=torch.bfloat16, device="cuda")
+    k, v = wide[:, :row].view(T, hkv, d), wide[:, row + gap:].view(T, hkv, d)
     before = bf16_to_numpy(k.contiguous())
     binding.pkv_quant_kv_read(k, v, c, s, torch.from_numpy(slots).cuda())
     want = oracle.quant_read(before, before.copy(), codes, scales, slots)
     for got, w in zip((k, v), want):
         got = bits_to_f64(bf16_to_numpy(got.contiguous()))
         assert np.array_equal(got, bits_to_f64(w), equal_nan=True)
-    assert (wide[:, row:row + 8] == 5.0).all()
+    assert (wide[:, row:row + gap] == 5.0).all()
     assert binding.pkv_get_device_errors(clear=True) == 0
 
 
