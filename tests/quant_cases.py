@@ -51,27 +51,33 @@ def quantised_step(step):
 
 
 def expected(step, pool, softcap=0.0, alibi_slopes=None, key_begin=None, key_end=None):
-    """(out, bound) over the 8-bit pool's values: the scored oracle's bound (bf16
-    weights and output, fp32 scores and sums), and what the decode's q adds: a q
-    row is held as two e4m3 numbers under one power of two, exactly but for
-    elements below 2^-6 / 224 of the row's largest, which are off by at most
-    2^-14 / 224 < 2^-21 of it. A score is then off by at most
-    e = scale 2^-21 max|q| sum|k_d|, an output by 2 e A <= 2 e max|v| over the seen keys."""
-    out, bound = oracle.scored_attention(step.q, pool, step.block_table, step.seq_lens,
-                                         step.query_start_loc, step.num_computed, step.scale,
-                                         softcap=softcap, slopes=alibi_slopes,
-                                         key_begin=key_begin, key_end=key_end)
+    """(out, bound) over the 8-bit pool's values: the scored oracle's bound (weights
+    and output rounded to bf16, fp32 scores and sums), and what the decode kernel's
+    f16 operands add below their normal numbers:
+      - a q row is held as f16 under a power of two that brings its largest to 224 ..
+        448. f16's 11 bits hold bf16's 8; elements below 2^-14 are off by 2^-25, so by
+        less than 2^-32 of top = max|q|: a score by e = scale 2^-32 top sum|k_d| (the
+        bound's D 2^-24 of |q||k| do not cover that where they are small), an output by
+        2 e A <= 2 e max|v|;
+      - a weight times V's scale is off by 2^-25 of the largest such product or less,
+        and a code is 448 at most: of n keys by n 2^-25 448 max_j(w_j 2^v_j), and
+        448 * 2^v < 2 max_d|v_jd|: n 2^-24 sum_j w_j max_d|v_jd|, the attention over
+        rows that are their largest magnitude throughout."""
+    args = (step.block_table, step.seq_lens, step.query_start_loc, step.num_computed, step.scale)
+    kw = dict(softcap=softcap, slopes=alibi_slopes, key_begin=key_begin, key_end=key_end)
+    out, bound = oracle.scored_attention(step.q, pool, *args, **kw)
+    flat = pool.copy()
+    flat[:, 1] = (pool[:, 1] & 0x7FFF).max(axis=-1, keepdims=True)
+    reach, _ = oracle.scored_attention(step.q, flat, *args, **kw)
     B, group = step.block_size, step.num_q_heads // step.num_kv_heads
     for r, s in enumerate(step.specs):
-        L = s.seq_len
-        j = np.arange(L)
+        j = np.arange(s.seq_len)
         blk = step.block_table[r][j // B].astype(np.int64)
         k, v = (np.nan_to_num(np.abs(oracle.bf16_bits_to_f64(pool[blk, i, j % B]))) for i in (0, 1))
-        reach = k.sum(axis=2).max(axis=0)  # [Hkv]
-        top = v.max(axis=(0, 2))
-        t0 = int(step.query_start_loc[r])
-        q = np.abs(oracle.bf16_bits_to_f64(step.q[t0:t0 + s.query_len])).max(axis=2)
-        e = step.scale * 2.0 ** -21 * q * np.repeat(reach, group)
-        bound[t0:t0 + s.query_len] += (2.2 * e * np.repeat(top, group))[..., None] * \
-            (bound[t0:t0 + s.query_len] > 0)
+        rows = slice(int(step.query_start_loc[r]), int(step.query_start_loc[r]) + s.query_len)
+        top = np.abs(oracle.bf16_bits_to_f64(step.q[rows])).max(axis=2)
+        e = step.scale * 2.0 ** -32 * top * np.repeat(k.sum(axis=2).max(axis=0), group)
+        more = 2 * (e * np.repeat(v.max(axis=(0, 2)), group))[..., None] + \
+            s.seq_len * 2.0 ** -24 * reach[rows]
+        bound[rows] += 1.1 * more * (bound[rows] > 0)
     return out, bound
