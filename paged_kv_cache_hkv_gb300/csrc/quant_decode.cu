@@ -25,10 +25,10 @@
 // maximum of s + v, in f16 (11 bits; below 2^-14 of the largest weight 2^-25 of
 // it). The sum of weights keeps a running maximum of s of its own, so that rows
 // of tiny or huge V change nothing in it, and O is scaled to it at the end.
-// (mma.m16n8k32 on the codes themselves is no shortcut: the compiler turns each into
-// conversions of both operands and two f16 products, 427 instructions a chunk and
-// warp instead of some 190, and 244 us instead of DECODE_LONG_US on 8 decodes of
-// 32767 to 131071 keys, 32 q and 8 kv heads, D = 128.)
+// (mma.m16n8k32 on the codes themselves is no shortcut: by the counters each becomes
+// conversions of both operands and f16 products, 427 instructions a chunk and warp
+// instead of 332, and 244 us instead of 207 on 8 decodes of 32767-131071 keys,
+// 32 q and 8 kv heads, D = 128, which the copies alone take 200 for.)
 // K, V and the scales of a chunk are a copy or two each: a 4-D box lands them as
 // [K|V][kv head][16 keys][D], swizzled, so that ldmatrix finds no bank conflict.
 #include <cfloat>
@@ -43,7 +43,21 @@ namespace pkv {
 static __device__ uint32_t g_errors_quant_decode;
 
 constexpr int kQuantWarps = 8;  // consumer warps of a CTA at most
-constexpr int kQuantDecodeThreads = (kQuantWarps + 1) * 32;
+
+// Warps of a CTA of nw consumers with mt unit tiles each. One tile: the consumers
+// and the producer. Several: three groups of four warps, of which the last holds the
+// producer and hands registers to the others: 4 x 32 x 56 + 8 x 32 x 224 are the
+// launch's 12 x 32 x 168. (Nine warps have 168 each, three of them sharing one of the SM's
+// four register files: with three tiles 107 us instead of 78 for 64 requests of five
+// tokens over 511-4095 keys, 32 q and 8 kv heads, D = 128.)
+__host__ __device__ constexpr int quant_threads(int nw, int mt) {
+  return mt == 1 ? (nw + 1) * 32 : 12 * 32;
+}
+__host__ __device__ constexpr int quant_producer(int nw, int mt) {
+  return mt == 1 ? nw : kQuantWarps;
+}
+constexpr int kProducerRegs = 56, kConsumerRegs = 224, kLaunchRegs = 168;
+static_assert(4 * kProducerRegs + 8 * kConsumerRegs <= 12 * kLaunchRegs, "registers of the launch");
 
 struct QuantDecodeParams : DecodeParams {
   const uint8_t* scales;
@@ -121,7 +135,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 
 template <int D, int SH, int MT, bool SCORED>
-__global__ void __launch_bounds__(kQuantDecodeThreads, MT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(quant_threads(kQuantWarps, MT), MT == 1 ? 2 : 1)
     quant_decode_kernel(const __grid_constant__ CUtensorMap kv_map, const QuantDecodeParams p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -134,7 +148,8 @@ __global__ void __launch_bounds__(kQuantDecodeThreads, MT == 1 ? 2 : 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(base + lay.bar_off);
   uint64_t* empty = full + S;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == NW && lane == 0) prefetch_tensormap(&kv_map);
+  const int producer = quant_producer(NW, MT);
+  if (warp == producer && lane == 0) prefetch_tensormap(&kv_map);
   pdl_wait();
 
   const long long Cn = p.splits, c = blockIdx.x;
@@ -160,7 +175,11 @@ __global__ void __launch_bounds__(kQuantDecodeThreads, MT == 1 ? 2 : 1)
                : 0;
   };
 
-  if (warp == NW) {
+  if (warp >= producer) {
+    if constexpr (MT > 1) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+      if (warp > producer) return;
+    }
     // ================= producer warp
     const uint64_t l2_policy = l2_evict_first_policy();
     // A request, the whole warp alike: its batch rows and keys, the keys [lo, hi)
@@ -333,6 +352,10 @@ __global__ void __launch_bounds__(kQuantDecodeThreads, MT == 1 ? 2 : 1)
     return;
   }
 
+  if constexpr (MT > 1) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
+    if (warp >= NW) return;
+  }
   // ================= consumer warp: unit tiles tile0 .. tile0+MT-1 of kv head hk
   const int hl = warp / WPH, hk = slab * KH + hl;
   const int tile0 = (warp - hl * WPH) * MT;
@@ -641,54 +664,64 @@ __global__ void __launch_bounds__(kQuantDecodeThreads, MT == 1 ? 2 : 1)
 // ------------------------------------------------------------------ host
 constexpr int kQuantMinStages = 2, kQuantMaxStages = 8;
 
-// Unit tiles of a consumer warp, the warps of a kv head, and the most rows of a
-// request on the stream. At most kQuantTiles tiles, whose O takes 96 registers of
-// a lane at D = 128: nine warps, three on one of the SM's four register files, have
-// 168 each.
+// How the kernel is laid out for a call: unit tiles of a consumer warp, warps of a
+// kv head, kv heads of a CTA, CTAs an SM is meant to hold (16 consumer warps with one
+// tile each, within the 20 warps that their registers allow; one CTA with more
+// tiles), and the most rows of a request on the stream.
 struct QuantShape {
-  int few, mt, wph;
+  int mt, wph, heads, ctas, few;
 };
-constexpr int kQuantTiles = 3;
 
 // Steps whose every request has so few new tokens that their units fit the CTA's
 // warps (kFewUnits) stream all of them. In a step with longer chunks those of one
 // tile do and the others go to the prefill kernel: most requests of such a step are
-// decodes, and one tile a warp streams them at the copy bandwidth (118 us for 320
-// decodes of 127-2047 keys and three tiles' 156).
-static QuantShape quant_shape(int max_query_len, int group) {
+// decodes, and one tile a warp streams them at the copy bandwidth (320 decodes of
+// 127-2047 keys: 116 us, with two tiles 156).
+//
+// More tiles a warp convert a head's K and V fewer times, fewer tiles leave room for
+// more warps. A warp takes some 1.5 us for a chunk with one tile among 16 warps, 1.2
+// and 1.5 with two and three among 8; the layout with the least time per chunk and
+// head wins. 64 requests over some 2300 keys, D = 128, us with tiles of 1, 2 and 3:
+// 32 q and 8 kv heads, 4 new tokens 103, 85, 85; 5 tokens 167, 150, 102; 16 tokens
+// 350, 288, 341. 128 requests over 9400 keys, 8 q heads and 1 kv head, 3 tokens: 135,
+// 391, 449.
+static QuantShape quant_shape(int max_query_len, int group, int num_kv_heads) {
   const bool all = max_query_len <= kFewUnits / group;
   const int tiles = all ? (max_query_len * group + 7) / 8 : 1;
-  QuantShape s;
-  s.wph = (tiles + kQuantTiles - 1) / kQuantTiles;
-  s.mt = (tiles + s.wph - 1) / s.wph;
-  s.few = all ? max_query_len : 8 / group;
-  return s;
+  const float chunk_us[4] = {0.f, 1.5f, 1.2f, 1.5f};
+  QuantShape best{};
+  float least = 0.f;
+  for (int most = 3; most >= 1; --most) {
+    QuantShape s;
+    s.wph = (tiles + most - 1) / most;
+    s.mt = (tiles + s.wph - 1) / s.wph;
+    s.heads = kQuantWarps / s.wph < num_kv_heads ? kQuantWarps / s.wph : num_kv_heads;
+    while (num_kv_heads % s.heads) --s.heads;
+    const int nw = s.heads * s.wph;
+    s.ctas = 1;
+    if (s.mt == 1) s.ctas = 16 / nw < 20 / (nw + 1) ? 16 / nw : 20 / (nw + 1);
+    const float us = chunk_us[s.mt] * s.wph / (nw * s.ctas);
+    if (best.mt == 0 || us < least) {
+      best = s;
+      least = us;
+    }
+  }
+  best.few = all ? max_query_len : 8 / group;
+  return best;
 }
 
 int quant_few_rows(int max_query_len, int group) {
-  return max_query_len < 1 ? 1 : quant_shape(max_query_len, group).few;
+  return max_query_len < 1 ? 1 : quant_shape(max_query_len, group, 1).few;
 }
 
 int quant_slab_heads(int num_kv_heads, int group, int max_query_len) {
-  const int most = kQuantWarps / quant_shape(max_query_len, group).wph;
-  int s = num_kv_heads <= most ? num_kv_heads : most;
-  while (num_kv_heads % s) --s;
-  return s;
-}
-
-// CTAs of nw consumer warps an SM is meant to hold: 16 such warps with one tile
-// each (8 decodes of 32767-131071 keys: 202 us, the copies alone 200, with 8 warps
-// 227), 8 with more, for their registers.
-static int quant_ctas(int nw, int mt) {
-  const int warps = mt == 1 ? 2 * kQuantWarps : kQuantWarps;
-  return warps / nw < 1 ? 1 : warps / nw;
+  return quant_shape(max_query_len, group, num_kv_heads).heads;
 }
 
 long long quant_most_splits(int num_kv_heads, int group, int num_sms) {
   int most = 1;
   for (int n = 1; n <= kFewUnits / group + 1; ++n) {
-    const QuantShape q = quant_shape(n, group);
-    const int ctas = quant_ctas(quant_slab_heads(num_kv_heads, group, n) * q.wph, q.mt);
+    const int ctas = quant_shape(n, group, num_kv_heads).ctas;
     if (ctas > most) most = ctas;
   }
   return static_cast<long long>(num_sms) * most;
@@ -708,8 +741,9 @@ static std::atomic<unsigned long long> g_quant_attr_done{0};
 static std::mutex g_quant_prep_mu;
 
 template <int D, int SH, int MT, bool SCORED>
-static cudaError_t quant_prepare(int kh, int hkv, int nw, int num_sms, QuantPrep* out) {
+static cudaError_t quant_prepare(int hkv, const QuantShape& shape, int num_sms, QuantPrep* out) {
   auto kern = quant_decode_kernel<D, SH, MT, SCORED>;
+  const int kh = shape.heads, nw = kh * shape.wph;
   cudaError_t e = smem_attr_once(kern, 227 * 1024, g_quant_attr_done<D, SH, MT, SCORED>);
   if (e != cudaSuccess) return e;
   int dev = 0;
@@ -721,10 +755,17 @@ static cudaError_t quant_prepare(int kh, int hkv, int nw, int num_sms, QuantPrep
       *out = d;
       return cudaSuccess;
     }
-  const int want = quant_ctas(nw, MT);
+  if constexpr (MT > 1) {
+    // the warps' exchange of registers waits for those of the launch
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, kern);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs < kLaunchRegs) return cudaErrorInvalidKernelImage;
+  }
+  const int want = shape.ctas;
   auto bytes = [&](int S) { return QuantLayout(D, kh, hkv, nw, MT, S).total + 1024u; };
   int fit = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kern, (nw + 1) * 32, bytes(kQuantMinStages));
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kern, quant_threads(nw, MT), bytes(kQuantMinStages));
   if (e != cudaSuccess) return e;
   const int ctas = fit < want ? (fit < 1 ? 1 : fit) : want;
   const size_t budget = 228u * 1024u / ctas - 1024u;
@@ -757,9 +798,9 @@ static cudaError_t quant_dispatch(int head_dim, int sh, int mt, bool scored, A&&
 
 template <int D, int SH, int MT, bool SCORED>
 struct QuantPrepareOp {
-  static cudaError_t run(int kh, int hkv, int nw, int sms, long long* splits) {
+  static cudaError_t run(int hkv, const QuantShape& shape, int sms, long long* splits) {
     QuantPrep d;
-    const cudaError_t e = quant_prepare<D, SH, MT, SCORED>(kh, hkv, nw, sms, &d);
+    const cudaError_t e = quant_prepare<D, SH, MT, SCORED>(hkv, shape, sms, &d);
     if (e == cudaSuccess) *splits = d.splits;
     return e;
   }
@@ -767,42 +808,41 @@ struct QuantPrepareOp {
 
 template <int D, int SH, int MT, bool SCORED>
 struct QuantLaunchOp {
-  static cudaError_t run(const QuantDecodeParams& p, const CUtensorMap& m, int sms, cudaStream_t s) {
+  static cudaError_t run(const QuantDecodeParams& p, const QuantShape& shape, const CUtensorMap& m,
+                         int sms, cudaStream_t s) {
     QuantPrep d;
-    const int nw = p.slab_heads * p.warps_per_head;
-    cudaError_t e = quant_prepare<D, SH, MT, SCORED>(p.slab_heads, p.num_kv_heads, nw, sms, &d);
+    cudaError_t e = quant_prepare<D, SH, MT, SCORED>(p.num_kv_heads, shape, sms, &d);
     if (e != cudaSuccess) return e;
     QuantDecodeParams q = p;
     q.stages = d.stages;
     const dim3 grid(static_cast<unsigned>(p.splits),
-                    static_cast<unsigned>(p.num_kv_heads / p.slab_heads));
-    return launch_pdl(quant_decode_kernel<D, SH, MT, SCORED>, grid, dim3((nw + 1) * 32), d.smem, s,
-                      m, q);
+                    static_cast<unsigned>(p.num_kv_heads / shape.heads));
+    return launch_pdl(quant_decode_kernel<D, SH, MT, SCORED>, grid,
+                      dim3(quant_threads(shape.heads * shape.wph, MT)), d.smem, s, m, q);
   }
 };
 
 cudaError_t quant_full_wave_splits(int head_dim, int num_kv_heads, int group, int block_shift,
                                    int max_query_len, bool scored, int num_sms, long long* splits) {
-  const QuantShape q = quant_shape(max_query_len, group);
-  const int kh = quant_slab_heads(num_kv_heads, group, max_query_len);
-  return quant_dispatch<QuantPrepareOp>(head_dim, block_shift, q.mt, scored, kh, num_kv_heads,
-                                        kh * q.wph, num_sms, splits);
+  const QuantShape q = quant_shape(max_query_len, group, num_kv_heads);
+  return quant_dispatch<QuantPrepareOp>(head_dim, block_shift, q.mt, scored, num_kv_heads, q,
+                                        num_sms, splits);
 }
 
 cudaError_t launch_quant_decode(const AttnArgs& a, const AttnWorkspace& ws,
                                 const CUtensorMap& kv_map, long long splits, int num_sms,
                                 cudaStream_t stream, void** trace) {
   const int group = a.num_q_heads / a.num_kv_heads;
-  const QuantShape shape = quant_shape(a.max_query_len, group);
+  const QuantShape shape = quant_shape(a.max_query_len, group, a.num_kv_heads);
   QuantDecodeParams p;
   static_cast<DecodeParams&>(p) = decode_params(a, ws, splits);
   p.scales = a.kv_scales;
   p.num_kv_heads = a.num_kv_heads;
   p.group_shift = __builtin_ctz(static_cast<unsigned>(group));
-  p.slab_heads = quant_slab_heads(a.num_kv_heads, group, a.max_query_len);
+  p.slab_heads = shape.heads;
   p.warps_per_head = shape.wph;
   cudaError_t e = quant_dispatch<QuantLaunchOp>(a.head_dim, a.block_shift, shape.mt, a.scored, p,
-                                                kv_map, num_sms, stream);
+                                                shape, kv_map, num_sms, stream);
   if (e == cudaSuccess && trace) e = cudaEventRecord(static_cast<cudaEvent_t>(trace[3]), stream);
   if (e != cudaSuccess) return e;
   return launch_combine(p, a.head_dim, decode_heads_per_warp(group), stream);

@@ -157,7 +157,8 @@ def test_a_sequence_served_from_prompt_to_last_token():
     rng = np.random.default_rng(2)
     plan = [(0, 130), (130, 70)] + [(200 + i, 1) for i in range(18)] + [(218, 4), (222, 4), (226, 1)]
     total = plan[-1][0] + plan[-1][1]
-    k, v, q = (torch.randn(total, h, d, device="cuda").bfloat16() for h in (hkv, hkv, hq))
+    g = torch.Generator(device="cuda").manual_seed(4)
+    k, v, q = (torch.randn(total, h, d, generator=g, device="cuda").bfloat16() for h in (hkv, hkv, hq))
     table = torch.from_numpy(rng.permutation(nb)[:-(-total // B)].astype(np.int32)).cuda().view(1, -1)
     codes = torch.zeros(nb, 2, B, hkv, d, dtype=torch.uint8, device="cuda").view(E4M3)
     scales = torch.zeros(nb, 2, B, hkv, dtype=torch.uint8, device="cuda")
@@ -194,7 +195,9 @@ def test_a_sequence_served_from_prompt_to_last_token():
     binding.pkv_quant_kv_read(*back, codes, scales, slots)
     for x, y in zip((kb, vb), back):
         x, y = bits_to_f64(x), bits_to_f64(bf16_to_numpy(y))
-        assert (np.abs(x - y) <= 2.0 ** -4 * np.abs(x) + 2.0 ** -19 * np.abs(x).max(-1, keepdims=True)).all()
+        # half a step: 2^-4 of the value, or 2^-10 2^e where codes are subnormal, and the
+        # row's largest is above 224 2^e: less than 2^-17 of it
+        assert (np.abs(x - y) <= 2.0 ** -4 * np.abs(x) + 2.0 ** -17 * np.abs(x).max(-1, keepdims=True)).all()
     assert binding.pkv_get_device_errors(clear=True) == 0
 
 
