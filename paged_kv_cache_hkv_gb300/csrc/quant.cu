@@ -15,10 +15,32 @@ static __device__ uint32_t g_errors_quant;
 // its largest magnitude by shuffles; the first of them stores the scale. Every
 // thread issues the loads of its kQuantVecs words before it uses the first. A CTA
 // per kQuantVecs * kQuantThreads words, however many: 16001 rows of 8 x 128 take
-// 23.8 us cold (floor 14.2), with four words a thread and two CTAs an SM 26.4; the
-// read of 131072 such rows 125 us (floor 119) and 144.
+// 21.1 us cold (floor 14.2), the read of 131072 such rows 123 us (floor 119); four
+// words a thread and two CTAs an SM were 10% and 15% slower.
 constexpr int kQuantVecs = 2;
 constexpr int kQuantThreads = 512;
+
+// Word w of such a stream: its token and its place in the token's 2 vec_per_row words.
+// Below 2^31 words by a product with the divisor's reciprocal to 32 bits above its
+// size, which is exact there (with the plain division and 64-bit slots the write
+// issued in 83% of its cycles and took 23.8 us for the 16001 rows).
+struct RowSplit {
+  uint32_t mul, shift;
+  int row_pair, vec_per_row;
+  template <typename Index>
+  __device__ __forceinline__ int operator()(Index w, Index* tok) const {
+    if constexpr (sizeof(Index) == 4)
+      *tok = static_cast<Index>((__umulhi(mul, static_cast<uint32_t>(w)) + static_cast<uint32_t>(w)) >> shift);
+    else
+      *tok = w / row_pair;
+    return static_cast<int>(w - *tok * row_pair);
+  }
+};
+
+// Pool row (block * 2 + k|v) * B + offset of a slot in the pool (below 2^31 rows).
+__device__ __forceinline__ int pool_row(int slot, int kv, int shift) {
+  return ((((slot >> shift) * 2) + kv) << shift) + (slot & ((1 << shift) - 1));
+}
 
 template <int D>
 __device__ __forceinline__ uint32_t row_amax(const uint4& v) {
@@ -33,8 +55,8 @@ __global__ void __launch_bounds__(kQuantThreads)
     quant_write_kernel(uint2* __restrict__ codes, uint8_t* __restrict__ scales,
                        const uint4* __restrict__ key, const uint4* __restrict__ value,
                        long long key_stride_v, long long value_stride_v,
-                       const int64_t* __restrict__ slots, Index total, Index row_pair,
-                       int vec_per_row, int shift, long long num_slots) {
+                       const int64_t* __restrict__ slots, Index total, RowSplit split, int shift,
+                       int num_slots) {
   pdl_trigger();
   pdl_wait();
   const Index stride = static_cast<Index>(gridDim.x) * blockDim.x;
@@ -45,37 +67,36 @@ __global__ void __launch_bounds__(kQuantThreads)
        w0 += stride * kQuantVecs) {
     uint4 val[kQuantVecs];
     long long slot[kQuantVecs];
-    int kv[kQuantVecs], e[kQuantVecs];
+    int rem[kQuantVecs];
 #pragma unroll
     for (int u = 0; u < kQuantVecs; ++u) {
       const Index w = w0 + u * stride;
       slot[u] = -1;
       val[u] = make_uint4(0, 0, 0, 0);
-      kv[u] = e[u] = 0;
+      rem[u] = 0;
       if (w < total) {
-        const Index tok = w / row_pair;
-        const int rem = static_cast<int>(w - tok * row_pair);
-        kv[u] = rem >= vec_per_row;
-        e[u] = rem - kv[u] * vec_per_row;
+        Index tok;
+        rem[u] = split(w, &tok);
         slot[u] = __ldg(slots + tok);
-        const uint4* src = kv[u] ? value + static_cast<long long>(tok) * value_stride_v
-                                 : key + static_cast<long long>(tok) * key_stride_v;
-        val[u] = __ldg(src + e[u]);
+        const uint4* src = rem[u] >= split.vec_per_row
+                               ? value + static_cast<long long>(tok) * value_stride_v - split.vec_per_row
+                               : key + static_cast<long long>(tok) * key_stride_v;
+        val[u] = __ldg(src + rem[u]);
       }
     }
 #pragma unroll
     for (int u = 0; u < kQuantVecs; ++u) {
       const uint32_t s = scale_byte(row_amax<D>(val[u]));
-      const long long at = slot[u];
-      if (at < 0) continue;  // padding row, or past the end
-      if (at >= num_slots) {
-        if (kv[u] == 0 && e[u] == 0) atomicOr(&g_errors_quant, kErrSlotRange);
+      if (slot[u] < 0) continue;  // padding row, or past the end
+      if (slot[u] >= num_slots) {
+        if (rem[u] == 0) atomicOr(&g_errors_quant, kErrSlotRange);
         continue;
       }
-      const long long blk = at >> shift, off = at & ((1 << shift) - 1);
-      const long long word = (((blk * 2 + kv[u]) << shift) + off) * vec_per_row + e[u];
+      const int kv = rem[u] >= split.vec_per_row, e = rem[u] - kv * split.vec_per_row;
+      const long long word =
+          static_cast<long long>(pool_row(static_cast<int>(slot[u]), kv, shift)) * split.vec_per_row + e;
       codes[word] = quant8(val[u], s);
-      if (e[u] % (D / 8) == 0) scales[word / (D / 8)] = static_cast<uint8_t>(s);
+      if (e % (D / 8) == 0) scales[word / (D / 8)] = static_cast<uint8_t>(s);
     }
   }
 }
@@ -110,46 +131,44 @@ __device__ __forceinline__ void store16(uint4* dst, const uint4& codes, float m)
 }
 
 // Rows read back: 16 codes in, 16 bf16 out per thread and word.
-template <int D, bool WIDE>
+template <int D, bool WIDE, typename Index>
 __global__ void __launch_bounds__(kQuantThreads)
     quant_read_kernel(uint4* __restrict__ key, uint4* __restrict__ value, long long key_stride_v,
                       long long value_stride_v, const uint4* __restrict__ codes,
                       const uint8_t* __restrict__ scales, const int64_t* __restrict__ slots,
-                      long long total, int row_pair, int vec_per_row, int shift,
-                      long long num_slots) {
+                      Index total, RowSplit split, int shift, int num_slots) {
   pdl_trigger();
   pdl_wait();
-  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
-  for (long long w0 = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; w0 < total;
+  const Index stride = static_cast<Index>(gridDim.x) * blockDim.x;
+  for (Index w0 = static_cast<Index>(blockIdx.x) * blockDim.x + threadIdx.x; w0 < total;
        w0 += stride * kQuantVecs) {
     uint4 val[kQuantVecs];
     float m[kQuantVecs];
     uint4* dst[kQuantVecs];
 #pragma unroll
     for (int u = 0; u < kQuantVecs; ++u) {
-      const long long w = w0 + u * stride;
+      const Index w = w0 + u * stride;
       dst[u] = nullptr;
       if (w >= total) continue;
-      const long long tok = w / row_pair;
-      const int rem = static_cast<int>(w - tok * row_pair);
-      const int kv = rem >= vec_per_row, e = rem - kv * vec_per_row;
+      Index tok;
+      const int rem = split(w, &tok);
+      const int kv = rem >= split.vec_per_row, e = rem - kv * split.vec_per_row;
       const long long at = __ldg(slots + tok);
       if (at < 0) continue;  // a row of padding stays as it is
       if (at >= num_slots) {
         if (rem == 0) atomicOr(&g_errors_quant, kErrSlotRange);
         continue;
       }
-      const long long blk = at >> shift, off = at & ((1 << shift) - 1);
-      const long long word = (((blk * 2 + kv) << shift) + off) * vec_per_row + e;
+      const long long word =
+          static_cast<long long>(pool_row(static_cast<int>(at), kv, shift)) * split.vec_per_row + e;
       val[u] = __ldg(codes + word);
       m[u] = scale_value(__ldg(scales + word / (D / 16)));
-      dst[u] = (kv ? value + tok * value_stride_v : key + tok * key_stride_v) + 2 * e;
+      dst[u] = (kv ? value + static_cast<long long>(tok) * value_stride_v
+                   : key + static_cast<long long>(tok) * key_stride_v) + 2 * e;
     }
 #pragma unroll
-    for (int u = 0; u < kQuantVecs; ++u) {
-      if (!dst[u]) continue;
-      store16<WIDE>(dst[u], val[u], m[u]);
-    }
+    for (int u = 0; u < kQuantVecs; ++u)
+      if (dst[u]) store16<WIDE>(dst[u], val[u], m[u]);
   }
 }
 
@@ -226,26 +245,41 @@ static int row_grid(long long words) {
   return static_cast<int>(need < (1ll << 30) ? need : 1ll << 30);
 }
 
+// Whether a launch's word numbers, those past the end included, stay below 2^31.
+static bool short_index(long long words) {
+  return words + 2ll * row_grid(words) * kQuantThreads * kQuantVecs < (1ll << 31);
+}
+
+// w / d = (umulhi(mul, w) + w) >> shift for w < 2^31, with 2^(shift - 1) < d <= 2^shift
+// and mul = floor(2^32 (2^shift - d) / d) + 1: (2^32 + mul) d exceeds 2^(32 + shift)
+// by at most d <= 2^shift.
+static RowSplit row_split(int vec_per_row) {
+  RowSplit s;
+  s.vec_per_row = vec_per_row;
+  s.row_pair = 2 * vec_per_row;
+  s.shift = 0;
+  while ((1ll << s.shift) < s.row_pair) ++s.shift;
+  s.mul = static_cast<uint32_t>(((((1ull << s.shift) - s.row_pair) << 32) / s.row_pair) + 1);
+  return s;
+}
+
 template <int D>
 static cudaError_t launch_quant_write_t(void* codes, uint8_t* scales, const void* key,
                                         const void* value, long long key_stride,
                                         long long value_stride, const int64_t* slots,
                                         int num_tokens, int num_blocks, int shift,
                                         int num_kv_heads, cudaStream_t stream) {
-  const int vec_per_row = num_kv_heads * D / 8;
-  const long long total = static_cast<long long>(num_tokens) * 2 * vec_per_row;
-  const int grid = row_grid(total);
-  const long long num_slots = static_cast<long long>(num_blocks) << shift;
-  // int indexes while w0 + kQuantVecs * stride stays below 2^31
-  if (total + 2ll * grid * kQuantThreads * kQuantVecs < (1ll << 31))
-    return launch_pdl(quant_write_kernel<D, int>, dim3(grid), dim3(kQuantThreads), 0, stream,
-                      static_cast<uint2*>(codes), scales, static_cast<const uint4*>(key),
-                      static_cast<const uint4*>(value), key_stride / 8, value_stride / 8, slots,
-                      static_cast<int>(total), 2 * vec_per_row, vec_per_row, shift, num_slots);
-  return launch_pdl(quant_write_kernel<D, long long>, dim3(grid), dim3(kQuantThreads), 0, stream,
-                    static_cast<uint2*>(codes), scales, static_cast<const uint4*>(key),
-                    static_cast<const uint4*>(value), key_stride / 8, value_stride / 8, slots,
-                    total, static_cast<long long>(2 * vec_per_row), vec_per_row, shift, num_slots);
+  const RowSplit split = row_split(num_kv_heads * D / 8);
+  const long long total = static_cast<long long>(num_tokens) * split.row_pair;
+  const dim3 grid(row_grid(total)), block(kQuantThreads);
+  const uint4 *k = static_cast<const uint4*>(key), *v = static_cast<const uint4*>(value);
+  if (short_index(total))
+    return launch_pdl(quant_write_kernel<D, int>, grid, block, 0, stream, static_cast<uint2*>(codes),
+                      scales, k, v, key_stride / 8, value_stride / 8, slots,
+                      static_cast<int>(total), split, shift, num_blocks << shift);
+  return launch_pdl(quant_write_kernel<D, long long>, grid, block, 0, stream,
+                    static_cast<uint2*>(codes), scales, k, v, key_stride / 8, value_stride / 8,
+                    slots, total, split, shift, num_blocks << shift);
 }
 
 cudaError_t launch_quant_write(void* codes, uint8_t* scales, const void* key, const void* value,
@@ -268,21 +302,36 @@ cudaError_t launch_quant_mapped_write(const WriteRowsArgs& w, cudaStream_t strea
                     dim3(grid), dim3(kQuantMappedWarps * 32), 0, stream, w);
 }
 
+template <int D, bool WIDE>
+static cudaError_t launch_quant_read_t(void* key, void* value, long long key_stride,
+                                       long long value_stride, const void* codes,
+                                       const uint8_t* scales, const int64_t* slots, int num_tokens,
+                                       int num_blocks, int shift, int num_kv_heads,
+                                       cudaStream_t stream) {
+  const RowSplit split = row_split(num_kv_heads * D / 16);
+  const long long total = static_cast<long long>(num_tokens) * split.row_pair;
+  const dim3 grid(row_grid(total)), block(kQuantThreads);
+  uint4 *k = static_cast<uint4*>(key), *v = static_cast<uint4*>(value);
+  if (short_index(total))
+    return launch_pdl(quant_read_kernel<D, WIDE, int>, grid, block, 0, stream, k, v, key_stride / 8,
+                      value_stride / 8, static_cast<const uint4*>(codes), scales, slots,
+                      static_cast<int>(total), split, shift, num_blocks << shift);
+  return launch_pdl(quant_read_kernel<D, WIDE, long long>, grid, block, 0, stream, k, v,
+                    key_stride / 8, value_stride / 8, static_cast<const uint4*>(codes), scales,
+                    slots, total, split, shift, num_blocks << shift);
+}
+
 cudaError_t launch_quant_read(void* key, void* value, long long key_stride, long long value_stride,
                               const void* codes, const uint8_t* scales, const int64_t* slots,
                               int num_tokens, int num_blocks, int shift, int num_kv_heads,
                               int head_dim, cudaStream_t stream) {
   if (num_tokens == 0) return cudaSuccess;
-  const int vec_per_row = num_kv_heads * head_dim / 16;
-  const long long total = static_cast<long long>(num_tokens) * 2 * vec_per_row;
   const bool wide = ((reinterpret_cast<uintptr_t>(key) | reinterpret_cast<uintptr_t>(value)) & 31) == 0 &&
                     key_stride % 16 == 0 && value_stride % 16 == 0;
-  auto kern = head_dim == 128 ? (wide ? quant_read_kernel<128, true> : quant_read_kernel<128, false>)
-                              : (wide ? quant_read_kernel<64, true> : quant_read_kernel<64, false>);
-  return launch_pdl(kern, dim3(row_grid(total)), dim3(kQuantThreads), 0, stream,
-                    static_cast<uint4*>(key), static_cast<uint4*>(value), key_stride / 8,
-                    value_stride / 8, static_cast<const uint4*>(codes), scales, slots, total,
-                    2 * vec_per_row, vec_per_row, shift, static_cast<long long>(num_blocks) << shift);
+  auto run = head_dim == 128 ? (wide ? launch_quant_read_t<128, true> : launch_quant_read_t<128, false>)
+                             : (wide ? launch_quant_read_t<64, true> : launch_quant_read_t<64, false>);
+  return run(key, value, key_stride, value_stride, codes, scales, slots, num_tokens, num_blocks,
+             shift, num_kv_heads, stream);
 }
 
 cudaError_t launch_quant_copy(void* dst, uint8_t* dst_scales, int dst_num_blocks, const void* src,

@@ -141,6 +141,23 @@ def test_scale_bytes_of_a_chunk(B, HKV):
                 assert area[(kr + (8 if B == 8 else 16)) * HKV + hk] == pool[blk, 1, off, hk]
 
 
+@pytest.mark.parametrize("vec_per_row", [1, 2, 3, 5, 8, 24, 64, 100, 128, 192, 640, 1000, 4096, 5000, 1 << 20])
+def test_words_are_split_into_tokens_exactly(vec_per_row):
+    """row_split's reciprocal over every kind of word number below 2^31."""
+    d = 2 * vec_per_row
+    shift = (d - 1).bit_length()
+    mul = ((((1 << shift) - d) << 32) // d) + 1
+    assert mul < 1 << 32
+    rng = np.random.default_rng(vec_per_row)
+    w = np.concatenate([rng.integers(0, 1 << 31, 5000), np.arange(3 * d if d < 5000 else 3),
+                        (1 << 31) - 1 - np.arange(min(3 * d, 5000)),
+                        d * rng.integers(0, (1 << 31) // d, 500), d * rng.integers(1, (1 << 31) // d + 1, 500) - 1])
+    w = w[(w >= 0) & (w < 1 << 31)].astype(np.uint64)
+    total = ((np.uint64(mul) * w) >> np.uint64(32)) + w
+    assert (total < 1 << 32).all()
+    assert np.array_equal(total >> np.uint64(shift), w // np.uint64(d))
+
+
 # ------------------------------------------------------------------ rows on the decode stream
 @pytest.mark.parametrize("group", [1, 2, 4, 8])
 def test_few_rows(lib, group):
