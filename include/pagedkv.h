@@ -172,7 +172,9 @@ typedef struct pkv_attention_options {
   int32_t shared_num_reqs;
   /* [0]: 0, or PKV_OPTIONS_SCORES when the struct has the field `scores` below
    * (a caller built before that field existed leaves it 0, and the library
-   * then does not read past trace_events). [1..3] must be zero. */
+   * then does not read past trace_events). [1]: 0, or for the calls on the 8-bit
+   * pool PKV_OPTIONS_FEW_ROWS' value (see pkv_quant_few_rows). [2], [3], and [1]
+   * of the other calls, must be zero. */
   int32_t reserved[4];
   /* Tracing: NULL, or PKV_TRACE_EVENTS cudaEvent_t handles (as void*) owned
    * by the caller. The call records them on `stream` around its kernels:
@@ -190,6 +192,9 @@ typedef struct pkv_attention_options {
 } pkv_attention_options;
 
 #define PKV_OPTIONS_SCORES 1
+/* Place in reserved[] of the most new tokens of a request that a call on the 8-bit
+ * pool takes on the decode kernels. */
+#define PKV_OPTIONS_FEW_ROWS 1
 
 #define PKV_TRACE_EVENTS 5
 
@@ -648,14 +653,18 @@ int32_t pkv_quant_paged_attention_with_write(
 /* pkv_quant_few_rows -- the most new tokens of a request that a call with this
  * max_query_len attends on the decode kernels (at least 1): max_query_len itself
  * while it times the q heads of a kv head is at most 64, else 8 / that many heads.
- * Needs no device. */
+ * options->reserved[PKV_OPTIONS_FEW_ROWS] sets another number, from 1 to 64 / that
+ * many heads (else PKV_ERR_BAD_SHAPE): for steps that hold long chunks beside
+ * requests of a few tokens, whose keys the default would expand. Decodes then
+ * share a kernel made for that many rows, so a larger number than the step needs
+ * slows them. Needs no device. */
 int32_t pkv_quant_few_rows(int32_t max_query_len, int32_t num_q_heads, int32_t num_kv_heads);
 
 /*
  * pkv_quant_attention_workspace_size -- bytes of device workspace for
  * pkv_quant_paged_attention with up to num_reqs requests and tables of that width.
  * chunk_keys: the most cache tokens that the requests of more than
- * pkv_quant_few_rows() new tokens hold between them in one step, counted in whole
+ * pkv_quant_few_rows() new tokens (or the options' number) hold between them in one step, counted in whole
  * blocks (the sum of ceil(L / block_size) * block_size); 4 * num_kv_heads *
  * head_dim bytes each. With key ranges the tokens in front of and behind those
  * that a request's rows see need not be counted. 0 is enough for steps without such

@@ -41,6 +41,7 @@ PKV_TRACE_EVENTS = 5
 
 
 PKV_OPTIONS_SCORES = 1
+PKV_OPTIONS_FEW_ROWS = 1
 
 
 class pkv_score_options(ctypes.Structure):
@@ -314,14 +315,18 @@ def _scores(q, softcap, alibi_slopes, key_begin, key_end):
     return o
 
 
-def _options(decode_splits, trace_events=None, shared_prefix=None, scores=None):
+def _options(decode_splits, trace_events=None, shared_prefix=None, scores=None, few_rows=None):
     """Options struct (or None for the defaults). shared_prefix: None, or
     (shared_prefix_len, shared_first_req, shared_num_reqs) -- see pagedkv.h;
-    scores: None, or what _scores returns."""
-    if decode_splits is None and trace_events is None and shared_prefix is None and scores is None:
+    scores: None, or what _scores returns; few_rows: 8-bit pool (see
+    pkv_quant_few_rows in pagedkv.h)."""
+    if decode_splits is None and trace_events is None and shared_prefix is None and (
+            scores is None and few_rows is None):
         return None
     o = pkv_attention_options()
     o.decode_splits = int(decode_splits or 0)
+    if few_rows is not None:
+        o.reserved[PKV_OPTIONS_FEW_ROWS] = int(few_rows)
     if shared_prefix is not None:
         o.shared_prefix_len, o.shared_first_req, o.shared_num_reqs = (int(x) for x in shared_prefix)
     if trace_events is not None:
@@ -706,10 +711,10 @@ def pkv_quant_few_rows(max_query_len: int, num_q_heads: int, num_kv_heads: int) 
     return int(n)
 
 
-def quant_chunk_keys(query_lens, seq_lens, group: int, block_size: int) -> int:
+def quant_chunk_keys(query_lens, seq_lens, group: int, block_size: int, few_rows=None) -> int:
     """chunk_keys of pkv_quant_attention_workspace_size for a step of these (host)
-    lengths; group: q heads per kv head."""
-    few = pkv_quant_few_rows(max(query_lens, default=0), group, 1)
+    lengths; group: q heads per kv head; few_rows: as in the attention call."""
+    few = few_rows or pkv_quant_few_rows(max(query_lens, default=0), group, 1)
     return sum(-(-L // block_size) * block_size for n, L in zip(query_lens, seq_lens) if n > few)
 
 
@@ -760,11 +765,13 @@ def pkv_quant_paged_attention(out, q, kv_cache, kv_scales, block_table, seq_lens
                               num_computed_tokens, *, max_query_len: int, max_seq_len: int,
                               scale: float, workspace, decode_splits=None, trace_events=None,
                               shared_prefix=None, softcap=0.0, alibi_slopes=None, key_begin=None,
-                              key_end=None, stream=None):
+                              key_end=None, few_rows=None, stream=None):
     """out [T, Hq, D] bf16 <- attention of one mixed step over the 8-bit pool (see
-    pagedkv.h); options as in pkv_paged_attention."""
+    pagedkv.h); options as in pkv_paged_attention. few_rows: the most new tokens of a
+    request that goes on the decode kernels, where the default (pkv_quant_few_rows)
+    is not wanted."""
     options = _options(decode_splits, trace_events, shared_prefix,
-                       _scores(q, softcap, alibi_slopes, key_begin, key_end))
+                       _scores(q, softcap, alibi_slopes, key_begin, key_end), few_rows)
     _check("pkv_quant_paged_attention", load().pkv_quant_paged_attention(
         *_quant_attention_args(out, q, kv_cache, kv_scales, block_table, seq_lens,
                                query_start_loc, num_computed_tokens, max_query_len, max_seq_len,
@@ -778,11 +785,12 @@ def pkv_quant_paged_attention_with_write(out, q, kv_cache, kv_scales, key, value
                                          workspace, slot_mapping=None, decode_splits=None,
                                          trace_events=None, shared_prefix=None, softcap=0.0,
                                          alibi_slopes=None, key_begin=None, key_end=None,
-                                         stream=None):
+                                         few_rows=None, stream=None):
     """The step of one layer on the 8-bit pool in one call: slot mapping and
-    quantised write of the new tokens, then attention (see pagedkv.h)."""
+    quantised write of the new tokens, then attention (see pagedkv.h;
+    few_rows: as in pkv_quant_paged_attention)."""
     options = _options(decode_splits, trace_events, shared_prefix,
-                       _scores(q, softcap, alibi_slopes, key_begin, key_end))
+                       _scores(q, softcap, alibi_slopes, key_begin, key_end), few_rows)
     _check("pkv_quant_paged_attention_with_write", load().pkv_quant_paged_attention_with_write(
         *_quant_attention_args(out, q, kv_cache, kv_scales, block_table, seq_lens,
                                query_start_loc, num_computed_tokens, max_query_len, max_seq_len,
@@ -860,7 +868,8 @@ class StepCalls:
                  kv_cache, key, value, out, q, seq_lens, max_query_len: int,
                  max_seq_len: int, scale: float, workspace, decode_splits=None,
                  shared_prefix=None, fused_write=False, write_in_attention=False, softcap=0.0,
-                 alibi_slopes=None, key_begin=None, key_end=None, kv_scales=None):
+                 alibi_slopes=None, key_begin=None, key_end=None, kv_scales=None,
+                 few_rows=None):
         self.fused_write = bool(fused_write)
         self.write_in_attention = bool(write_in_attention)
         self._write, self._mapped_write, self._attend, self._attend_write = (
@@ -878,8 +887,11 @@ class StepCalls:
                                 kv_cache, kv_scales, key, value, out, q, seq_lens, max_query_len,
                                 max_seq_len, scale, workspace,
                                 _options(decode_splits, None, shared_prefix,
-                                         _scores(q, softcap, alibi_slopes, key_begin, key_end)))
+                                         _scores(q, softcap, alibi_slopes, key_begin, key_end),
+                                         few_rows))
             return
+        if few_rows is not None:
+            raise ValueError("few_rows is for the 8-bit pool (kv_scales)")
         _require(slot_mapping, torch.int64, "slot_mapping")
         for t, n in ((block_table, "block_table"), (query_start_loc, "query_start_loc"),
                      (num_computed_tokens, "num_computed_tokens"), (seq_lens, "seq_lens")):

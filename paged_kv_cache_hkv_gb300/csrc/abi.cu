@@ -262,23 +262,19 @@ size_t expanded_block_bytes(const pkv_cache_layout& l) {
   return static_cast<size_t>(4) * l.block_size * l.num_kv_heads * l.head_dim;
 }
 
-// One full wave of the 8-bit decode, or the caller's choice.
-int32_t quant_splits_for(DeviceInfo* d, const pkv_cache_layout& l, int group, int max_query_len,
-                         bool scored, const pkv_attention_options* opt, long long* splits) {
-  if (opt) {
-    if (opt->reserved[0] != 0 && opt->reserved[0] != PKV_OPTIONS_SCORES) return PKV_ERR_BAD_SHAPE;
-    for (int i = 1; i < 4; ++i)
-      if (opt->reserved[i] != 0) return PKV_ERR_BAD_SHAPE;
-    if (opt->decode_splits < 0) return PKV_ERR_BAD_SHAPE;
-    if (opt->decode_splits > 0) {
-      *splits = opt->decode_splits;
-      return PKV_OK;
-    }
-  }
-  cudaError_t e = pkv::quant_full_wave_splits(l.head_dim, l.num_kv_heads, group,
-                                              block_shift_of(l.block_size), max_query_len, scored,
-                                              d->num_sms, splits);
-  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "decode occupancy");
+// Options of a call on the 8-bit pool: the most rows of a request on the decode
+// stream (*few: the default is given, 0 = not asked for), and the splits if the
+// caller chose them (*splits, else left as it is).
+int32_t quant_options(const pkv_attention_options* opt, int group, int* few, long long* splits) {
+  if (!opt) return PKV_OK;
+  if (opt->reserved[0] != 0 && opt->reserved[0] != PKV_OPTIONS_SCORES) return PKV_ERR_BAD_SHAPE;
+  if (opt->reserved[2] != 0 || opt->reserved[3] != 0 || opt->decode_splits < 0)
+    return PKV_ERR_BAD_SHAPE;
+  const int rows = opt->reserved[PKV_OPTIONS_FEW_ROWS];
+  if (rows < 0 || rows > pkv::kFewUnits / group) return PKV_ERR_BAD_SHAPE;
+  if (rows > 0) *few = rows;
+  if (opt->decode_splits > 0) *splits = opt->decode_splits;
+  return PKV_OK;
 }
 
 // Ranges (CTAs) the decode stream is split into: the caller's choice, else
@@ -523,9 +519,20 @@ static int32_t attention_impl(void* out, const void* q, int64_t q_row_stride, co
   if (st != PKV_OK) return st;
   const int group = num_q_heads / layout.num_kv_heads;
   long long splits = 0;
-  st = quant ? quant_splits_for(d, layout, group, max_query_len, a.scored, options, &splits)
-             : decode_splits_for(d, layout.head_dim, layout.num_kv_heads, group,
-                                 layout.block_size, options, &splits);
+  a.few = 1;
+  if (quant) {
+    a.few = pkv::quant_few_rows(max_query_len, group);
+    st = quant_options(options, group, &a.few, &splits);
+    if (st == PKV_OK && splits == 0) {
+      const cudaError_t e = pkv::quant_full_wave_splits(
+          layout.head_dim, layout.num_kv_heads, group, block_shift_of(layout.block_size), a.few,
+          a.scored, d->num_sms, &splits);
+      if (e != cudaSuccess) return cuda_fail(e, "decode occupancy");
+    }
+  } else {
+    st = decode_splits_for(d, layout.head_dim, layout.num_kv_heads, group, layout.block_size,
+                           options, &splits);
+  }
   if (st != PKV_OK) return st;
   SharedHint sh;
   st = shared_hint(options, layout, group, num_reqs, d->num_sms, &sh);
@@ -541,9 +548,7 @@ static int32_t attention_impl(void* out, const void* q, int64_t q_row_stride, co
           ? pkv::quant_most_splits(layout.num_kv_heads, group, d->num_sms)
           : splits;
   WsLayout wl = ws_layout(num_reqs, virt, gw, layout.head_dim, ws_splits, sh, num_q_heads);
-  a.few = 1;
   if (quant) {
-    a.few = pkv::quant_few_rows(max_query_len, group);
     quant_ws_layout(&wl, num_reqs, max_blocks_per_req, num_q_heads, layout.head_dim, ws_splits,
                     pkv::kFewUnits / group);
     if (workspace_bytes < wl.quant_total + expanded_block_bytes(layout)) return PKV_ERR_WORKSPACE;
@@ -639,7 +644,7 @@ static int32_t attention_impl(void* out, const void* q, int64_t q_row_stride, co
                                    static_cast<cuuint64_t>(B) * Hkv * D};
     const cuuint32_t box[4] = {
         static_cast<cuuint32_t>(D), B < 16 ? 8u : 16u,
-        static_cast<cuuint32_t>(pkv::quant_slab_heads(Hkv, group, max_query_len)), 2};
+        static_cast<cuuint32_t>(pkv::quant_slab_heads(Hkv, group, a.few)), 2};
     st = make_map_n(&kv_map, kv_cache, 4, dims, strides, box,
                     D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                     CU_TENSOR_MAP_DATA_TYPE_UINT8);
@@ -890,14 +895,9 @@ int64_t pkv_quant_attention_workspace_size(int32_t num_reqs, int32_t max_blocks_
   if (st != PKV_OK) return st;
   const int group = num_q_heads / layout.num_kv_heads;
   long long splits = pkv::quant_most_splits(layout.num_kv_heads, group, d->num_sms);
-  if (options) {
-    if (options->reserved[0] != 0 && options->reserved[0] != PKV_OPTIONS_SCORES)
-      return PKV_ERR_BAD_SHAPE;
-    for (int i = 1; i < 4; ++i)
-      if (options->reserved[i] != 0) return PKV_ERR_BAD_SHAPE;
-    if (options->decode_splits < 0) return PKV_ERR_BAD_SHAPE;
-    if (options->decode_splits > 0) splits = options->decode_splits;
-  }
+  int few = 0;
+  st = quant_options(options, group, &few, &splits);
+  if (st != PKV_OK) return st;
   SharedHint sh;
   st = shared_hint(options, layout, group, num_reqs, d->num_sms, &sh);
   if (st != PKV_OK) return st;

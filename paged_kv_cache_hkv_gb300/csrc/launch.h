@@ -230,18 +230,18 @@ cudaError_t launch_expand(const AttnArgs& a, const ExpandArgs& x, int num_sms,
 // Query rows x q heads of one kv head that the 8-bit decode holds at most: 8
 // warps of 16.
 constexpr int kFewUnits = 64;
-// Requests of up to this many new tokens are on the 8-bit pool's decode stream
-// (quant_decode.cu).
+// Requests of up to this many new tokens are on the 8-bit pool's decode stream by
+// default (quant_decode.cu); `few` below: of up to how many they are.
 int quant_few_rows(int max_query_len, int group);
-// The most splits that quant_full_wave_splits gives for any max_query_len.
+// The most splits that quant_full_wave_splits gives for any `few`.
 long long quant_most_splits(int num_kv_heads, int group, int num_sms);
 cudaError_t quant_full_wave_splits(int head_dim, int num_kv_heads, int group, int block_shift,
-                                   int max_query_len, bool scored, int num_sms, long long* splits);
+                                   int few, bool scored, int num_sms, long long* splits);
 cudaError_t launch_quant_decode(const AttnArgs& a, const AttnWorkspace& ws,
                                 const CUtensorMap& kv_map, long long splits, int num_sms,
                                 cudaStream_t stream, void** trace);
 // kv heads of one CTA of the 8-bit decode
-int quant_slab_heads(int num_kv_heads, int group, int max_query_len);
+int quant_slab_heads(int num_kv_heads, int group, int few);
 
 cudaError_t read_errors_kvwrite(uint32_t* out, bool clear);
 cudaError_t read_errors_decode(uint32_t* out, bool clear);

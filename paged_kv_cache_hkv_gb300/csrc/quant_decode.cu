@@ -667,17 +667,11 @@ constexpr int kQuantMinStages = 2, kQuantMaxStages = 8;
 // How the kernel is laid out for a call: unit tiles of a consumer warp, warps of a
 // kv head, kv heads of a CTA, CTAs an SM is meant to hold (16 consumer warps with one
 // tile each, within the 20 warps that their registers allow; one CTA with more
-// tiles), and the most rows of a request on the stream.
+// tiles). `few`: the most rows of a request on the stream.
 struct QuantShape {
-  int mt, wph, heads, ctas, few;
+  int mt, wph, heads, ctas;
 };
 
-// Steps whose every request has so few new tokens that their units fit the CTA's
-// warps (kFewUnits) stream all of them. In a step with longer chunks those of one
-// tile do and the others go to the prefill kernel: most requests of such a step are
-// decodes, and one tile a warp streams them at the copy bandwidth (320 decodes of
-// 127-2047 keys: 116 us, with two tiles 156).
-//
 // More tiles a warp convert a head's K and V fewer times, fewer tiles leave room for
 // more warps. A warp takes some 1.5 us for a chunk with one tile among 16 warps, 1.2
 // and 1.5 with two and three among 8; the layout with the least time per chunk and
@@ -685,9 +679,8 @@ struct QuantShape {
 // 32 q and 8 kv heads, 4 new tokens 103, 85, 85; 5 tokens 167, 150, 102; 16 tokens
 // 350, 288, 341. 128 requests over 9400 keys, 8 q heads and 1 kv head, 3 tokens: 135,
 // 391, 449.
-static QuantShape quant_shape(int max_query_len, int group, int num_kv_heads) {
-  const bool all = max_query_len <= kFewUnits / group;
-  const int tiles = all ? (max_query_len * group + 7) / 8 : 1;
+static QuantShape quant_shape(int few, int group, int num_kv_heads) {
+  const int tiles = (few * group + 7) / 8;
   const float chunk_us[4] = {0.f, 1.5f, 1.2f, 1.5f};
   QuantShape best{};
   float least = 0.f;
@@ -706,21 +699,27 @@ static QuantShape quant_shape(int max_query_len, int group, int num_kv_heads) {
       least = us;
     }
   }
-  best.few = all ? max_query_len : 8 / group;
   return best;
 }
 
+// Steps whose every request has so few new tokens that their units fit the CTA's
+// warps (kFewUnits) stream all of them. In a step with longer chunks those of one
+// tile do and the others go to the prefill kernel: most requests of such a step are
+// decodes, and one tile a warp streams them at the copy bandwidth (320 decodes of
+// 127-2047 keys: 116 us, with two tiles 156).
+//
 int quant_few_rows(int max_query_len, int group) {
-  return max_query_len < 1 ? 1 : quant_shape(max_query_len, group, 1).few;
+  if (max_query_len < 1) return 1;
+  return max_query_len <= kFewUnits / group ? max_query_len : 8 / group;
 }
 
-int quant_slab_heads(int num_kv_heads, int group, int max_query_len) {
-  return quant_shape(max_query_len, group, num_kv_heads).heads;
+int quant_slab_heads(int num_kv_heads, int group, int few) {
+  return quant_shape(few, group, num_kv_heads).heads;
 }
 
 long long quant_most_splits(int num_kv_heads, int group, int num_sms) {
   int most = 1;
-  for (int n = 1; n <= kFewUnits / group + 1; ++n) {
+  for (int n = 1; n <= kFewUnits / group; ++n) {
     const int ctas = quant_shape(n, group, num_kv_heads).ctas;
     if (ctas > most) most = ctas;
   }
@@ -823,8 +822,8 @@ struct QuantLaunchOp {
 };
 
 cudaError_t quant_full_wave_splits(int head_dim, int num_kv_heads, int group, int block_shift,
-                                   int max_query_len, bool scored, int num_sms, long long* splits) {
-  const QuantShape q = quant_shape(max_query_len, group, num_kv_heads);
+                                   int few, bool scored, int num_sms, long long* splits) {
+  const QuantShape q = quant_shape(few, group, num_kv_heads);
   return quant_dispatch<QuantPrepareOp>(head_dim, block_shift, q.mt, scored, num_kv_heads, q,
                                         num_sms, splits);
 }
@@ -833,7 +832,7 @@ cudaError_t launch_quant_decode(const AttnArgs& a, const AttnWorkspace& ws,
                                 const CUtensorMap& kv_map, long long splits, int num_sms,
                                 cudaStream_t stream, void** trace) {
   const int group = a.num_q_heads / a.num_kv_heads;
-  const QuantShape shape = quant_shape(a.max_query_len, group, a.num_kv_heads);
+  const QuantShape shape = quant_shape(a.few, group, a.num_kv_heads);
   QuantDecodeParams p;
   static_cast<DecodeParams&>(p) = decode_params(a, ws, splits);
   p.scales = a.kv_scales;

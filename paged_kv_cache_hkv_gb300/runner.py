@@ -49,7 +49,7 @@ class DeviceStep:
 
     def __init__(self, step, device="cuda", decode_splits=None, upload_pool=True,
                  shared_prefix=None, fused_write=False, write_in_attention=False, softcap=0.0,
-                 alibi_slopes=None, key_begin=None, key_end=None, quantised=False):
+                 alibi_slopes=None, key_begin=None, key_end=None, quantised=False, few_rows=None):
         """shared_prefix: None, or (shared_prefix_len, shared_first_req,
         shared_num_reqs) for the attention call (see pagedkv.h); "auto" takes
         it from the step's shared prefix when its sharing requests form one
@@ -60,7 +60,7 @@ class DeviceStep:
         key_begin, key_end [T] (host arrays): capped, biased or range-masked
         scores. quantised: the step's pool is quantised as it is uploaded, and
         the calls are those of the 8-bit pool (kv_cache holds codes, kv_scales
-        their scales)."""
+        their scales); few_rows: their option."""
         self.step = step
         self.device = torch.device(device)
         dev = self.device
@@ -90,7 +90,7 @@ class DeviceStep:
             key_end=None if key_end is None else _i32(key_end, dev))
         self.layout = binding.pkv_cache_layout(step.num_blocks, step.block_size,
                                                step.num_kv_heads, step.head_dim)
-        self.quantised = quantised
+        self.quantised, self.few_rows = quantised, few_rows
         self.kv_scales = None
         if quantised:
             if not upload_pool:
@@ -101,7 +101,7 @@ class DeviceStep:
                 max_blocks_per_req=step.max_blocks_per_req,
                 chunk_keys=binding.quant_chunk_keys(
                     step.query_len.tolist(), step.seq_lens.tolist(),
-                    step.num_q_heads // step.num_kv_heads, step.block_size),
+                    step.num_q_heads // step.num_kv_heads, step.block_size, few_rows),
                 decode_splits=decode_splits, shared_prefix=shared_prefix)
         else:
             nbytes = binding.pkv_attention_workspace_size(step.num_reqs, step.num_q_heads,
@@ -151,26 +151,29 @@ class DeviceStep:
 
     def attend_with_write(self, stream=None):
         s = self.step
-        call, pool = ((binding.pkv_quant_paged_attention_with_write,
-                       (self.kv_cache, self.kv_scales)) if self.quantised else
-                      (binding.pkv_paged_attention_with_write, (self.kv_cache,)))
+        call, pool, more = (
+            (binding.pkv_quant_paged_attention_with_write, (self.kv_cache, self.kv_scales),
+             {"few_rows": self.few_rows}) if self.quantised else
+            (binding.pkv_paged_attention_with_write, (self.kv_cache,), {}))
         call(
             self.out, self.q, *pool, self.k, self.v, self.block_table, self.seq_lens,
             self.query_start_loc, self.num_computed, max_query_len=s.max_query_len,
             max_seq_len=s.max_seq_len, scale=s.scale, workspace=self.workspace,
             slot_mapping=self.slot_mapping, decode_splits=self.decode_splits,
-            shared_prefix=self.shared_prefix, stream=stream, **self.scores)
+            shared_prefix=self.shared_prefix, stream=stream, **more, **self.scores)
 
     def attend(self, stream=None):
         s = self.step
-        call, pool = ((binding.pkv_quant_paged_attention, (self.kv_cache, self.kv_scales))
-                      if self.quantised else (binding.pkv_paged_attention, (self.kv_cache,)))
+        call, pool, more = (
+            (binding.pkv_quant_paged_attention, (self.kv_cache, self.kv_scales),
+             {"few_rows": self.few_rows}) if self.quantised else
+            (binding.pkv_paged_attention, (self.kv_cache,), {}))
         call(
             self.out, self.q, *pool, self.block_table, self.seq_lens,
             self.query_start_loc, self.num_computed, max_query_len=s.max_query_len,
             max_seq_len=s.max_seq_len, scale=s.scale, workspace=self.workspace,
             decode_splits=self.decode_splits, shared_prefix=self.shared_prefix, stream=stream,
-            **self.scores)
+            **more, **self.scores)
 
     def run(self, stream=None):
         """The whole step: slot mapping, cache write (one launch with
@@ -188,7 +191,7 @@ class DeviceStep:
                 self.kv_cache, self.kv_scales, self.k, self.v, self.out, self.q, self.seq_lens,
                 self.workspace, sc["alibi_slopes"], sc["key_begin"], sc["key_end"])
         settings = (sc["softcap"], self.decode_splits, self.shared_prefix, self.fused_write,
-                    self.write_in_attention)
+                    self.write_in_attention, self.few_rows)
         if settings != self._calls_settings or not all(map(operator.is_, bufs, self._calls_bufs)):
             s = self.step
             self._calls = binding.StepCalls(
@@ -199,7 +202,7 @@ class DeviceStep:
                 max_seq_len=s.max_seq_len, scale=s.scale, workspace=self.workspace,
                 decode_splits=self.decode_splits, shared_prefix=self.shared_prefix,
                 fused_write=self.fused_write, write_in_attention=self.write_in_attention,
-                kv_scales=self.kv_scales, **self.scores)
+                kv_scales=self.kv_scales, few_rows=self.few_rows, **self.scores)
             self._calls_bufs, self._calls_settings = bufs, settings
         return self._calls
 

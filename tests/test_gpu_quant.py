@@ -207,9 +207,10 @@ def scores_for(step, mod, seed=0):
     return out
 
 
-def check(step, what="", flags=0, decode_splits=None, shared_prefix=None, write=True, **scores):
+def check(step, what="", flags=0, decode_splits=None, shared_prefix=None, write=True, few_rows=None,
+          **scores):
     ds = DeviceStep(step, quantised=True, write_in_attention=write, decode_splits=decode_splits,
-                    shared_prefix=shared_prefix, **scores)
+                    shared_prefix=shared_prefix, few_rows=few_rows, **scores)
     ds.out.fill_(7.0)
     ds.run()
     torch.cuda.synchronize()
@@ -250,6 +251,19 @@ def test_any_split_of_the_decode_stream(splits, mod, rows):
     specs = [RequestSpec(c, 1 + (i % rows)) for i, c in enumerate((0, 1, 15, 16, 17, 700, 1499, 31, 2200, 64))]
     step = make_step(specs, num_q_heads=8, num_kv_heads=2, head_dim=128, seed=3)
     check(step, decode_splits=splits, **scores_for(step, MODS[mod], seed=splits))
+
+
+@pytest.mark.parametrize("mod", ["plain", "cap-alibi", "random"])
+@pytest.mark.parametrize("few", [1, 2, 4, 6, 16])
+def test_a_chosen_number_of_rows_beside_long_chunks(few, mod):
+    """Requests of up to few_rows new tokens on the decode kernels, the others and a
+    shared prefix on the prefill kernel, whatever the longest is."""
+    specs = [RequestSpec(70, 20), RequestSpec(33, 1), RequestSpec(400, 5), RequestSpec(200, 90),
+             RequestSpec(901, 4), RequestSpec(17, 3), RequestSpec(5, 16)] + [
+        RequestSpec(64 + s, 1, shares_prefix=True) for s in (0, 9, 40)] + [RequestSpec(320, 2)]
+    step = make_step(specs, num_q_heads=16, num_kv_heads=4, head_dim=128, prefix_tokens=64, seed=few)
+    check(step, few_rows=few, shared_prefix="auto", **scores_for(step, MODS[mod], seed=few))
+    check(step, few_rows=few, write=False, **scores_for(step, MODS[mod], seed=few))
 
 
 @pytest.mark.parametrize("mod", MODS)

@@ -173,11 +173,30 @@ def test_few_rows(lib, group):
     assert lib.pkv_quant_few_rows(1, 4, 0) == E("PKV_ERR_BAD_SHAPE")
 
 
+def test_options_of_the_rows(lib):
+    def opt(**kw):
+        o = binding.pkv_attention_options()
+        for i, v in kw.items():
+            o.reserved[int(i[1:])] = v
+        return ctypes.pointer(o)
+
+    for rows in (0, 1, 16, 32):  # 2 q heads per kv head; the next check decides
+        assert _attn(lib, opt=opt(r1=rows), q=None) == E("PKV_ERR_NULL_POINTER")
+    for bad in (dict(r1=-1), dict(r1=33), dict(r2=1), dict(r3=1), dict(r0=2)):
+        # (without a GPU the device is asked for first)
+        assert lib.pkv_quant_attention_workspace_size(4, 8, 4, _layout(), 0, opt(**bad)) < 0
+        assert _attn(lib, opt=opt(**bad)) < 0
+    assert binding._options(None, few_rows=3).contents.reserved[E("PKV_OPTIONS_FEW_ROWS")] == 3
+    with pytest.raises(ValueError):
+        binding.StepCalls(**{k: v for k, v in tensors().items() if k != "kv_scales"}, **SIZES, few_rows=2)
+
+
 def test_chunk_keys(lib):
     assert binding.quant_chunk_keys([1, 1, 1], [100, 5, 17], 4, 16) == 0
     assert binding.quant_chunk_keys([5, 16, 1], [100, 50, 17], 4, 16) == 0  # 16 x 4 units
     assert binding.quant_chunk_keys([5, 17, 2], [100, 50, 17], 4, 16) == 112 + 64
     assert binding.quant_chunk_keys([], [], 4, 16) == 0
+    assert binding.quant_chunk_keys([5, 17, 2], [100, 50, 17], 4, 16, few_rows=5) == 64
 
 
 # ------------------------------------------------------------------ refusals of the C calls
