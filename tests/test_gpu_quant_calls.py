@@ -227,6 +227,22 @@ def test_q_and_v_of_any_size(hq, hkv, d):
     assert binding.pkv_get_device_errors(clear=True) == 0
 
 
+def test_traced_calls():
+    for step in steps(3):
+        ds = DeviceStep(step, quantised=True)
+        ds.slot_map_and_write()
+        events = [torch.cuda.Event(enable_timing=True) for _ in range(binding.PKV_TRACE_EVENTS)]
+        for e in events:
+            e.record()
+        binding.pkv_quant_paged_attention(
+            ds.out, ds.q, ds.kv_cache, ds.kv_scales, ds.block_table, ds.seq_lens, ds.query_start_loc,
+            ds.num_computed, max_query_len=step.max_query_len, max_seq_len=step.max_seq_len,
+            scale=step.scale, workspace=ds.workspace, trace_events=events)
+        torch.cuda.synchronize()
+        assert all(a.elapsed_time(b) > 0 for a, b in zip(events, events[1:]))
+        assert_within(ds.out_host(), *expected(step, quantised_step(step)[2]))
+
+
 def test_values_of_nothing():
     """All V rows zero, and all K rows zero: outputs 0, and the mean of V."""
     step = make_step([RequestSpec(200, 1), RequestSpec(33, 4), RequestSpec(60, 40)], num_q_heads=8,
