@@ -10,6 +10,7 @@ call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -573,6 +574,10 @@ def pkv_release_blocks(block_table, release_rows, release_tokens, free_queue, fr
         _stream(stream, block_table.device.index)))
 
 
+# (a struct of its fields alone, which no call changes)
+_layout_struct = functools.lru_cache(maxsize=64)(pkv_cache_layout)
+
+
 def _quant_pool(kv_cache, kv_scales, names=("kv_cache", "kv_scales"), pinned=False):
     """Layout and device index of an 8-bit pool: codes [num_blocks, 2, B, Hkv, D]
     e4m3 and their scales [num_blocks, 2, B, Hkv] uint8. (The checks of these calls
@@ -587,12 +592,13 @@ def _quant_pool(kv_cache, kv_scales, names=("kv_cache", "kv_scales"), pinned=Fal
     shape = kv_cache.shape
     if len(shape) != 5 or shape[1] != 2 or not kv_cache.is_contiguous():
         raise ValueError(f"{names[0]} must be a contiguous [num_blocks, 2, block_size, Hkv, D] tensor")
-    if kv_scales.shape != shape[:4] or not kv_scales.is_contiguous():
+    nb, _, bs, hkv, d = shape
+    if kv_scales.shape != (nb, 2, bs, hkv) or not kv_scales.is_contiguous():
         raise ValueError(f"{names[1]} must be a contiguous [num_blocks, 2, block_size, Hkv] tensor")
     device = kv_cache.get_device()
     if kv_scales.get_device() != device:
         raise ValueError(f"tensors on {kv_cache.device} and {kv_scales.device} in one call")
-    return pkv_cache_layout(shape[0], shape[2], shape[3], shape[4]), device
+    return _layout_struct(nb, bs, hkv, d), device
 
 
 def _quant_rows(t, n, num_tokens, heads, dim, device):
@@ -711,10 +717,14 @@ def pkv_quant_few_rows(max_query_len: int, num_q_heads: int, num_kv_heads: int) 
     return int(n)
 
 
-def quant_chunk_keys(query_lens, seq_lens, group: int, block_size: int, few_rows=None) -> int:
+def quant_chunk_keys(query_lens, seq_lens, group: int, block_size: int, few_rows=None,
+                     max_query_len=None) -> int:
     """chunk_keys of pkv_quant_attention_workspace_size for a step of these (host)
-    lengths; group: q heads per kv head; few_rows: as in the attention call."""
-    few = few_rows or pkv_quant_few_rows(max(query_lens, default=0), group, 1)
+    lengths; group: q heads per kv head; few_rows, max_query_len: as in the attention
+    call (the longest of query_lens where not given)."""
+    if max_query_len is None:
+        max_query_len = max(query_lens, default=0)
+    few = few_rows or pkv_quant_few_rows(max_query_len, group, 1)
     return sum(-(-L // block_size) * block_size for n, L in zip(query_lens, seq_lens) if n > few)
 
 

@@ -707,7 +707,6 @@ static QuantShape quant_shape(int few, int group, int num_kv_heads) {
 // tile do and the others go to the prefill kernel: most requests of such a step are
 // decodes, and one tile a warp streams them at the copy bandwidth (320 decodes of
 // 127-2047 keys: 116 us, with two tiles 156).
-//
 int quant_few_rows(int max_query_len, int group) {
   if (max_query_len < 1) return 1;
   return max_query_len <= kFewUnits / group ? max_query_len : 8 / group;
@@ -774,7 +773,10 @@ static cudaError_t quant_prepare(int hkv, const QuantShape& shape, int num_sms, 
   const size_t share = 228u * 1024u / (ctas + 1) + 1024u;
   const size_t smem = bytes(S) > share ? bytes(S) : share;
   *out = QuantPrep{dev, kh, hkv, nw, num_sms, S, static_cast<long long>(num_sms) * ctas, smem};
-  g_quant_prep<D, SH, MT, SCORED>.push_back(*out);
+  try {
+    g_quant_prep<D, SH, MT, SCORED>.push_back(*out);
+  } catch (...) {  // (no memory to keep it: worked out again by the next call)
+  }
   return cudaSuccess;
 }
 

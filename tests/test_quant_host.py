@@ -430,3 +430,19 @@ def test_binding_refuses_tensors_off_the_current_device(library, monkeypatch):
         with pytest.raises(ValueError):
             _call(name)
     assert library.names == []
+
+
+def test_chunk_keys_of_a_longer_maximum(lib):
+    """A call whose max_query_len is above the step's longest request expands more."""
+    assert binding.quant_chunk_keys([5, 3, 1], [100, 50, 17], 4, 16) == 0
+    assert binding.quant_chunk_keys([5, 3, 1], [100, 50, 17], 4, 16, max_query_len=16) == 0
+    assert binding.quant_chunk_keys([5, 3, 1], [100, 50, 17], 4, 16, max_query_len=17) == 112 + 64
+    assert binding.quant_chunk_keys([5, 3, 1], [100, 50, 17], 4, 16, few_rows=3, max_query_len=17) == 112
+
+
+@pytest.mark.parametrize("name", ["pkv_quant_kv_write", "pkv_quant_kv_read"])
+def test_scales_of_another_shape_are_refused(library, name):
+    for shape in ((NB, 2, 16, HKV, 1), (NB, 2, 16), (NB, 2, 8, HKV), (NB, 1, 16, HKV), (NB, 2, 16, HKV + 1)):
+        with pytest.raises(ValueError):
+            _call(name, kv_scales=Stand(torch.uint8, *shape))
+    assert library.names == []
