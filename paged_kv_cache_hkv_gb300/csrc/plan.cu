@@ -326,7 +326,10 @@ __device__ void plan_block(const AttnArgs& a, const AttnWorkspace& ws, int tile_
   }
   // (thread 0 may still be about to list the shared-prefix items: plan_expand
   // starts with a barrier)
-  if constexpr (QUANT) plan_expand<SCORED>(a, ws, total.b + (shared_items > 0 ? 1 : 0));
+  if constexpr (QUANT) {
+    const int nreq = total.b + (shared_items > 0 ? 1 : 0);
+    if (nreq > 0) plan_expand<SCORED>(a, ws, nreq);
+  }
 }
 
 template <bool SCORED, bool QUANT>
