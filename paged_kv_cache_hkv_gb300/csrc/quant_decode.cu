@@ -716,13 +716,23 @@ int quant_slab_heads(int num_kv_heads, int group, int few) {
   return quant_shape(few, group, num_kv_heads).heads;
 }
 
+// Ranges of the stream by default: the CTAs of all slabs of kv heads are one wave of
+// the device. (A wave per slab instead, 64 requests over some 2300 keys: 16 q and kv
+// heads, D = 64, 70 us instead of 65; 40 of D = 128 247 instead of 228, four tokens
+// each 282 instead of 252; 30 requests over 500 keys, 12 of D = 64, 23 instead of 20.)
+static long long quant_wave(int num_sms, int ctas, int slabs) {
+  const long long c = static_cast<long long>(num_sms) * ctas / slabs;
+  return c > 1 ? c : 1;
+}
+
 long long quant_most_splits(int num_kv_heads, int group, int num_sms) {
-  int most = 1;
+  long long most = 1;
   for (int n = 1; n <= kFewUnits / group; ++n) {
-    const int ctas = quant_shape(n, group, num_kv_heads).ctas;
-    if (ctas > most) most = ctas;
+    const QuantShape s = quant_shape(n, group, num_kv_heads);
+    const long long c = quant_wave(num_sms, s.ctas, num_kv_heads / s.heads);
+    if (c > most) most = c;
   }
-  return static_cast<long long>(num_sms) * most;
+  return most;
 }
 
 // Launch shape of one instantiation on one device, worked out once.
@@ -772,7 +782,7 @@ static cudaError_t quant_prepare(int hkv, const QuantShape& shape, int num_sms, 
   // more than 1 / (ctas + 1) of the SM's shared memory, see decode_smem_bytes
   const size_t share = 228u * 1024u / (ctas + 1) + 1024u;
   const size_t smem = bytes(S) > share ? bytes(S) : share;
-  *out = QuantPrep{dev, kh, hkv, nw, num_sms, S, static_cast<long long>(num_sms) * ctas, smem};
+  *out = QuantPrep{dev, kh, hkv, nw, num_sms, S, quant_wave(num_sms, ctas, hkv / kh), smem};
   try {
     g_quant_prep<D, SH, MT, SCORED>.push_back(*out);
   } catch (...) {  // (no memory to keep it: worked out again by the next call)
