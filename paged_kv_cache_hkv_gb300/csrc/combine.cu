@@ -26,14 +26,23 @@ namespace pkv {
 //
 // FEW: requests of several rows are on the stream (8-bit pool), their partials in
 // the slots 2 c (a CTA that goes on with the request) and 2 c + 1 (the CTA that
-// begins it). The (row, q head) pairs of a request go to kFewCombineWarps warps in
-// turn (a CTA per row instead took 31 us, cold, where 16 rows were the most and
-// hardly any request had two, and 20 warps for up to 20 pairs 26 us instead of 20).
+// begins it). The (row, q head) pairs of a request go to FEW warps in turn. Most CTAs
+// find nothing to merge, so what counts is that few waves of them run: 4 warps where
+// a request has 8 pairs at most, which are mostly decodes (step of 320 decodes and
+// two chunks, 32 q and 8 kv heads: 11.5 us cold, with 8 warps 15.1, with 10 15.7), else
+// 10, with registers for four CTAs an SM (64 requests of five tokens: 16.7 us, with 8
+// warps 20.0, with 4 31, with 20 26). DEEP's registers leave room for 8.
 constexpr int kCombineLoads = 32;
-constexpr int kFewCombineWarps = 8;
+constexpr int kFewWarps = 4, kFewPairs = 8, kManyWarps = 10, kManyWarpsDeep = 8;
 
-template <int D, int GW, bool DEEP, bool FEW>
-__global__ void __launch_bounds__((FEW ? kFewCombineWarps : GW) * 32) combine_kernel(const DecodeParams p) {
+__host__ __device__ constexpr int combine_threads(int gw, int few) { return (few ? few : gw) * 32; }
+__host__ __device__ constexpr int combine_ctas(bool deep, int few) {  // an SM has room for
+  return deep || few == 0 ? 0 : few == kFewWarps ? 10 : 4;
+}
+
+template <int D, int GW, bool DEEP, int FEW>
+__global__ void __launch_bounds__(combine_threads(GW, FEW), combine_ctas(DEEP, FEW))
+    combine_kernel(const DecodeParams p) {
   const long long c = blockIdx.x;
   const int vg = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -67,7 +76,7 @@ __global__ void __launch_bounds__((FEW ? kFewCombineWarps : GW) * 32) combine_ke
   const int nd = static_cast<int>(owner_cta(pr + nblk - 1, N, Cn) - cf + 1);
   const int ns = si >= 0 ? p.shared_pieces : 0;
   const int npieces = nd + ns;
-  for (int item = warp; item < rows * GW; item += FEW ? kFewCombineWarps : GW) {
+  for (int item = warp; item < rows * GW; item += FEW ? FEW : GW) {
     const int h = item % GW, i = item / GW;
     const long long srow = static_cast<long long>(si) * p.num_q_heads + vg * GW + h;
     const long long sstride = static_cast<long long>(p.shared_num) * p.num_q_heads;
@@ -184,16 +193,19 @@ __global__ void __launch_bounds__((FEW ? kFewCombineWarps : GW) * 32) combine_ke
 // launch longer (31.5 instead of 31.0 us for the mixed step's prefill rows).
 constexpr long long kDeepPieces = 8;
 
+template <int D, int GW, int FEW, int DEEP_FEW>
+static cudaError_t launch_combine_few(const DecodeParams& p, cudaStream_t stream) {
+  return launch_pdl(
+      p.deep_combine ? combine_kernel<D, GW, true, DEEP_FEW> : combine_kernel<D, GW, false, FEW>,
+      dim3(static_cast<unsigned>(p.splits + p.shared_num), static_cast<unsigned>(p.virt_heads)),
+      dim3(combine_threads(GW, p.deep_combine ? DEEP_FEW : FEW)), 0, stream, p);
+}
+
 template <int D, int GW>
 static cudaError_t launch_combine_t(const DecodeParams& p, cudaStream_t stream) {
-  auto kern = p.few > 1 ? (p.deep_combine ? combine_kernel<D, GW, true, true>
-                                          : combine_kernel<D, GW, false, true>)
-                        : (p.deep_combine ? combine_kernel<D, GW, true, false>
-                                          : combine_kernel<D, GW, false, false>);
-  return launch_pdl(kern,
-                    dim3(static_cast<unsigned>(p.splits + p.shared_num),
-                         static_cast<unsigned>(p.virt_heads)),
-                    dim3((p.few > 1 ? kFewCombineWarps : GW) * 32), 0, stream, p);
+  return p.few <= 1                ? launch_combine_few<D, GW, 0, 0>(p, stream)
+         : p.few * GW <= kFewPairs ? launch_combine_few<D, GW, kFewWarps, kFewWarps>(p, stream)
+                                   : launch_combine_few<D, GW, kManyWarps, kManyWarpsDeep>(p, stream);
 }
 
 cudaError_t launch_combine(const DecodeParams& p, int head_dim, int gw, cudaStream_t stream) {
