@@ -676,8 +676,8 @@ struct QuantShape {
 // more warps. A warp takes some 1.5 us for a chunk with one tile among 16 warps, 1.2
 // and 1.5 with two and three among 8; the layout with the least time per chunk and
 // head wins. 64 requests over some 2300 keys, D = 128, us with tiles of 1, 2 and 3:
-// 32 q and 8 kv heads, 4 new tokens 103, 85, 85; 5 tokens 167, 150, 102; 16 tokens
-// 350, 288, 341. 128 requests over 9400 keys, 8 q heads and 1 kv head, 3 tokens: 135,
+// 32 q and 8 kv heads, 4 new tokens 94, 86, 86; 5 tokens 147, 141, 101; 16 tokens
+// 286, 257, 305. 128 requests over 9400 keys, 8 q heads and 1 kv head, 3 tokens: 135,
 // 391, 449.
 static QuantShape quant_shape(int few, int group, int num_kv_heads) {
   const int tiles = (few * group + 7) / 8;
