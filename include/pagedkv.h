@@ -564,8 +564,9 @@ int64_t pkv_release_workspace_size(int32_t num_released, int32_t max_blocks_per_
  *   value = code * 2^(scale - 127).
  * A row is the K (or V) of one token and kv head. With a = its largest magnitude,
  * e the least integer >= -117 with a <= 448 * 2^e: scale = e + 127, and each code
- * is the e4m3 number nearest to x * 2^-e, ties to even. So a value is kept to
- * 2^-4 of its size, or to 2^-10 * 2^e where that is more; every value that a pool
+ * is the e4m3 number nearest to x * 2^-e, ties to even; where that would be 256
+ * and e is 120 (magnitudes of 1.9375 * 2^127 and above) it is 240, for 2^128 is no
+ * bf16. So a value is kept to 2^-4 of its size, or to 2^-10 * 2^e where that is more; every value that a pool
  * holds is a bf16, and rows read back and written again keep their values. A row
  * with an infinity or a NaN is held as NaN in all its elements: codes 0 and scale
  * 255 (0 * 2^128 in fp32). Scale bytes other than 10 .. 247 and 255, and the NaN

@@ -3,8 +3,9 @@
 A K (or V) row of one token and kv head is held as e4m3 codes and one scale byte
 s: value = code * 2^(s - 127). With a the row's largest magnitude, e is the least
 integer >= -117 with a <= 448 * 2^e, s = e + 127, and each code is the e4m3 number
-nearest to x * 2^-e, ties to the even code. A row with an infinity or a NaN is
-held as NaN: codes 0x7f, scale 255. The pages name no such cache: the definition
+nearest to x * 2^-e, ties to the even code, or 240 where that is 256 and e is 120
+(2^128 is no bf16). A row with an infinity or a NaN is held as NaN: codes 0, scale
+255. The pages name no such cache: the definition
 is the library's own.
 """
 
@@ -53,6 +54,7 @@ def quantise_rows(bits):
     lo = hi - 1
     up, down = MAGNITUDES[hi] - y, y - MAGNITUDES[lo]
     code = np.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
+    code = np.where((e == 120)[..., None], np.minimum(code, 0x77), code)  # 0x77: 240
     code = code | np.where(np.signbit(x), 0x80, 0)
     code = np.where(bad[..., None], 0, code)
     return code.astype(np.uint8), np.where(bad, 255, e + 127).astype(np.uint8)

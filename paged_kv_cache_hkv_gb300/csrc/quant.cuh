@@ -7,7 +7,8 @@
 // a scale of 448 / a exactly would gain no accuracy over the next power of two;
 // the power makes the division exact, and code * 2^e, four significant bits, is
 // exactly a bf16: rows read back are exact, and attention over rows turned into
-// bf16 is attention over what the pool holds. A row with an infinity or a NaN
+// bf16 is attention over what the pool holds. (Under 2^120, the scale of rows above
+// 1.75 * 2^127, a code is 240 at most: 256 * 2^120 is no bf16, nor an fp32.) A row with an infinity or a NaN
 // is held as NaN: codes 0 and scale 255, 0 times fp32's 2^128, an infinity. (So no
 // code is a NaN, and a weight of 0 leaves nothing of a masked row.)
 #pragma once
@@ -21,6 +22,8 @@ namespace pkv {
 // 2^-117 times the smallest code, 2^-9, is bf16's (and fp32's) smallest normal number.
 constexpr int kLeastExp = -117;
 constexpr uint32_t kNanScale = 255u;
+constexpr uint32_t kTopScale = 247u;            // 2^120
+constexpr uint32_t kTopPair = 0x7f707f70u;      // two bf16 of 240 * 2^120
 
 // Scale byte of a row whose largest bf16 magnitude has the bits `amax`
 // (exponent E, mantissa M): 448 = 1.75 * 2^8, so e is E - 127 - 8, plus one where
@@ -77,11 +80,22 @@ __device__ __forceinline__ float mul_subnormal(float x, float m) {
   return r;
 }
 
+// The smaller magnitude of every half of two words, its sign kept.
+__device__ __forceinline__ uint32_t least_pair(uint32_t x, uint32_t top) {
+  uint32_t r;
+  asm("min.u16x2 %0, %1, %2;" : "=r"(r) : "r"(x & 0x7fff7fffu), "r"(top));
+  return r | (x & 0x80008000u);
+}
+
 // Eight bf16 to eight codes under the scale byte s.
 __device__ __forceinline__ uint2 quant8(const uint4& v, uint32_t s) {
-  if (s == kNanScale) return make_uint2(0u, 0u);
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if (s >= kTopScale) {
+    if (s == kNanScale) return make_uint2(0u, 0u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = least_pair(w[i], kTopPair);
+  }
   const float m = __uint_as_float((254u - s) << 23);  // 2^(127 - s)
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
