@@ -628,17 +628,22 @@ __global__ void __launch_bounds__(quant_threads(kQuantWarps, MT), MT == 1 ? 2 : 
           const int u = 8 * (tile0 + mt) + 2 * t4 + j, i = u >> gsh, h = u & (G - 1);
           if (i >= n) continue;
           const int head = hk * G + h;
-          // O's weights are 2^(s + v - m_w): to 2^(s - m_s)
-          float f = exp2f(m_w[mt][j] - m_s[mt][j]);
+          // O's weights are 2^(s + v - m_w): to 2^(s - m_s), by 2^-117 to 2^120
+          const float up = m_w[mt][j] - m_s[mt][j];
           if (out_base < 0) {
-            f = SCORED && l == 0.f ? 0.f : f / l;  // no key seen: zeros
+            // The sum l may be 2^20 and more: 2^up / l could be below 2^-126, a zero,
+            // where O times it is not. What is below 2^-64 of 2^up comes last (else
+            // `last` is 1).
+            const float low = fminf(up + 64.f, 0.f), last = exp2f(low);
+            const float f = SCORED && l == 0.f ? 0.f : exp2f(up - low) / l;  // no key seen: zeros
             uint16_t* dst =
                 p.out + ((static_cast<long long>(t) + i) * p.num_q_heads + head) * D + 2 * g;
 #pragma unroll
             for (int i2 = 0; i2 < D / 16; ++i2)
               *reinterpret_cast<uint32_t*>(dst + 16 * i2) =
-                  pack_bf16x2(o[mt][i2][j] * f, o[mt][i2][2 + j] * f);
+                  pack_bf16x2(o[mt][i2][j] * f * last, o[mt][i2][2 + j] * f * last);
           } else {
+            const float f = exp2f(up);
             // n == 1: out_base is (r + c) * V, virtual heads of G or 4 q heads;
             // several rows: a slot of the few-row partials
             const long long slot =

@@ -1,11 +1,13 @@
-"""The 8-bit pool at the ends of bf16's exponent range: every finite row has finite
-values."""
+"""The 8-bit pool at both ends of bf16's exponent range: every finite row has finite
+values, and attention over rows of any size is right relative to their size."""
 
 import numpy as np
 import pytest
 
 import oracle
 from parity import bits_to_f64
+from quant_cases import expected, quantised_step
+from score_cases import key_ranges
 
 torch = pytest.importorskip("torch")
 
@@ -16,7 +18,7 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU containers
 
 from paged_kv_cache_hkv_gb300 import binding  # noqa: E402
 from paged_kv_cache_hkv_gb300.runner import DeviceStep, bf16_to_numpy  # noqa: E402
-from paged_kv_cache_hkv_gb300.synth import RequestSpec, make_step  # noqa: E402
+from paged_kv_cache_hkv_gb300.synth import RequestSpec, f32_to_bf16_bits, make_step  # noqa: E402
 
 
 @pytest.fixture(autouse=True)
@@ -55,3 +57,58 @@ def test_the_largest_rows_read_back_as_the_largest_values(hkv, d, B):
             got, wrote = bits_to_f64(bf16_to_numpy(got)), bits_to_f64(wrote)
             assert np.isfinite(got).all()
             assert (np.abs(got - wrote) <= 2.0 ** -4 * np.abs(wrote)).all()
+
+
+def sized(step, power):
+    """The step's V rows times 2^power (their NaN padding as it is)."""
+    for x in (step.v, step.kv_cache[:, 1]):
+        x[...] = f32_to_bf16_bits(np.ldexp(bits_to_f64(x), power).astype(np.float32))
+
+
+def run_within(step, decode_splits, **scores):
+    ds = DeviceStep(step, quantised=True, write_in_attention=True, decode_splits=decode_splits, **scores)
+    ds.out.fill_(7.0)
+    ds.run()
+    torch.cuda.synchronize()
+    assert binding.pkv_get_device_errors(clear=True) == 0
+    ref, bound = expected(step, quantised_step(step)[2], **scores)
+    got = bits_to_f64(ds.out_host())
+    # numbers below 2^-126 are zeros: the output's, and a weight's product's
+    assert (np.abs(got - ref) <= bound + 2.0 ** -126).all(), np.nanmax(np.abs(got - ref) / (bound + 2.0 ** -126))
+    return got
+
+
+def even_step(rows, d, group, seed):
+    """Long and short requests whose keys weigh about the same: the sums of the
+    softmax are as large as their numbers of keys."""
+    specs = [RequestSpec(c, 1 + i % rows) for i, c in enumerate((2300, 40, 1100, 0, 17, 3100))]
+    step = make_step(specs, num_q_heads=2 * group, num_kv_heads=2, head_dim=d, seed=seed)
+    step.q = f32_to_bf16_bits((bits_to_f64(step.q) / 32).astype(np.float32))
+    return step
+
+
+@pytest.mark.parametrize("mask", [None, "prefix"])
+@pytest.mark.parametrize("splits", [None, 1, 3])
+@pytest.mark.parametrize("rows,d,group", [(1, 128, 4), (4, 128, 4), (5, 64, 8), (3, 64, 1)])
+@pytest.mark.parametrize("power", [-112, -105])
+def test_v_rows_of_the_smallest_sizes(power, rows, d, group, splits, mask):
+    step = even_step(rows, d, group, seed=rows)
+    sized(step, power)
+    scores = dict(zip(("key_begin", "key_end"), key_ranges(step, mask, seed=d))) if mask else {}
+    got = run_within(step, splits, **scores)
+    assert np.abs(got).max() > 0
+
+
+@pytest.mark.parametrize("splits", [None, 1, 2])
+def test_v_rows_of_both_ends_in_one_request(splits):
+    """Requests of tiny rows, of huge ones, and of both: where a piece of a request holds
+    huge rows, what tiny ones add is beyond the result's bits."""
+    step = even_step(1, 128, 4, seed=9)
+    tiny = {int(b) for b in step.block_table[0] if b >= 0} | {int(b) for b in step.block_table[2][:30] if b >= 0}
+    small = np.array(sorted(tiny))
+    big = np.array([b for b in range(step.num_blocks) if b not in tiny])
+    for blocks, power in ((small, -112), (big, 110)):
+        x = step.kv_cache[blocks, 1]
+        step.kv_cache[blocks, 1] = f32_to_bf16_bits(np.ldexp(bits_to_f64(x), power).astype(np.float32))
+    step.v = f32_to_bf16_bits(np.ldexp(bits_to_f64(step.v), -112).astype(np.float32))
+    run_within(step, splits)
