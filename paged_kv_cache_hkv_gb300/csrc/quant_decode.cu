@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(quant_threads(kQuantWarps, MT), MT == 1 ? 2 : 
           if (i >= n) continue;
           const int head = hk * G + h;
           // O's weights are 2^(s + v - m_w): to 2^(s - m_s), by 2^-117 to 2^120
-          const float up = m_w[mt][j] - m_s[mt][j];
+          float up = m_w[mt][j] - m_s[mt][j];
           if (out_base < 0) {
             // The sum l may be 2^20 and more: 2^up / l could be below 2^-126, a zero,
             // where O times it is not. What is below 2^-64 of 2^up comes last (else
@@ -643,6 +643,14 @@ __global__ void __launch_bounds__(quant_threads(kQuantWarps, MT), MT == 1 ? 2 : 
               *reinterpret_cast<uint32_t*>(dst + 16 * i2) =
                   pack_bf16x2(o[mt][i2][j] * f * last, o[mt][i2][2 + j] * f * last);
           } else {
+            // The combine sums l * V: a piece of V's above 2^72 or so is kept as 2^-48 of
+            // itself under a maximum of 48 more, the same to the combine, so that no sum
+            // of fewer than 2^40 weights passes fp32's largest number.
+            if (up > 64.f) {
+              up -= 48.f;
+              l *= 0x1p-48f;
+              m_s[mt][j] += 48.f;
+            }
             const float f = exp2f(up);
             // n == 1: out_base is (r + c) * V, virtual heads of G or 4 q heads;
             // several rows: a slot of the few-row partials

@@ -99,6 +99,22 @@ def test_v_rows_of_the_smallest_sizes(power, rows, d, group, splits, mask):
     assert np.abs(got).max() > 0
 
 
+@pytest.mark.parametrize("mask", [None, "prefix"])
+@pytest.mark.parametrize("splits", [None, 1, 3])
+@pytest.mark.parametrize("rows,d,group", [(1, 128, 4), (4, 128, 4), (5, 64, 8), (3, 64, 1)])
+@pytest.mark.parametrize("power", [70, 118, "top"])
+def test_v_rows_of_the_largest_sizes(power, rows, d, group, splits, mask):
+    step = even_step(rows, d, group, seed=rows + 50)
+    if power == "top":  # one sign a dim: the outputs are as large as the rows
+        sign = (np.arange(d) % 3 == 0).astype(np.uint16) << np.uint16(15)
+        for x in (step.v, step.kv_cache[:, 1]):
+            x[...] = np.where((x & 0x7FFF) > 0x7F80, x, sign | np.uint16(0x7F7F))
+    else:
+        sized(step, power)
+    scores = dict(zip(("key_begin", "key_end"), key_ranges(step, mask, seed=d))) if mask else {}
+    assert np.isfinite(run_within(step, splits, **scores)).all()
+
+
 @pytest.mark.parametrize("splits", [None, 1, 2])
 def test_v_rows_of_both_ends_in_one_request(splits):
     """Requests of tiny rows, of huge ones, and of both: where a piece of a request holds
