@@ -129,27 +129,31 @@ __device__ __forceinline__ void quant_token_rows(const WriteRowsArgs& w, long lo
   if (slot < 0) return;
   const long long blk = slot >> w.shift, off = slot & ((1 << w.shift) - 1);
   // (the whole warp: the row's largest magnitude goes by shuffles)
-  auto store = [&](const uint4& val, int v, int e) {
+  bool rare = false;
+  auto store = [&](const uint4& val, int v, int e, bool usual) {
     uint32_t m = amax8(val);
 #pragma unroll
     for (int d = 1; d < D / 8; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
     if (e >= w.vec_per_row) return;
     const uint32_t s = scale_byte(m);
     const long long word = (((blk * 2 + v) << w.shift) + off) * w.vec_per_row + e;
-    reinterpret_cast<uint2*>(w.pool)[word] = quant8(val, s);
+    rare |= usual && s >= kTopScale;
+    reinterpret_cast<uint2*>(w.pool)[word] = usual ? quant8_usual(val, s) : quant8(val, s);
     if (e % (D / 8) == 0) w.scales[word / (D / 8)] = static_cast<uint8_t>(s);
   };
 #pragma unroll
   for (int i = 0; i < kQuantPrefetch; ++i)
     if (32 * i < w.vec_per_row) {
-      store(x[0][i], 0, lane + 32 * i);
-      store(x[1][i], 1, lane + 32 * i);
+      store(x[0][i], 0, lane + 32 * i, true);
+      store(x[1][i], 1, lane + 32 * i, true);
     }
-  for (int e0 = 32 * kQuantPrefetch; e0 < w.vec_per_row; e0 += 32)  // rows over 2 KB
+  // Rows over 2 KB; and all words once more where one is under a rare scale, whose
+  // handling beside each of the eight stores above took 0.4 us of a step of 11.
+  for (int e0 = __any_sync(0xffffffffu, rare) ? 0 : 32 * kQuantPrefetch; e0 < w.vec_per_row; e0 += 32)
 #pragma unroll
     for (int v = 0; v < 2; ++v)
       store(e0 + lane < w.vec_per_row ? __ldg(src[v] + e0 + lane) : make_uint4(0, 0, 0, 0), v,
-            e0 + lane);
+            e0 + lane, false);
 }
 
 }  // namespace pkv
