@@ -426,8 +426,11 @@ __global__ void __launch_bounds__(quant_threads(kQuantWarps, MT), MT == 1 ? 2 : 
             qs[(mt * (D / 16) + x) * 32] = v;
           }
         }
-        // (a row with an infinity or a NaN makes all its scores NaN)
-        const float f_mine = p.scale_log2 * scale_value(sb);
+        // A row with an infinity or a NaN makes all its scores NaN. So does a place
+        // without a row: its zeros would score 0 for keys that no row sees, under whatever
+        // V scale lies there, and a rescale that these ask for would move the bits
+        // of the tile's rows. (A NaN asks for none and stays in its own place.)
+        const float f_mine = i < n ? p.scale_log2 * scale_value(sb) : __uint_as_float(0x7fffffffu);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           fq[mt][j] = __shfl_sync(0xffffffffu, f_mine, 8 * t4 + 4 * j);
@@ -436,7 +439,7 @@ __global__ void __launch_bounds__(quant_threads(kQuantWarps, MT), MT == 1 ? 2 : 
           l_run[mt][j] = 0.f;
           if constexpr (SCORED) {
             lim_lo[mt][j] = ref[mt][j] = 0;
-            lim_hi[mt][j] = 0x7fffffff;  // (a place without a unit masks nothing)
+            lim_hi[mt][j] = 0x7fffffff;  // (a place without a row masks nothing)
             slope2[mt][j] = 0.f;
             if (ij < n) {
               const int pos = L - n + ij;
