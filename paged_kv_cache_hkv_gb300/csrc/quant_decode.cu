@@ -142,8 +142,8 @@ __global__ void __launch_bounds__(quant_threads(kQuantWarps, MT), MT == 1 ? 2 : 
   const int KH = p.slab_heads, WPH = p.warps_per_head, NW = KH * WPH, HKV = p.num_kv_heads;
   const uint32_t S = static_cast<uint32_t>(p.stages);
   const QuantLayout lay(D, KH, HKV, NW, MT, p.stages);
-  // of a stage: (flags, first key, out_base, which of the 16 keys hold rows that the
-  // request sees: first | end << 8), and with kFirst (batch row, rows, keys, shared keys)
+  // of a stage: (flags, first key, out_base, keys of the 16 in front of the end of what
+  // the request sees), and with kFirst (batch row, rows, keys, shared keys)
   int4* meta = reinterpret_cast<int4*>(base + lay.meta_off);
   uint64_t* full = reinterpret_cast<uint64_t*>(base + lay.bar_off);
   uint64_t* empty = full + S;
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(quant_threads(kQuantWarps, MT), MT == 1 ? 2 : 
         const bool last = blk == nblk - 1 || x == x1 - 1;
         meta[2 * s] = make_int4((new_piece ? kFirst : 0) | (last ? kLast : 0) | (valid ? 0 : kInvalid),
                                 k0, out_base,
-                                max(0, q.lo - k0) | (max(0, min(kChunkKeys, q.hi - k0)) << 8));
+                                min(kChunkKeys, q.hi - k0));
         if (new_piece) meta[2 * s + 1] = make_int4(q.t, q.n, q.L, key_base(r));
         unsigned char* stage = base + s * lay.stage_bytes;
         unsigned char* sc = stage + lay.kv_bytes;
@@ -586,15 +586,29 @@ __global__ void __launch_bounds__(quant_threads(kQuantWarps, MT), MT == 1 ? 2 : 
         pb[mt][1] = transpose8(pack_f16x2(pv[2], pv[3]));
       }
       // ---- O^T += V^T P^T
+      // Rows that no unit sees may hold NaN codes, which weight 0 does not undo: those
+      // behind the request's last key, and with key ranges any. (A NaN score counts as
+      // unseen: its weight is NaN whatever the codes are.)
       uint32_t keep[2] = {0xffffffffu, 0xffffffffu};  // of keys 2 t4, 2 t4 + 1 and those + 8
-      const bool edge = m.w != (kChunkKeys << 8);
+      const bool edge = SCORED ? !whole : m.w < kChunkKeys;
       if (edge) {
-        // rows that are not the request's may hold NaN codes, which weight 0 does not undo
-        const int a = m.w & 255, z = m.w >> 8;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int j = 8 * x + 2 * t4;
-          keep[x] = (j >= a && j < z ? 0xffffu : 0u) | (j + 1 >= a && j + 1 < z ? 0xffff0000u : 0u);
+          bool lo, hi;
+          if constexpr (SCORED) {
+            bool seen = false;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+              seen = seen || sv[mt][2 * x] > -INFINITY || sv[mt][2 * x + 1] > -INFINITY;
+            const uint32_t b = __ballot_sync(0xffffffffu, seen) >> (8 * t4);  // four lanes a key
+            lo = b & 0xfu;
+            hi = b & 0xf0u;
+          } else {
+            const int j = 8 * x + 2 * t4;
+            lo = j < m.w;
+            hi = j + 1 < m.w;
+          }
+          keep[x] = (lo ? 0xffffu : 0u) | (hi ? 0xffff0000u : 0u);
         }
       }
 #pragma unroll
