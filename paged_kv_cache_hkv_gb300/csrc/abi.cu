@@ -238,10 +238,10 @@ WsLayout ws_layout(int num_reqs, int virt_heads, int gw, int head_dim, long long
   return w;
 }
 
-// The further arrays of a call on the 8-bit pool with at most `few` rows (more
-// than one) of a request on the decode stream.
+// The further arrays of a call on the 8-bit pool that leaves partials of at most
+// `few_rows` rows, two per CTA and row of a request on the decode stream.
 void quant_ws_layout(WsLayout* w, int num_reqs, int max_blocks, int num_q_heads, int head_dim,
-                     long long splits, int few) {
+                     long long few_rows) {
   size_t off = w->total;
   w->ex_first = off;
   off += round256((num_reqs + 1) * sizeof(int32_t));
@@ -249,7 +249,7 @@ void quant_ws_layout(WsLayout* w, int num_reqs, int max_blocks, int num_q_heads,
   off += round256((num_reqs + 2) * sizeof(int32_t));
   w->ex_table = off;
   off += round256(static_cast<size_t>(num_reqs) * max_blocks * sizeof(int32_t));
-  const size_t rows = static_cast<size_t>(2 * splits) * few * num_q_heads;
+  const size_t rows = static_cast<size_t>(few_rows) * num_q_heads;
   w->few_ml = off;
   off += round256(rows * sizeof(float2));
   w->few_o = off;
@@ -260,6 +260,19 @@ void quant_ws_layout(WsLayout* w, int num_reqs, int max_blocks, int num_q_heads,
 // bytes of a block expanded to bf16
 size_t expanded_block_bytes(const pkv_cache_layout& l) {
   return static_cast<size_t>(4) * l.block_size * l.num_kv_heads * l.head_dim;
+}
+
+// Ranges and rows of few-row partials that an 8-bit call's workspace is laid out for:
+// the most of any number of rows a request (so that one workspace serves every step),
+// or with a caller's splits those and as many rows as there can be.
+void quant_ws_splits(int num_kv_heads, int group, int num_sms, const pkv_attention_options* opt,
+                     long long* splits, long long* few_rows) {
+  if (opt && opt->decode_splits > 0) {
+    *splits = opt->decode_splits;
+    *few_rows = 2ll * opt->decode_splits * (pkv::kFewUnits / group);
+  } else {
+    pkv::quant_most_splits(num_kv_heads, group, num_sms, splits, few_rows);
+  }
 }
 
 // Options of a call on the 8-bit pool: the most rows of a request on the decode
@@ -542,15 +555,12 @@ static int32_t attention_impl(void* out, const void* q, int64_t q_row_stride, co
     return PKV_ERR_BAD_SHAPE;
   const int gw = pkv::decode_heads_per_warp(group);
   const int virt = layout.num_kv_heads * (group / gw);
-  // (8-bit pool: laid out for the most splits and rows, as its size was asked for)
-  const long long ws_splits =
-      quant && !(options && options->decode_splits > 0)
-          ? pkv::quant_most_splits(layout.num_kv_heads, group, d->num_sms)
-          : splits;
+  // (8-bit pool: laid out for the most of any step, as its size was asked for)
+  long long ws_splits = splits, few_rows = 0;
+  if (quant) quant_ws_splits(layout.num_kv_heads, group, d->num_sms, options, &ws_splits, &few_rows);
   WsLayout wl = ws_layout(num_reqs, virt, gw, layout.head_dim, ws_splits, sh, num_q_heads);
   if (quant) {
-    quant_ws_layout(&wl, num_reqs, max_blocks_per_req, num_q_heads, layout.head_dim, ws_splits,
-                    pkv::kFewUnits / group);
+    quant_ws_layout(&wl, num_reqs, max_blocks_per_req, num_q_heads, layout.head_dim, few_rows);
     if (workspace_bytes < wl.quant_total + expanded_block_bytes(layout)) return PKV_ERR_WORKSPACE;
   }
   if (workspace_bytes < wl.total) return PKV_ERR_WORKSPACE;
@@ -894,18 +904,18 @@ int64_t pkv_quant_attention_workspace_size(int32_t num_reqs, int32_t max_blocks_
   st = device_info(&d);
   if (st != PKV_OK) return st;
   const int group = num_q_heads / layout.num_kv_heads;
-  long long splits = pkv::quant_most_splits(layout.num_kv_heads, group, d->num_sms);
+  long long splits = 0, few_rows = 0;
   int few = 0;
   st = quant_options(options, group, &few, &splits);
   if (st != PKV_OK) return st;
+  quant_ws_splits(layout.num_kv_heads, group, d->num_sms, options, &splits, &few_rows);
   SharedHint sh;
   st = shared_hint(options, layout, group, num_reqs, d->num_sms, &sh);
   if (st != PKV_OK) return st;
   const int gw = pkv::decode_heads_per_warp(group);
   const int virt = layout.num_kv_heads * (group / gw);
   WsLayout wl = ws_layout(num_reqs, virt, gw, layout.head_dim, splits, sh, num_q_heads);
-  quant_ws_layout(&wl, num_reqs, max_blocks_per_req, num_q_heads, layout.head_dim, splits,
-                  pkv::kFewUnits / group);
+  quant_ws_layout(&wl, num_reqs, max_blocks_per_req, num_q_heads, layout.head_dim, few_rows);
   const int64_t keys = chunk_keys + sh.len;
   const int64_t blocks = (keys + layout.block_size - 1) / layout.block_size + 1;
   return static_cast<int64_t>(wl.quant_total + blocks * expanded_block_bytes(layout));

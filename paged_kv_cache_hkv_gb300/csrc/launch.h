@@ -43,7 +43,9 @@ struct AttnWorkspace {
   uint4* ex_pool;        // [ex_capacity] bf16 blocks
   int ex_capacity;
   // 8-bit pool: partials of requests with several rows on the decode stream, two
-  // per CTA (the request it goes on with, the one it leaves): [2 C][few][Hq]
+  // per CTA (the request it goes on with, the one it leaves): [2 C][few][Hq]. (The
+  // more rows, the fewer CTAs a wave has: for the largest C times the largest few it
+  // would be five times as large, 162 MB instead of 30 with 32 q and 8 kv heads.)
   float2* few_ml;
   float* few_o;          // [2 C][few][Hq][D]
 };
@@ -233,8 +235,10 @@ constexpr int kFewUnits = 64;
 // Requests of up to this many new tokens are on the 8-bit pool's decode stream by
 // default (quant_decode.cu); `few` below: of up to how many they are.
 int quant_few_rows(int max_query_len, int group);
-// The most splits that quant_full_wave_splits gives for any `few`.
-long long quant_most_splits(int num_kv_heads, int group, int num_sms);
+// The most splits that quant_full_wave_splits gives for any `few`, and the most
+// rows of partials, two per split and row, that it asks for together with its `few`.
+void quant_most_splits(int num_kv_heads, int group, int num_sms, long long* splits,
+                       long long* few_rows);
 cudaError_t quant_full_wave_splits(int head_dim, int num_kv_heads, int group, int block_shift,
                                    int few, bool scored, int num_sms, long long* splits);
 cudaError_t launch_quant_decode(const AttnArgs& a, const AttnWorkspace& ws,

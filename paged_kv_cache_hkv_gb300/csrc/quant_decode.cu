@@ -755,14 +755,16 @@ static long long quant_wave(int num_sms, int ctas, int slabs) {
   return c > 1 ? c : 1;
 }
 
-long long quant_most_splits(int num_kv_heads, int group, int num_sms) {
-  long long most = 1;
+void quant_most_splits(int num_kv_heads, int group, int num_sms, long long* splits,
+                       long long* few_rows) {
+  *splits = 1;
+  *few_rows = 0;  // (a request of one row leaves its partials elsewhere)
   for (int n = 1; n <= kFewUnits / group; ++n) {
     const QuantShape s = quant_shape(n, group, num_kv_heads);
     const long long c = quant_wave(num_sms, s.ctas, num_kv_heads / s.heads);
-    if (c > most) most = c;
+    if (c > *splits) *splits = c;
+    if (n > 1 && 2 * c * n > *few_rows) *few_rows = 2 * c * n;
   }
-  return most;
 }
 
 // Launch shape of one instantiation on one device, worked out once.
