@@ -572,7 +572,9 @@ int64_t pkv_release_workspace_size(int32_t num_released, int32_t max_blocks_per_
  * 255 (0 * 2^128 in fp32). Scale bytes other than 10 .. 247 and 255, and the NaN
  * codes, stand in no row that was written by this library; what the calls make of
  * them is undefined.
- * Layout limits are the bf16 pool's.
+ * Layout limits are the bf16 pool's; attention has two chunks' codes and the scales
+ * of all kv heads in shared memory: fewer than 1800 kv heads always fit, with more
+ * the call may return PKV_ERR_UNSUPPORTED.
  */
 
 /* pkv_quant_kv_write -- pkv_paged_kv_write into the 8-bit pool: quantise each new

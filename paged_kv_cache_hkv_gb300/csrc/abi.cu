@@ -527,16 +527,21 @@ static int32_t attention_impl(void* out, const void* q, int64_t q_row_stride, co
     return PKV_ERR_MISALIGNED;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return PKV_ERR_WORKSPACE;
 
-  DeviceInfo* d;
-  st = device_info(&d);
-  if (st != PKV_OK) return st;
   const int group = num_q_heads / layout.num_kv_heads;
   long long splits = 0;
   a.few = 1;
   if (quant) {
     a.few = pkv::quant_few_rows(max_query_len, group);
     st = quant_options(options, group, &a.few, &splits);
-    if (st == PKV_OK && splits == 0) {
+    if (st != PKV_OK) return st;
+    if (!pkv::quant_stages_fit(layout.head_dim, layout.num_kv_heads, group, a.few))
+      return PKV_ERR_UNSUPPORTED;
+  }
+  DeviceInfo* d;
+  st = device_info(&d);
+  if (st != PKV_OK) return st;
+  if (quant) {
+    if (splits == 0) {
       const cudaError_t e = pkv::quant_full_wave_splits(
           layout.head_dim, layout.num_kv_heads, group, block_shift_of(layout.block_size), a.few,
           a.scored, d->num_sms, &splits);

@@ -244,6 +244,9 @@ cudaError_t quant_full_wave_splits(int head_dim, int num_kv_heads, int group, in
 cudaError_t launch_quant_decode(const AttnArgs& a, const AttnWorkspace& ws,
                                 const CUtensorMap& kv_map, long long splits, int num_sms,
                                 cudaStream_t stream, void** trace);
+// Whether a CTA of the 8-bit decode has shared memory for two stages, each with the
+// scales of all kv heads.
+bool quant_stages_fit(int head_dim, int num_kv_heads, int group, int few);
 // kv heads of one CTA of the 8-bit decode
 int quant_slab_heads(int num_kv_heads, int group, int few);
 

@@ -746,6 +746,14 @@ int quant_slab_heads(int num_kv_heads, int group, int few) {
   return quant_shape(few, group, num_kv_heads).heads;
 }
 
+constexpr int kQuantSmem = 227 * 1024;
+
+bool quant_stages_fit(int head_dim, int num_kv_heads, int group, int few) {
+  const QuantShape s = quant_shape(few, group, num_kv_heads);
+  return QuantLayout(head_dim, s.heads, num_kv_heads, s.heads * s.wph, s.mt, kQuantMinStages).total +
+             1024u <= kQuantSmem;
+}
+
 // Ranges of the stream by default: the CTAs of all slabs of kv heads are one wave of
 // the device. (A wave per slab instead, 64 requests over some 2300 keys: 16 q and kv
 // heads, D = 64, 70 us instead of 65; 40 of D = 128 247 instead of 228, four tokens
@@ -784,7 +792,7 @@ template <int D, int SH, int MT, bool SCORED>
 static cudaError_t quant_prepare(int hkv, const QuantShape& shape, int num_sms, QuantPrep* out) {
   auto kern = quant_decode_kernel<D, SH, MT, SCORED>;
   const int kh = shape.heads, nw = kh * shape.wph;
-  cudaError_t e = smem_attr_once(kern, 227 * 1024, g_quant_attr_done<D, SH, MT, SCORED>);
+  cudaError_t e = smem_attr_once(kern, kQuantSmem, g_quant_attr_done<D, SH, MT, SCORED>);
   if (e != cudaSuccess) return e;
   int dev = 0;
   e = cudaGetDevice(&dev);
