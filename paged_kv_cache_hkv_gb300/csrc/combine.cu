@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(combine_threads(GW, FEW), combine_ctas(DEEP, F
   const long long N = p.hdr[kHdrDecodeBlocks];
   const long long cf = owner_cta(pr, N, Cn);
   if (si < 0 && (cf != c - 1 || in_shared_run(r))) return;
-  const int row = __ldg(p.qsl + r);
+  const int row = FEW ? __ldg(p.qsl + r) : 0;
   const int rows = FEW ? __ldg(p.qsl + r + 1) - row : 1;
   const bool few = FEW && rows > 1;
   // pieces j < nd: the decode partial of CTA cf + j, in slot (r + cf + j) * V
@@ -76,8 +76,8 @@ __global__ void __launch_bounds__(combine_threads(GW, FEW), combine_ctas(DEEP, F
   const int nd = static_cast<int>(owner_cta(pr + nblk - 1, N, Cn) - cf + 1);
   const int ns = si >= 0 ? p.shared_pieces : 0;
   const int npieces = nd + ns;
-  for (int item = warp; item < rows * GW; item += FEW ? FEW : GW) {
-    const int h = item % GW, i = item / GW;
+  auto merge = [&](int item) {
+    const int h = FEW ? item % GW : item, i = FEW ? item / GW : 0;
     const long long srow = static_cast<long long>(si) * p.num_q_heads + vg * GW + h;
     const long long sstride = static_cast<long long>(p.shared_num) * p.num_q_heads;
 
@@ -172,8 +172,9 @@ __global__ void __launch_bounds__(combine_threads(GW, FEW), combine_ctas(DEEP, F
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, off);
     const float inv = p.scored && Ls == 0.f ? 0.f : 1.f / Ls;  // no key seen: zeros
-    uint16_t* dst =
-        p.out + ((static_cast<long long>(row) + i) * p.num_q_heads + vg * GW + h) * D + lane * E;
+    // (a single row's place is read here: held through the loops it spilled a register)
+    const long long out_row = FEW ? static_cast<long long>(row) + i : __ldg(p.qsl + r);
+    uint16_t* dst = p.out + (out_row * p.num_q_heads + vg * GW + h) * D + lane * E;
     if constexpr (E == 4) {
       uint2 ov;
       ov.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
@@ -182,6 +183,11 @@ __global__ void __launch_bounds__(combine_threads(GW, FEW), combine_ctas(DEEP, F
     } else {
       *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
     }
+  };
+  if constexpr (FEW > 0) {
+    for (int item = warp; item < rows * GW; item += FEW) merge(item);
+  } else {
+    merge(warp);
   }
 }
 
