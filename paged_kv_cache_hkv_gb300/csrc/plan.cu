@@ -72,8 +72,10 @@ __device__ __forceinline__ bool lengths_bad(const AttnArgs& a, int r, int q0, in
 // them), is-prefill, prefill work items.
 // A decode request that takes its shared prefix from the shared items
 // streams only the chunks past the prefix.
-// SCORED: it streams the chunks of its row's key range.
-template <bool SCORED>
+// SCORED: it streams the chunks of its rows' key ranges. (QUANT: several rows can be.
+// The bf16 pool's decodes have one; with the loop over rows its scored calls took
+// 0.3 us more.)
+template <bool SCORED, bool QUANT>
 __device__ __forceinline__ Int3 plan_counts(const AttnArgs& a, const AttnWorkspace& ws, int r,
                                             int tile_q, bool flag) {
   Int3 v{0, 0, 0};
@@ -87,7 +89,8 @@ __device__ __forceinline__ Int3 plan_counts(const AttnArgs& a, const AttnWorkspa
     const int i = r - a.shared_first;
     if constexpr (SCORED) {
       const bool shared = a.shared_num > 0 && i >= 0 && i < a.shared_num && ws.casc_use[i];
-      v.a = range_chunks(rows_keys(a.score, q0, c, n, L, shared ? a.shared_len : 0));
+      const int base = shared ? a.shared_len : 0;
+      v.a = range_chunks(QUANT ? rows_keys(a.score, q0, c, n, L, base) : row_keys(a.score, q0, c, L, base));
     } else if (a.shared_num > 0 && i >= 0 && i < a.shared_num && ws.casc_use[i]) {
       v.a -= a.shared_len / kChunkKeys;
     }
@@ -279,7 +282,7 @@ __device__ void plan_block(const AttnArgs& a, const AttnWorkspace& ws, int tile_
   const int r0 = min(R, static_cast<int>(threadIdx.x) * per), r1 = min(R, r0 + per);
   Int3 sum{0, 0, 0};
   for (int r = r0; r < r1; ++r) {
-    const Int3 v = plan_counts<SCORED>(a, ws, r, tile_q, true);
+    const Int3 v = plan_counts<SCORED, QUANT>(a, ws, r, tile_q, true);
     sum.a += v.a;
     sum.b += v.b;
     sum.c += v.c;
@@ -293,7 +296,7 @@ __device__ void plan_block(const AttnArgs& a, const AttnWorkspace& ws, int tile_
   if (N == 0)
     for (long long c = threadIdx.x; c < C; c += blockDim.x) ws.bound[c] = -1;
   for (int r = r0; r < r1; ++r) {
-    const Int3 v = plan_counts<SCORED>(a, ws, r, tile_q, false);
+    const Int3 v = plan_counts<SCORED, QUANT>(a, ws, r, tile_q, false);
     if (v.a > 0) {
       const long long c_lo = (static_cast<long long>(run.a) * C + N - 1) / N;
       long long c_hi = ((static_cast<long long>(run.a) + v.a) * C + N - 1) / N;
