@@ -3,6 +3,7 @@
 // expanded to bf16 for the tensor-core prefill kernel. The format: quant.cuh.
 #include "launch.h"
 #include "quant.cuh"
+#include "row_split.h"
 #include "write_rows.cuh"
 
 namespace pkv {
@@ -19,23 +20,6 @@ static __device__ uint32_t g_errors_quant;
 // words a thread and two CTAs an SM were 10% and 15% slower.
 constexpr int kQuantVecs = 2;
 constexpr int kQuantThreads = 512;
-
-// Word w of such a stream: its token and its place in the token's 2 vec_per_row words.
-// Below 2^31 words by a product with the divisor's reciprocal to 32 bits above its
-// size, which is exact there (with the plain division and 64-bit slots the write
-// issued in 83% of its cycles and took 23.8 us for the 16001 rows).
-struct RowSplit {
-  uint32_t mul, shift;
-  int row_pair, vec_per_row;
-  template <typename Index>
-  __device__ __forceinline__ int operator()(Index w, Index* tok) const {
-    if constexpr (sizeof(Index) == 4)
-      *tok = static_cast<Index>((__umulhi(mul, static_cast<uint32_t>(w)) + static_cast<uint32_t>(w)) >> shift);
-    else
-      *tok = w / row_pair;
-    return static_cast<int>(w - *tok * row_pair);
-  }
-};
 
 // Pool row (block * 2 + k|v) * B + offset of a slot in the pool (below 2^31 rows).
 __device__ __forceinline__ int pool_row(int slot, int kv, int shift) {
@@ -248,19 +232,6 @@ static int row_grid(long long words) {
 // Whether a launch's word numbers, those past the end included, stay below 2^31.
 static bool short_index(long long words) {
   return words + 2ll * row_grid(words) * kQuantThreads * kQuantVecs < (1ll << 31);
-}
-
-// w / d = (umulhi(mul, w) + w) >> shift for w < 2^31, with 2^(shift - 1) < d <= 2^shift
-// and mul = floor(2^32 (2^shift - d) / d) + 1: (2^32 + mul) d exceeds 2^(32 + shift)
-// by at most d <= 2^shift.
-static RowSplit row_split(int vec_per_row) {
-  RowSplit s;
-  s.vec_per_row = vec_per_row;
-  s.row_pair = 2 * vec_per_row;
-  s.shift = 0;
-  while ((1ll << s.shift) < s.row_pair) ++s.shift;
-  s.mul = static_cast<uint32_t>(((((1ull << s.shift) - s.row_pair) << 32) / s.row_pair) + 1);
-  return s;
 }
 
 template <int D>
