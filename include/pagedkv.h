@@ -571,7 +571,8 @@ int64_t pkv_release_workspace_size(int32_t num_released, int32_t max_blocks_per_
  * with an infinity or a NaN is held as NaN in all its elements: codes 0 and scale
  * 255 (0 * 2^128 in fp32). Scale bytes other than 10 .. 247 and 255, and the NaN
  * codes, stand in no row that was written by this library; what the calls make of
- * them is undefined.
+ * them is undefined, but for keys that no query row sees: those reach no output,
+ * and no bit of it, whatever they hold.
  * Layout limits are the bf16 pool's; attention has two chunks' codes and the scales
  * of all kv heads in shared memory: fewer than 1800 kv heads always fit, with more
  * the call may return PKV_ERR_UNSUPPORTED.
@@ -624,6 +625,14 @@ int32_t pkv_quant_copy_blocks(void* dst_pool, uint8_t* dst_scales, int32_t dst_n
  * a shared prefix are expanded to bf16 in the workspace first, and the tensor-core
  * prefill kernel runs over those: the results of such rows are bit for bit those
  * of pkv_paged_attention over the same values.
+ *
+ * Precision: fp32 scores and sums. On the decode kernels a weight times V's scale is
+ * an f16: 11 bits down to 2^-14 of the largest such product that a CTA meets in the
+ * request, then off by 2^-25 of it at most, and zero below that. n keys together
+ * lose n * 2^-25 of the largest V or less: of note where a V row is 2^14 times as
+ * large as the others, in the dims that it leaves small. Outputs below
+ * 2^-126 are zeros. Rows of chunks and a shared prefix: bf16 weights, and fp32 sums
+ * of weight * V, which pass the largest number where V is near it.
  *
  * workspace      at least pkv_quant_attention_workspace_size() bytes, 256-byte
  *                aligned, private to this call while it runs. What lies behind the

@@ -229,8 +229,8 @@ cudaError_t launch_quant_copy(void* dst, uint8_t* dst_scales, int dst_num_blocks
 cudaError_t launch_expand(const AttnArgs& a, const ExpandArgs& x, int num_sms,
                           cudaStream_t stream);
 
-// Query rows x q heads of one kv head that the 8-bit decode holds at most: 8
-// warps of 16.
+// Query rows x q heads of one kv head (units) that the 8-bit decode holds at most:
+// eight tiles of 8, in as many warps of a tile each or in fewer of two or three.
 constexpr int kFewUnits = 64;
 // Requests of up to this many new tokens are on the 8-bit pool's decode stream by
 // default (quant_decode.cu); `few` below: of up to how many they are.

@@ -16,8 +16,9 @@ static __device__ uint32_t g_errors_quant;
 // its largest magnitude by shuffles; the first of them stores the scale. Every
 // thread issues the loads of its kQuantVecs words before it uses the first. A CTA
 // per kQuantVecs * kQuantThreads words, however many: 16001 rows of 8 x 128 take
-// 21.1 us cold (floor 14.2), the read of 131072 such rows 123 us (floor 119); four
-// words a thread and two CTAs an SM were 10% and 15% slower.
+// 21.1 us cold (floor 14.2; with the words stored unconverted 17 of 20.9 on warm
+// buffers), the read of 131072 such rows 123 us (floor 119); four words a thread and
+// two CTAs an SM were 10% and 15% slower.
 constexpr int kQuantVecs = 2;
 constexpr int kQuantThreads = 512;
 

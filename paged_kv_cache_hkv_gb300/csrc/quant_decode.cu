@@ -23,8 +23,9 @@
 //     S^T's registers through movmatrix.
 // V's scales 2^v go into the exponent of P: weight 2^(s + v - M), M the running
 // maximum of s + v, in f16 (11 bits; below 2^-14 of the largest weight 2^-25 of
-// it). The sum of weights keeps a running maximum of s of its own, so that rows
-// of tiny or huge V change nothing in it, and O is scaled to it at the end.
+// it: seen in dims that a V row far larger than the others leaves small). The sum
+// of weights keeps a running maximum of s of its own, so that rows of tiny or huge
+// V change nothing in it, and O is scaled to it at the end.
 // (mma.m16n8k32 on the codes themselves is no shortcut: by the counters each becomes
 // conversions of both operands and f16 products, 427 instructions a chunk and warp
 // instead of 332, and 244 us instead of 207 on 8 decodes of 32767-131071 keys,
